@@ -1,7 +1,8 @@
 /*
  * rf.h — C ABI of librf.so: the RidgeFill upper-layer KV fill, its calibration
- * statistics and closed-form ridge solve, and the cross-model per-head ridge
- * mapper, for one NVIDIA GB300 (sm_103a).
+ * statistics and closed-form ridge solve, the cross-model per-head ridge
+ * mapper, and the operators that decode from a filled cache (rotation, attention
+ * of drafted trees, verification, eviction), for one NVIDIA GB300 (sm_103a).
  *
  * Sources cited below:
  *   [RF] RidgeFill review (jaehun.me, English edition of the review of arXiv
@@ -98,7 +99,16 @@ enum rf_stage {
   RF_STAGE_SELECT_GEMM = 18,   /* source selection: split tensor-core products    */
   RF_STAGE_SELECT_FACTOR = 19, /* source selection: batched Cholesky and inverse  */
   RF_STAGE_SELECT_SCORE = 20,  /* source selection: set-up, scores, argmax, copies */
-  RF_STAGE_SELECT_SPLIT = 21   /* source selection: fp32 -> three bf16 planes      */
+  RF_STAGE_SELECT_SPLIT = 21,  /* source selection: fp32 -> three bf16 planes      */
+  RF_STAGE_ROPE = 22,          /* rf_rope                                          */
+  RF_STAGE_TREE_BUILD = 23,    /* rf_tree_build                                    */
+  RF_STAGE_ATTENTION = 24,     /* rf_tree_attention: the attention kernel          */
+  RF_STAGE_ATTN_COMBINE = 25,  /* rf_tree_attention: joining of split sequences     */
+  RF_STAGE_VERIFY = 26,        /* rf_verify_draft                                  */
+  RF_STAGE_COMMIT = 27,        /* rf_commit_draft                                  */
+  RF_STAGE_ATTN_WEIGHTS = 28,  /* rf_attn_weights                                  */
+  RF_STAGE_EVICT_SELECT = 29,  /* rf_evict: which rows stay                        */
+  RF_STAGE_EVICT_MOVE = 30     /* rf_evict: rows into the holes                    */
 };
 rf_status rf_profile_start(int max_records);
 /* Diagnostic: runs the tensor-core GEMM kernel on a problem whose operand copies
@@ -510,6 +520,96 @@ rf_status rf_select_sources(const rf_select_desc* desc, const rf_calib_stats* st
                             double lambda, int alpha_mode,
                             int32_t* src_layers, float* r2, int32_t* dev_status,
                             void* workspace, size_t workspace_bytes, rf_stream_t stream);
+
+/* ===================================================================== *
+ * Decoding from a filled cache: rotation, attention of drafted trees,
+ * verification of drafted tokens, eviction.
+ *
+ * A decoding step drafts a tree of n_nodes tokens per sequence. Node 0 is its root
+ * (the last token accepted, whose K and V are not in the cache yet), every other
+ * node's parent has a lower index. The drafted rows' K and V stay in buffers of
+ * their own until the tokens are verified; only accepted rows join the cache. With
+ * n_nodes = 1 a step is plain decoding of one token.
+ * A cache of one layer holds, for sequence b, row t, KV head h, channel c, element
+ * b*seq_stride + t*row_stride + h*head_dim + c; lens[b] rows are in use. What lies
+ * in rows beyond lens[b] is never used, whatever its bits are.
+ * ===================================================================== */
+
+/* Element types and channel pairings of rf_rope; frequency scalings for contexts
+ * longer than the model was trained on. */
+#define RF_BF16 0
+#define RF_F32 1
+#define RF_ROPE_HALF 0        /* channel i turns with i + rot_dim/2                     */
+#define RF_ROPE_INTERLEAVED 1 /* channel 2i turns with 2i + 1                           */
+#define RF_ROPE_SCALE_NONE 0
+#define RF_ROPE_SCALE_LINEAR 1
+#define RF_ROPE_SCALE_BASE 2
+#define RF_ROPE_SCALE_WAVELENGTH 3
+#define RF_ROPE_SCALE_RAMP 4
+
+typedef struct rf_rope_desc {
+  int64_t n_rows;       /* tokens, at most 2^24                                         */
+  int64_t n_heads;      /* heads of a row, head_dim channels each, one after another    */
+  int64_t head_dim;     /* a multiple of 8, at most 256                                 */
+  int64_t rot_dim;      /* the first rot_dim channels of a head turn (even, at most     */
+                        /* head_dim); the others are copied                             */
+  int64_t ld_in;        /* row strides                                                  */
+  int64_t ld_out;
+  int64_t pos_offset;   /* position of row 0 when no positions are given                */
+  double theta;         /* base                                                         */
+  double factor;        /* s >= 1: how many times longer the context is (see below)     */
+  double original_rows; /* R: context the model was trained on (WAVELENGTH, RAMP)       */
+  double low_turns;     /* turns within R rows below which a frequency is divided by s  */
+  double high_turns;    /* turns within R rows above which a frequency stays            */
+  double amplitude;     /* the rotation is multiplied by it; 0 = 1                      */
+  int32_t layout;       /* RF_ROPE_HALF or RF_ROPE_INTERLEAVED                          */
+  int32_t dtype;        /* RF_BF16 or RF_F32, of in and out                             */
+  int32_t transpose;    /* nonzero: the transposed rotation, which is the gradient's    */
+                        /* (and the inverse where amplitude is 1)                       */
+  int32_t scaling;      /* RF_ROPE_SCALE_*                                              */
+} rf_rope_desc;
+
+/* out[t][h] = amplitude * R(p_t) in[t][h], with p_t = positions[t] (device int32) or
+ * t + pos_offset when positions is NULL. Pair i of a head turns by p_t f_i,
+ *   f_i = theta^(-2i/rot_dim)                                          (NONE)
+ *   f_i / s                                                            (LINEAR)
+ *   (theta s^(rot_dim/(rot_dim-2)))^(-2i/rot_dim)                      (BASE, rot_dim > 2)
+ *   f_i (w + (1-w)/s), w = clamp((R f_i/2pi - low)/(high - low), 0, 1)  (WAVELENGTH)
+ *   f_i ((1-w) + w/s), w = clamp((i - lo)/(hi - lo), 0, 1),            (RAMP)
+ *     lo = max(floor(d(high)), 0), hi = min(ceil(d(low)), rot_dim - 1),
+ *     d(x) = rot_dim ln(R/(2 pi x)) / (2 ln theta).
+ * The angle is reduced mod 2 pi in 64-bit fixed point; bf16 rows take their sine and
+ * cosine to about 2^-21, fp32 rows to fp32. in and out 16-byte aligned, strides
+ * multiples of 8 elements; out may be in (with ld_out = ld_in). No workspace. */
+rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out, const int32_t* positions,
+                  rf_stream_t stream);
+
+/* Words of a node's mask: bit j % 64 of word j / 64 says whether it sees node j. */
+#define RF_TREE_WORDS(n_nodes) (((n_nodes) + 63) / 64)
+#define RF_TREE_MAX_NODES 1024
+
+/* From each sequence's parents (device int32 [n_seqs][n_nodes]; parents[0] = -1, else
+ * 0 <= parents[i] < i):
+ *   mask       [n_seqs][n_nodes][RF_TREE_WORDS(n_nodes)] uint64: a node sees itself
+ *              and its ancestors (may be NULL)
+ *   positions  [n_seqs][n_nodes] int32: next_pos[b] + the node's depth (may be NULL)
+ *   next_pos   [n_seqs] int32: position of node 0 (not read when positions is NULL)
+ * n_nodes <= RF_TREE_MAX_NODES. A sequence with other parents records
+ * RF_ERR_INVALID_ARG in *dev_status and its outputs are not written. */
+rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_t* parents, const int32_t* next_pos,
+                        uint64_t* mask, int32_t* positions, int32_t* dev_status, rf_stream_t stream);
+
+/* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c. */
+typedef struct rf_cache_desc {
+  int64_t n_layers;
+  int64_t n_seqs;
+  int64_t n_kv_heads;
+  int64_t head_dim;     /* a multiple of 8, at most 256                                 */
+  int64_t capacity;     /* rows per sequence, at most 2^24                              */
+  int64_t row_stride;
+  int64_t seq_stride;
+  int64_t layer_stride;
+} rf_cache_desc;
 
 #ifdef __cplusplus
 }

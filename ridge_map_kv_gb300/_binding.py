@@ -42,6 +42,17 @@ RF_SOLVE_DIGITS7 = 8
 RF_MAPS_BF16 = 0
 RF_MAPS_INT8 = 1
 
+RF_BF16 = 0
+RF_F32 = 1
+RF_ROPE_HALF = 0
+RF_ROPE_INTERLEAVED = 1
+RF_ROPE_SCALE_NONE = 0
+RF_ROPE_SCALE_LINEAR = 1
+RF_ROPE_SCALE_BASE = 2
+RF_ROPE_SCALE_WAVELENGTH = 3
+RF_ROPE_SCALE_RAMP = 4
+RF_TREE_MAX_NODES = 1024
+
 
 class rf_map_source(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("on_host", ctypes.c_int32), ("A", c_void_p), ("row_scale", c_void_p)]
@@ -73,6 +84,32 @@ class rf_xmodel_desc(ctypes.Structure):
     _fields_ = [("L_src", c_int64), ("L_tgt", c_int64), ("k", c_int64), ("n_kv_heads", c_int64),
                 ("head_dim", c_int64), ("N", c_int64), ("theta_src", c_double), ("theta_tgt", c_double),
                 ("pos_offset", c_int64), ("flags", ctypes.c_uint64)]
+
+
+class rf_rope_desc(ctypes.Structure):
+    _fields_ = [("n_rows", c_int64), ("n_heads", c_int64), ("head_dim", c_int64), ("rot_dim", c_int64),
+                ("ld_in", c_int64), ("ld_out", c_int64), ("pos_offset", c_int64), ("theta", c_double),
+                ("factor", c_double), ("original_rows", c_double), ("low_turns", c_double),
+                ("high_turns", c_double), ("amplitude", c_double), ("layout", c_int32), ("dtype", c_int32),
+                ("transpose", c_int32), ("scaling", c_int32)]
+
+
+class rf_attn_desc(ctypes.Structure):
+    _fields_ = [("n_seqs", c_int64), ("n_q_heads", c_int64), ("n_kv_heads", c_int64), ("head_dim", c_int64),
+                ("n_nodes", c_int64), ("capacity", c_int64), ("q_row_stride", c_int64), ("q_seq_stride", c_int64),
+                ("draft_row_stride", c_int64), ("draft_seq_stride", c_int64), ("cache_row_stride", c_int64),
+                ("cache_seq_stride", c_int64), ("out_row_stride", c_int64), ("out_seq_stride", c_int64),
+                ("scale", c_double), ("flags", ctypes.c_uint64)]
+
+
+class rf_verify_desc(ctypes.Structure):
+    _fields_ = [("n_seqs", c_int64), ("n_nodes", c_int64), ("vocab", c_int64), ("ld_target", c_int64),
+                ("ld_draft", c_int64), ("ld_noise", c_int64)]
+
+
+class rf_cache_desc(ctypes.Structure):
+    _fields_ = [("n_layers", c_int64), ("n_seqs", c_int64), ("n_kv_heads", c_int64), ("head_dim", c_int64),
+                ("capacity", c_int64), ("row_stride", c_int64), ("seq_stride", c_int64), ("layer_stride", c_int64)]
 
 
 _SIGS = {
@@ -118,6 +155,8 @@ _SIGS = {
     "rf_select_workspace_bytes": (c_size_t, [POINTER(rf_select_desc)]),
     "rf_select_sources": (c_int, [POINTER(rf_select_desc), POINTER(rf_calib_stats), c_double, c_int, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "rf_rope": (c_int, [POINTER(rf_rope_desc), c_void_p, c_void_p, c_void_p, c_void_p]),
+    "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
 }
 
 _lib = None
@@ -340,3 +379,15 @@ def rf_select_sources(desc, stats, lam, alpha_mode, src_layers, r2=None, dev_sta
     _check(lib().rf_select_sources(ctypes.byref(desc), arr, float(lam), int(alpha_mode), _p(src_layers), _p(r2),
                                    _p(dev_status), _p(workspace), int(workspace_bytes), _s(stream)),
            "rf_select_sources")
+
+
+# ------------------------------------------------------- decoding from a filled cache
+def rf_rope(desc, inp, out, positions=None, stream=None):
+    """Rotary positions of rows of heads: both pairings, part of a head, stretched frequencies (see include/rf.h)."""
+    _check(lib().rf_rope(ctypes.byref(desc), _p(inp), _p(out), _p(positions), _s(stream)), "rf_rope")
+
+
+def rf_tree_build(n_seqs, n_nodes, parents, next_pos=None, mask=None, positions=None, dev_status=None, stream=None):
+    """Mask words ([n_seqs][n_nodes][(n_nodes + 63) // 64], 64 bits each) and positions of drafted trees."""
+    _check(lib().rf_tree_build(int(n_seqs), int(n_nodes), _p(parents), _p(next_pos), _p(mask), _p(positions),
+                               _p(dev_status), _s(stream)), "rf_tree_build")

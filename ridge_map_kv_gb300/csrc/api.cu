@@ -94,6 +94,30 @@ rf_status make_tmap_bf16_3d(CUtensorMap* tm, const void* base, uint64_t inner, u
   return RF_OK;
 }
 
+rf_status make_tmap_bf16_4d(CUtensorMap* tm, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                            const uint32_t (&box)[4]) {
+  auto fn = encode_fn();
+  if (!fn) return fail(RF_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[4], str[3];
+  cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+  }
+  cuuint64_t tight = dims[0] * 2;
+  for (int i = 0; i < 3; ++i) {
+    str[i] = dims[i + 1] == 1 ? tight : strides[i] * 2;
+    tight = str[i] * dims[i + 1];
+  }
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, str, bx, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(RF_ERR_CUDA, "cuTensorMapEncodeTiled (4-D) failed (%d): dims %llu x %llu x %llu x %llu", (int)r,
+                (unsigned long long)d[0], (unsigned long long)d[1], (unsigned long long)d[2], (unsigned long long)d[3]);
+  return RF_OK;
+}
+
 rf_status set_smem_attr(const void* kernel, size_t bytes, uint64_t* done_mask) {
   static std::mutex mu;
   int dev = 0;
@@ -241,6 +265,15 @@ const char* rf_stage_name(int s) {
     case RF_STAGE_SELECT_FACTOR: return "select_factor";
     case RF_STAGE_SELECT_SCORE: return "select_score";
     case RF_STAGE_SELECT_SPLIT: return "select_split";
+    case RF_STAGE_ROPE: return "rope";
+    case RF_STAGE_TREE_BUILD: return "tree_build";
+    case RF_STAGE_ATTENTION: return "attention";
+    case RF_STAGE_ATTN_COMBINE: return "attention_combine";
+    case RF_STAGE_VERIFY: return "verify";
+    case RF_STAGE_COMMIT: return "commit";
+    case RF_STAGE_ATTN_WEIGHTS: return "attention_weights";
+    case RF_STAGE_EVICT_SELECT: return "evict_select";
+    case RF_STAGE_EVICT_MOVE: return "evict_move";
     default: return "unknown";
   }
 }

@@ -39,6 +39,11 @@ rf_status make_tmap_bf16_3d(CUtensorMap* tm, const void* base, uint64_t inner, u
                             uint64_t mid_stride_elems, uint64_t outer_stride_elems, uint32_t box_inner,
                             uint32_t box_mid);
 
+// 4-D variant: dims[0..3], strides (elements) of dims 1..3, box {box[0..3]}. The stride of
+// a dimension of size 1 does not matter (the tightest legal one is encoded).
+rf_status make_tmap_bf16_4d(CUtensorMap* tm, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                            const uint32_t (&box)[4]);
+
 // Bump allocator over the caller workspace (256-byte aligned regions).
 struct Carve {
   uint8_t* base;
@@ -89,6 +94,9 @@ rf_status chol_inv_block(float* A, long long lda, long long sA, float* W, long l
 // RF_ERR_NOT_SPD.
 rf_status spd_inverse(float* H, int n, float* Linv, float* Hinv, float* ctmp, __nv_bfloat16* planes, bool pair,
                       int32_t* dev_status, int sms, cudaStream_t s);
+
+// Checks of an rf_cache_desc that the calls writing to a cache share (evict.cu).
+rf_status check_cache_desc(const rf_cache_desc* d);
 
 // Brackets one kernel launch with profiling events when rf_profile_start is active.
 struct ProfScope {
