@@ -611,6 +611,25 @@ typedef struct rf_cache_desc {
   int64_t layer_stride;
 } rf_cache_desc;
 
+/* Evicts rows of little weight: in every layer, sequence and KV head, min(lens[b], keep)
+ * rows stay. Rows whose position is below n_sink or at least next_pos[b] - n_recent rank
+ * as +inf, the others by score (NaN as -inf); the highest ranks stay, the lowest row
+ * index first among equals. Rows that stay and lie below `keep` do not move; the i-th
+ * (ascending) that lies beyond moves into the i-th (ascending) hole below, so each head
+ * moves as few rows as can be. Attention does not depend on the rows' order; `pos`
+ * holds each row's position.
+ *   score_in, pos_in, score_out, pos_out  [n_layers][n_seqs][n_kv_heads][capacity]; out
+ *       may be in; entries beyond new_lens[b] are not written
+ *   new_lens [n_seqs] int32 (may be lens)
+ * A length outside [0, capacity] records RF_ERR_INVALID_ARG and that sequence stays as
+ * it is. keep >= 1. */
+size_t rf_evict_workspace_bytes(const rf_cache_desc* desc, int64_t keep);
+rf_status rf_evict(const rf_cache_desc* desc, int64_t keep, int64_t n_sink, int64_t n_recent,
+                   const int32_t* lens, const int32_t* next_pos, rf_bf16* k_cache, rf_bf16* v_cache,
+                   const float* score_in, const int32_t* pos_in, float* score_out, int32_t* pos_out,
+                   int32_t* new_lens, int32_t* dev_status,
+                   void* workspace, size_t workspace_bytes, rf_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -157,6 +157,8 @@ _SIGS = {
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "rf_rope": (c_int, [POINTER(rf_rope_desc), c_void_p, c_void_p, c_void_p, c_void_p]),
     "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
+    "rf_evict_workspace_bytes": (c_size_t, [POINTER(rf_cache_desc), c_int64]),
+    "rf_evict": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 3 + [c_void_p] * 11 + [c_size_t, c_void_p]),
 }
 
 _lib = None
@@ -391,3 +393,21 @@ def rf_tree_build(n_seqs, n_nodes, parents, next_pos=None, mask=None, positions=
     """Mask words ([n_seqs][n_nodes][(n_nodes + 63) // 64], 64 bits each) and positions of drafted trees."""
     _check(lib().rf_tree_build(int(n_seqs), int(n_nodes), _p(parents), _p(next_pos), _p(mask), _p(positions),
                                _p(dev_status), _s(stream)), "rf_tree_build")
+
+
+
+
+
+
+
+
+def rf_evict_workspace_bytes(desc: rf_cache_desc, keep: int) -> int:
+    return int(lib().rf_evict_workspace_bytes(ctypes.byref(desc), int(keep)))
+
+
+def rf_evict(desc, keep, n_sink, n_recent, lens, next_pos, k_cache, v_cache, score_in, pos_in, score_out, pos_out,
+             new_lens, dev_status=None, workspace=None, workspace_bytes=0, stream=None):
+    """Keeps the rows of the highest accumulated weight in every layer, sequence and KV head."""
+    _check(lib().rf_evict(ctypes.byref(desc), int(keep), int(n_sink), int(n_recent), _p(lens), _p(next_pos),
+                          _p(k_cache), _p(v_cache), _p(score_in), _p(pos_in), _p(score_out), _p(pos_out),
+                          _p(new_lens), _p(dev_status), _p(workspace), int(workspace_bytes), _s(stream)), "rf_evict")
