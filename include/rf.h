@@ -599,6 +599,39 @@ rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out, const int
 rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_t* parents, const int32_t* next_pos,
                         uint64_t* mask, int32_t* positions, int32_t* dev_status, rf_stream_t stream);
 
+typedef struct rf_verify_desc {
+  int64_t n_seqs;
+  int64_t n_nodes;    /* 1 .. RF_TREE_MAX_NODES                                        */
+  int64_t vocab;      /* V < 2^31                                                      */
+  int64_t ld_target;  /* row strides, >= vocab (any value)                              */
+  int64_t ld_draft;
+  int64_t ld_noise;
+} rf_verify_desc;
+
+/* Verifies each sequence's drafted tokens against the target's probabilities, so that
+ * the tokens kept are distributed as the target's own. From node c = 0, with
+ * r = target row of c and Z = 1: c's children x are tried in index order; child x (its
+ * token t) is accepted when u[x] q(t) Z < r(t), and then c = x starts over. A refused
+ * one leaves r <- max(r/Z - q, 0) and Z <- sum r (r and Z stay when that sum is 0).
+ * With no child left the next token is the lowest argmax of r(t)/noise(t) over r > 0.
+ *   target   [n_seqs*n_nodes][ld_target] fp32: probabilities after each node
+ *   draft    [n_seqs*n_nodes][ld_draft] fp32: q, the distribution that each node's
+ *            children were drawn from; NULL: children were chosen outright, q(t) = 1 at
+ *            the child's own token and 0 elsewhere (a refused one leaves r without its
+ *            token)
+ *   tokens   [n_seqs][n_nodes] int32 (node 0's is not read), parents as for rf_tree_build
+ *   u        [n_seqs][n_nodes] fp32 uniform in [0, 1) (node 0's is not read)
+ *   noise    [n_seqs][ld_noise] fp32, exponentially distributed, > 0
+ * Outputs: path [n_seqs][n_nodes] int32, the accepted nodes in order (node 0 first),
+ * then -1; n_path [n_seqs] int32; next_token [n_seqs] int32. A sequence with wrong
+ * parents or tokens outside [0, vocab) records RF_ERR_INVALID_ARG and gets n_path 0,
+ * next_token -1. Sums are fp32; r/Z, its difference to q and r/noise are rounded one by
+ * one (IEEE), u q Z from the left. No workspace. */
+rf_status rf_verify_draft(const rf_verify_desc* desc, const float* target, const float* draft,
+                          const int32_t* tokens, const int32_t* parents, const float* u, const float* noise,
+                          int32_t* path, int32_t* n_path, int32_t* next_token, int32_t* dev_status,
+                          rf_stream_t stream);
+
 /* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c. */
 typedef struct rf_cache_desc {
   int64_t n_layers;
@@ -610,6 +643,23 @@ typedef struct rf_cache_desc {
   int64_t seq_stride;
   int64_t layer_stride;
 } rf_cache_desc;
+
+/* Appends the accepted rows of every layer to the cache: for j < n_path[b],
+ *   cache row lens[b] + j <- drafted row path[b][j],
+ *   score[l][b][h][lens[b]+j] <- 0, pos[l][b][h][lens[b]+j] <- next_pos[b] + j,
+ *   new_lens[b] = lens[b] + n_path[b], new_next_pos[b] = next_pos[b] + n_path[b].
+ * score, pos [n_layers][n_seqs][n_kv_heads][capacity] (either may be NULL); k_draft,
+ * v_draft: element l*draft_layer_stride + b*draft_seq_stride + i*draft_row_stride +
+ * h*head_dim + c. new_lens may be lens, new_next_pos may be next_pos, which may be NULL
+ * together with new_next_pos and pos. A sequence whose rows do not fit, or whose path or
+ * counts are out of range, records RF_ERR_INVALID_ARG and keeps its lengths and rows. */
+rf_status rf_commit_draft(const rf_cache_desc* desc, int64_t n_nodes, int64_t draft_row_stride,
+                          int64_t draft_seq_stride, int64_t draft_layer_stride,
+                          const int32_t* path, const int32_t* n_path,
+                          const int32_t* lens, const int32_t* next_pos,
+                          const rf_bf16* k_draft, const rf_bf16* v_draft,
+                          rf_bf16* k_cache, rf_bf16* v_cache, float* score, int32_t* pos,
+                          int32_t* new_lens, int32_t* new_next_pos, int32_t* dev_status, rf_stream_t stream);
 
 /* Evicts rows of little weight: in every layer, sequence and KV head, min(lens[b], keep)
  * rows stay. Rows whose position is below n_sink or at least next_pos[b] - n_recent rank

@@ -157,6 +157,8 @@ _SIGS = {
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "rf_rope": (c_int, [POINTER(rf_rope_desc), c_void_p, c_void_p, c_void_p, c_void_p]),
     "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
+    "rf_verify_draft": (c_int, [POINTER(rf_verify_desc)] + [c_void_p] * 11),
+    "rf_commit_draft": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 4 + [c_void_p] * 14),
     "rf_evict_workspace_bytes": (c_size_t, [POINTER(rf_cache_desc), c_int64]),
     "rf_evict": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 3 + [c_void_p] * 11 + [c_size_t, c_void_p]),
 }
@@ -397,6 +399,22 @@ def rf_tree_build(n_seqs, n_nodes, parents, next_pos=None, mask=None, positions=
 
 
 
+def rf_verify_draft(desc, target, draft, tokens, parents, u, noise, path, n_path, next_token, dev_status=None,
+                    stream=None):
+    """Accepts or refuses drafted tokens from given random numbers; ``draft=None``: children chosen outright."""
+    _check(lib().rf_verify_draft(ctypes.byref(desc), _p(target), _p(draft), _p(tokens), _p(parents), _p(u), _p(noise),
+                                 _p(path), _p(n_path), _p(next_token), _p(dev_status), _s(stream)),
+           "rf_verify_draft")
+
+
+def rf_commit_draft(desc, n_nodes, draft_row_stride, draft_seq_stride, draft_layer_stride, path, n_path, lens, next_pos,
+                    k_draft, v_draft, k_cache, v_cache, score, pos, new_lens, new_next_pos, dev_status=None,
+                    stream=None):
+    """Appends the accepted rows of every layer to the cache."""
+    _check(lib().rf_commit_draft(ctypes.byref(desc), int(n_nodes), int(draft_row_stride), int(draft_seq_stride),
+                                 int(draft_layer_stride), _p(path), _p(n_path), _p(lens), _p(next_pos), _p(k_draft),
+                                 _p(v_draft), _p(k_cache), _p(v_cache), _p(score), _p(pos), _p(new_lens),
+                                 _p(new_next_pos), _p(dev_status), _s(stream)), "rf_commit_draft")
 
 
 

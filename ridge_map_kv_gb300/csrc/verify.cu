@@ -1,0 +1,407 @@
+// Verification of drafted tokens (rf_verify_draft) and the accepted rows' way into the
+// cache (rf_commit_draft).
+//
+// The walk: from the root, children x of the current node are tried in index order. With
+// k refusals so far the target's row p has become r_k, r_0 = p, Z_0 = 1,
+//   r_{j+1} = max(r_j / Z_j - q, 0),  Z_{j+1} = sum r_{j+1}     (or, for children chosen
+//   outright, r_{j+1} = r_j without its token),
+// and x is accepted when u q(x) Z_k < r_k(x). A test needs r_k at one token only, which
+// the chain above gives from p and q at that token, so the walk itself reads three
+// numbers a node, fetched for every node at once beforehand. A whole row is read where a
+// sum Z is needed (a refused child with a sibling behind it) and once at the end, for
+// the lowest argmax of r / noise. What bounds a call is the latency of these steps at
+// small sizes and the last row's bytes at large ones.
+//
+// One cluster of CTAs a sequence: every thread follows the same walk through shared
+// memory, each CTA sums or scans its share of the vocabulary, and the shares meet
+// through distributed shared memory, in a fixed order.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "rf_device.cuh"
+#include "rf_host.h"
+
+namespace rf {
+namespace cg = cooperative_groups;
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyCtas = 8;  // CTAs of a cluster (the portable limit)
+
+struct VerifyArgs {
+  const float* target;
+  const float* draft;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const float* u;
+  const float* noise;
+  int32_t* path;
+  int32_t* n_path;
+  int32_t* next_token;
+  int32_t* dev_status;
+  long long ld_target, ld_draft, ld_noise;
+  int n, vocab;
+};
+
+struct VerifyShared {
+  int up[RF_TREE_MAX_NODES];
+  int token[RF_TREE_MAX_NODES];
+  float u[RF_TREE_MAX_NODES];
+  float p[RF_TREE_MAX_NODES];  // target probability of the node's token at its parent
+  float q[RF_TREE_MAX_NODES];
+  float z[RF_TREE_MAX_NODES];      // Z_j of the refusals at the current node
+  int refused[RF_TREE_MAX_NODES];  // their nodes
+  int path[RF_TREE_MAX_NODES];
+  float part_sum[2];               // this CTA's share, by the parity of the exchange
+  unsigned long long part_best[2];
+  float warp_sum[kVerifyThreads / 32];
+  unsigned long long warp_best[kVerifyThreads / 32];
+};
+
+// r_k(t) from p(t), q(t) and the refusals.
+template <bool kDraft>
+__device__ __forceinline__ float residual(const VerifyShared& sh, float p, float q, int t, int k) {
+  float r = p;
+  for (int j = 0; j < k; ++j) {
+    if constexpr (kDraft) r = fmaxf(__fsub_rn(__fdiv_rn(r, sh.z[j]), q), 0.0f);
+    else r = sh.token[sh.refused[j]] == t ? 0.0f : r;
+  }
+  return r;
+}
+
+template <bool kDraft>
+__global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant__ VerifyArgs a) {
+  __shared__ VerifyShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = static_cast<int>(cl.block_rank()), ctas = static_cast<int>(cl.num_blocks());
+  const long long b = blockIdx.x / static_cast<unsigned>(ctas);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = a.n;
+  bool bad = false;
+  for (int i = tid; i < n; i += kVerifyThreads) {
+    const int p = a.parents[b * n + i];
+    sh.up[i] = p;
+    bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
+    if (i > 0) {
+      const int t = a.tokens[b * n + i];
+      sh.token[i] = t;
+      bad |= t < 0 || t >= a.vocab;
+      sh.u[i] = a.u[b * n + i];
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {  // every CTA of the cluster sees the same
+    if (rank == 0) {
+      for (int i = tid; i < n; i += kVerifyThreads) a.path[b * n + i] = -1;
+      if (tid == 0) {
+        a.n_path[b] = 0;
+        a.next_token[b] = -1;
+        record_status(a.dev_status, RF_ERR_INVALID_ARG);
+      }
+    }
+    return;
+  }
+  for (int i = 1 + tid; i < n; i += kVerifyThreads) {
+    const long long row = b * n + sh.up[i];
+    sh.p[i] = a.target[row * a.ld_target + sh.token[i]];
+    sh.q[i] = kDraft ? a.draft[row * a.ld_draft + sh.token[i]] : 1.0f;
+  }
+  __syncthreads();
+
+  const int share = ((a.vocab + ctas - 1) / ctas + 3) & ~3;
+  const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
+  int cur = 0, k = 0, n_acc = 1, turn = 0;
+  if (tid == 0) {
+    sh.path[0] = 0;
+    sh.z[0] = 1.0f;
+  }
+  __syncthreads();
+  // The next child of `cur` after node `c`, or n: 32 nodes at a time.
+  auto next_child = [&](int c) {
+    for (int c0 = c + 1; c0 < n; c0 += 32) {
+      const unsigned hit = __ballot_sync(0xffffffffu, c0 + lane < n && sh.up[c0 + lane] == cur);
+      if (hit) return c0 + __ffs(hit) - 1;
+    }
+    return n;
+  };
+  int c = next_child(0);
+  while (c < n) {
+    const float r = residual<kDraft>(sh, sh.p[c], sh.q[c], sh.token[c], k);
+    if (__fmul_rn(__fmul_rn(sh.u[c], sh.q[c]), sh.z[k]) < r) {
+      __syncthreads();  // the refusals of the node left behind are read no more
+      if (tid == 0) {
+        sh.path[n_acc] = c;
+        sh.z[0] = 1.0f;
+      }
+      ++n_acc;
+      cur = c;
+      k = 0;
+      c = next_child(c);
+      __syncthreads();
+      continue;
+    }
+    const int sibling = next_child(c);
+    __syncthreads();
+    if (tid == 0) sh.refused[k] = c;
+    __syncthreads();
+    ++k;
+    if (sibling < n) {
+      // Z_k, this CTA's share, then the cluster's
+      const float* p = a.target + (b * n + cur) * a.ld_target;
+      const float* q = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
+      float sum = 0.0f;
+      for (int t = v0 + tid; t < v1; t += kVerifyThreads) sum += residual<kDraft>(sh, p[t], kDraft ? q[t] : 0.0f, t, k);
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) sh.warp_sum[warp] = sum;
+      __syncthreads();
+      if (tid == 0) {
+        float s = 0.0f;
+        for (int w = 0; w < kVerifyThreads / 32; ++w) s += sh.warp_sum[w];
+        sh.part_sum[turn & 1] = s;
+      }
+      cl.sync();
+      float z = 0.0f;
+      for (int j = 0; j < ctas; ++j) z += *cl.map_shared_rank(&sh.part_sum[turn & 1], j);
+      ++turn;
+      if (z > 0.0f) {
+        if (tid == 0) sh.z[k] = z;
+      } else {
+        --k;  // nothing would be left: the residual stays
+      }
+      __syncthreads();
+    }
+    c = sibling;
+  }
+
+  // The lowest argmax of r / noise: the score's bits (scores are >= 0) above the
+  // complement of the token.
+  const float* p = a.target + (b * n + cur) * a.ld_target;
+  const float* q = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
+  const float* e = a.noise + b * a.ld_noise;
+  int token = 0;
+  while (true) {
+    unsigned long long best = 0;
+    for (int t = v0 + tid; t < v1; t += kVerifyThreads) {
+      const float r = residual<kDraft>(sh, p[t], kDraft ? q[t] : 0.0f, t, k);
+      const float score = r > 0.0f ? __fdiv_rn(r, e[t]) : 0.0f;
+      const unsigned long long key =
+          (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(t));
+      best = max(best, key);
+    }
+    for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == 0) sh.warp_best[warp] = best;
+    __syncthreads();
+    if (tid == 0) {
+      unsigned long long m = 0;
+      for (int w = 0; w < kVerifyThreads / 32; ++w) m = max(m, sh.warp_best[w]);
+      sh.part_best[turn & 1] = m;
+    }
+    cl.sync();
+    unsigned long long m = 0;
+    for (int j = 0; j < ctas; ++j) m = max(m, *cl.map_shared_rank(&sh.part_best[turn & 1], j));
+    ++turn;
+    token = static_cast<int>(0xffffffffu - static_cast<unsigned>(m & 0xffffffffu));
+    // All zero: the last refusal's residual is empty, so the one before it stands.
+    if ((m >> 32) != 0 || k == 0) break;
+    --k;
+    __syncthreads();
+  }
+  if (rank == 0) {
+    for (int i = tid; i < n; i += kVerifyThreads) a.path[b * n + i] = i < n_acc ? sh.path[i] : -1;
+    if (tid == 0) {
+      a.n_path[b] = n_acc;
+      a.next_token[b] = token;
+    }
+  }
+  cl.sync();  // no CTA leaves while another may read its share
+}
+
+struct CommitArgs {
+  const int32_t* path;
+  const int32_t* n_path;
+  const int32_t* lens;
+  const int32_t* next_pos;
+  const __nv_bfloat16* kd;
+  const __nv_bfloat16* vd;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  float* score;
+  int32_t* pos;
+  int32_t* new_lens;
+  int32_t* new_next_pos;
+  int32_t* dev_status;
+  long long row_stride, seq_stride, layer_stride, draft_row, draft_seq, draft_layer;
+  int n_seqs, heads, width, capacity, n;  // width = heads * head_dim
+};
+
+// Layer blockIdx.x, sequence blockIdx.y. new_lens may be lens itself, so the lengths are
+// written by a second, one-CTA launch behind all of these reads.
+__global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitArgs a) {
+  const int l = blockIdx.x, b = blockIdx.y;
+  const int cnt = a.n_path[b], len = a.lens[b];
+  if (cnt <= 0 || cnt > a.n || len < 0 || len > a.capacity - cnt) return;
+  bool bad = false;
+  for (int j = threadIdx.x; j < cnt; j += 256) {
+    const int i = a.path[static_cast<long long>(b) * a.n + j];
+    bad |= i < 0 || i >= a.n;
+  }
+  if (__syncthreads_or(bad)) return;
+  const int pieces = a.width / 8;
+  for (int x = threadIdx.x; x < cnt * pieces; x += 256) {
+    const int j = x / pieces, c = (x - j * pieces) * 8;
+    const long long src = l * a.draft_layer + b * a.draft_seq +
+                          static_cast<long long>(a.path[static_cast<long long>(b) * a.n + j]) * a.draft_row + c;
+    const long long dst = l * a.layer_stride + b * a.seq_stride + static_cast<long long>(len + j) * a.row_stride + c;
+    const uint4 k = *reinterpret_cast<const uint4*>(a.kd + src), v = *reinterpret_cast<const uint4*>(a.vd + src);
+    *reinterpret_cast<uint4*>(a.k + dst) = k;
+    *reinterpret_cast<uint4*>(a.v + dst) = v;
+  }
+  for (int x = threadIdx.x; x < cnt * a.heads; x += 256) {
+    const int h = x / cnt, j = x - h * cnt;
+    const long long at = ((static_cast<long long>(l) * a.n_seqs + b) * a.heads + h) * a.capacity + len + j;
+    if (a.score != nullptr) a.score[at] = 0.0f;
+    if (a.pos != nullptr) a.pos[at] = a.next_pos[b] + j;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_commit_lens(const __grid_constant__ CommitArgs a) {
+  for (int b = blockIdx.x * 256 + threadIdx.x; b < a.n_seqs; b += gridDim.x * 256) {
+    const int cnt = a.n_path[b], len = a.lens[b];
+    bool ok = cnt >= 0 && cnt <= a.n && len >= 0 && len <= a.capacity - cnt;
+    for (int j = 0; ok && j < cnt; ++j) {
+      const int i = a.path[static_cast<long long>(b) * a.n + j];
+      ok = i >= 0 && i < a.n;
+    }
+    if (!ok) record_status(a.dev_status, RF_ERR_INVALID_ARG);
+    if (a.new_lens != nullptr) a.new_lens[b] = len + (ok ? cnt : 0);
+    if (a.new_next_pos != nullptr) a.new_next_pos[b] = a.next_pos[b] + (ok ? cnt : 0);
+  }
+}
+
+}  // namespace rf
+
+using namespace rf;
+
+extern "C" rf_status rf_verify_draft(const rf_verify_desc* d, const float* target, const float* draft,
+                                     const int32_t* tokens, const int32_t* parents, const float* u, const float* noise,
+                                     int32_t* path, int32_t* n_path, int32_t* next_token, int32_t* dev_status,
+                                     rf_stream_t stream) {
+  clear_error();
+  if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
+  if (d->n_seqs < 0 || d->n_nodes <= 0 || d->vocab <= 0)
+    return fail(RF_ERR_INVALID_ARG, "need n_seqs >= 0, n_nodes, vocab > 0");
+  if (d->n_nodes > RF_TREE_MAX_NODES || d->vocab >= (int64_t(1) << 31) - 64 || d->n_seqs > (int64_t(1) << 24))
+    return fail(RF_ERR_SHAPE, "n_nodes must be <= %d, vocab < 2^31 - 64, n_seqs <= 2^24", RF_TREE_MAX_NODES);
+  if (d->ld_target < d->vocab || d->ld_noise < d->vocab || (draft != nullptr && d->ld_draft < d->vocab))
+    return fail(RF_ERR_ALIGN, "row strides must be >= vocab");
+  if (d->n_seqs == 0) return RF_OK;
+  if (!target || !noise || !path || !n_path || !next_token || !parents || (d->n_nodes > 1 && (!tokens || !u)))
+    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(target) | reinterpret_cast<uintptr_t>(draft) |
+                         reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(parents) |
+                         reinterpret_cast<uintptr_t>(u) | reinterpret_cast<uintptr_t>(noise) |
+                         reinterpret_cast<uintptr_t>(path) | reinterpret_cast<uintptr_t>(n_path) |
+                         reinterpret_cast<uintptr_t>(next_token);
+  if (bits & 3u) return fail(RF_ERR_ALIGN, "arrays must be 4-byte aligned");
+  int sms = 0;
+  rf_status st = current_device(&sms);
+  if (st != RF_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  VerifyArgs a{};
+  a.target = target;
+  a.draft = draft;
+  a.tokens = tokens;
+  a.parents = parents;
+  a.u = u;
+  a.noise = noise;
+  a.path = path;
+  a.n_path = n_path;
+  a.next_token = next_token;
+  a.dev_status = dev_status;
+  a.ld_target = d->ld_target;
+  a.ld_draft = d->ld_draft;
+  a.ld_noise = d->ld_noise;
+  a.n = static_cast<int>(d->n_nodes);
+  a.vocab = static_cast<int>(d->vocab);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(d->n_seqs) * kVerifyCtas);
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kVerifyCtas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ProfScope prof(s, RF_STAGE_VERIFY);
+  return cuda_check(draft != nullptr ? cudaLaunchKernelEx(&cfg, k_verify<true>, a)
+                                     : cudaLaunchKernelEx(&cfg, k_verify<false>, a),
+                    "k_verify launch");
+}
+
+extern "C" rf_status rf_commit_draft(const rf_cache_desc* d, int64_t n_nodes, int64_t draft_row_stride,
+                                     int64_t draft_seq_stride, int64_t draft_layer_stride, const int32_t* path,
+                                     const int32_t* n_path, const int32_t* lens, const int32_t* next_pos,
+                                     const rf_bf16* k_draft, const rf_bf16* v_draft, rf_bf16* k_cache, rf_bf16* v_cache,
+                                     float* score, int32_t* pos, int32_t* new_lens, int32_t* new_next_pos,
+                                     int32_t* dev_status, rf_stream_t stream) {
+  clear_error();
+  rf_status st = check_cache_desc(d);
+  if (st != RF_OK) return st;
+  if (n_nodes <= 0) return fail(RF_ERR_INVALID_ARG, "need n_nodes > 0");
+  if (n_nodes > (int64_t(1) << 20)) return fail(RF_ERR_SHAPE, "n_nodes must be <= 2^20");
+  const int64_t width = d->n_kv_heads * d->head_dim;
+  if (draft_row_stride < width || draft_row_stride % 8 || draft_seq_stride % 8 || draft_layer_stride % 8 ||
+      draft_seq_stride < 0 || draft_layer_stride < 0)
+    return fail(RF_ERR_ALIGN, "draft strides must be multiples of 8, the row stride >= n_kv_heads*head_dim");
+  if (n_nodes * (width / 8) >= (int64_t(1) << 31) || n_nodes * d->n_kv_heads >= (int64_t(1) << 31))
+    return fail(RF_ERR_SHAPE, "n_nodes * n_kv_heads * head_dim is too large");
+  if (d->n_seqs == 0) return RF_OK;
+  if (!path || !n_path || !lens || (d->n_layers > 0 && (!k_draft || !v_draft || !k_cache || !v_cache)) ||
+      (!next_pos && (pos || new_next_pos)))
+    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
+  if (!aligned16(k_draft) || !aligned16(v_draft) || !aligned16(k_cache) || !aligned16(v_cache))
+    return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(path) | reinterpret_cast<uintptr_t>(n_path) |
+                         reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(next_pos) |
+                         reinterpret_cast<uintptr_t>(score) | reinterpret_cast<uintptr_t>(pos) |
+                         reinterpret_cast<uintptr_t>(new_lens) | reinterpret_cast<uintptr_t>(new_next_pos);
+  if (bits & 3u) return fail(RF_ERR_ALIGN, "arrays must be 4-byte aligned");
+  int sms = 0;
+  if ((st = current_device(&sms)) != RF_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CommitArgs a{};
+  a.path = path;
+  a.n_path = n_path;
+  a.lens = lens;
+  a.next_pos = next_pos;
+  a.kd = reinterpret_cast<const __nv_bfloat16*>(k_draft);
+  a.vd = reinterpret_cast<const __nv_bfloat16*>(v_draft);
+  a.k = reinterpret_cast<__nv_bfloat16*>(k_cache);
+  a.v = reinterpret_cast<__nv_bfloat16*>(v_cache);
+  a.score = score;
+  a.pos = pos;
+  a.new_lens = new_lens;
+  a.new_next_pos = new_next_pos;
+  a.dev_status = dev_status;
+  a.row_stride = d->row_stride;
+  a.seq_stride = d->seq_stride;
+  a.layer_stride = d->layer_stride;
+  a.draft_row = draft_row_stride;
+  a.draft_seq = draft_seq_stride;
+  a.draft_layer = draft_layer_stride;
+  a.n_seqs = static_cast<int>(d->n_seqs);
+  a.heads = static_cast<int>(d->n_kv_heads);
+  a.width = static_cast<int>(width);
+  a.capacity = static_cast<int>(d->capacity);
+  a.n = static_cast<int>(n_nodes);
+  if (d->n_layers > 0) {
+    ProfScope prof(s, RF_STAGE_COMMIT);
+    k_commit<<<dim3(static_cast<unsigned>(d->n_layers), static_cast<unsigned>(d->n_seqs)), 256, 0, s>>>(a);
+  }
+  if ((st = cuda_check(cudaGetLastError(), "k_commit launch")) != RF_OK) return st;
+  ProfScope prof(s, RF_STAGE_COMMIT);
+  k_commit_lens<<<static_cast<unsigned>((d->n_seqs + 255) / 256), 256, 0, s>>>(a);
+  return cuda_check(cudaGetLastError(), "k_commit_lens launch");
+}
