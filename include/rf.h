@@ -599,6 +599,47 @@ rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out, const int
 rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_t* parents, const int32_t* next_pos,
                         uint64_t* mask, int32_t* positions, int32_t* dev_status, rf_stream_t stream);
 
+typedef struct rf_attn_desc {
+  int64_t n_seqs;           /* sequences                                                */
+  int64_t n_q_heads;        /* query heads, a multiple of n_kv_heads; query head i reads */
+                            /* KV head i / (n_q_heads/n_kv_heads); at most 128 per KV head */
+  int64_t n_kv_heads;
+  int64_t head_dim;         /* 64 or 128                                                */
+  int64_t n_nodes;          /* queries (drafted rows) per sequence                      */
+  int64_t capacity;         /* cache rows per sequence, 0 <= lens[b] <= capacity        */
+  int64_t q_row_stride;     /* q: element b*q_seq_stride + i*q_row_stride + head*head_dim + c */
+  int64_t q_seq_stride;
+  int64_t draft_row_stride; /* k_draft, v_draft, likewise                               */
+  int64_t draft_seq_stride;
+  int64_t cache_row_stride; /* k_cache, v_cache, likewise                               */
+  int64_t cache_seq_stride;
+  int64_t out_row_stride;   /* out, likewise                                            */
+  int64_t out_seq_stride;
+  double scale;             /* scores are scale * q.k (scale > 0)                       */
+  uint64_t flags;           /* 0                                                        */
+} rf_attn_desc;
+
+/* Attention of the drafted rows over the cache and over each other. For sequence b,
+ * node i, query head a (KV head h):
+ *   S = {cache rows t < lens[b]} + {drafted rows j that node i sees},
+ *   lse = ln sum_{j in S} exp(scale q.k_j),  out = sum_{j in S} exp(scale q.k_j - lse) v_j.
+ *   tree_mask  [n_seqs][n_nodes][RF_TREE_WORDS(n_nodes)] uint64 (device), any bits (n_nodes
+ *              <= RF_TREE_MAX_NODES; bits beyond n_nodes are ignored), or NULL: node i
+ *              sees drafted rows j <= i (rows in order, n_nodes <= 2^20)
+ *   lens       [n_seqs] int32 (device); a length outside [0, capacity] records
+ *              RF_ERR_INVALID_ARG in *dev_status and that sequence is not written
+ *   out bf16;  lse [n_seqs][n_nodes][n_q_heads] fp32 (may be NULL)
+ * A row that sees nothing gives out = 0 and lse = -inf. Rows that are not seen have no
+ * influence, NaN and infinities among them. Scores, statistics and sums are fp32; a
+ * weight is rounded to bf16 for its product with v. The keys are split over the GPU in
+ * equal shares whatever the lengths are, and split rows are joined in a fixed order. */
+size_t rf_attn_workspace_bytes(const rf_attn_desc* desc);
+rf_status rf_tree_attention(const rf_attn_desc* desc, const rf_bf16* q,
+                            const rf_bf16* k_cache, const rf_bf16* v_cache, const int32_t* lens,
+                            const rf_bf16* k_draft, const rf_bf16* v_draft, const uint64_t* tree_mask,
+                            rf_bf16* out, float* lse, int32_t* dev_status,
+                            void* workspace, size_t workspace_bytes, rf_stream_t stream);
+
 typedef struct rf_verify_desc {
   int64_t n_seqs;
   int64_t n_nodes;    /* 1 .. RF_TREE_MAX_NODES                                        */

@@ -157,6 +157,8 @@ _SIGS = {
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "rf_rope": (c_int, [POINTER(rf_rope_desc), c_void_p, c_void_p, c_void_p, c_void_p]),
     "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
+    "rf_attn_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
+    "rf_tree_attention": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
     "rf_verify_draft": (c_int, [POINTER(rf_verify_desc)] + [c_void_p] * 11),
     "rf_commit_draft": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 4 + [c_void_p] * 14),
     "rf_evict_workspace_bytes": (c_size_t, [POINTER(rf_cache_desc), c_int64]),
@@ -397,6 +399,16 @@ def rf_tree_build(n_seqs, n_nodes, parents, next_pos=None, mask=None, positions=
                                _p(dev_status), _s(stream)), "rf_tree_build")
 
 
+def rf_attn_workspace_bytes(desc: rf_attn_desc) -> int:
+    return int(lib().rf_attn_workspace_bytes(ctypes.byref(desc)))
+
+
+def rf_tree_attention(desc, q, k_cache, v_cache, lens, k_draft, v_draft, tree_mask, out, lse=None, dev_status=None,
+                      workspace=None, workspace_bytes=0, stream=None):
+    """Attention of drafted rows over a cache and over each other; ``tree_mask=None``: rows in order."""
+    _check(lib().rf_tree_attention(ctypes.byref(desc), _p(q), _p(k_cache), _p(v_cache), _p(lens), _p(k_draft),
+                                   _p(v_draft), _p(tree_mask), _p(out), _p(lse), _p(dev_status), _p(workspace),
+                                   int(workspace_bytes), _s(stream)), "rf_tree_attention")
 
 
 def rf_verify_draft(desc, target, draft, tokens, parents, u, noise, path, n_path, next_token, dev_status=None,

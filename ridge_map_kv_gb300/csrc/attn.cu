@@ -1,0 +1,961 @@
+// Attention of drafted rows over a cache and over each other (rf_tree_attention).
+//
+// out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q.k_j - m): one pass over the keys with
+// a running maximum m and sum per query row. The G query heads of a KV head share its
+// keys, so the rows of an item are (node, head) pairs, node-major, up to 128 to a tile
+// (one TMEM lane each).
+//
+// Bound: with R rows to a KV head a key costs 4 R hd flops against 4 hd bytes, so below
+// about R = 275 (the ratio of the measured rates) the cache's bytes are the floor, above
+// it the two matrix products.
+//
+// Work split. A unit is one 128-key tile of one item (sequence, KV head, row tiles); the
+// units of all items are laid end to end and cut into equal shares, one per CTA and one
+// CTA per SM, whatever the lengths are (they are known on the device only). A CTA works
+// through at most a few segments of items; the rows of an item that was cut leave
+// unnormalised sums, maxima and totals in the workspace, and k_attn_combine joins them in
+// the order of the cuts.
+//
+// Two streams per CTA, each with its own score tile S_s and accumulator O_s in TMEM and
+// its own four softmax warps, so that one stream's matrix products run while the other's
+// weights are formed:
+//   up to 128 rows   one row tile; the streams take alternate key tiles, and their
+//                    accumulators are joined when a segment ends;
+//   more rows        two row tiles; every key tile serves both.
+//
+//   warps 0-3, 4-7   softmax of stream 0 / 1: a thread is a row. S_s -> weights in bf16,
+//                    written back over S_s as the A operand of the second product. The
+//                    accumulator is rescaled only when the maximum has grown by more than
+//                    a factor 2^8 (weights stay below 2^8 of the reference, which fp32
+//                    sums and bf16 weights hold without loss), so rarely after the first
+//                    tiles.
+//   warp 8           TMA: query tiles, then K and V tiles through one ring
+//   warp 9           MMA: S_s = Q K^T, O_s += P_s V (P_s from TMEM). It also clears what
+//                    the second product must not see: V rows beyond a sequence's length
+//                    (any bits; their weights are 0, but 0 x NaN is NaN), and elements of
+//                    drafted V rows that are not finite. Rows that do see such an element
+//                    get it in the epilogue.
+#include <algorithm>
+#include <cmath>
+
+#include "rf_device.cuh"
+#include "rf_host.h"
+
+namespace rf {
+
+constexpr int kAtTile = 128;      // keys of a tile, rows of a row tile
+constexpr int kAtThreads = 320;
+constexpr int kAtMaxCtas = 160;   // bounds the workspace
+constexpr int kAtMaxStages = 8;
+constexpr float kAtLog2e = 1.4426950408889634f;
+constexpr float kAtRescale = 8.0f;  // log2 of the growth of the maximum that is let pass
+
+// What a CTA's share starts with; also what k_attn_combine needs of it.
+struct AttnPlan {
+  long long item;  // linear index, -1: no share
+  int b, h, mt, t0, n_tiles, pad;
+};
+
+struct AttnArgs {
+  CUtensorMap tm_q, tm_k, tm_v, tm_kd, tm_vd;
+  const int32_t* lens;
+  const unsigned long long* mask;
+  const __nv_bfloat16* v_draft;
+  __nv_bfloat16* out;
+  float* lse;
+  float* part_o;     // [2 * ctas][rows of an item][head_dim]
+  float2* part_ml;   // [2 * ctas][rows of an item]
+  AttnPlan* plan;    // [ctas]
+  int32_t* dev_status;
+  uint64_t timeout_ns;
+  long long out_row, out_seq, draft_row, draft_seq;
+  int n_seqs, heads, group, n, capacity, words;
+  int npt;        // nodes of a row tile
+  int m_items;    // items (groups of row tiles) of a sequence and head
+  int draft_sum;  // draft tiles summed over those items
+  float scale;
+};
+
+struct AttnShared {
+  uint64_t full[kAtMaxStages], empty[kAtMaxStages];
+  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], o_final, o_empty, ml_full, mma_done;
+  AttnPlan plan;
+  long long units;
+  float2 ml[2][2][kAtTile];  // [segment parity][stream][row]: maximum and total
+  int bad[2];                // a drafted V row of the segment is not finite
+  uint32_t tmem;
+  int abort;
+};
+
+template <int kHD, bool kDual>
+struct AttnCfg {
+  static constexpr int kTileBytes = kAtTile * kHD * 2;
+  static constexpr int kQBytes = (kDual ? 2 : 1) * kTileBytes;
+  static constexpr int kStages = kHD == 128 ? (kDual ? 4 : 5) : 8;
+  static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kStages) * kTileBytes + sizeof(AttnShared) + 64;
+  static constexpr int kRows = (kDual ? 2 : 1) * kAtTile;  // of an item
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Cache and draft tiles of one item.
+struct ItemShape {
+  int len, cached, tiles;  // rows in use, cache tiles, all tiles
+};
+template <bool kDual>
+__device__ __forceinline__ int draft_tiles(const AttnArgs& a, int mt) {
+  const int seen = a.mask != nullptr ? a.n : min(a.n, (mt + 1) * a.npt * (kDual ? 2 : 1));
+  return (seen + kAtTile - 1) / kAtTile;
+}
+__device__ __forceinline__ int length_of(const AttnArgs& a, int b) {  // -1: out of range
+  const int len = a.lens[b];
+  return len < 0 || len > a.capacity ? -1 : len;
+}
+template <bool kDual>
+__device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt) {
+  ItemShape s;
+  s.len = length_of(a, b);
+  s.cached = (max(s.len, 0) + kAtTile - 1) / kAtTile;
+  s.tiles = s.len < 0 ? 0 : s.cached + draft_tiles<kDual>(a, mt);
+  return s;
+}
+
+// A CTA's share, segment by segment; every role walks it alike.
+template <bool kDual>
+struct Walk {
+  int b, h, mt, t0, t1;
+  long long left;
+  ItemShape shape;
+  __device__ __forceinline__ Walk(const AttnArgs& a, const AttnShared* sh) {
+    b = sh->plan.b;
+    h = sh->plan.h;
+    mt = sh->plan.mt;
+    t0 = sh->plan.t0;
+    left = sh->units;
+    shape = ItemShape{0, 0, 0};
+    if (left > 0) {
+      shape = item_shape<kDual>(a, b, mt);
+      t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), t0 + left));
+    }
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    left -= t1 - t0;
+    if (left <= 0) return;
+    t0 = 0;
+    do {
+      if (++mt == a.m_items) {
+        mt = 0;
+        if (++h == a.heads) {
+          h = 0;
+          ++b;
+        }
+      }
+      shape = item_shape<kDual>(a, b, mt);
+    } while (shape.tiles == 0);
+    t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), left));
+  }
+};
+
+// The start of share `cta` of `ctas`: one warp sums the sequences' units, then finds the
+// sequence, head, item and tile of its first unit.
+template <bool kDual>
+__device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas) {
+  const int lane = threadIdx.x & 31;
+  auto units_of = [&](int b) -> long long {
+    if (b >= a.n_seqs) return 0;
+    const int len = length_of(a, b);
+    if (len < 0) {
+      record_status(a.dev_status, RF_ERR_INVALID_ARG);
+      return 0;
+    }
+    return static_cast<long long>(a.heads) *
+           (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile) + a.draft_sum);
+  };
+  long long total = 0;
+  for (int b = lane; b < a.n_seqs; b += 32) total += units_of(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const long long shares = min(static_cast<long long>(ctas), total);
+  AttnPlan p{-1, 0, 0, 0, 0, 0, 0};
+  long long units = 0;
+  if (cta < shares) {
+    const long long first = total * cta / shares;
+    units = total * (cta + 1) / shares - first;
+    long long base = 0;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      const long long own = units_of(b0 + lane);
+      long long x = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, first < base + x);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        p.b = b0 + at;
+        long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
+        const long long per_head = __shfl_sync(0xffffffffu, own, at) / a.heads;
+        p.h = static_cast<int>(r / per_head);
+        r -= p.h * per_head;
+        p.mt = 0;
+        if (a.mask != nullptr) {
+          const int tiles = item_shape<kDual>(a, p.b, 0).tiles;
+          p.mt = static_cast<int>(r / tiles);
+          r -= static_cast<long long>(p.mt) * tiles;
+          p.n_tiles = tiles;
+        } else {
+          while (r >= (p.n_tiles = item_shape<kDual>(a, p.b, p.mt).tiles)) {
+            r -= p.n_tiles;
+            ++p.mt;
+          }
+        }
+        p.t0 = static_cast<int>(r);
+        p.item = (static_cast<long long>(p.b) * a.heads + p.h) * a.m_items + p.mt;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  if (lane == 0) {
+    sh->plan = p;
+    sh->units = units;
+    a.plan[cta] = p;
+  }
+}
+
+// One softmax step of a row: 128 scores at `ts` -> bf16 weights over them.
+// `keep` (when kMasked) holds the row's visible keys.
+template <bool kMasked>
+__device__ __forceinline__ float row_max(uint32_t ts, const uint32_t (&keep)[4]) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32];
+    tmem_ld32(ts + c * 32, r);
+    tmem_wait_ld32(r);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float s = kMasked ? ((keep[c] >> i) & 1u ? u2f(r[i]) : -INFINITY) : u2f(r[i]);
+      mx = fmaxf(mx, s);
+    }
+  }
+  return mx;
+}
+template <bool kMasked>
+__device__ __forceinline__ float row_weights(uint32_t ts, const uint32_t (&keep)[4], float sc, float off) {
+  float total = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t r[32], w[16];
+    tmem_ld32(ts + c * 32, r);
+    tmem_wait_ld32(r);
+    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float p0 = exp2_fast(fmaf(u2f(r[i]), sc, off)), p1 = exp2_fast(fmaf(u2f(r[i + 1]), sc, off));
+      if (kMasked) {
+        p0 = (keep[c] >> i) & 1u ? p0 : 0.0f;
+        p1 = (keep[c] >> (i + 1)) & 1u ? p1 : 0.0f;
+      }
+      l0 += p0;
+      l1 += p1;
+      w[i / 2] = pack_bf16x2(p0, p1);
+    }
+    total += l0 + l1;
+    tmem_st16(ts + c * 16, w);
+  }
+  tmem_wait_st();
+  return total;
+}
+
+// Bits of the keys of tile `t` that query node `node` sees.
+__device__ __forceinline__ void visible(const AttnArgs& a, const ItemShape& s, int b, int node, int t, uint32_t (&keep)[4]) {
+  int limit;  // keys of the tile that exist for this row
+  if (t < s.cached) {
+    limit = s.len - t * kAtTile;
+  } else {
+    const int j0 = (t - s.cached) * kAtTile;
+    limit = (a.mask != nullptr ? a.n : min(a.n, node + 1)) - j0;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int k = limit - c * 32;
+    keep[c] = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+  }
+  if (t >= s.cached && a.mask != nullptr) {
+    const int w0 = (t - s.cached) * 2;
+    const unsigned long long* words = a.mask + (static_cast<long long>(b) * a.n + node) * a.words;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const unsigned long long m = w0 + c < a.words ? words[w0 + c] : 0ull;
+      keep[2 * c] &= static_cast<uint32_t>(m);
+      keep[2 * c + 1] &= static_cast<uint32_t>(m >> 32);
+    }
+  }
+}
+
+template <int kHD, bool kDual>
+__global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ AttnArgs a) {
+  using Cfg = AttnCfg<kHD, kDual>;
+  constexpr int kChunks = kHD / 64;                 // 64-channel slabs of a tile, 16 KB each
+  constexpr int kSlab = kAtTile * 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  AttnShared* sh = reinterpret_cast<AttnShared*>(smem + Cfg::kQBytes + Cfg::kStages * Cfg::kTileBytes);
+  const uint32_t s_q = smem_u32(smem), s_ring = s_q + Cfg::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh->abort;
+  const uint64_t timeout = a.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < Cfg::kStages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->q_full, 1);
+    mbar_init(&sh->q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->s_full[s], 1);
+      mbar_init(&sh->p_full[s], 4);
+      mbar_init(&sh->o_done[s], 1);
+    }
+    mbar_init(&sh->o_final, 2);
+    mbar_init(&sh->o_empty, 8);
+    mbar_init(&sh->ml_full, 8);
+    mbar_init(&sh->mma_done, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+    tma_prefetch_desc(&a.tm_kd);
+    tma_prefetch_desc(&a.tm_vd);
+  }
+  if (warp == 9) {
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == 0) find_share<kDual>(a, sh, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, q_phase = 0;
+      long long issued = 0;
+      bool ok = true, q_inflight = false;
+      auto load = [&](const Walk<kDual>& w, int t, bool v) {
+        if (!mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, timeout)) return false;
+        mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
+        const bool draft = t >= w.shape.cached;
+        const CUtensorMap* tm = draft ? (v ? &a.tm_vd : &a.tm_kd) : (v ? &a.tm_v : &a.tm_k);
+        const int row = (draft ? t - w.shape.cached : t) * kAtTile;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, w.b);
+        ++issued;
+        if (++stage == Cfg::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        return true;
+      };
+      for (Walk<kDual> w(a, sh); w.more() && ok; w.next(a)) {
+        if (!mbar_wait(&sh->q_empty, q_phase ^ 1u, abort_flag, timeout)) break;
+        mbar_arrive_expect_tx(&sh->q_full, (kDual ? 2 : 1) * kChunks * 64 * 2 * a.group * a.npt);
+        q_inflight = true;
+        for (int s = 0; s < (kDual ? 2 : 1); ++s)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, &a.tm_q, smem_u32(&sh->q_full), c * 64, w.h * a.group,
+                        (w.mt * (kDual ? 2 : 1) + s) * a.npt, w.b);
+        q_phase ^= 1u;
+        // the order in which warp 9 takes them
+        if (kDual) {
+          for (int t = w.t0; t < w.t1 && ok; ++t) ok = load(w, t, false) && load(w, t, true);
+        } else {
+          ok = load(w, w.t0, false);
+          for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load(w, t, false) && load(w, t - 1, true);
+          ok = ok && load(w, w.t1 - 1, true);
+        }
+      }
+      // Drain: every issued copy lands before the CTA may exit.
+      int dummy = 0;
+      if (q_inflight) mbar_wait(&sh->q_full, q_phase ^ 1u, &dummy, timeout);
+      for (long long i = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); i < issued; ++i)
+        mbar_wait(&sh->full[i % Cfg::kStages], static_cast<uint32_t>((i / Cfg::kStages) & 1), &dummy, timeout);
+    }
+  } else if (warp == 9) {
+    constexpr uint32_t idesc_s = make_idesc_bf16(kAtTile, kAtTile, 0, 0);
+    constexpr uint32_t idesc_o = make_idesc_bf16(kAtTile, kHD, 0, 1);
+    int stage = 0;
+    uint32_t phase = 0, q_phase = 0, o_phase = 0, p_phase[2] = {0, 0};
+    int seg = 0;
+    auto advance = [&] {
+      if (++stage == Cfg::kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    auto wait = [&](uint64_t* bar, uint32_t par) {  // whole warp
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, timeout));
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    auto qk = [&](int s, int q) {  // S_s = Q_q K^T of the current stage
+      if (lane == 0) {
+        const uint32_t k0 = s_ring + stage * Cfg::kTileBytes, q0 = s_q + q * Cfg::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kHD / 16; ++k) {
+          const uint32_t off = (k / 4) * kSlab + (k % 4) * 32;
+          tc_mma_bf16(tmem + s * kAtTile, make_sdesc_sw128(q0 + off, 16, 1024), make_sdesc_sw128(k0 + off, 16, 1024),
+                      idesc_s, k > 0 ? 1u : 0u);
+        }
+        tc_commit(&sh->s_full[s]);
+      }
+    };
+    auto pv = [&](int s, bool fresh) {  // O_s (+)= P_s V of the current stage
+      if (lane == 0) {
+        const uint32_t v0 = s_ring + stage * Cfg::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kAtTile / 16; ++k)
+          tc_mma_bf16_ts(tmem + 256 + s * 128, tmem + s * kAtTile + k * 8, make_sdesc_sw128(v0 + k * 2048, kSlab, 1024),
+                         idesc_o, fresh && k == 0 ? 0u : 1u);
+        tc_commit(&sh->o_done[s]);
+      }
+    };
+    auto release = [&] {
+      if (lane == 0) tc_commit(&sh->empty[stage]);
+      advance();
+    };
+    // Clears V elements of the current stage that no product may see (whole warp).
+    auto clean = [&](const Walk<kDual>& w, int t) {
+      const uint32_t v0 = s_ring + stage * Cfg::kTileBytes;
+      if (t < w.shape.cached) {
+        const int rows = w.shape.len - t * kAtTile;
+        if (rows >= kAtTile) return;
+        for (int i = rows * 8 + lane; i < kAtTile * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) st_shared_v4(v0 + c * kSlab + i * 16, 0, 0, 0, 0);
+      } else {
+        const int rows = min(kAtTile, a.n - (t - w.shape.cached) * kAtTile);
+        bool bad = false;
+        for (int i = lane; i < rows * 8; i += 32)
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            const uint32_t at = v0 + c * kSlab + i * 16;
+            uint4 v = ld_shared_v4(at);
+            uint32_t* x = reinterpret_cast<uint32_t*>(&v);
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((x[e] & 0x7f80u) == 0x7f80u) {
+                x[e] &= 0xffff0000u;
+                hit = true;
+              }
+              if ((x[e] & 0x7f800000u) == 0x7f800000u) {
+                x[e] &= 0xffffu;
+                hit = true;
+              }
+            }
+            if (hit) {
+              st_shared_v4(at, x[0], x[1], x[2], x[3]);
+              bad = true;
+            }
+          }
+        if (bad) sh->bad[seg & 1] = 1;
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+    };
+    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+      const int n_tiles = w.t1 - w.t0;
+      if (lane == 0) sh->bad[seg & 1] = 0;
+      __syncwarp();
+      if (!wait(&sh->q_full, q_phase)) goto mma_done;
+      q_phase ^= 1u;
+      if (kDual) {
+        if (!wait(&sh->full[stage], phase)) goto mma_done;
+        qk(0, 0);
+        qk(1, 1);
+        if (n_tiles == 1 && lane == 0) tc_commit(&sh->q_empty);
+        release();
+        if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
+        for (int i = 0; i < n_tiles; ++i) {
+          const int v_stage = stage;
+          if (!wait(&sh->full[stage], phase)) goto mma_done;
+          clean(w, w.t0 + i);
+          advance();
+          const int k_stage = stage;
+          const bool more = i + 1 < n_tiles;
+          for (int s = 0; s < 2; ++s) {
+            if (!wait(&sh->p_full[s], p_phase[s])) goto mma_done;
+            p_phase[s] ^= 1u;
+            stage = v_stage;
+            pv(s, i == 0);
+            if (s == 1 && lane == 0) tc_commit(&sh->empty[v_stage]);
+            stage = k_stage;
+            if (more) {
+              if (s == 0 && !wait(&sh->full[stage], phase)) goto mma_done;
+              qk(s, s);
+            }
+          }
+          if (more) {
+            if (i + 2 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
+            release();
+          }
+        }
+      } else {
+        for (int i = 0; i < 2 && i < n_tiles; ++i) {
+          if (i == 1) {
+            // (the ring holds K0, K1, V0, ...)
+          }
+          if (!wait(&sh->full[stage], phase)) goto mma_done;
+          qk(i, 0);
+          if (i + 1 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
+          release();
+        }
+        if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
+        for (int i = 0; i < n_tiles; ++i) {
+          const int s = i & 1;
+          if (!wait(&sh->full[stage], phase)) goto mma_done;
+          clean(w, w.t0 + i);
+          if (!wait(&sh->p_full[s], p_phase[s])) goto mma_done;
+          p_phase[s] ^= 1u;
+          pv(s, i < 2);
+          release();
+          if (i + 2 < n_tiles) {
+            if (!wait(&sh->full[stage], phase)) goto mma_done;
+            qk(s, 0);
+            if (i + 3 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
+            release();
+          }
+        }
+      }
+      if (lane == 0) {
+        tc_commit(&sh->o_final);
+        mbar_arrive(&sh->o_final);  // and what this warp found in V
+      }
+      o_phase ^= 1u;
+      ++seg;
+    }
+  mma_done:
+    if (lane == 0) {
+      tc_commit(&sh->mma_done);
+      int dummy = 0;
+      mbar_wait(&sh->mma_done, 0, &dummy, timeout);
+    }
+    __syncwarp();
+  } else {
+    const int s = warp >> 2;             // stream
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + s * kAtTile;
+    const float sc = a.scale * kAtLog2e;
+    uint32_t s_phase = 0, o_phase = 0, f_phase = 0;
+    int seg = 0;
+    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+      const int n_tiles = w.t1 - w.t0;
+      const int node0 = (w.mt * (kDual ? 2 : 1) + (kDual ? s : 0)) * a.npt;
+      const int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile
+      const bool idle = (warp & 3) * 32 >= rows;                   // a warp without rows
+      const int node = min(node0 + row / a.group, a.n - 1);
+      float m = -INFINITY, l = 0.0f;
+      bool first = true;
+      for (int i = kDual ? 0 : s; i < n_tiles; i += kDual ? 1 : 2) {
+        bool ok = mbar_wait(&sh->s_full[s], s_phase, abort_flag, timeout);
+        if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+        s_phase ^= 1u;
+        tc_fence_after();
+        if (!idle) {
+          const int t = w.t0 + i;
+          const bool masked = t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len;
+          uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          float mx;
+          if (masked) {
+            visible(a, w.shape, w.b, node, t, keep);
+            mx = row_max<true>(ts, keep);
+          } else {
+            mx = row_max<false>(ts, keep);
+          }
+          mx = fmaxf(mx, m);
+          const bool grown = m == -INFINITY ? mx > -INFINITY : (mx - m) * sc > kAtRescale;
+          if (__any_sync(0xffffffffu, grown)) {
+            // With nothing seen so far l and the accumulator's row are 0 (or not written yet).
+            const float f = grown ? (m == -INFINITY ? 0.0f : exp2_fast((m - mx) * sc)) : 1.0f;
+            if (!first) {
+              ok = mbar_wait(&sh->o_done[s], o_phase ^ 1u, abort_flag, timeout);  // the previous tile's product
+              if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < kHD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tmem + lanes + 256 + s * 128 + c, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(u2f(o[e]) * f);
+                tmem_st16(tmem + lanes + 256 + s * 128 + c, o);
+              }
+            }
+            l *= f;
+            if (grown) m = mx;
+          }
+          const float off = m == -INFINITY ? 0.0f : -m * sc;
+          l += masked ? row_weights<true>(ts, keep, sc, off) : row_weights<false>(ts, keep, sc, off);
+        }
+        first = false;
+        o_phase ^= 1u;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[s]);
+      }
+      // Epilogue.
+      if (!kDual) {
+        sh->ml[seg & 1][s][row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->ml_full);
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->ml_full, f_phase, abort_flag, timeout))) goto softmax_done;
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->o_final, f_phase, abort_flag, timeout))) goto softmax_done;
+      f_phase ^= 1u;
+      tc_fence_after();
+      {
+        // stream sums to join (one row tile): this warp takes half of the channels of both
+        float f0 = 1.0f, f1 = 0.0f;
+        if (!kDual) {
+          const float2 u = sh->ml[seg & 1][0][row], v = sh->ml[seg & 1][1][row];
+          m = fmaxf(u.x, v.x);
+          f0 = u.x == -INFINITY ? 0.0f : exp2_fast((u.x - m) * sc);
+          f1 = v.x == -INFINITY ? 0.0f : exp2_fast((v.x - m) * sc);
+          l = u.y * f0 + v.y * f1;
+          if (m == INFINITY) l = NAN;  // inf - inf above
+        }
+        const bool whole = w.t0 == 0 && w.t1 == w.shape.tiles;
+        const bool bad = *reinterpret_cast<volatile int*>(&sh->bad[seg & 1]) != 0;
+        const bool write = row < rows;
+        const int head = w.h * a.group + row % a.group;
+        const long long slot = 2LL * blockIdx.x + (w.t0 > 0 ? 0 : 1);
+        const long long prow = slot * Cfg::kRows + (kDual ? s * kAtTile : 0) + row;
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        if (!idle) {
+          constexpr int kCols = kDual ? kHD : kHD / 2;
+          const int col0 = kDual ? 0 : s * kCols;
+          const uint32_t to = tmem + lanes + 256 + (kDual ? s * 128 : 0) + col0;
+#pragma unroll 1
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + c, o);
+            tmem_wait_ld16(o);
+            float x[16];
+            if (!kDual) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = f0 != 0.0f ? u2f(o[e]) * f0 : 0.0f;
+              if (n_tiles > 1) {
+                tmem_ld16(to + 128 + c, o);
+                tmem_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] += f1 != 0.0f ? u2f(o[e]) * f1 : 0.0f;
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) x[e] = u2f(o[e]);
+            }
+            if (bad) {  // elements that the product did not see: an infinity or NaN swallows any sum
+              const int d1 = min(a.n, (w.t1 - w.shape.cached) * kAtTile);
+              for (int j = max(0, w.t0 - w.shape.cached) * kAtTile; j < d1; ++j) {
+                const bool sees = a.mask != nullptr
+                                      ? (a.mask[(static_cast<long long>(w.b) * a.n + node) * a.words + (j >> 6)] >> (j & 63)) & 1u
+                                      : j <= node;
+                if (!sees) continue;
+                const __nv_bfloat16* v = a.v_draft + w.b * a.draft_seq + j * a.draft_row + w.h * kHD + col0 + c;
+                for (int e = 0; e < 16; ++e) {
+                  const float y = __bfloat162float(v[e]);
+                  if (!isfinite(y)) x[e] += y;
+                }
+              }
+            }
+            if (write) {
+              if (whole) {
+                uint32_t pk[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
+                __nv_bfloat16* dst = a.out + w.b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + col0 + c;
+                st_global_v4(dst, pk[0], pk[1], pk[2], pk[3]);
+                st_global_v4(dst + 8, pk[4], pk[5], pk[6], pk[7]);
+              } else {
+                float4* dst = reinterpret_cast<float4*>(a.part_o + prow * kHD + col0 + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+              }
+            }
+          }
+          if (write && (kDual || s == 0)) {
+            if (!whole) a.part_ml[prow] = make_float2(m, l);
+            else if (a.lse != nullptr)
+              a.lse[(static_cast<long long>(w.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
+                  l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->o_empty);
+      ++seg;
+    }
+  softmax_done:;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && sh->abort) record_status(a.dev_status, RF_ERR_TIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the rows of items that were cut. Block x: the cut before share x + 1; the first
+// cut inside an item answers for it. A warp takes a row at a time.
+struct CombineArgs {
+  const AttnPlan* plan;
+  const float* part_o;
+  const float2* part_ml;
+  __nv_bfloat16* out;
+  float* lse;
+  long long out_row, out_seq;
+  int n, heads, group, npt, tiles, ctas;  // tiles: row tiles of an item
+  float scale;
+};
+constexpr int kCombineWarps = 4;
+
+template <int kHD>
+__global__ void __launch_bounds__(32 * kCombineWarps) k_attn_combine(const __grid_constant__ CombineArgs a) {
+  const int c = blockIdx.x + 1;
+  const AttnPlan p = a.plan[c];
+  if (p.item < 0 || p.t0 == 0) return;
+  const AttnPlan before = a.plan[c - 1];
+  if (before.item == p.item && before.t0 > 0) return;
+  int parts = 2;  // from share c - 1, from share c, ...
+  while (c + parts - 1 < a.ctas) {
+    const AttnPlan q = a.plan[c + parts - 1];
+    if (q.item != p.item || q.t0 == 0) break;
+    ++parts;
+  }
+  const int lane = threadIdx.x & 31;
+  const int item_rows = a.tiles * kAtTile;
+  const float sc = a.scale * kAtLog2e;
+  constexpr int kPer = kHD / 32;
+  auto slot_of = [&](int i) { return i == 0 ? 2LL * (c - 1) + 1 : 2LL * (c - 1 + i); };
+  for (int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); r < item_rows; r += gridDim.y * kCombineWarps) {
+    const int in_tile = r % kAtTile;
+    if (in_tile >= a.npt * a.group) continue;
+    const int node = (p.mt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
+    if (node >= a.n) continue;
+    const int head = p.h * a.group + in_tile % a.group;
+    float m = -INFINITY;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[slot_of(i) * item_rows + r].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f, x[kPer] = {};
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const long long at = slot_of(i) * item_rows + r;
+      const float2 ml = a.part_ml[at];
+      const float f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2_fast((ml.x - m) * sc);
+      l += ml.y * f;
+      float v[kPer];
+      if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at * kHD + lane * 4);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + at * kHD + lane * 2);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = fmaf(v[e], f, x[e]);
+    }
+    // A part whose rows see nothing yet but a non-finite value cannot be: what is seen has weight.
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    __nv_bfloat16* dst = a.out + p.b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + lane * kPer;
+    if constexpr (kPer == 4) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+    } else {
+      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(x[0] * inv, x[1] * inv);
+    }
+    if (lane == 0 && a.lse != nullptr)
+      a.lse[(static_cast<long long>(p.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
+          l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+  }
+}
+
+rf_status check_attn_desc(const rf_attn_desc* d) {
+  if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
+  if (d->n_seqs < 0 || d->n_q_heads <= 0 || d->n_kv_heads <= 0 || d->n_nodes <= 0 || d->capacity <= 0)
+    return fail(RF_ERR_INVALID_ARG, "need n_seqs >= 0, n_q_heads, n_kv_heads, n_nodes, capacity > 0");
+  if (!(d->scale > 0.0) || !std::isfinite(static_cast<float>(d->scale)) || !(static_cast<float>(d->scale) > 0.0f))
+    return fail(RF_ERR_INVALID_ARG, "scale must be a finite fp32 number > 0");
+  if (d->flags != 0) return fail(RF_ERR_INVALID_ARG, "flags must be 0");
+  if (d->head_dim != 64 && d->head_dim != 128) return fail(RF_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (d->n_q_heads % d->n_kv_heads != 0 || d->n_q_heads / d->n_kv_heads > 128)
+    return fail(RF_ERR_SHAPE, "n_q_heads must be a multiple of n_kv_heads, at most 128 times it");
+  if (d->n_nodes > (int64_t(1) << 20) || d->capacity > (int64_t(1) << 30) || d->n_seqs > (int64_t(1) << 20) ||
+      d->n_q_heads > (int64_t(1) << 20))
+    return fail(RF_ERR_SHAPE, "need n_nodes, n_seqs, n_q_heads <= 2^20, capacity <= 2^30");
+  const int64_t qw = d->n_q_heads * d->head_dim, kw = d->n_kv_heads * d->head_dim;
+  const int64_t rows[4] = {d->q_row_stride, d->draft_row_stride, d->cache_row_stride, d->out_row_stride};
+  const int64_t seqs[4] = {d->q_seq_stride, d->draft_seq_stride, d->cache_seq_stride, d->out_seq_stride};
+  const int64_t least[4] = {qw, kw, kw, qw};
+  for (int i = 0; i < 4; ++i) {
+    if (rows[i] < least[i] || rows[i] % 8 || seqs[i] % 8 || (d->n_seqs > 1 && seqs[i] <= 0))
+      return fail(RF_ERR_ALIGN, "strides must be multiples of 8, row strides >= heads*head_dim, sequence strides > 0");
+    if (rows[i] >= (int64_t(1) << 39) || seqs[i] >= (int64_t(1) << 39)) return fail(RF_ERR_SHAPE, "strides must be < 2^39");
+  }
+  return RF_OK;
+}
+
+struct AttnLayout {
+  float* part_o;
+  float2* part_ml;
+  AttnPlan* plan;
+  int tiles;  // row tiles of an item
+  size_t bytes;
+};
+
+static AttnLayout attn_layout(const rf_attn_desc* d, void* ws) {
+  AttnLayout l;
+  l.tiles = d->n_nodes * (d->n_q_heads / d->n_kv_heads) > kAtTile ? 2 : 1;
+  const size_t rows = static_cast<size_t>(2 * kAtMaxCtas) * l.tiles * kAtTile;
+  Carve c(ws);
+  l.part_o = c.take<float>(rows * d->head_dim);
+  l.part_ml = c.take<float2>(rows);
+  l.plan = c.take<AttnPlan>(kAtMaxCtas);
+  l.bytes = c.bytes();
+  return l;
+}
+
+template <int kHD, bool kDual>
+static rf_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t s) {
+  static uint64_t done = 0;
+  using Cfg = AttnCfg<kHD, kDual>;
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory beyond the 227 KB a CTA may hold");
+  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual>), Cfg::kSmem, &done);
+  if (st != RF_OK) return st;
+  ProfScope prof(s, RF_STAGE_ATTENTION);
+  k_attn<kHD, kDual><<<ctas, kAtThreads, Cfg::kSmem, s>>>(a);
+  return cuda_check(cudaGetLastError(), "k_attn launch");
+}
+
+}  // namespace rf
+
+using namespace rf;
+
+extern "C" size_t rf_attn_workspace_bytes(const rf_attn_desc* desc) {
+  if (check_attn_desc(desc) != RF_OK) return 0;
+  return attn_layout(desc, nullptr).bytes;
+}
+
+extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, const rf_bf16* k_cache,
+                                       const rf_bf16* v_cache, const int32_t* lens, const rf_bf16* k_draft,
+                                       const rf_bf16* v_draft, const uint64_t* tree_mask, rf_bf16* out, float* lse,
+                                       int32_t* dev_status, void* workspace, size_t workspace_bytes,
+                                       rf_stream_t stream) {
+  clear_error();
+  rf_status st = check_attn_desc(d);
+  if (st != RF_OK) return st;
+  if (tree_mask != nullptr && d->n_nodes > RF_TREE_MAX_NODES)
+    return fail(RF_ERR_SHAPE, "n_nodes must be <= %d with a mask", RF_TREE_MAX_NODES);
+  if (d->n_seqs == 0) return RF_OK;
+  if (!q || !k_cache || !v_cache || !lens || !k_draft || !v_draft || !out)
+    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_draft) || !aligned16(v_draft) ||
+      !aligned16(out))
+    return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(RF_ERR_ALIGN, "arrays must be aligned to their elements");
+  const AttnLayout lay = attn_layout(d, workspace);
+  if (workspace == nullptr || workspace_bytes < lay.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
+  int sms = 0;
+  if ((st = current_device(&sms)) != RF_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs;
+  const int group = static_cast<int>(Hq / H);
+  AttnArgs a{};
+  a.npt = kAtTile / group;
+  const uint64_t cap = d->capacity;
+  // a box of a row tile: every head of the group, npt nodes
+  if ((st = make_tmap_bf16_4d(&a.tm_q, q, {hd, Hq, n, B}, {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
+                              {64, (uint32_t)group, (uint32_t)a.npt, 1})) != RF_OK)
+    return st;
+  const uint64_t cs[3] = {hd, (uint64_t)d->cache_row_stride, (uint64_t)d->cache_seq_stride};
+  const uint64_t ds[3] = {hd, (uint64_t)d->draft_row_stride, (uint64_t)d->draft_seq_stride};
+  const uint64_t cd[4] = {hd, H, cap, B}, dd[4] = {hd, H, n, B};
+  const uint32_t box[4] = {64, 1, kAtTile, 1};
+  if ((st = make_tmap_bf16_4d(&a.tm_k, k_cache, cd, cs, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_v, v_cache, cd, cs, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_kd, k_draft, dd, ds, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_vd, v_draft, dd, ds, box)) != RF_OK) return st;
+  a.lens = lens;
+  a.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  a.v_draft = reinterpret_cast<const __nv_bfloat16*>(v_draft);
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.part_o = lay.part_o;
+  a.part_ml = lay.part_ml;
+  a.plan = lay.plan;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  a.out_row = d->out_row_stride;
+  a.out_seq = d->out_seq_stride;
+  a.draft_row = d->draft_row_stride;
+  a.draft_seq = d->draft_seq_stride;
+  a.n_seqs = static_cast<int>(B);
+  a.heads = static_cast<int>(H);
+  a.group = group;
+  a.n = static_cast<int>(n);
+  a.capacity = static_cast<int>(cap);
+  a.words = static_cast<int>(RF_TREE_WORDS(n));
+  a.scale = static_cast<float>(d->scale);
+  const int64_t per = static_cast<int64_t>(a.npt) * lay.tiles;  // nodes of an item
+  a.m_items = static_cast<int>((n + per - 1) / per);
+  int64_t draft_sum = 0;
+  for (int64_t mt = 0; mt < a.m_items; ++mt) {
+    const int64_t seen = tree_mask != nullptr ? static_cast<int64_t>(n) : std::min<int64_t>(n, (mt + 1) * per);
+    draft_sum += (seen + kAtTile - 1) / kAtTile;
+  }
+  if (draft_sum >= (int64_t(1) << 31)) return fail(RF_ERR_SHAPE, "n_nodes is too large");
+  a.draft_sum = static_cast<int>(draft_sum);
+  const int64_t most = static_cast<int64_t>(B * H) * (a.m_items * static_cast<int64_t>((cap + kAtTile - 1) / kAtTile) + draft_sum);
+  const int ctas = static_cast<int>(std::min<int64_t>(most, std::min(sms, kAtMaxCtas)));
+  if (hd == 128) st = lay.tiles == 2 ? launch_attn<128, true>(a, ctas, s) : launch_attn<128, false>(a, ctas, s);
+  else st = lay.tiles == 2 ? launch_attn<64, true>(a, ctas, s) : launch_attn<64, false>(a, ctas, s);
+  if (st != RF_OK || ctas < 2) return st;
+  CombineArgs c{};
+  c.plan = lay.plan;
+  c.part_o = lay.part_o;
+  c.part_ml = lay.part_ml;
+  c.out = a.out;
+  c.lse = lse;
+  c.out_row = a.out_row;
+  c.out_seq = a.out_seq;
+  c.n = a.n;
+  c.heads = a.heads;
+  c.group = group;
+  c.npt = a.npt;
+  c.tiles = lay.tiles;
+  c.ctas = ctas;
+  c.scale = a.scale;
+  const int rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, lay.tiles * kAtTile));
+  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps));
+  ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
+  if (hd == 128) k_attn_combine<128><<<grid, 32 * kCombineWarps, 0, s>>>(c);
+  else k_attn_combine<64><<<grid, 32 * kCombineWarps, 0, s>>>(c);
+  return cuda_check(cudaGetLastError(), "k_attn_combine launch");
+}
