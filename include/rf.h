@@ -702,6 +702,26 @@ rf_status rf_commit_draft(const rf_cache_desc* desc, int64_t n_nodes, int64_t dr
                           rf_bf16* k_cache, rf_bf16* v_cache, float* score, int32_t* pos,
                           int32_t* new_lens, int32_t* new_next_pos, int32_t* dev_status, rf_stream_t stream);
 
+/* Adds the attention weights that each cached row received. The queries are the nodes
+ * path[b][0 .. n_path[b]-1] (all n_nodes rows in order when path and n_path are NULL);
+ * their own rows are the last of the cache's lens[b] rows (after rf_commit_draft). For
+ * every cache row t < lens[b] and KV head h:
+ *   score_out[b][h][t] = decay score_in[b][h][t]
+ *       + sum over j with t <= lens[b] - n + j, and the KV head's query heads a, of
+ *         exp(scale q[path[j]][a].k_t - lse[path[j]][a]),   n = n_path[b] or n_nodes.
+ * q, lse, desc as for rf_tree_attention; score [n_seqs][n_kv_heads][capacity] fp32,
+ * score_out may be score_in; entries t >= lens[b] are not written. A query whose lse is
+ * -inf adds nothing. decay 0 does not read score_in (which may be NULL then). A sequence
+ * with a length, count or path out of range records RF_ERR_INVALID_ARG and is not
+ * written (n <= lens[b] is required). Sums are fp32, in an order that depends on the
+ * sizes alone. */
+size_t rf_attn_weights_workspace_bytes(const rf_attn_desc* desc);
+rf_status rf_attn_weights(const rf_attn_desc* desc, const rf_bf16* q, const float* lse,
+                          const int32_t* path, const int32_t* n_path,
+                          const rf_bf16* k_cache, const int32_t* lens, double decay,
+                          const float* score_in, float* score_out, int32_t* dev_status,
+                          void* workspace, size_t workspace_bytes, rf_stream_t stream);
+
 /* Evicts rows of little weight: in every layer, sequence and KV head, min(lens[b], keep)
  * rows stay. Rows whose position is below n_sink or at least next_pos[b] - n_recent rank
  * as +inf, the others by score (NaN as -inf); the highest ranks stay, the lowest row

@@ -161,6 +161,9 @@ _SIGS = {
     "rf_tree_attention": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
     "rf_verify_draft": (c_int, [POINTER(rf_verify_desc)] + [c_void_p] * 11),
     "rf_commit_draft": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 4 + [c_void_p] * 14),
+    "rf_attn_weights_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
+    "rf_attn_weights": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 6 + [c_double] + [c_void_p] * 4 +
+                        [c_size_t, c_void_p]),
     "rf_evict_workspace_bytes": (c_size_t, [POINTER(rf_cache_desc), c_int64]),
     "rf_evict": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 3 + [c_void_p] * 11 + [c_size_t, c_void_p]),
 }
@@ -429,6 +432,16 @@ def rf_commit_draft(desc, n_nodes, draft_row_stride, draft_seq_stride, draft_lay
                                  _p(new_next_pos), _p(dev_status), _s(stream)), "rf_commit_draft")
 
 
+def rf_attn_weights_workspace_bytes(desc: rf_attn_desc) -> int:
+    return int(lib().rf_attn_weights_workspace_bytes(ctypes.byref(desc)))
+
+
+def rf_attn_weights(desc, q, lse, path, n_path, k_cache, lens, decay, score_in, score_out, dev_status=None,
+                    workspace=None, workspace_bytes=0, stream=None):
+    """score_out = decay * score_in + the attention weights that each cached row received."""
+    _check(lib().rf_attn_weights(ctypes.byref(desc), _p(q), _p(lse), _p(path), _p(n_path), _p(k_cache), _p(lens),
+                                 float(decay), _p(score_in), _p(score_out), _p(dev_status), _p(workspace),
+                                 int(workspace_bytes), _s(stream)), "rf_attn_weights")
 
 
 def rf_evict_workspace_bytes(desc: rf_cache_desc, keep: int) -> int:

@@ -96,12 +96,6 @@ struct AttnCfg {
   static constexpr int kRows = (kDual ? 2 : 1) * kAtTile;  // of an item
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Cache and draft tiles of one item.
 struct ItemShape {
   int len, cached, tiles;  // rows in use, cache tiles, all tiles
@@ -258,7 +252,7 @@ __device__ __forceinline__ float row_weights(uint32_t ts, const uint32_t (&keep)
     float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      float p0 = exp2_fast(fmaf(u2f(r[i]), sc, off)), p1 = exp2_fast(fmaf(u2f(r[i + 1]), sc, off));
+      float p0 = exp2f_ftz(fmaf(u2f(r[i]), sc, off)), p1 = exp2f_ftz(fmaf(u2f(r[i + 1]), sc, off));
       if (kMasked) {
         p0 = (keep[c] >> i) & 1u ? p0 : 0.0f;
         p1 = (keep[c] >> (i + 1)) & 1u ? p1 : 0.0f;
@@ -518,9 +512,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
       } else {
         for (int i = 0; i < 2 && i < n_tiles; ++i) {
-          if (i == 1) {
-            // (the ring holds K0, K1, V0, ...)
-          }
           if (!wait(&sh->full[stage], phase)) goto mma_done;
           qk(i, 0);
           if (i + 1 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
@@ -593,7 +584,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           const bool grown = m == -INFINITY ? mx > -INFINITY : (mx - m) * sc > kAtRescale;
           if (__any_sync(0xffffffffu, grown)) {
             // With nothing seen so far l and the accumulator's row are 0 (or not written yet).
-            const float f = grown ? (m == -INFINITY ? 0.0f : exp2_fast((m - mx) * sc)) : 1.0f;
+            const float f = grown ? (m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc)) : 1.0f;
             if (!first) {
               ok = mbar_wait(&sh->o_done[s], o_phase ^ 1u, abort_flag, timeout);  // the previous tile's product
               if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
@@ -636,8 +627,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         if (!kDual) {
           const float2 u = sh->ml[seg & 1][0][row], v = sh->ml[seg & 1][1][row];
           m = fmaxf(u.x, v.x);
-          f0 = u.x == -INFINITY ? 0.0f : exp2_fast((u.x - m) * sc);
-          f1 = v.x == -INFINITY ? 0.0f : exp2_fast((v.x - m) * sc);
+          f0 = u.x == -INFINITY ? 0.0f : exp2f_ftz((u.x - m) * sc);
+          f1 = v.x == -INFINITY ? 0.0f : exp2f_ftz((v.x - m) * sc);
           l = u.y * f0 + v.y * f1;
           if (m == INFINITY) l = NAN;  // inf - inf above
         }
@@ -772,7 +763,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_attn_combine(const __gri
     for (int i = 0; i < parts; ++i) {
       const long long at = slot_of(i) * item_rows + r;
       const float2 ml = a.part_ml[at];
-      const float f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2_fast((ml.x - m) * sc);
+      const float f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2f_ftz((ml.x - m) * sc);
       l += ml.y * f;
       float v[kPer];
       if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at * kHD + lane * 4);

@@ -1,0 +1,488 @@
+// Accumulated attention weights of cached rows (rf_attn_weights).
+//
+// score_out[t] = decay score_in[t] + sum over queries c that see t of
+//                exp(scale q_c.k_t - lse_c).
+// The statistics are known, so a key's sum needs no other key: each key tile is read
+// once, and what is written is one number a key. The product is taken as S = K Qᵀ, keys
+// along the TMEM lanes: a thread owns a key and sums over its columns, so there is no
+// reduction across threads but that of the two warps that share a key's columns.
+//
+// Bound: the keys' bytes up to a few hundred queries (2 hd bytes a key against 2 R hd
+// flops and R exponentials); beyond, the exponentials and the product.
+//
+// The queries of a KV head (nodes of the path times query heads, R of them) stay in
+// shared memory, up to 640 rows of 128 channels; the product takes them in steps of up
+// to 256 columns, two of which are in TMEM at a time. More queries are taken in further
+// launches. Units (128-key tiles) of all sequences and heads are cut into equal shares,
+// one per CTA.
+//
+//   warps 0-3, 4-7   sums: a thread is a key; the first four warps take a step's first
+//                    half of the columns, the others the second
+//   warp 8           TMA: key tiles, in 64-channel slabs
+//   warp 9           MMA
+//   warps 10-13      the queries of the next (sequence, head): gathered along the path
+#include <algorithm>
+#include <cmath>
+
+#include "rf_device.cuh"
+#include "rf_host.h"
+
+namespace rf {
+
+constexpr int kWtTile = 128;
+constexpr int kWtThreads = 448;
+constexpr int kWtLoaders = 128;      // threads of warps 10-13
+constexpr int kWtMaxSeqs = 1024;     // lengths and counts are kept in shared memory
+constexpr int kWtStep = 256;         // columns of a step
+constexpr int kWtMaxStages = 12;
+constexpr int kWtSlab = kWtTile * 128;
+constexpr int kWtQBytes = 640 * 128 * 2;  // the most that queries may take
+constexpr float kWtLog2e = 1.4426950408889634f;
+
+struct WeightArgs {
+  CUtensorMap tm_k;
+  const __nv_bfloat16* q;
+  const float* lse;
+  const int32_t* path;
+  const int32_t* n_path;
+  const int32_t* lens;
+  const float* score_in;  // nullptr: decay is 0
+  float* score_out;
+  int32_t* dev_status;
+  uint64_t timeout_ns;
+  long long q_row, q_seq;
+  int n_seqs, heads, group, n, capacity;
+  int j0, j_max;   // this launch takes path positions j0 .. j0 + j_max - 1
+  int rows_cap;    // query rows that fit in shared memory (a multiple of 16)
+  int stages;
+  float scale, decay;
+};
+
+struct WeightShared {
+  uint64_t full[kWtMaxStages], empty[kWtMaxStages];
+  uint64_t q_full, q_empty, t_full[2], t_empty[2], half_full[4], mma_done;
+  float half[4][kWtTile];  // the second warps' sums
+  int b, h, t;             // first unit of the share
+  long long units;
+  uint32_t tmem;
+  int abort;
+};
+
+template <int kHD>
+struct WeightWalk {
+  const int *len, *cnt;
+  int b, h, t, tiles;
+  long long left;
+  __device__ __forceinline__ WeightWalk(const WeightShared* sh, const int* len_, const int* cnt_) : len(len_), cnt(cnt_) {
+    b = sh->b;
+    h = sh->h;
+    t = sh->t;
+    left = sh->units;
+    tiles = left > 0 ? (len[b] + kWtTile - 1) / kWtTile : 0;
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  // True when the next unit belongs to another sequence or head.
+  __device__ __forceinline__ bool last_of_item() const { return t + 1 == tiles || left == 1; }
+  __device__ __forceinline__ void next(const WeightArgs& a) {
+    --left;
+    if (++t < tiles || left <= 0) return;
+    t = 0;
+    if (++h == a.heads) {
+      h = 0;
+      do ++b;
+      while (len[b] <= 0);
+      tiles = (len[b] + kWtTile - 1) / kWtTile;
+    }
+  }
+  // Query rows of the item in this launch, and the columns and number of its steps.
+  __device__ __forceinline__ int rows(const WeightArgs& a) const { return min(max(cnt[b] - a.j0, 0), a.j_max) * a.group; }
+};
+__device__ __forceinline__ int weight_steps(int rows) { return max(1, (rows + kWtStep - 1) / kWtStep); }
+// Columns of a step: equal shares, multiples of 16.
+__device__ __forceinline__ int weight_cols(int rows) {
+  const int s = weight_steps(rows);
+  return max(16, ((rows + s - 1) / s + 15) & ~15);
+}
+
+template <int kHD>
+__global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_constant__ WeightArgs a) {
+  constexpr int kSlabs = kHD / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int q_slab = a.rows_cap * 128;  // a multiple of 1 KB: rows_cap is one of 16
+  uint8_t* p = smem + kSlabs * q_slab + a.stages * kWtSlab;
+  WeightShared* sh = reinterpret_cast<WeightShared*>(p);
+  float* neg_lse = reinterpret_cast<float*>(p + ((sizeof(WeightShared) + 15) & ~size_t(15)));  // -lse log2 e, a column each
+  int* len = reinterpret_cast<int*>(neg_lse + a.rows_cap);
+  int* cnt = len + a.n_seqs;
+  const uint32_t s_q = smem_u32(smem), s_ring = s_q + kSlabs * q_slab;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort_flag = &sh->abort;
+  const uint64_t timeout = a.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&sh->full[i], 1);
+      mbar_init(&sh->empty[i], 1);
+    }
+    mbar_init(&sh->q_full, kWtLoaders);
+    mbar_init(&sh->q_empty, 9);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->t_full[i], 1);
+      mbar_init(&sh->t_empty[i], 8);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh->half_full[i], 4);
+    mbar_init(&sh->mma_done, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8 && lane == 0) tma_prefetch_desc(&a.tm_k);
+  if (warp == 9) {
+    tmem_alloc(&sh->tmem, 512);
+    tmem_relinquish();
+  }
+  // Lengths and counts, one warp a sequence: -1 for what may not be touched.
+  for (int b = warp; b < a.n_seqs; b += kWtThreads / 32) {
+    const int m = a.lens[b], c = a.n_path != nullptr ? a.n_path[b] : a.n;
+    bool bad = m < 0 || m > a.capacity || c < 0 || c > a.n || c > m;
+    if (!bad && a.path != nullptr)
+      for (int j = lane; j < c; j += 32) {
+        const int i = a.path[static_cast<long long>(b) * a.n + j];
+        bad |= i < 0 || i >= a.n;
+      }
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      if (bad) record_status(a.dev_status, RF_ERR_INVALID_ARG);
+      len[b] = bad || (a.j0 > 0 && c <= a.j0) ? -1 : m;
+      cnt[b] = bad ? 0 : c;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) {  // this CTA's share
+    auto units_of = [&](int b) -> long long {
+      return b < a.n_seqs ? static_cast<long long>(a.heads) * ((max(len[b], 0) + kWtTile - 1) / kWtTile) : 0;
+    };
+    long long total = 0;
+    for (int b = lane; b < a.n_seqs; b += 32) total += units_of(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const long long shares = min(static_cast<long long>(gridDim.x), total);
+    long long units = 0;
+    int fb = 0, fh = 0, ft = 0;
+    if (blockIdx.x < shares) {
+      const long long first = total * blockIdx.x / shares;
+      units = total * (blockIdx.x + 1) / shares - first;
+      long long base = 0;
+      for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+        const long long own = units_of(b0 + lane);
+        long long x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, first < base + x);
+        if (hit) {
+          const int at = __ffs(hit) - 1;
+          fb = b0 + at;
+          const long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
+          const long long per_head = __shfl_sync(0xffffffffu, own, at) / a.heads;
+          fh = static_cast<int>(r / per_head);
+          ft = static_cast<int>(r - fh * per_head);
+          break;
+        }
+        base += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    if (lane == 0) {
+      sh->b = fb;
+      sh->h = fh;
+      sh->t = ft;
+      sh->units = units;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = sh->tmem;
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a)) {
+#pragma unroll
+        for (int c = 0; c < kSlabs; ++c) {
+          if (!mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, timeout)) goto load_done;
+          mbar_arrive_expect_tx(&sh->full[stage], kWtSlab);
+          tma_load_4d(s_ring + stage * kWtSlab, &a.tm_k, smem_u32(&sh->full[stage]), c * 64, w.h, w.t * kWtTile, w.b);
+          ++issued;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    load_done:
+      int dummy = 0;
+      for (long long i = (issued > a.stages ? issued - a.stages : 0); i < issued; ++i)
+        mbar_wait(&sh->full[i % a.stages], static_cast<uint32_t>((i / a.stages) & 1), &dummy, timeout);
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, q_phase = 0, step = 0;
+      bool fresh = true;  // the next unit starts an item
+      for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a)) {
+        if (fresh) {
+          if (!mbar_wait(&sh->q_full, q_phase, abort_flag, timeout)) goto mma_done;
+          q_phase ^= 1u;
+          tc_fence_after();
+        }
+        const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
+        const uint32_t idesc = make_idesc_bf16(kWtTile, cols, 0, 0);
+        int st[kSlabs];
+#pragma unroll
+        for (int c = 0; c < kSlabs; ++c) {
+          st[c] = stage;
+          if (!mbar_wait(&sh->full[stage], phase, abort_flag, timeout)) goto mma_done;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        for (int i = 0; i < steps; ++i, ++step) {
+          const uint32_t buf = step & 1u;
+          if (!mbar_wait(&sh->t_empty[buf], ((step >> 1) & 1u) ^ 1u, abort_flag, timeout)) goto mma_done;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < kHD / 16; ++k)
+            tc_mma_bf16(tmem + buf * kWtStep, make_sdesc_sw128(s_ring + st[k / 4] * kWtSlab + (k % 4) * 32, 16, 1024),
+                        make_sdesc_sw128(s_q + (k / 4) * q_slab + i * cols * 128 + (k % 4) * 32, 16, 1024), idesc,
+                        k > 0 ? 1u : 0u);
+          tc_commit(&sh->t_full[buf]);
+        }
+#pragma unroll
+        for (int c = 0; c < kSlabs; ++c) tc_commit(&sh->empty[st[c]]);
+        fresh = w.last_of_item();
+        if (fresh) tc_commit(&sh->q_empty);
+      }
+    mma_done:
+      tc_commit(&sh->mma_done);
+      int dummy = 0;
+      mbar_wait(&sh->mma_done, 0, &dummy, timeout);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    const int tid = static_cast<int>(threadIdx.x) - 320;
+    uint32_t q_phase = 0;
+    constexpr int kPieces = kHD / 8;
+    for (WeightWalk<kHD> w(sh, len, cnt); w.more();) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty, q_phase ^ 1u, abort_flag, timeout))) break;
+      q_phase ^= 1u;
+      const int rows = w.rows(a), cols = weight_cols(rows) * weight_steps(rows);
+      const long long q_heads = static_cast<long long>(a.heads) * a.group;
+      for (int r = tid; r < cols; r += kWtLoaders) {
+        float x = -INFINITY;  // a column that adds nothing
+        if (r < rows) {
+          const int j = a.j0 + r / a.group;
+          const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
+          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node) * q_heads + w.h * a.group + r % a.group];
+          if (l != -INFINITY) x = -l * kWtLog2e;
+        }
+        neg_lse[r] = x;
+      }
+#pragma unroll 4
+      for (int x = tid; x < cols * kPieces; x += kWtLoaders) {
+        const int r = x / kPieces, pc = x % kPieces;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int j = a.j0 + r / a.group;
+          const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
+          const long long head = static_cast<long long>(w.h) * a.group + r % a.group;
+          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node) * q_heads + head];
+          // a query that sees nothing is left out whatever its bits are
+          if (l != -INFINITY)
+            v = *reinterpret_cast<const uint4*>(a.q + w.b * a.q_seq + node * a.q_row + head * kHD + pc * 8);
+        }
+        st_shared_v4(s_q + (pc / 8) * q_slab + r * 128 + (((pc & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+      }
+      fence_proxy_async_shared();
+      mbar_arrive(&sh->q_full);
+      // on to the next item
+      while (!w.last_of_item()) w.next(a);
+      w.next(a);
+    }
+  } else {
+    const int part = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float sc = a.scale * kWtLog2e;
+    uint32_t step = 0, q_phase = 0, unit = 0;
+    bool fresh = true;
+    for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a), ++unit) {
+      if (fresh) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_full, q_phase, abort_flag, timeout))) goto sum_done;
+        q_phase ^= 1u;
+      }
+      const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
+      const int m = len[w.b], c = cnt[w.b];
+      const int key = w.t * kWtTile + row;
+      const long long at = (static_cast<long long>(w.b) * a.heads + w.h) * a.capacity + key;
+      float base = 0.0f;
+      if (part == 0 && key < m && a.score_in != nullptr) base = a.score_in[at] * a.decay;
+      // The first query sees rows up to m - c; the j-th up to m - c + j.
+      const bool masked = rows == 0 || (w.t + 1) * kWtTile > m - c + a.j0 + 1;
+      const int half = ((cols / 16 + 1) / 2) * 16;  // columns of the first warps
+      const int c0 = part == 0 ? 0 : half, c1 = part == 0 ? half : cols;
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+      for (int i = 0; i < steps; ++i, ++step) {
+        const uint32_t buf = step & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->t_full[buf], (step >> 1) & 1u, abort_flag, timeout))) goto sum_done;
+        tc_fence_after();
+        for (int x = c0; x < c1; x += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + lanes + buf * kWtStep + x, r);
+          tmem_wait_ld16(r);
+          const float4* nl = reinterpret_cast<const float4*>(neg_lse + i * cols + x);
+          if (!masked) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 l = nl[e];
+              s0 += exp2f_ftz(fmaf(u2f(r[4 * e]), sc, l.x));
+              s1 += exp2f_ftz(fmaf(u2f(r[4 * e + 1]), sc, l.y));
+              s2 += exp2f_ftz(fmaf(u2f(r[4 * e + 2]), sc, l.z));
+              s3 += exp2f_ftz(fmaf(u2f(r[4 * e + 3]), sc, l.w));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int col = i * cols + x + e;
+              const int last = m - c + a.j0 + col / a.group;
+              const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, neg_lse[col]));
+              s0 += col < rows && key <= last ? y : 0.0f;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->t_empty[buf]);
+      }
+      fresh = w.last_of_item();
+      if (fresh && lane == 0) mbar_arrive(&sh->q_empty);  // neg_lse is read no more
+      const float sum = (s0 + s1) + (s2 + s3);
+      // The two warps of a key meet. The second ones reach unit u + 4 only after the first
+      // ones have handed back a step of unit u + 2, hence are done with slot and barrier of
+      // unit u.
+      float* slot = sh->half[unit & 3u];
+      if (part == 1) {
+        slot[row] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->half_full[unit & 3u]);
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->half_full[unit & 3u], (unit >> 2) & 1u, abort_flag, timeout))) goto sum_done;
+        if (key < m) a.score_out[at] = base + (sum + slot[row]);
+      }
+    }
+  sum_done:;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && sh->abort) record_status(a.dev_status, RF_ERR_TIMEOUT);
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kHD>
+static rf_status launch_weights(WeightArgs a, int ctas, size_t smem, cudaStream_t s) {
+  static uint64_t done = 0;
+  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn_weights<kHD>), 227 * 1024, &done);
+  if (st != RF_OK) return st;
+  ProfScope prof(s, RF_STAGE_ATTN_WEIGHTS);
+  k_attn_weights<kHD><<<ctas, kWtThreads, smem, s>>>(a);
+  return cuda_check(cudaGetLastError(), "k_attn_weights launch");
+}
+
+static rf_status check_weights(const rf_attn_desc* d) {
+  rf_status st = check_attn_desc(d);
+  if (st != RF_OK) return st;
+  if (d->n_seqs > kWtMaxSeqs) return fail(RF_ERR_SHAPE, "n_seqs must be <= %d", kWtMaxSeqs);
+  return RF_OK;
+}
+
+}  // namespace rf
+
+using namespace rf;
+
+extern "C" size_t rf_attn_weights_workspace_bytes(const rf_attn_desc* desc) {
+  return check_weights(desc) == RF_OK ? 256 : 0;
+}
+
+extern "C" rf_status rf_attn_weights(const rf_attn_desc* d, const rf_bf16* q, const float* lse, const int32_t* path,
+                                     const int32_t* n_path, const rf_bf16* k_cache, const int32_t* lens, double decay,
+                                     const float* score_in, float* score_out, int32_t* dev_status, void* workspace,
+                                     size_t workspace_bytes, rf_stream_t stream) {
+  clear_error();
+  rf_status st = check_weights(d);
+  if (st != RF_OK) return st;
+  if (!std::isfinite(decay)) return fail(RF_ERR_INVALID_ARG, "decay must be finite");
+  if (d->n_seqs == 0) return RF_OK;
+  if (!q || !lse || !k_cache || !lens || !score_out || (decay != 0.0 && !score_in) || (path == nullptr) != (n_path == nullptr))
+    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL, path and n_path both or neither");
+  if (!aligned16(q) || !aligned16(k_cache)) return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(path) |
+                         reinterpret_cast<uintptr_t>(n_path) | reinterpret_cast<uintptr_t>(lens) |
+                         reinterpret_cast<uintptr_t>(score_in) | reinterpret_cast<uintptr_t>(score_out);
+  if (bits & 3u) return fail(RF_ERR_ALIGN, "arrays must be 4-byte aligned");
+  if (workspace == nullptr || workspace_bytes < 256 || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(RF_ERR_WORKSPACE, "workspace needs 256 bytes, 256-byte aligned (got %zu)", workspace_bytes);
+  int sms = 0;
+  if ((st = current_device(&sms)) != RF_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const uint64_t hd = d->head_dim, H = d->n_kv_heads, B = d->n_seqs, cap = d->capacity;
+  WeightArgs a{};
+  if ((st = make_tmap_bf16_4d(&a.tm_k, k_cache, {hd, H, cap, B},
+                              {hd, (uint64_t)d->cache_row_stride, (uint64_t)d->cache_seq_stride}, {64, 1, kWtTile, 1})) != RF_OK)
+    return st;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.lse = lse;
+  a.path = path;
+  a.n_path = n_path;
+  a.lens = lens;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  a.q_row = d->q_row_stride;
+  a.q_seq = d->q_seq_stride;
+  a.n_seqs = static_cast<int>(B);
+  a.heads = static_cast<int>(H);
+  a.group = static_cast<int>(d->n_q_heads / d->n_kv_heads);
+  a.n = static_cast<int>(d->n_nodes);
+  a.capacity = static_cast<int>(cap);
+  a.scale = static_cast<float>(d->scale);
+  // As many path positions a launch as their query rows fit in shared memory.
+  const int64_t most = kWtQBytes / (2 * static_cast<int64_t>(hd));
+  a.j_max = static_cast<int>(std::min<int64_t>(d->n_nodes, std::max<int64_t>(most / a.group, 1)));
+  // Steps round a launch's rows up by at most 16 columns each.
+  const int rows = a.j_max * a.group;
+  const int steps = std::max(1, (rows + kWtStep - 1) / kWtStep);
+  a.rows_cap = std::max(16, (((rows + steps - 1) / steps + 15) & ~15)) * steps;
+  const size_t fixed = 1024 + static_cast<size_t>(a.rows_cap) * hd * 2 + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
+                       static_cast<size_t>(a.rows_cap) * 4 + static_cast<size_t>(B) * 8;
+  a.stages = static_cast<int>(std::min<size_t>((227 * 1024 - fixed) / kWtSlab, kWtMaxStages));
+  const size_t smem = fixed + static_cast<size_t>(a.stages) * kWtSlab;
+  const int64_t units = static_cast<int64_t>(B * H) * static_cast<int64_t>((cap + kWtTile - 1) / kWtTile);
+  const int ctas = static_cast<int>(std::min<int64_t>(units, sms));
+  for (int64_t j0 = 0; j0 < d->n_nodes; j0 += a.j_max) {
+    a.j0 = static_cast<int>(j0);
+    a.decay = j0 == 0 ? static_cast<float>(decay) : 1.0f;
+    a.score_in = j0 == 0 ? (decay != 0.0 ? score_in : nullptr) : score_out;
+    a.score_out = score_out;
+    st = hd == 128 ? launch_weights<128>(a, ctas, smem, s) : launch_weights<64>(a, ctas, smem, s);
+    if (st != RF_OK) return st;
+  }
+  return RF_OK;
+}

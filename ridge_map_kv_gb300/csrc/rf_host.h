@@ -98,6 +98,9 @@ rf_status spd_inverse(float* H, int n, float* Linv, float* Hinv, float* ctmp, __
 // Checks of an rf_cache_desc that the calls writing to a cache share (evict.cu).
 rf_status check_cache_desc(const rf_cache_desc* d);
 
+// Checks of an rf_attn_desc (attn.cu).
+rf_status check_attn_desc(const rf_attn_desc* d);
+
 // Brackets one kernel launch with profiling events when rf_profile_start is active.
 struct ProfScope {
   cudaStream_t stream;
