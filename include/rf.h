@@ -643,7 +643,7 @@ rf_status rf_tree_attention(const rf_attn_desc* desc, const rf_bf16* q,
 typedef struct rf_verify_desc {
   int64_t n_seqs;
   int64_t n_nodes;    /* 1 .. RF_TREE_MAX_NODES                                        */
-  int64_t vocab;      /* V < 2^31                                                      */
+  int64_t vocab;      /* V <= 2^31 - 65536                                             */
   int64_t ld_target;  /* row strides, >= vocab (any value)                              */
   int64_t ld_draft;
   int64_t ld_noise;

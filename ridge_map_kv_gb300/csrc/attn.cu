@@ -29,6 +29,7 @@
 //                    a factor 2^8 (weights stay below 2^8 of the reference, which fp32
 //                    sums and bf16 weights hold without loss), so rarely after the first
 //                    tiles.
+//   (warps 10, 11)   fill the third warpgroup, which gives registers to the first two
 //   warp 8           TMA: query tiles, then K and V tiles through one ring
 //   warp 9           MMA: S_s = Q K^T, O_s += P_s V (P_s from TMEM). It also clears what
 //                    the second product must not see: V rows beyond a sequence's length
@@ -44,7 +45,12 @@
 namespace rf {
 
 constexpr int kAtTile = 128;      // keys of a tile, rows of a row tile
-constexpr int kAtThreads = 320;
+constexpr int kAtThreads = 384;
+// Registers a thread: 168 at the launch, then 208 for the softmax warps, which hold a row's 128
+// scores and 64 packed weights, and 88 for the others: 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kAtRegsSoftmax = 208, kAtRegsOther = 88;
+static_assert(256 * kAtRegsSoftmax + 128 * kAtRegsOther <= kAtThreads * 168, "more registers than the launch has");
+constexpr int kAtFirst = 96;      // keys of the first part in which a tile's weights are handed over
 constexpr int kAtMaxCtas = 160;   // bounds the workspace
 constexpr int kAtMaxStages = 8;
 constexpr float kAtLog2e = 1.4426950408889634f;
@@ -78,7 +84,7 @@ struct AttnArgs {
 
 struct AttnShared {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_done[2], o_final, o_empty, ml_full, mma_done;
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean, mma_done[2];
   AttnPlan plan;
   long long units;
   float2 ml[2][2][kAtTile];  // [segment parity][stream][row]: maximum and total
@@ -95,6 +101,13 @@ struct AttnCfg {
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kStages) * kTileBytes + sizeof(AttnShared) + 64;
   static constexpr int kRows = (kDual ? 2 : 1) * kAtTile;  // of an item
 };
+
+// The value that lane 0 of a converged warp holds; every lane holds it, but only so does
+// the compiler know, and keep what depends on it in uniform registers.
+template <class T>
+__device__ __forceinline__ T uniform(T x) {
+  return __shfl_sync(0xffffffffu, x, 0);
+}
 
 // Cache and draft tiles of one item.
 struct ItemShape {
@@ -118,21 +131,34 @@ __device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt
   return s;
 }
 
-// A CTA's share, segment by segment; every role walks it alike.
-template <bool kDual>
+// A CTA's share, segment by segment; every role walks it alike, a thread alone or (kWarp) a
+// converged warp.
+template <bool kDual, bool kWarp>
 struct Walk {
   int b, h, mt, t0, t1;
   long long left;
   ItemShape shape;
+  template <class T>
+  static __device__ __forceinline__ T same(T x) {
+    if constexpr (kWarp) return uniform(x);
+    else return x;
+  }
+  __device__ __forceinline__ void look(const AttnArgs& a) {
+    shape = item_shape<kDual>(a, b, mt);
+    shape.len = same(shape.len);
+    shape.cached = same(shape.cached);
+    shape.tiles = same(shape.tiles);
+  }
   __device__ __forceinline__ Walk(const AttnArgs& a, const AttnShared* sh) {
-    b = sh->plan.b;
-    h = sh->plan.h;
-    mt = sh->plan.mt;
-    t0 = sh->plan.t0;
-    left = sh->units;
+    b = same(sh->plan.b);
+    h = same(sh->plan.h);
+    mt = same(sh->plan.mt);
+    t0 = same(sh->plan.t0);
+    left = same(sh->units);
     shape = ItemShape{0, 0, 0};
+    t1 = 0;
     if (left > 0) {
-      shape = item_shape<kDual>(a, b, mt);
+      look(a);
       t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), t0 + left));
     }
   }
@@ -149,7 +175,7 @@ struct Walk {
           ++b;
         }
       }
-      shape = item_shape<kDual>(a, b, mt);
+      look(a);
     } while (shape.tiles == 0);
     t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), left));
   }
@@ -223,49 +249,56 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
   }
 }
 
-// One softmax step of a row: 128 scores at `ts` -> bf16 weights over them.
-// `keep` (when kMasked) holds the row's visible keys.
+// A row's 128 scores, from `ts`, and their maximum; keys that are not seen (kMasked) become
+// -inf. The second half is on its way while the first half's maximum is taken.
 template <bool kMasked>
-__device__ __forceinline__ float row_max(uint32_t ts, const uint32_t (&keep)[4]) {
-  float mx = -INFINITY;
+__device__ __forceinline__ float row_scores(uint32_t ts, const uint32_t (&keep)[4], uint32_t (&r)[4][32]) {
+  float m[4];
+  auto take = [&](int c) {
+    if (kMasked) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32];
-    tmem_ld32(ts + c * 32, r);
-    tmem_wait_ld32(r);
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float s = kMasked ? ((keep[c] >> i) & 1u ? u2f(r[i]) : -INFINITY) : u2f(r[i]);
-      mx = fmaxf(mx, s);
+      for (int i = 0; i < 32; ++i) r[c][i] = (keep[c] >> i) & 1u ? r[c][i] : 0xff800000u;
     }
-  }
-  return mx;
+    m[c] = fmaxf(u2f(r[c][0]), u2f(r[c][1]));
+#pragma unroll
+    for (int i = 2; i < 32; i += 2) m[c] = fmaxf(fmaxf(m[c], u2f(r[c][i])), u2f(r[c][i + 1]));
+  };
+  tmem_ld32(ts, r[0]);
+  tmem_ld32(ts + 32, r[1]);
+  tmem_wait_ld32(r[0]);
+  tmem_wait_ld32(r[1]);
+  tmem_ld32(ts + 64, r[2]);
+  tmem_ld32(ts + 96, r[3]);
+  take(0);
+  take(1);
+  tmem_wait_ld32(r[2]);
+  tmem_wait_ld32(r[3]);
+  take(2);
+  take(3);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
-template <bool kMasked>
-__device__ __forceinline__ float row_weights(uint32_t ts, const uint32_t (&keep)[4], float sc, float off) {
-  float total = 0.0f;
+// The weights 2^(s sc + off) of 32-key groups c0 .. c1 - 1, written over the scores in bf16;
+// adds to their sums.
+__device__ __forceinline__ void row_weights(uint32_t ts, uint32_t (&r)[4][32], int c0, int c1, float sc, float off,
+                                            float2& t0, float2& t1) {
+  const float2 sc2 = make_float2(sc, sc), off2 = make_float2(off, off);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t r[32], w[16];
-    tmem_ld32(ts + c * 32, r);
-    tmem_wait_ld32(r);
-    float l0 = 0.0f, l1 = 0.0f;
+  for (int c = c0; c < c1; ++c) {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float p0 = exp2f_ftz(fmaf(u2f(r[i]), sc, off)), p1 = exp2f_ftz(fmaf(u2f(r[i + 1]), sc, off));
-      if (kMasked) {
-        p0 = (keep[c] >> i) & 1u ? p0 : 0.0f;
-        p1 = (keep[c] >> (i + 1)) & 1u ? p1 : 0.0f;
-      }
-      l0 += p0;
-      l1 += p1;
-      w[i / 2] = pack_bf16x2(p0, p1);
+    for (int i = 0; i < 32; i += 4) {
+      float2 x = fma_x2(make_float2(u2f(r[c][i]), u2f(r[c][i + 1])), sc2, off2);
+      float2 y = fma_x2(make_float2(u2f(r[c][i + 2]), u2f(r[c][i + 3])), sc2, off2);
+      x = make_float2(exp2f_ftz(x.x), exp2f_ftz(x.y));
+      y = make_float2(exp2f_ftz(y.x), exp2f_ftz(y.y));
+      t0 = add_x2(t0, x);
+      t1 = add_x2(t1, y);
+      w[i / 2] = pack_bf16x2(x.x, x.y);
+      w[i / 2 + 1] = pack_bf16x2(y.x, y.y);
     }
-    total += l0 + l1;
     tmem_st16(ts + c * 16, w);
   }
   tmem_wait_st();
-  return total;
 }
 
 // Bits of the keys of tile `t` that query node `node` sees.
@@ -299,30 +332,35 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   using Cfg = AttnCfg<kHD, kDual>;
   constexpr int kChunks = kHD / 64;                 // 64-channel slabs of a tile, 16 KB each
   constexpr int kSlab = kAtTile * 128;
+  constexpr int kMmaWarps = kDual ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   AttnShared* sh = reinterpret_cast<AttnShared*>(smem + Cfg::kQBytes + Cfg::kStages * Cfg::kTileBytes);
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + Cfg::kQBytes;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
   const uint64_t timeout = a.timeout_ns;
 
+  pdl_launch_dependents();  // k_attn_combine's CTAs may take their places as this kernel's leave
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg::kStages; ++i) {
       mbar_init(&sh->full[i], 1);
-      mbar_init(&sh->empty[i], 1);
+      mbar_init(&sh->empty[i], kMmaWarps);
     }
     mbar_init(&sh->q_full, 1);
-    mbar_init(&sh->q_empty, 1);
+    mbar_init(&sh->q_empty, kMmaWarps);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->s_full[s], 1);
-      mbar_init(&sh->p_full[s], 4);
-      mbar_init(&sh->o_done[s], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&sh->p_full[s][i], 4);
     }
-    mbar_init(&sh->o_final, 2);
+    mbar_init(&sh->o_final, kMmaWarps + 1);
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->ml_full, 8);
-    mbar_init(&sh->mma_done, 1);
+    mbar_init(&sh->v_clean, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->turn[i], 1);
+      mbar_init(&sh->mma_done[i], 1);
+    }
     sh->abort = 0;
     fence_mbar_init();
   }
@@ -341,15 +379,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = uniform(sh->tmem);
 
   if (warp == 8) {
+    regs_dec<kAtRegsOther>();
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, q_phase = 0;
       long long issued = 0;
       bool ok = true, q_inflight = false;
-      auto load = [&](const Walk<kDual>& w, int t, bool v) {
+      auto load = [&](const Walk<kDual, false>& w, int t, bool v) {
         if (!mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, timeout)) return false;
         mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
         const bool draft = t >= w.shape.cached;
@@ -365,7 +404,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         return true;
       };
-      for (Walk<kDual> w(a, sh); w.more() && ok; w.next(a)) {
+      for (Walk<kDual, false> w(a, sh); w.more() && ok; w.next(a)) {
         if (!mbar_wait(&sh->q_empty, q_phase ^ 1u, abort_flag, timeout)) break;
         mbar_arrive_expect_tx(&sh->q_full, (kDual ? 2 : 1) * kChunks * 64 * 2 * a.group * a.npt);
         q_inflight = true;
@@ -390,11 +429,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       for (long long i = (issued > Cfg::kStages ? issued - Cfg::kStages : 0); i < issued; ++i)
         mbar_wait(&sh->full[i % Cfg::kStages], static_cast<uint32_t>((i / Cfg::kStages) & 1), &dummy, timeout);
     }
-  } else if (warp == 9) {
+  } else if (warp == 9 || (kDual && warp == 10)) {
+    regs_dec<kAtRegsOther>();
     constexpr uint32_t idesc_s = make_idesc_bf16(kAtTile, kAtTile, 0, 0);
     constexpr uint32_t idesc_o = make_idesc_bf16(kAtTile, kHD, 0, 1);
+    const uint32_t issue = lane == 0;
     int stage = 0;
-    uint32_t phase = 0, q_phase = 0, o_phase = 0, p_phase[2] = {0, 0};
+    uint32_t phase = 0, q_phase = 0, o_phase = 0, c_phase = 0, turn_phase = warp == 9 ? 1 : 0, p_phase[2] = {0, 0};
     int seg = 0;
     auto advance = [&] {
       if (++stage == Cfg::kStages) {
@@ -407,156 +448,188 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       if (ok) tc_fence_after();
       return ok;
     };
-    auto qk = [&](int s, int q) {  // S_s = Q_q K^T of the current stage
-      if (lane == 0) {
-        const uint32_t k0 = s_ring + stage * Cfg::kTileBytes, q0 = s_q + q * Cfg::kTileBytes;
+    // Products are issued back to back behind all of their waits: the pipe takes one as the
+    // last ends, so whatever stands between two of them is lost time.
+    auto qk = [&](int s, int q, int k_stage) {  // S_s = Q_q K^T
+      const uint32_t k0 = s_ring + k_stage * Cfg::kTileBytes, q0 = s_q + q * Cfg::kTileBytes;
 #pragma unroll
-        for (int k = 0; k < kHD / 16; ++k) {
-          const uint32_t off = (k / 4) * kSlab + (k % 4) * 32;
-          tc_mma_bf16(tmem + s * kAtTile, make_sdesc_sw128(q0 + off, 16, 1024), make_sdesc_sw128(k0 + off, 16, 1024),
-                      idesc_s, k > 0 ? 1u : 0u);
-        }
-        tc_commit(&sh->s_full[s]);
+      for (int k = 0; k < kHD / 16; ++k) {
+        const uint32_t off = (k / 4) * kSlab + (k % 4) * 32;
+        tc_mma_bf16_warp(tmem + s * kAtTile, make_sdesc_sw128(q0 + off, 16, 1024), make_sdesc_sw128(k0 + off, 16, 1024),
+                         idesc_s, k > 0 ? 1u : 0u, issue);
       }
     };
-    auto pv = [&](int s, bool fresh) {  // O_s (+)= P_s V of the current stage
-      if (lane == 0) {
-        const uint32_t v0 = s_ring + stage * Cfg::kTileBytes;
+    // O_s (+)= P_s V, the first part of whose weights is there; the second comes while the
+    // first's products run.
+    auto pv = [&](int s, int v_stage, bool fresh) {
+      const uint32_t v0 = s_ring + v_stage * Cfg::kTileBytes;
 #pragma unroll
-        for (int k = 0; k < kAtTile / 16; ++k)
-          tc_mma_bf16_ts(tmem + 256 + s * 128, tmem + s * kAtTile + k * 8, make_sdesc_sw128(v0 + k * 2048, kSlab, 1024),
-                         idesc_o, fresh && k == 0 ? 0u : 1u);
-        tc_commit(&sh->o_done[s]);
+      for (int part = 0; part < 2; ++part) {
+        if (part == 1 && !wait(&sh->p_full[s][1], p_phase[s])) return false;
+#pragma unroll
+        for (int k = part * kAtFirst / 16; k < (part == 0 ? kAtFirst : kAtTile) / 16; ++k)
+          tc_mma_bf16_ts_warp(tmem + 256 + s * 128, tmem + s * kAtTile + k * 8,
+                              make_sdesc_sw128(v0 + k * 2048, kSlab, 1024), idesc_o, fresh && k == 0 ? 0u : 1u, issue);
       }
+      p_phase[s] ^= 1u;
+      return true;
     };
-    auto release = [&] {
-      if (lane == 0) tc_commit(&sh->empty[stage]);
+    // Two row tiles: the two issuing warps take turns.
+    auto my_turn = [&] {
+      const bool ok = wait(&sh->turn[warp - 9], turn_phase);
+      turn_phase ^= 1u;
+      return ok;
+    };
+    auto your_turn = [&] {
+      if (lane == 0) mbar_arrive(&sh->turn[10 - warp]);
+    };
+    // The next tile of the ring: its stage, or -1 after an abort.
+    auto take = [&] {
+      const int st = stage;
+      if (!wait(&sh->full[st], phase)) return -1;
       advance();
+      return st;
     };
-    // Clears V elements of the current stage that no product may see (whole warp).
-    auto clean = [&](const Walk<kDual>& w, int t) {
-      const uint32_t v0 = s_ring + stage * Cfg::kTileBytes;
+    auto to_clean = [&](const Walk<kDual, true>& w, int t) { return t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len; };
+    // Clears V elements of stage `st` that no product may see (whole warp).
+    auto clean = [&](const Walk<kDual, true>& w, int t, int st) {
+      const uint32_t v0 = s_ring + st * Cfg::kTileBytes;
       if (t < w.shape.cached) {
         const int rows = w.shape.len - t * kAtTile;
-        if (rows >= kAtTile) return;
         for (int i = rows * 8 + lane; i < kAtTile * 8; i += 32)
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) st_shared_v4(v0 + c * kSlab + i * 16, 0, 0, 0, 0);
       } else {
+        // 0 times a number is 0, 0 times an infinity or NaN is NaN: one multiply-add finds
+        // out about two elements. What it finds is rare and looked for one by one.
         const int rows = min(kAtTile, a.n - (t - w.shape.cached) * kAtTile);
-        bool bad = false;
-        for (int i = lane; i < rows * 8; i += 32)
+        const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+        __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            const uint32_t at = v0 + c * kSlab + i * 16;
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll 8
+          for (int i = lane; i < rows * 8; i += 32) {
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + Cfg::kQBytes + st * Cfg::kTileBytes + c * kSlab + i * 16);
+            const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[e] = __hfma2(x[e], zero, acc[e]);
+          }
+        const __nv_bfloat162 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+        if (__any_sync(0xffffffffu, __hisnan(sum.x) || __hisnan(sum.y))) {
+          for (int i = lane; i < rows * 8 * kChunks; i += 32) {
+            const uint32_t at = v0 + (i / (rows * 8)) * kSlab + (i % (rows * 8)) * 16;
             uint4 v = ld_shared_v4(at);
             uint32_t* x = reinterpret_cast<uint32_t*>(&v);
-            bool hit = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if ((x[e] & 0x7f80u) == 0x7f80u) {
-                x[e] &= 0xffff0000u;
-                hit = true;
-              }
-              if ((x[e] & 0x7f800000u) == 0x7f800000u) {
-                x[e] &= 0xffffu;
-                hit = true;
-              }
+              if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
+              if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
             }
-            if (hit) {
-              st_shared_v4(at, x[0], x[1], x[2], x[3]);
-              bad = true;
-            }
+            st_shared_v4(at, x[0], x[1], x[2], x[3]);
           }
-        if (bad) sh->bad[seg & 1] = 1;
+          sh->bad[seg & 1] = 1;
+        }
       }
       fence_proxy_async_shared();
       __syncwarp();
     };
-    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, true> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
-      if (lane == 0) sh->bad[seg & 1] = 0;
+      if (warp == 9 && lane == 0) sh->bad[seg & 1] = 0;
       __syncwarp();
       if (!wait(&sh->q_full, q_phase)) goto mma_done;
       q_phase ^= 1u;
       if (kDual) {
-        if (!wait(&sh->full[stage], phase)) goto mma_done;
-        qk(0, 0);
-        qk(1, 1);
-        if (n_tiles == 1 && lane == 0) tc_commit(&sh->q_empty);
-        release();
+        // Warp 9 issues stream 0's products, warp 10 stream 1's, a tile's second product and the
+        // next tile's first in one go, in turn: so one stream's products run while the other's
+        // weights are formed, and a warp's own waits and commits fall into the other's turn.
+        const int s = warp - 9;
+        int k = take();
+        if (k < 0 || !my_turn()) goto mma_done;
+        qk(s, s, k);
+        tc_commit_warp(&sh->s_full[s], issue);  // before the other's products, not behind them
+        your_turn();
+        tc_commit_warp(&sh->empty[k], issue);
+        if (n_tiles == 1) tc_commit_warp(&sh->q_empty, issue);
         if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
         for (int i = 0; i < n_tiles; ++i) {
-          const int v_stage = stage;
-          if (!wait(&sh->full[stage], phase)) goto mma_done;
-          clean(w, w.t0 + i);
-          advance();
-          const int k_stage = stage;
           const bool more = i + 1 < n_tiles;
-          for (int s = 0; s < 2; ++s) {
-            if (!wait(&sh->p_full[s], p_phase[s])) goto mma_done;
-            p_phase[s] ^= 1u;
-            stage = v_stage;
-            pv(s, i == 0);
-            if (s == 1 && lane == 0) tc_commit(&sh->empty[v_stage]);
-            stage = k_stage;
-            if (more) {
-              if (s == 0 && !wait(&sh->full[stage], phase)) goto mma_done;
-              qk(s, s);
+          const int v = take();
+          if (v < 0) goto mma_done;
+          if (to_clean(w, w.t0 + i)) {
+            if (s == 0) {
+              clean(w, w.t0 + i, v);
+              if (lane == 0) mbar_arrive(&sh->v_clean);
+            } else {
+              if (!wait(&sh->v_clean, c_phase)) goto mma_done;
+              c_phase ^= 1u;
             }
           }
+          k = more ? take() : 0;
+          if (k < 0) goto mma_done;
+          if (!wait(&sh->p_full[s][0], p_phase[s])) goto mma_done;
+          if (!my_turn() || !pv(s, v, i == 0)) goto mma_done;
           if (more) {
-            if (i + 2 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
-            release();
+            qk(s, s, k);
+            tc_commit_warp(&sh->s_full[s], issue);
           }
+          your_turn();
+          tc_commit_warp(&sh->empty[v], issue);
+          if (more) tc_commit_warp(&sh->empty[k], issue);
+          if (i + 2 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
         }
       } else {
         for (int i = 0; i < 2 && i < n_tiles; ++i) {
-          if (!wait(&sh->full[stage], phase)) goto mma_done;
-          qk(i, 0);
-          if (i + 1 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
-          release();
+          const int k = take();
+          if (k < 0) goto mma_done;
+          qk(i, 0, k);
+          tc_commit_warp(&sh->s_full[i], issue);
+          tc_commit_warp(&sh->empty[k], issue);
+          if (i + 1 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
         }
         if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
         for (int i = 0; i < n_tiles; ++i) {
           const int s = i & 1;
-          if (!wait(&sh->full[stage], phase)) goto mma_done;
-          clean(w, w.t0 + i);
-          if (!wait(&sh->p_full[s], p_phase[s])) goto mma_done;
-          p_phase[s] ^= 1u;
-          pv(s, i < 2);
-          release();
-          if (i + 2 < n_tiles) {
-            if (!wait(&sh->full[stage], phase)) goto mma_done;
-            qk(s, 0);
-            if (i + 3 == n_tiles && lane == 0) tc_commit(&sh->q_empty);
-            release();
+          const bool more = i + 2 < n_tiles;
+          const int v = take();
+          if (v < 0) goto mma_done;
+          if (to_clean(w, w.t0 + i)) clean(w, w.t0 + i, v);
+          const int k = more ? take() : 0;
+          if (k < 0) goto mma_done;
+          if (!wait(&sh->p_full[s][0], p_phase[s]) || !pv(s, v, i < 2)) goto mma_done;
+          tc_commit_warp(&sh->empty[v], issue);
+          if (more) {
+            qk(s, 0, k);
+            tc_commit_warp(&sh->s_full[s], issue);
           }
+          if (more) tc_commit_warp(&sh->empty[k], issue);
+          if (i + 3 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
         }
       }
-      if (lane == 0) {
-        tc_commit(&sh->o_final);
-        mbar_arrive(&sh->o_final);  // and what this warp found in V
-      }
+      tc_commit_warp(&sh->o_final, issue);
+      if (warp == 9 && lane == 0) mbar_arrive(&sh->o_final);  // and what it found in V
       o_phase ^= 1u;
       ++seg;
     }
   mma_done:
+    tc_commit_warp(&sh->mma_done[warp - 9], issue);
     if (lane == 0) {
-      tc_commit(&sh->mma_done);
       int dummy = 0;
-      mbar_wait(&sh->mma_done, 0, &dummy, timeout);
+      mbar_wait(&sh->mma_done[warp - 9], 0, &dummy, timeout);
     }
     __syncwarp();
+  } else if (warp >= 10) {
+    regs_dec<kAtRegsOther>();
   } else {
+    regs_inc<kAtRegsSoftmax>();
     const int s = warp >> 2;             // stream
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kAtTile;
     const float sc = a.scale * kAtLog2e;
-    uint32_t s_phase = 0, o_phase = 0, f_phase = 0;
+    uint32_t s_phase = 0, f_phase = 0;
     int seg = 0;
-    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, true> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
       const int node0 = (w.mt * (kDual ? 2 : 1) + (kDual ? s : 0)) * a.npt;
       const int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile
@@ -572,23 +645,20 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         if (!idle) {
           const int t = w.t0 + i;
           const bool masked = t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len;
-          uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+          uint32_t keep[4] = {}, r[4][32];
           float mx;
           if (masked) {
             visible(a, w.shape, w.b, node, t, keep);
-            mx = row_max<true>(ts, keep);
+            mx = row_scores<true>(ts, keep, r);
           } else {
-            mx = row_max<false>(ts, keep);
+            mx = row_scores<false>(ts, keep, r);
           }
           mx = fmaxf(mx, m);
           const bool grown = m == -INFINITY ? mx > -INFINITY : (mx - m) * sc > kAtRescale;
           if (__any_sync(0xffffffffu, grown)) {
             // With nothing seen so far l and the accumulator's row are 0 (or not written yet).
             const float f = grown ? (m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc)) : 1.0f;
-            if (!first) {
-              ok = mbar_wait(&sh->o_done[s], o_phase ^ 1u, abort_flag, timeout);  // the previous tile's product
-              if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
-              tc_fence_after();
+            if (!first) {  // the previous product is done: this tile's scores were issued behind it
 #pragma unroll 1
               for (int c = 0; c < kHD; c += 16) {
                 uint32_t o[16];
@@ -603,13 +673,21 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
             if (grown) m = mx;
           }
           const float off = m == -INFINITY ? 0.0f : -m * sc;
-          l += masked ? row_weights<true>(ts, keep, sc, off) : row_weights<false>(ts, keep, sc, off);
+          float2 l0 = make_float2(l, 0.0f), l1 = make_float2(0.0f, 0.0f);
+          row_weights(ts, r, 0, kAtFirst / 32, sc, off, l0, l1);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[s][0]);
+          row_weights(ts, r, kAtFirst / 32, 4, sc, off, l0, l1);
+          l = (l0.x + l0.y) + (l1.x + l1.y);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->p_full[s][1]);
+        } else if (lane == 0) {
+          mbar_arrive(&sh->p_full[s][0]);
+          mbar_arrive(&sh->p_full[s][1]);
         }
         first = false;
-        o_phase ^= 1u;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[s]);
       }
       // Epilogue.
       if (!kDual) {
@@ -717,7 +795,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
 }
 
 // Joins the rows of items that were cut. Block x: the cut before share x + 1; the first
-// cut inside an item answers for it. A warp takes a row at a time.
+// cut inside an item answers for it. A warp takes a row: its lanes read the parts' maxima
+// and totals side by side, then the row's sums part after part, eight loads at a time.
+// Launched as a dependent of k_attn: its CTAs wait in place for that one's end.
 struct CombineArgs {
   const AttnPlan* plan;
   const float* part_o;
@@ -728,22 +808,34 @@ struct CombineArgs {
   int n, heads, group, npt, tiles, ctas;  // tiles: row tiles of an item
   float scale;
 };
-constexpr int kCombineWarps = 4;
+constexpr int kCombineWarps = 16;
+constexpr int kCombineBatch = 8;  // parts whose sums are in flight together
 
 template <int kHD>
-__global__ void __launch_bounds__(32 * kCombineWarps) k_attn_combine(const __grid_constant__ CombineArgs a) {
-  const int c = blockIdx.x + 1;
-  const AttnPlan p = a.plan[c];
-  if (p.item < 0 || p.t0 == 0) return;
-  const AttnPlan before = a.plan[c - 1];
-  if (before.item == p.item && before.t0 > 0) return;
-  int parts = 2;  // from share c - 1, from share c, ...
-  while (c + parts - 1 < a.ctas) {
-    const AttnPlan q = a.plan[c + parts - 1];
-    if (q.item != p.item || q.t0 == 0) break;
-    ++parts;
+__global__ void __launch_bounds__(32 * kCombineWarps, 2) k_attn_combine(const __grid_constant__ CombineArgs a) {
+  pdl_wait();
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  // lane i: the share c - 1 + i
+  const int mine = min(c - 1 + lane, a.ctas - 1);
+  const AttnPlan q = a.plan[mine];
+  const long long item = __shfl_sync(0xffffffffu, q.item, 1);
+  const long long item_before = __shfl_sync(0xffffffffu, q.item, 0);
+  const int t_cut = __shfl_sync(0xffffffffu, q.t0, 1), t_before = __shfl_sync(0xffffffffu, q.t0, 0);
+  if (item < 0 || t_cut == 0) return;
+  if (item_before == item && t_before > 0) return;
+  const int pb = __shfl_sync(0xffffffffu, q.b, 1), ph = __shfl_sync(0xffffffffu, q.h, 1), pmt = __shfl_sync(0xffffffffu, q.mt, 1);
+  // parts of the item: from share c - 1, and from every share from c on that starts inside it
+  int parts = 1;
+  for (int i0 = 0;; i0 += 32) {
+    const int i = c + i0 + lane;
+    const bool in = i < a.ctas && a.plan[i].item == item && a.plan[i].t0 > 0;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    if (m != 0xffffffffu) {
+      parts += __ffs(~m) - 1;
+      break;
+    }
+    parts += 32;
   }
-  const int lane = threadIdx.x & 31;
   const int item_rows = a.tiles * kAtTile;
   const float sc = a.scale * kAtLog2e;
   constexpr int kPer = kHD / 32;
@@ -751,36 +843,51 @@ __global__ void __launch_bounds__(32 * kCombineWarps) k_attn_combine(const __gri
   for (int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); r < item_rows; r += gridDim.y * kCombineWarps) {
     const int in_tile = r % kAtTile;
     if (in_tile >= a.npt * a.group) continue;
-    const int node = (p.mt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
+    const int node = (pmt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
     if (node >= a.n) continue;
-    const int head = p.h * a.group + in_tile % a.group;
+    const int head = ph * a.group + in_tile % a.group;
+    float v[kCombineBatch][kPer];
+    auto load = [&](int i0) {
+#pragma unroll
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const long long at = slot_of(min(i0 + j, parts - 1)) * item_rows + r;
+        if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[j]) = *reinterpret_cast<const float4*>(a.part_o + at * kHD + lane * 4);
+        else *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(a.part_o + at * kHD + lane * 2);
+      }
+    };
+    load(0);  // on its way before the statistics are looked at
     float m = -INFINITY;
     for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[slot_of(i) * item_rows + r].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.0f, x[kPer] = {};
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const long long at = slot_of(i) * item_rows + r;
-      const float2 ml = a.part_ml[at];
-      const float f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2f_ftz((ml.x - m) * sc);
-      l += ml.y * f;
-      float v[kPer];
-      if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(a.part_o + at * kHD + lane * 4);
-      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(a.part_o + at * kHD + lane * 2);
+    for (int i0 = 0; i0 < parts; i0 += kCombineBatch) {
+      if (i0 > 0) load(i0);
+      float f = 0.0f, lp = 0.0f;
+      if (lane < kCombineBatch && i0 + lane < parts) {
+        const float2 ml = a.part_ml[slot_of(i0 + lane) * item_rows + r];
+        f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2f_ftz((ml.x - m) * sc);
+        lp = ml.y * f;
+      }
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) x[e] = fmaf(v[e], f, x[e]);
+      for (int j = 0; j < kCombineBatch; ++j) {
+        const float g = __shfl_sync(0xffffffffu, f, j), gl = __shfl_sync(0xffffffffu, lp, j);
+        if (i0 + j < parts) {
+          l += gl;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) x[e] = fmaf(v[j][e], g, x[e]);
+        }
+      }
     }
-    // A part whose rows see nothing yet but a non-finite value cannot be: what is seen has weight.
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    __nv_bfloat16* dst = a.out + p.b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + lane * kPer;
+    __nv_bfloat16* dst = a.out + pb * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + lane * kPer;
     if constexpr (kPer == 4) {
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
     } else {
       *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(x[0] * inv, x[1] * inv);
     }
     if (lane == 0 && a.lse != nullptr)
-      a.lse[(static_cast<long long>(p.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
+      a.lse[(static_cast<long long>(pb) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
           l == 0.0f ? -INFINITY : m * a.scale + logf(l);
   }
 }
@@ -944,9 +1051,8 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   c.ctas = ctas;
   c.scale = a.scale;
   const int rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, lay.tiles * kAtTile));
-  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + kCombineWarps - 1) / kCombineWarps));
+  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(std::min((rows + kCombineWarps - 1) / kCombineWarps, 4)));
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
-  if (hd == 128) k_attn_combine<128><<<grid, 32 * kCombineWarps, 0, s>>>(c);
-  else k_attn_combine<64><<<grid, 32 * kCombineWarps, 0, s>>>(c);
-  return cuda_check(cudaGetLastError(), "k_attn_combine launch");
+  return cuda_check(launch_dependent(hd == 128 ? k_attn_combine<128> : k_attn_combine<64>, grid, dim3(32 * kCombineWarps), 0, s, c),
+                    "k_attn_combine launch");
 }

@@ -20,7 +20,8 @@
 //                    half of the columns, the others the second
 //   warp 8           TMA: key tiles, in 64-channel slabs
 //   warp 9           MMA
-//   warps 10-13      the queries of the next (sequence, head): gathered along the path
+//   warps 10-13      the queries of the next (sequence, head), gathered along the path into
+//                    the other of two buffers (or, where two do not fit, once the one is free)
 #include <algorithm>
 #include <cmath>
 
@@ -53,14 +54,15 @@ struct WeightArgs {
   long long q_row, q_seq;
   int n_seqs, heads, group, n, capacity;
   int j0, j_max;   // this launch takes path positions j0 .. j0 + j_max - 1
-  int rows_cap;    // query rows that fit in shared memory (a multiple of 16)
+  int rows_cap;    // query rows of one buffer (a multiple of 16)
+  int bufs;        // query buffers: 2 where that leaves the ring its stages, else 1
   int stages;
   float scale, decay;
 };
 
 struct WeightShared {
   uint64_t full[kWtMaxStages], empty[kWtMaxStages];
-  uint64_t q_full, q_empty, t_full[2], t_empty[2], half_full[4], mma_done;
+  uint64_t q_full[2], q_empty[2], t_full[2], t_empty[2], half_full[4], mma_done;
   float half[4][kWtTile];  // the second warps' sums
   int b, h, t;             // first unit of the share
   long long units;
@@ -110,12 +112,12 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int q_slab = a.rows_cap * 128;  // a multiple of 1 KB: rows_cap is one of 16
-  uint8_t* p = smem + kSlabs * q_slab + a.stages * kWtSlab;
+  uint8_t* p = smem + a.bufs * kSlabs * q_slab + a.stages * kWtSlab;
   WeightShared* sh = reinterpret_cast<WeightShared*>(p);
   float* neg_lse = reinterpret_cast<float*>(p + ((sizeof(WeightShared) + 15) & ~size_t(15)));  // -lse log2 e, a column each
-  int* len = reinterpret_cast<int*>(neg_lse + a.rows_cap);
+  int* len = reinterpret_cast<int*>(neg_lse + a.bufs * a.rows_cap);
   int* cnt = len + a.n_seqs;
-  const uint32_t s_q = smem_u32(smem), s_ring = s_q + kSlabs * q_slab;
+  const uint32_t s_q = smem_u32(smem), s_ring = s_q + a.bufs * kSlabs * q_slab;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
   const uint64_t timeout = a.timeout_ns;
@@ -125,8 +127,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
       mbar_init(&sh->full[i], 1);
       mbar_init(&sh->empty[i], 1);
     }
-    mbar_init(&sh->q_full, kWtLoaders);
-    mbar_init(&sh->q_empty, 9);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->q_full[i], kWtLoaders);
+      mbar_init(&sh->q_empty[i], 9);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->t_full[i], 1);
       mbar_init(&sh->t_empty[i], 8);
@@ -232,12 +236,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
   } else if (warp == 9) {
     if (lane == 0) {
       int stage = 0;
-      uint32_t phase = 0, q_phase = 0, step = 0;
+      uint32_t phase = 0, step = 0, item = 0;
+      int qb = 0;         // query buffer of the item
       bool fresh = true;  // the next unit starts an item
       for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a)) {
         if (fresh) {
-          if (!mbar_wait(&sh->q_full, q_phase, abort_flag, timeout)) goto mma_done;
-          q_phase ^= 1u;
+          qb = a.bufs == 2 ? item & 1u : 0;
+          const uint32_t par = (a.bufs == 2 ? item >> 1 : item) & 1u;
+          if (!mbar_wait(&sh->q_full[qb], par, abort_flag, timeout)) goto mma_done;
+          ++item;
           tc_fence_after();
         }
         const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
@@ -259,14 +266,14 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
 #pragma unroll
           for (int k = 0; k < kHD / 16; ++k)
             tc_mma_bf16(tmem + buf * kWtStep, make_sdesc_sw128(s_ring + st[k / 4] * kWtSlab + (k % 4) * 32, 16, 1024),
-                        make_sdesc_sw128(s_q + (k / 4) * q_slab + i * cols * 128 + (k % 4) * 32, 16, 1024), idesc,
+                        make_sdesc_sw128(s_q + (qb * kSlabs + k / 4) * q_slab + i * cols * 128 + (k % 4) * 32, 16, 1024), idesc,
                         k > 0 ? 1u : 0u);
           tc_commit(&sh->t_full[buf]);
         }
 #pragma unroll
         for (int c = 0; c < kSlabs; ++c) tc_commit(&sh->empty[st[c]]);
         fresh = w.last_of_item();
-        if (fresh) tc_commit(&sh->q_empty);
+        if (fresh) tc_commit(&sh->q_empty[qb]);
       }
     mma_done:
       tc_commit(&sh->mma_done);
@@ -275,41 +282,50 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     }
     __syncwarp();
   } else if (warp >= 10) {
-    const int tid = static_cast<int>(threadIdx.x) - 320;
-    uint32_t q_phase = 0;
-    constexpr int kPieces = kHD / 8;
-    for (WeightWalk<kHD> w(sh, len, cnt); w.more();) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty, q_phase ^ 1u, abort_flag, timeout))) break;
-      q_phase ^= 1u;
+    // Warp w of the four takes rows 32 w .. 32 w + 31 of every 128: first their statistics and
+    // addresses (a lane a row), then their pieces, in asynchronous copies.
+    const int w0 = (warp - 10) * 32;
+    uint32_t item = 0;
+    constexpr int kPieces = kHD / 8, kRowsAtOnce = 32 / kPieces;
+    for (WeightWalk<kHD> w(sh, len, cnt); w.more(); ++item) {
+      const int qb = a.bufs == 2 ? item & 1u : 0;
+      const uint32_t par = ((a.bufs == 2 ? item >> 1 : item) & 1u) ^ 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty[qb], par, abort_flag, timeout))) break;
       const int rows = w.rows(a), cols = weight_cols(rows) * weight_steps(rows);
       const long long q_heads = static_cast<long long>(a.heads) * a.group;
-      for (int r = tid; r < cols; r += kWtLoaders) {
-        float x = -INFINITY;  // a column that adds nothing
-        if (r < rows) {
-          const int j = a.j0 + r / a.group;
-          const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
-          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node) * q_heads + w.h * a.group + r % a.group];
-          if (l != -INFINITY) x = -l * kWtLog2e;
-        }
-        neg_lse[r] = x;
-      }
-#pragma unroll 4
-      for (int x = tid; x < cols * kPieces; x += kWtLoaders) {
-        const int r = x / kPieces, pc = x % kPieces;
-        uint4 v = make_uint4(0, 0, 0, 0);
+      const uint32_t q0 = s_q + qb * kSlabs * q_slab;
+      for (int r0 = w0; r0 < cols; r0 += kWtLoaders) {
+        const int r = r0 + lane;
+        float x = -INFINITY;  // a column that adds nothing; its row is 0, whatever the query's bits are
+        const __nv_bfloat16* src = nullptr;
         if (r < rows) {
           const int j = a.j0 + r / a.group;
           const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
           const long long head = static_cast<long long>(w.h) * a.group + r % a.group;
           const float l = a.lse[(static_cast<long long>(w.b) * a.n + node) * q_heads + head];
-          // a query that sees nothing is left out whatever its bits are
-          if (l != -INFINITY)
-            v = *reinterpret_cast<const uint4*>(a.q + w.b * a.q_seq + node * a.q_row + head * kHD + pc * 8);
+          if (l != -INFINITY) {
+            x = -l * kWtLog2e;
+            src = a.q + w.b * a.q_seq + node * a.q_row + head * kHD;
+          }
         }
-        st_shared_v4(s_q + (pc / 8) * q_slab + r * 128 + (((pc & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+        if (r < cols) neg_lse[qb * a.rows_cap + r] = x;
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(src);
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kRowsAtOnce) {
+          const int ri = i + lane / kPieces, pc = lane % kPieces;
+          const unsigned long long from = __shfl_sync(0xffffffffu, mine, ri);
+          const int rr = r0 + ri;
+          if (rr < cols) {
+            const uint32_t dst = q0 + (pc / 8) * q_slab + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+            if (from != 0ull)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + pc * 16ull) : "memory");
+            else st_shared_v4(dst, 0, 0, 0, 0);
+          }
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async_shared();
-      mbar_arrive(&sh->q_full);
+      mbar_arrive(&sh->q_full[qb]);
       // on to the next item
       while (!w.last_of_item()) w.next(a);
       w.next(a);
@@ -319,12 +335,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sc = a.scale * kWtLog2e;
-    uint32_t step = 0, q_phase = 0, unit = 0;
+    uint32_t step = 0, unit = 0, item = 0;
+    int qb = 0;
     bool fresh = true;
     for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a), ++unit) {
       if (fresh) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_full, q_phase, abort_flag, timeout))) goto sum_done;
-        q_phase ^= 1u;
+        qb = a.bufs == 2 ? item & 1u : 0;
+        const uint32_t par = (a.bufs == 2 ? item >> 1 : item) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_full[qb], par, abort_flag, timeout))) goto sum_done;
+        ++item;
       }
       const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
       const int m = len[w.b], c = cnt[w.b];
@@ -336,6 +355,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
       const bool masked = rows == 0 || (w.t + 1) * kWtTile > m - c + a.j0 + 1;
       const int half = ((cols / 16 + 1) / 2) * 16;  // columns of the first warps
       const int c0 = part == 0 ? 0 : half, c1 = part == 0 ? half : cols;
+      const float* item_lse = neg_lse + qb * a.rows_cap;
       float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
       for (int i = 0; i < steps; ++i, ++step) {
         const uint32_t buf = step & 1u;
@@ -345,7 +365,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
           uint32_t r[16];
           tmem_ld16(tmem + lanes + buf * kWtStep + x, r);
           tmem_wait_ld16(r);
-          const float4* nl = reinterpret_cast<const float4*>(neg_lse + i * cols + x);
+          const float4* nl = reinterpret_cast<const float4*>(item_lse + i * cols + x);
           if (!masked) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -360,7 +380,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
             for (int e = 0; e < 16; ++e) {
               const int col = i * cols + x + e;
               const int last = m - c + a.j0 + col / a.group;
-              const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, neg_lse[col]));
+              const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, item_lse[col]));
               s0 += col < rows && key <= last ? y : 0.0f;
             }
           }
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
         if (lane == 0) mbar_arrive(&sh->t_empty[buf]);
       }
       fresh = w.last_of_item();
-      if (fresh && lane == 0) mbar_arrive(&sh->q_empty);  // neg_lse is read no more
+      if (fresh && lane == 0) mbar_arrive(&sh->q_empty[qb]);  // neg_lse is read no more
       const float sum = (s0 + s1) + (s2 + s3);
       // The two warps of a key meet. The second ones reach unit u + 4 only after the first
       // ones have handed back a step of unit u + 2, hence are done with slot and barrier of
@@ -470,10 +490,16 @@ extern "C" rf_status rf_attn_weights(const rf_attn_desc* d, const rf_bf16* q, co
   const int rows = a.j_max * a.group;
   const int steps = std::max(1, (rows + kWtStep - 1) / kWtStep);
   a.rows_cap = std::max(16, (((rows + steps - 1) / steps + 15) & ~15)) * steps;
-  const size_t fixed = 1024 + static_cast<size_t>(a.rows_cap) * hd * 2 + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
-                       static_cast<size_t>(a.rows_cap) * 4 + static_cast<size_t>(B) * 8;
-  a.stages = static_cast<int>(std::min<size_t>((227 * 1024 - fixed) / kWtSlab, kWtMaxStages));
-  const size_t smem = fixed + static_cast<size_t>(a.stages) * kWtSlab;
+  // A second query buffer lets the next item's queries come in early; the ring keeps at
+  // least five slabs (80 KB: more than the bytes in flight that hide memory's latency).
+  auto fixed = [&](int bufs) {
+    return 1024 + static_cast<size_t>(bufs) * a.rows_cap * (hd * 2 + 4) + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
+           static_cast<size_t>(B) * 8;
+  };
+  constexpr size_t kMost = 227 * 1024;
+  a.bufs = fixed(2) + 5 * kWtSlab <= kMost ? 2 : 1;
+  a.stages = static_cast<int>(std::min<size_t>((kMost - fixed(a.bufs)) / kWtSlab, kWtMaxStages));
+  const size_t smem = fixed(a.bufs) + static_cast<size_t>(a.stages) * kWtSlab;
   const int64_t units = static_cast<int64_t>(B * H) * static_cast<int64_t>((cap + kWtTile - 1) / kWtTile);
   const int ctas = static_cast<int>(std::min<int64_t>(units, sms));
   for (int64_t j0 = 0; j0 < d->n_nodes; j0 += a.j_max) {

@@ -6,11 +6,13 @@
 // move. Sources lie beyond `keep` and destinations below, so the moves of a unit are
 // independent of one another and run in any order, in place.
 //
-//   k_evict_select  one CTA a unit: rank keys in shared memory, the keep-th largest by a
-//                   radix selection of 11 + 11 + 10 bits, then three ordered passes in
-//                   which a warp owns a contiguous run of rows and a lane one row of
-//                   each 32, so ranks come from ballots: ties, counts, lists. It also
-//                   writes the scores and positions of the rows that stay in place.
+//   k_evict_select  one CTA a unit, a warp a contiguous run of rows and a lane one row of
+//                   each 32. Rank keys stay in registers (up to 32 a thread; beyond
+//                   32,768 rows they are formed anew from memory in every pass). The
+//                   keep-th largest comes from a radix selection of 11 + 11 + 10 bits;
+//                   ranks among equals and the places of holes and movers come from
+//                   ballots. It also writes the scores and positions of the rows that
+//                   stay in place.
 //   k_evict_move    the listed rows of K and V, their scores and positions.
 //
 // Bound: reading scores and positions and writing the kept ones (16 bytes a row) and the
@@ -22,10 +24,7 @@
 
 namespace rf {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int64_t kSelSmemKeys = 48 * 1024;  // keys that fit in shared memory beside the histogram
 constexpr int kMoveRows = 64;                // moves of one CTA of k_evict_move
 
 struct EvictArgs {
@@ -54,34 +53,38 @@ __device__ __forceinline__ unsigned rank_key(float score, bool sure) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+template <int kThreads>
 struct SelShared {
   int hist[kSelBins];
-  int warp_a[kSelWarps];
-  int warp_b[kSelWarps];
+  int warp_a[kThreads / 32];
+  int warp_b[kThreads / 32];
   unsigned prefix;
   int left;
 };
 
-// Exclusive scan over the CTA's warps of one value per warp (lane 0's), in shared memory.
+// Exclusive scan over the CTA's warps of one value per warp, in shared memory.
+template <int kThreads>
 __device__ __forceinline__ void scan_warps(int* v) {
   __syncthreads();
   if (threadIdx.x < 32) {
-    const int own = v[threadIdx.x];
+    const int own = threadIdx.x < kThreads / 32 ? v[threadIdx.x] : 0;
     int x = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (static_cast<int>(threadIdx.x) >= o) x += y;
     }
-    v[threadIdx.x] = x - own;
+    if (threadIdx.x < kThreads / 32) v[threadIdx.x] = x - own;
   }
   __syncthreads();
 }
 
-template <bool kSmem>
-__global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_constant__ EvictArgs a) {
-  extern __shared__ unsigned keys[];
-  __shared__ SelShared sh;
+// kItems keys a thread in registers, or 0: formed from memory in every pass.
+template <int kThreads, int kItems>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ SelShared<kThreads> sh;
+  pdl_launch_dependents();
   const int unit = blockIdx.x;
   const int b = (unit / a.heads) % a.n_seqs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -98,7 +101,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
   }
   const int keep = a.keep;
   if (len <= keep) {
-    for (int t = tid; t < len; t += kSelThreads) {
+#pragma unroll 4
+    for (int t = tid; t < len; t += kThreads) {
       a.score_out[base + t] = score[t];
       a.pos_out[base + t] = pos[t];
     }
@@ -106,14 +110,32 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
     return;
   }
   const long long newest = static_cast<long long>(a.next_pos[b]) - a.recent;
+  // Warp w owns rows [r0, r1), lane i of it rows r0 + i, r0 + 32 + i, ...
+  const int run = ((len + kWarps - 1) / kWarps + 31) & ~31;
+  const int r0 = min(warp * run, len), r1 = min(r0 + run, len);
   auto key_of = [&](int t) {
     const int p = pos[t];
     return rank_key(score[t], p < a.sink || p >= newest);
   };
-  auto key_at = [&](int t) { return kSmem ? keys[t] : key_of(t); };
-  if constexpr (kSmem) {
-    for (int t = tid; t < len; t += kSelThreads) keys[t] = key_of(t);
+  unsigned keys[kItems > 0 ? kItems : 1];
+  if constexpr (kItems > 0) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int t = r0 + i * 32 + lane;
+      keys[i] = t < r1 ? key_of(t) : 0u;
+    }
   }
+  // Calls f(row, key, whether the row is one of the warp's) for all of a thread's rows, in
+  // order; every lane of a warp makes the same calls.
+  auto each = [&](auto f) {
+    if constexpr (kItems > 0) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if (r0 + i * 32 < r1) f(r0 + i * 32 + lane, keys[i], r0 + i * 32 + lane < r1);
+    } else {
+      for (int t = r0 + lane; t - lane < r1; t += 32) f(t, t < r1 ? key_of(t) : 0u, t < r1);
+    }
+  };
   // The keep-th largest key, digit by digit: among the keys that share the digits found
   // so far, the bin that holds the rank still wanted.
   unsigned prefix = 0, mask = 0;
@@ -122,92 +144,96 @@ __global__ void __launch_bounds__(kSelThreads, 1) k_evict_select(const __grid_co
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const unsigned digit = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+    for (int i = tid; i < kSelBins; i += kThreads) sh.hist[i] = 0;
     __syncthreads();
-    for (int t = tid; t < len; t += kSelThreads) {
-      const unsigned k = key_at(t);
-      if ((k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & digit], 1);
+    each([&](int, unsigned k, bool in) {
+      if (in && (k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & digit], 1);
+    });
+    __syncthreads();
+    // Thread i holds kBins bins from the top down: an inclusive scan.
+    constexpr int kBins = kSelBins / kThreads;
+    int h[kBins], x = 0;
+#pragma unroll
+    for (int j = 0; j < kBins; ++j) {
+      h[j] = sh.hist[kSelBins - 1 - (kBins * tid + j)];
+      x += h[j];
     }
-    __syncthreads();
-    // Thread i holds the two bins 2047 - 2i and 2046 - 2i: an inclusive scan from the top.
-    const int hi = sh.hist[kSelBins - 1 - 2 * tid], lo = sh.hist[kSelBins - 2 - 2 * tid];
-    int x = hi + lo;
+    const int own = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) sh.warp_a[warp] = x;
-    scan_warps(sh.warp_a);
-    const int before = sh.warp_a[warp] + x - hi - lo;  // keys in higher bins
-    if (before < left && before + hi + lo >= left) {   // one thread
-      const bool top = before + hi >= left;
-      sh.prefix = static_cast<unsigned>(kSelBins - 1 - 2 * tid - (top ? 0 : 1)) << shift;
-      sh.left = left - before - (top ? 0 : hi);
+    scan_warps<kThreads>(sh.warp_a);
+    int before = sh.warp_a[warp] + x - own;             // keys in higher bins
+    if (before < left && before + own >= left) {        // one thread
+#pragma unroll
+      for (int j = 0; j < kBins; ++j) {
+        if (before < left && before + h[j] >= left) {
+          sh.prefix = static_cast<unsigned>(kSelBins - 1 - (kBins * tid + j)) << shift;
+          sh.left = left - before;
+        }
+        before += h[j];
+      }
     }
     __syncthreads();
     prefix |= sh.prefix;
     mask |= digit << shift;
     left = sh.left;
-    __syncthreads();
   }
   const unsigned bar = prefix;  // rows above stay, and the first `left` of those equal to it
-  // Ordered passes: warp w owns rows [r0, r1).
-  const int run = ((len + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int r0 = min(warp * run, len), r1 = min(r0 + run, len);
   const unsigned below = (1u << lane) - 1u;
   int n_eq = 0;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const int t = t0 + lane;
-    n_eq += __popc(__ballot_sync(0xffffffffu, t < r1 && key_at(t) == bar));
-  }
-  if (lane == 0) sh.warp_a[warp] = n_eq;
-  scan_warps(sh.warp_a);
-  const int eq0 = sh.warp_a[warp];
+  each([&](int, unsigned k, bool in) { n_eq += __popc(__ballot_sync(0xffffffffu, in && k == bar)); });
   __syncthreads();
-  auto stays = [&](int t, int& eq) {  // warp-collective; eq: equal rows before t0
-    const unsigned k = t < r1 ? key_at(t) : 0u;
-    const bool same = t < r1 && k == bar;
+  if (lane == 0) sh.warp_a[warp] = n_eq;
+  scan_warps<kThreads>(sh.warp_a);
+  const int eq0 = sh.warp_a[warp];
+  int eq = eq0;
+  auto stays = [&](unsigned k, bool in) {  // warp-collective; eq: equal rows before these 32
+    const bool same = in && k == bar;
     const unsigned m = __ballot_sync(0xffffffffu, same);
-    const bool stay = t < r1 && (k > bar || (same && eq + __popc(m & below) < left));
+    const bool stay = in && (k > bar || (same && eq + __popc(m & below) < left));
     eq += __popc(m);
     return stay;
   };
-  int holes = 0, movers = 0, eq = eq0;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const int t = t0 + lane;
-    const bool stay = stays(t, eq);
-    holes += __popc(__ballot_sync(0xffffffffu, t < r1 && t < keep && !stay));
+  int holes = 0, movers = 0;
+  each([&](int t, unsigned k, bool in) {
+    const bool stay = stays(k, in);
+    holes += __popc(__ballot_sync(0xffffffffu, in && t < keep && !stay));
     movers += __popc(__ballot_sync(0xffffffffu, t >= keep && stay));
-  }
+  });
+  __syncthreads();
   if (lane == 0) {
     sh.warp_a[warp] = holes;
     sh.warp_b[warp] = movers;
   }
-  scan_warps(sh.warp_a);
-  scan_warps(sh.warp_b);
+  scan_warps<kThreads>(sh.warp_a);
+  scan_warps<kThreads>(sh.warp_b);
   int hole = sh.warp_a[warp], mover = sh.warp_b[warp];
   int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves;
   int32_t* src = dst + a.max_moves;
+  const bool copy = a.score_out != a.score_in || a.pos_out != a.pos_in;
   eq = eq0;
-  for (int t0 = r0; t0 < r1; t0 += 32) {
-    const int t = t0 + lane;
-    const bool stay = stays(t, eq);
-    const bool is_hole = t < r1 && t < keep && !stay, is_mover = t >= keep && stay;
+  each([&](int t, unsigned k, bool in) {
+    const bool stay = stays(k, in);
+    const bool is_hole = in && t < keep && !stay, is_mover = t >= keep && stay;
     const unsigned mh = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_mover);
     if (is_hole) dst[hole + __popc(mh & below)] = t;
     if (is_mover) src[mover + __popc(mm & below)] = t;
-    if (stay && t < keep) {
+    hole += __popc(mh);
+    mover += __popc(mm);
+    if (copy && stay && t < keep) {
       a.score_out[base + t] = score[t];
       a.pos_out[base + t] = pos[t];
     }
-    hole += __popc(mh);
-    mover += __popc(mm);
-  }
-  if (warp == kSelWarps - 1 && lane == 0) a.n_moves[unit] = mover;  // as many holes as movers
+  });
+  if (warp == kWarps - 1 && lane == 0) a.n_moves[unit] = mover;  // as many holes as movers
 }
 
 __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs a) {
+  pdl_wait();
   const int unit = blockIdx.y;
   const int n = a.n_moves[unit];
   const int i0 = blockIdx.x * kMoveRows;
@@ -346,18 +372,15 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
   const unsigned units = static_cast<unsigned>(d->n_layers * d->n_seqs * d->n_kv_heads);
   {
     ProfScope prof(s, RF_STAGE_EVICT_SELECT);
-    if (d->capacity <= kSelSmemKeys) {
-      static uint64_t done = 0;
-      const void* fn = reinterpret_cast<const void*>(&k_evict_select<true>);
-      if ((st = set_smem_attr(fn, kSelSmemKeys * 4, &done)) != RF_OK) return st;
-      k_evict_select<true><<<units, kSelThreads, static_cast<size_t>(d->capacity) * 4, s>>>(a);
-    } else {
-      k_evict_select<false><<<units, kSelThreads, 0, s>>>(a);
-    }
+    // Threads and keys a thread by the cache's capacity: small CTAs leave room for several on
+    // an SM, and a CTA of 1,024 threads has 64 registers a thread for 32 keys.
+    if (d->capacity <= 2048) k_evict_select<256, 8><<<units, 256, 0, s>>>(a);
+    else if (d->capacity <= 8192) k_evict_select<512, 16><<<units, 512, 0, s>>>(a);
+    else if (d->capacity <= 32768) k_evict_select<1024, 32><<<units, 1024, 0, s>>>(a);
+    else k_evict_select<1024, 0><<<units, 1024, 0, s>>>(a);
   }
   if ((st = cuda_check(cudaGetLastError(), "k_evict_select launch")) != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_EVICT_MOVE);
   const unsigned chunks = static_cast<unsigned>(std::max<int64_t>((lay.max_moves + kMoveRows - 1) / kMoveRows, 1));
-  k_evict_move<<<dim3(chunks, units), 256, 0, s>>>(a);
-  return cuda_check(cudaGetLastError(), "k_evict_move launch");
+  return cuda_check(launch_dependent(k_evict_move, dim3(chunks, units), dim3(256), 0, s, a), "k_evict_move launch");
 }

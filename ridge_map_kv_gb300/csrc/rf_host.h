@@ -101,6 +101,25 @@ rf_status check_cache_desc(const rf_cache_desc* d);
 // Checks of an rf_attn_desc (attn.cu).
 rf_status check_attn_desc(const rf_attn_desc* d);
 
+// Launches `kernel` so that its CTAs may start while the stream's previous kernel is still
+// running, once that one's CTAs have all exited or called pdl_launch_dependents(); the
+// kernel itself calls pdl_wait() (rf_device.cuh) before it touches what the previous one
+// writes, which returns when that one has finished and its writes are visible.
+template <class... A>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Brackets one kernel launch with profiling events when rf_profile_start is active.
 struct ProfScope {
   cudaStream_t stream;

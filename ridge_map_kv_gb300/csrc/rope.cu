@@ -6,11 +6,12 @@
 // the angle p f_i. Each row is read once and written once and a pair costs six
 // operations, so memory is the bound at any row count that fills the GPU.
 //
-// A thread takes 8 pairs (16 channels, two 16-byte accesses of bf16) of one row, or 16
-// channels that do not turn, in `hpt` heads one after another: the 8 angles are formed
-// once and serve all of them. Lanes cover a head's channels, so a warp's accesses are
-// whole sectors. Where rot_dim or head_dim is no multiple of 16 a thread takes one
-// pair at a time instead.
+// A thread takes one or two 16-byte pieces of a head, at the same channels of `hpt` heads:
+// in the half layout a piece of the first half and its partner of the second, in the
+// interleaved one a piece of whole pairs. Its angles are formed once and serve all of its
+// heads, four of which are loaded before any is stored. Neighbouring lanes take
+// neighbouring pieces, so a warp's accesses are whole sectors. Where rot_dim or head_dim
+// does not divide into such pieces a thread takes one pair at a time instead.
 #include <algorithm>
 #include <cmath>
 
@@ -45,23 +46,15 @@ __device__ __forceinline__ void turn_cs(unsigned long long q, unsigned long long
   else sincospif(static_cast<float>(turns) * 4.6566128730773926e-10f, &s, &c);                         // 2 / 2^32
 }
 
-template <class T, int N>
-struct Chunk {
-  T v[N];
-};
-
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void from_f(float& d, float x) { d = x; }
 __device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
 
-// NP pairs of consecutive indices: 8, moved 16 bytes at a time, or 1.
 template <class T, int N>
 __device__ __forceinline__ void load_vec(const T* p, T (&v)[N]) {
-  if constexpr (N * sizeof(T) % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(N * sizeof(T) / 16); ++i)
-      reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(p)[i];
+  if constexpr (N * sizeof(T) == 16) {
+    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = p[i];
@@ -69,77 +62,82 @@ __device__ __forceinline__ void load_vec(const T* p, T (&v)[N]) {
 }
 template <class T, int N>
 __device__ __forceinline__ void store_vec(T* p, const T (&v)[N]) {
-  if constexpr (N * sizeof(T) % 16 == 0) {
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(N * sizeof(T) / 16); ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(v)[i];
+  if constexpr (N * sizeof(T) == 16) {
+    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = v[i];
   }
 }
 
-template <class T, int NP, bool kHalf>
+// kWide: 16-byte pieces; else one pair (or two channels that do not turn) a thread.
+template <class T, bool kWide, bool kHalf>
+struct RopeShape {
+  static constexpr int kVec = kWide ? 16 / static_cast<int>(sizeof(T)) : kHalf ? 1 : 2;  // channels of a piece
+  static constexpr int kPieces = kHalf ? 2 : 1;
+  static constexpr int kChannels = kVec * kPieces;                                       // of a thread and head
+  static constexpr int kPairs = kChannels / 2;
+};
+constexpr int kRopeHeads = 4;  // heads whose loads are in flight together
+
+template <class T, bool kWide, bool kHalf>
 __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
+  using S = RopeShape<T, kWide, kHalf>;
   const unsigned idx = blockIdx.x * 256u + threadIdx.x;
   if (idx >= static_cast<unsigned>(a.n_rows) * static_cast<unsigned>(a.items)) return;
   const int row = static_cast<int>(idx / static_cast<unsigned>(a.items));
   const int item = static_cast<int>(idx - static_cast<unsigned>(row) * static_cast<unsigned>(a.items));
   const int h0 = static_cast<int>(blockIdx.y) * a.hpt, h1 = min(h0 + a.hpt, a.n_heads);
-  const int half = a.rot >> 1;
-  const int pair0 = item * NP;
-  const bool turns = pair0 < half;
-  // the chunk's first and second channels: apart by half the turned part, or (interleaved,
-  // and where nothing turns) 2 NP in a row
-  const int c1 = turns && kHalf ? pair0 : 2 * pair0;
-  const int c2 = turns && kHalf ? pair0 + half : 2 * pair0 + NP;
+  const int pair0 = item * S::kPairs;
+  const bool turns = 2 * pair0 < a.rot;
+  if (!turns && a.in == a.out) return;
+  // First channels of the thread's pieces. Channels that do not turn follow one another.
+  const int c1 = kHalf && turns ? pair0 : item * S::kChannels;
+  const int c2 = kHalf && turns ? pair0 + (a.rot >> 1) : c1 + S::kVec;
   const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
   T* out = static_cast<T*>(a.out) + row * a.ld_out;
-  if (!turns) {
-    if (a.in == a.out) return;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      alignas(16) T u[NP], w[NP];
-      load_vec(in + h * a.head_dim + c1, u);
-      load_vec(in + h * a.head_dim + c2, w);
-      store_vec(out + h * a.head_dim + c1, u);
-      store_vec(out + h * a.head_dim + c2, w);
+  float c[S::kPairs], s[S::kPairs];
+  if (turns) {
+    const long long p = a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset;
+#pragma unroll
+    for (int i = 0; i < S::kPairs; ++i) {
+      turn_cs<T>(static_cast<unsigned long long>(p), tab.g[pair0 + i], c[i], s[i]);
+      c[i] *= a.amp;
+      s[i] *= a.amp * a.sign;
     }
-    return;
-  }
-  const long long p = a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset;
-  float c[NP], s[NP];
+  } else {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    turn_cs<T>(static_cast<unsigned long long>(p), tab.g[pair0 + i], c[i], s[i]);
-    c[i] *= a.amp;
-    s[i] *= a.amp * a.sign;
-  }
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    alignas(16) T u[NP], w[NP];
-    load_vec(in + h * a.head_dim + c1, u);
-    load_vec(in + h * a.head_dim + c2, w);
-    if constexpr (kHalf || NP == 1) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float x1 = to_f(u[i]), x2 = to_f(w[i]);
-        from_f(u[i], x1 * c[i] - x2 * s[i]);
-        from_f(w[i], x2 * c[i] + x1 * s[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NP / 2; ++i) {
-        const float x1 = to_f(u[2 * i]), x2 = to_f(u[2 * i + 1]);
-        from_f(u[2 * i], x1 * c[i] - x2 * s[i]);
-        from_f(u[2 * i + 1], x2 * c[i] + x1 * s[i]);
-        const float y1 = to_f(w[2 * i]), y2 = to_f(w[2 * i + 1]);
-        from_f(w[2 * i], y1 * c[NP / 2 + i] - y2 * s[NP / 2 + i]);
-        from_f(w[2 * i + 1], y2 * c[NP / 2 + i] + y1 * s[NP / 2 + i]);
-      }
+    for (int i = 0; i < S::kPairs; ++i) {
+      c[i] = 1.0f;
+      s[i] = 0.0f;
     }
-    store_vec(out + h * a.head_dim + c1, u);
-    store_vec(out + h * a.head_dim + c2, w);
+  }
+  for (int h = h0; h < h1; h += kRopeHeads) {
+    alignas(16) T u[kRopeHeads][S::kVec], w[kRopeHeads][S::kVec];
+#pragma unroll
+    for (int j = 0; j < kRopeHeads; ++j) {
+      if (h + j >= h1) break;
+      const int at = (h + j) * a.head_dim;
+      load_vec(in + at + c1, u[j]);
+      if constexpr (kHalf) load_vec(in + at + c2, w[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kRopeHeads; ++j) {
+      if (h + j >= h1) break;
+      if (turns) {
+#pragma unroll
+        for (int i = 0; i < S::kPairs; ++i) {
+          T& d1 = kHalf ? u[j][i] : u[j][(2 * i) % S::kVec];
+          T& d2 = kHalf ? w[j][i] : u[j][(2 * i + 1) % S::kVec];
+          const float x1 = to_f(d1), x2 = to_f(d2);
+          from_f(d1, x1 * c[i] - x2 * s[i]);
+          from_f(d2, x2 * c[i] + x1 * s[i]);
+        }
+      }
+      const int at = (h + j) * a.head_dim;
+      store_vec(out + at + c1, u[j]);
+      if constexpr (kHalf) store_vec(out + at + c2, w[j]);
+    }
   }
 }
 
@@ -214,10 +212,29 @@ static rf_status check_rope(const rf_rope_desc* d) {
   return RF_OK;
 }
 
-template <class T, int NP>
-static void launch_rope(const RopeArgs& a, const RopeTable& t, dim3 grid, bool half, cudaStream_t s) {
-  if (half) k_rope<T, NP, true><<<grid, 256, 0, s>>>(a, t);
-  else k_rope<T, NP, false><<<grid, 256, 0, s>>>(a, t);
+template <class T, bool kWide, bool kHalf>
+static void launch_rope(RopeArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
+  a.items = a.head_dim / RopeShape<T, kWide, kHalf>::kChannels;
+  // Heads per thread: as many (multiples of the four that are loaded together) as still
+  // leave two waves of threads; all of them one by one in the smallest calls.
+  const long long threads1 = static_cast<long long>(a.n_rows) * a.items;
+  a.hpt = 1;
+  while (a.hpt < 16 && threads1 * a.n_heads / (2 * a.hpt) >= 4096LL * sms) a.hpt *= 2;
+  const dim3 grid(static_cast<unsigned>((threads1 + 255) / 256), static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
+  k_rope<T, kWide, kHalf><<<grid, 256, 0, s>>>(a, t);
+}
+template <class T>
+static void launch_rope(RopeArgs& a, const RopeTable& t, bool half, int sms, cudaStream_t s) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  const int unit = half ? 2 * kVec : kVec;  // channels of a thread and head
+  const bool wide = a.rot % unit == 0 && a.head_dim % unit == 0;
+  if (half) {
+    if (wide) launch_rope<T, true, true>(a, t, sms, s);
+    else launch_rope<T, false, true>(a, t, sms, s);
+  } else {
+    if (wide) launch_rope<T, true, false>(a, t, sms, s);
+    else launch_rope<T, false, false>(a, t, sms, s);
+  }
 }
 
 // Masks and positions of drafted trees, one CTA a sequence. A thread per node climbs its
@@ -272,7 +289,6 @@ extern "C" rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out
   if ((st = current_device(&sms)) != RF_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const RopeTable tab = rope_table(desc);
-  const bool wide = desc->rot_dim % 16 == 0 && desc->head_dim % 16 == 0;
   RopeArgs a{};
   a.in = in;
   a.out = out;
@@ -284,23 +300,12 @@ extern "C" rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out
   a.n_heads = static_cast<int>(desc->n_heads);
   a.head_dim = static_cast<int>(desc->head_dim);
   a.rot = static_cast<int>(desc->rot_dim);
-  a.items = a.head_dim / (wide ? 16 : 2);
   a.amp = desc->amplitude == 0.0 ? 1.0f : static_cast<float>(desc->amplitude);
   a.sign = desc->transpose ? -1.0f : 1.0f;
-  // Heads per thread: as many (up to 8) as still leave a few waves of threads.
-  const long long threads1 = static_cast<long long>(a.n_rows) * a.items;
-  a.hpt = 1;
-  while (a.hpt < 8 && threads1 * a.n_heads / (2 * a.hpt) >= 2048LL * sms) a.hpt *= 2;
-  const dim3 grid(static_cast<unsigned>((threads1 + 255) / 256), static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
   const bool half = desc->layout == RF_ROPE_HALF;
   ProfScope prof(s, RF_STAGE_ROPE);
-  if (desc->dtype == RF_BF16) {
-    if (wide) launch_rope<__nv_bfloat16, 8>(a, tab, grid, half, s);
-    else launch_rope<__nv_bfloat16, 1>(a, tab, grid, half, s);
-  } else {
-    if (wide) launch_rope<float, 8>(a, tab, grid, half, s);
-    else launch_rope<float, 1>(a, tab, grid, half, s);
-  }
+  if (desc->dtype == RF_BF16) launch_rope<__nv_bfloat16>(a, tab, half, sms, s);
+  else launch_rope<float>(a, tab, half, sms, s);
   return cuda_check(cudaGetLastError(), "k_rope launch");
 }
 

@@ -25,8 +25,10 @@
 namespace rf {
 namespace cg = cooperative_groups;
 
-constexpr int kVerifyThreads = 512;
-constexpr int kVerifyCtas = 8;  // CTAs of a cluster (the portable limit)
+constexpr int kVerifyThreads = 1024;
+constexpr int kVerifyCtas = 8;      // CTAs of a cluster (the portable limit)
+constexpr int kVerifyBatch = 8;     // values of each row that a thread has in flight
+constexpr int kVerifyShare = 2048;  // least tokens of a CTA
 
 struct VerifyArgs {
   const float* target;
@@ -69,6 +71,27 @@ __device__ __forceinline__ float residual(const VerifyShared& sh, float p, float
   return r;
 }
 
+// f(t, p(t), q(t), e(t)) for the tokens v0 <= t < v1 of this thread; q and e may be NULL.
+template <class F>
+__device__ __forceinline__ void scan_row(int v0, int v1, const float* __restrict__ p, const float* __restrict__ q,
+                                         const float* __restrict__ e, F f) {
+  for (int t0 = v0 + static_cast<int>(threadIdx.x); t0 < v1; t0 += kVerifyThreads * kVerifyBatch) {
+    float pv[kVerifyBatch], qv[kVerifyBatch], ev[kVerifyBatch];
+#pragma unroll
+    for (int i = 0; i < kVerifyBatch; ++i) {
+      const int t = t0 + i * kVerifyThreads;
+      pv[i] = t < v1 ? __ldg(p + t) : 0.0f;
+      qv[i] = q != nullptr && t < v1 ? __ldg(q + t) : 0.0f;
+      ev[i] = e != nullptr && t < v1 ? __ldg(e + t) : 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kVerifyBatch; ++i) {
+      const int t = t0 + i * kVerifyThreads;
+      if (t < v1) f(t, pv[i], qv[i], ev[i]);
+    }
+  }
+}
+
 template <bool kDraft>
 __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant__ VerifyArgs a) {
   __shared__ VerifyShared sh;
@@ -106,10 +129,13 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
     sh.p[i] = a.target[row * a.ld_target + sh.token[i]];
     sh.q[i] = kDraft ? a.draft[row * a.ld_draft + sh.token[i]] : 1.0f;
   }
-  __syncthreads();
-
   const int share = ((a.vocab + ctas - 1) / ctas + 3) & ~3;
   const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
+  // the noise is read in any case, and at the end
+  for (int t = v0 + tid * 32; t < v1; t += kVerifyThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.noise + b * a.ld_noise + t));
+  __syncthreads();
+
   int cur = 0, k = 0, n_acc = 1, turn = 0;
   if (tid == 0) {
     sh.path[0] = 0;
@@ -150,14 +176,14 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
       const float* p = a.target + (b * n + cur) * a.ld_target;
       const float* q = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
       float sum = 0.0f;
-      for (int t = v0 + tid; t < v1; t += kVerifyThreads) sum += residual<kDraft>(sh, p[t], kDraft ? q[t] : 0.0f, t, k);
+      scan_row(v0, v1, p, q, nullptr, [&](int t, float pt, float qt, float) { sum += residual<kDraft>(sh, pt, qt, t, k); });
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) sh.warp_sum[warp] = sum;
       __syncthreads();
-      if (tid == 0) {
-        float s = 0.0f;
-        for (int w = 0; w < kVerifyThreads / 32; ++w) s += sh.warp_sum[w];
-        sh.part_sum[turn & 1] = s;
+      if (warp == 0) {
+        float s = lane < kVerifyThreads / 32 ? sh.warp_sum[lane] : 0.0f;
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) sh.part_sum[turn & 1] = s;
       }
       cl.sync();
       float z = 0.0f;
@@ -181,20 +207,19 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
   int token = 0;
   while (true) {
     unsigned long long best = 0;
-    for (int t = v0 + tid; t < v1; t += kVerifyThreads) {
-      const float r = residual<kDraft>(sh, p[t], kDraft ? q[t] : 0.0f, t, k);
-      const float score = r > 0.0f ? __fdiv_rn(r, e[t]) : 0.0f;
-      const unsigned long long key =
-          (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(t));
-      best = max(best, key);
-    }
+    scan_row(v0, v1, p, q, e, [&](int t, float pt, float qt, float et) {
+      const float r = residual<kDraft>(sh, pt, qt, t, k);
+      const float score = r > 0.0f ? __fdiv_rn(r, et) : 0.0f;
+      best = max(best, (static_cast<unsigned long long>(__float_as_uint(score)) << 32) |
+                           (0xffffffffu - static_cast<unsigned>(t)));
+    });
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) sh.warp_best[warp] = best;
     __syncthreads();
-    if (tid == 0) {
-      unsigned long long m = 0;
-      for (int w = 0; w < kVerifyThreads / 32; ++w) m = max(m, sh.warp_best[w]);
-      sh.part_best[turn & 1] = m;
+    if (warp == 0) {
+      unsigned long long m = lane < kVerifyThreads / 32 ? sh.warp_best[lane] : 0ull;
+      for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane == 0) sh.part_best[turn & 1] = m;
     }
     cl.sync();
     unsigned long long m = 0;
@@ -232,21 +257,36 @@ struct CommitArgs {
   int32_t* dev_status;
   long long row_stride, seq_stride, layer_stride, draft_row, draft_seq, draft_layer;
   int n_seqs, heads, width, capacity, n;  // width = heads * head_dim
+  int lens_here;  // k_commit itself writes the lengths (new ones lie apart from the old)
 };
 
-// Layer blockIdx.x, sequence blockIdx.y. new_lens may be lens itself, so the lengths are
-// written by a second, one-CTA launch behind all of these reads.
+// Whether sequence b's rows may be appended (whole CTA).
+__device__ __forceinline__ bool commit_ok(const CommitArgs& a, int b, int cnt, int len) {
+  bool bad = cnt < 0 || cnt > a.n || len < 0 || len > a.capacity - cnt;
+  if (!bad)
+    for (int j = threadIdx.x; j < cnt; j += blockDim.x) {
+      const int i = a.path[static_cast<long long>(b) * a.n + j];
+      bad |= i < 0 || i >= a.n;
+    }
+  return !__syncthreads_or(bad);
+}
+
+__device__ __forceinline__ void write_lens(const CommitArgs& a, int b, bool ok, int cnt, int len, int next) {
+  if (!ok) record_status(a.dev_status, RF_ERR_INVALID_ARG);
+  if (a.new_lens != nullptr) a.new_lens[b] = len + (ok ? cnt : 0);
+  if (a.new_next_pos != nullptr) a.new_next_pos[b] = next + (ok ? cnt : 0);
+}
+
+// Layer blockIdx.x, sequence blockIdx.y.
 __global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitArgs a) {
+  pdl_launch_dependents();
   const int l = blockIdx.x, b = blockIdx.y;
   const int cnt = a.n_path[b], len = a.lens[b];
-  if (cnt <= 0 || cnt > a.n || len < 0 || len > a.capacity - cnt) return;
-  bool bad = false;
-  for (int j = threadIdx.x; j < cnt; j += 256) {
-    const int i = a.path[static_cast<long long>(b) * a.n + j];
-    bad |= i < 0 || i >= a.n;
-  }
-  if (__syncthreads_or(bad)) return;
+  const bool ok = commit_ok(a, b, cnt, len);
+  if (a.lens_here && l == 0 && threadIdx.x == 0) write_lens(a, b, ok, cnt, len, a.next_pos != nullptr ? a.next_pos[b] : 0);
+  if (!ok) return;
   const int pieces = a.width / 8;
+#pragma unroll 4
   for (int x = threadIdx.x; x < cnt * pieces; x += 256) {
     const int j = x / pieces, c = (x - j * pieces) * 8;
     const long long src = l * a.draft_layer + b * a.draft_seq +
@@ -264,18 +304,15 @@ __global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitAr
   }
 }
 
-__global__ void __launch_bounds__(256) k_commit_lens(const __grid_constant__ CommitArgs a) {
-  for (int b = blockIdx.x * 256 + threadIdx.x; b < a.n_seqs; b += gridDim.x * 256) {
-    const int cnt = a.n_path[b], len = a.lens[b];
-    bool ok = cnt >= 0 && cnt <= a.n && len >= 0 && len <= a.capacity - cnt;
-    for (int j = 0; ok && j < cnt; ++j) {
-      const int i = a.path[static_cast<long long>(b) * a.n + j];
-      ok = i >= 0 && i < a.n;
-    }
-    if (!ok) record_status(a.dev_status, RF_ERR_INVALID_ARG);
-    if (a.new_lens != nullptr) a.new_lens[b] = len + (ok ? cnt : 0);
-    if (a.new_next_pos != nullptr) a.new_next_pos[b] = a.next_pos[b] + (ok ? cnt : 0);
-  }
+// Where new_lens is lens (or new_next_pos next_pos) the lengths are written behind all of
+// k_commit's reads: by a dependent launch, one CTA a sequence.
+__global__ void __launch_bounds__(64) k_commit_lens(const __grid_constant__ CommitArgs a) {
+  const int b = blockIdx.x;
+  const int cnt = a.n_path[b], len = a.lens[b];
+  const int next = a.next_pos != nullptr ? a.next_pos[b] : 0;
+  const bool ok = commit_ok(a, b, cnt, len);
+  pdl_wait();
+  if (threadIdx.x == 0) write_lens(a, b, ok, cnt, len, next);
 }
 
 }  // namespace rf
@@ -290,8 +327,8 @@ extern "C" rf_status rf_verify_draft(const rf_verify_desc* d, const float* targe
   if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_seqs < 0 || d->n_nodes <= 0 || d->vocab <= 0)
     return fail(RF_ERR_INVALID_ARG, "need n_seqs >= 0, n_nodes, vocab > 0");
-  if (d->n_nodes > RF_TREE_MAX_NODES || d->vocab >= (int64_t(1) << 31) - 64 || d->n_seqs > (int64_t(1) << 24))
-    return fail(RF_ERR_SHAPE, "n_nodes must be <= %d, vocab < 2^31 - 64, n_seqs <= 2^24", RF_TREE_MAX_NODES);
+  if (d->n_nodes > RF_TREE_MAX_NODES || d->vocab > (int64_t(1) << 31) - 65536 || d->n_seqs > (int64_t(1) << 24))
+    return fail(RF_ERR_SHAPE, "n_nodes must be <= %d, vocab <= 2^31 - 65536, n_seqs <= 2^24", RF_TREE_MAX_NODES);
   if (d->ld_target < d->vocab || d->ld_noise < d->vocab || (draft != nullptr && d->ld_draft < d->vocab))
     return fail(RF_ERR_ALIGN, "row strides must be >= vocab");
   if (d->n_seqs == 0) return RF_OK;
@@ -324,12 +361,15 @@ extern "C" rf_status rf_verify_draft(const rf_verify_desc* d, const float* targe
   a.n = static_cast<int>(d->n_nodes);
   a.vocab = static_cast<int>(d->vocab);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(d->n_seqs) * kVerifyCtas);
+  // a power of two of CTAs, so many that each has a few tokens a thread
+  unsigned ctas = 1;
+  while (ctas < kVerifyCtas && static_cast<int64_t>(ctas) * kVerifyShare < d->vocab) ctas *= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(d->n_seqs) * ctas);
   cfg.blockDim = dim3(kVerifyThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kVerifyCtas;
+  at[0].val.clusterDim.x = ctas;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
@@ -396,12 +436,14 @@ extern "C" rf_status rf_commit_draft(const rf_cache_desc* d, int64_t n_nodes, in
   a.width = static_cast<int>(width);
   a.capacity = static_cast<int>(d->capacity);
   a.n = static_cast<int>(n_nodes);
+  a.lens_here = d->n_layers > 0 && new_lens != lens && (new_next_pos == nullptr || new_next_pos != next_pos);
   if (d->n_layers > 0) {
     ProfScope prof(s, RF_STAGE_COMMIT);
     k_commit<<<dim3(static_cast<unsigned>(d->n_layers), static_cast<unsigned>(d->n_seqs)), 256, 0, s>>>(a);
+    if ((st = cuda_check(cudaGetLastError(), "k_commit launch")) != RF_OK) return st;
   }
-  if ((st = cuda_check(cudaGetLastError(), "k_commit launch")) != RF_OK) return st;
+  if (a.lens_here) return RF_OK;
   ProfScope prof(s, RF_STAGE_COMMIT);
-  k_commit_lens<<<static_cast<unsigned>((d->n_seqs + 255) / 256), 256, 0, s>>>(a);
-  return cuda_check(cudaGetLastError(), "k_commit_lens launch");
+  return cuda_check(launch_dependent(k_commit_lens, dim3(static_cast<unsigned>(d->n_seqs)), dim3(64), 0, s, a),
+                    "k_commit_lens launch");
 }
