@@ -7,12 +7,16 @@
 // independent of one another and run in any order, in place.
 //
 //   k_evict_select  one CTA a unit, a warp a contiguous run of rows and a lane one row of
-//                   each 32. Rank keys stay in registers (up to 32 a thread; beyond
-//                   32,768 rows they are formed anew from memory in every pass). The
-//                   keep-th largest comes from a radix selection of 11 + 11 + 10 bits;
-//                   ranks among equals and the places of holes and movers come from
-//                   ballots. It also writes the scores and positions of the rows that
-//                   stay in place.
+//                   each 32. Rank keys stay in registers or shared memory (beyond 49,152
+//                   rows they are formed anew from memory in every pass). The keep-th
+//                   largest is searched bit by bit, by counting the keys that reach a
+//                   candidate: two instructions a key and one barrier a step, from the
+//                   highest bit in which keys differ until a candidate is reached by just
+//                   `keep`, about 18 steps for 4,000 different scores. (Histograms of 8-bit
+//                   digits take 3 passes, but shared-memory atomics ran at about a lane a
+//                   cycle: 35 us for 16,384 rows.) Ranks among equals and the places of
+//                   holes and movers come from ballots. It also writes the scores and
+//                   positions of the rows that stay in place.
 //   k_evict_move    the listed rows of K and V, their scores and positions.
 //
 // Bound: reading scores and positions and writing the kept ones (16 bytes a row) and the
@@ -24,7 +28,6 @@
 
 namespace rf {
 
-constexpr int kSelBins = 2048;
 constexpr int kMoveRows = 64;                // moves of one CTA of k_evict_move
 
 struct EvictArgs {
@@ -53,13 +56,13 @@ __device__ __forceinline__ unsigned rank_key(float score, bool sure) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+constexpr size_t kSelKeyBytes = 192 * 1024;  // of shared memory for keys
+
 template <int kThreads>
 struct SelShared {
-  int hist[kSelBins];
+  int count[2][kThreads / 32];  // by the parity of the step
   int warp_a[kThreads / 32];
   int warp_b[kThreads / 32];
-  unsigned prefix;
-  int left;
 };
 
 // Exclusive scan over the CTA's warps of one value per warp, in shared memory.
@@ -79,16 +82,22 @@ __device__ __forceinline__ void scan_warps(int* v) {
   __syncthreads();
 }
 
-// kItems keys a thread in registers, or 0: formed from memory in every pass.
-template <int kThreads, int kItems>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict_select(const __grid_constant__ EvictArgs a) {
+// Rows are taken in groups of 32, one a lane: warp w owns the groups from w * per_warp on,
+// kItems at a time (a "load" of groups). kKeys says where keys are between passes.
+enum { kInRegisters, kInShared, kInMemory };  // (one load a warp), (formed once), (formed in every pass)
+template <int kThreads, int kItems, int kKeys, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_constant__ EvictArgs a) {
+  static_assert(kItems <= 32, "a lane remembers one group's ballot");
   constexpr int kWarps = kThreads / 32;
+  constexpr int kSelBatch = kItems < 8 ? kItems : 8;  // rows of a thread whose loads are in flight together
   __shared__ SelShared<kThreads> sh;
   pdl_launch_dependents();
   const int unit = blockIdx.x;
   const int b = (unit / a.heads) % a.n_seqs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int len = a.lens[b];
+  // rows from position `newest` on are sure to stay (saturated: positions are 32-bit)
+  const int newest = static_cast<int>(max(static_cast<long long>(a.next_pos[b]) - a.recent, -2147483648ll));
   const long long base = static_cast<long long>(unit) * a.capacity;
   const float* score = a.score_in + base;
   const int32_t* pos = a.pos_in + base;
@@ -100,110 +109,189 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict_select(cons
     return;
   }
   const int keep = a.keep;
-  if (len <= keep) {
-#pragma unroll 4
-    for (int t = tid; t < len; t += kThreads) {
-      a.score_out[base + t] = score[t];
-      a.pos_out[base + t] = pos[t];
+  const bool copy = a.score_out != a.score_in || a.pos_out != a.pos_in;
+  // Rows [t0, t0 + 32 n) of a warp, lane by lane: those in `mine` (bit i: row t0 + 32 i + lane)
+  // are copied to the outputs, eight at a time.
+  auto copy_rows = [&](int t0, unsigned mine) {
+#pragma unroll
+    for (int i0 = 0; i0 < kItems; i0 += kSelBatch) {
+      if (__ballot_sync(0xffffffffu, (mine >> i0) & ((1u << kSelBatch) - 1u)) == 0) continue;
+      float f[kSelBatch];
+      int32_t q[kSelBatch];
+#pragma unroll
+      for (int i = 0; i < kSelBatch; ++i) {
+        if ((mine >> (i0 + i)) & 1u) {
+          f[i] = score[t0 + (i0 + i) * 32 + lane];
+          q[i] = pos[t0 + (i0 + i) * 32 + lane];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSelBatch; ++i) {
+        if ((mine >> (i0 + i)) & 1u) {
+          a.score_out[base + t0 + (i0 + i) * 32 + lane] = f[i];
+          a.pos_out[base + t0 + (i0 + i) * 32 + lane] = q[i];
+        }
+      }
     }
+  };
+  const int groups = (len + 31) / 32, per_warp = (groups + kWarps - 1) / kWarps;
+  const int g0 = min(warp * per_warp, groups), g1 = min(g0 + per_warp, groups);  // this warp's groups
+  if (len <= keep) {
+    if (copy)
+      for (int g = g0; g < g1; g += kItems) {
+        unsigned mine = 0;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) mine |= g + i < g1 && (g + i) * 32 + lane < len ? 1u << i : 0u;
+        copy_rows(g * 32, mine);
+      }
     if (tid == 0) a.n_moves[unit] = 0;
     return;
   }
-  const long long newest = static_cast<long long>(a.next_pos[b]) - a.recent;
-  // Warp w owns rows [r0, r1), lane i of it rows r0 + i, r0 + 32 + i, ...
-  const int run = ((len + kWarps - 1) / kWarps + 31) & ~31;
-  const int r0 = min(warp * run, len), r1 = min(r0 + run, len);
-  auto key_of = [&](int t) {
-    const int p = pos[t];
-    return rank_key(score[t], p < a.sink || p >= newest);
-  };
-  unsigned keys[kItems > 0 ? kItems : 1];
-  if constexpr (kItems > 0) {
+  // Keys of a load of groups from g on; 0, which is below every key, where there is no row.
+  auto load_keys = [&](int g, unsigned (&k)[kItems]) {
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int t = r0 + i * 32 + lane;
-      keys[i] = t < r1 ? key_of(t) : 0u;
+    for (int i0 = 0; i0 < kItems; i0 += kSelBatch) {
+      float f[kSelBatch];
+      int32_t q[kSelBatch];
+#pragma unroll
+      for (int i = 0; i < kSelBatch; ++i) {
+        const int t = min((g + i0 + i) * 32 + lane, len - 1);
+        if (i0 + i < kItems) {
+          f[i] = score[t];
+          q[i] = pos[t];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kSelBatch; ++i)
+        if (i0 + i < kItems) {
+          const int t = (g + i0 + i) * 32 + lane;
+          k[i0 + i] = g + i0 + i < g1 && t < len ? rank_key(f[i], q[i] < a.sink || q[i] >= newest) : 0u;
+        }
     }
-  }
-  // Calls f(row, key, whether the row is one of the warp's) for all of a thread's rows, in
-  // order; every lane of a warp makes the same calls.
-  auto each = [&](auto f) {
-    if constexpr (kItems > 0) {
+  };
+  unsigned keys[kItems];
+  extern __shared__ unsigned shared_keys[];  // a warp touches its own groups' alone
+  if constexpr (kKeys == kInRegisters) load_keys(g0, keys);
+  if constexpr (kKeys == kInShared) {
+    for (int g = g0; g < g1; g += kItems) {
+      load_keys(g, keys);
 #pragma unroll
       for (int i = 0; i < kItems; ++i)
-        if (r0 + i * 32 < r1) f(r0 + i * 32 + lane, keys[i], r0 + i * 32 + lane < r1);
+        if (g + i < g1) shared_keys[(g + i) * 32 + lane] = keys[i];
+    }
+  }
+  // Calls f(first group, keys) for each of the warp's loads.
+  auto each = [&](auto f) {
+    if constexpr (kKeys == kInRegisters) {
+      f(g0, keys);
     } else {
-      for (int t = r0 + lane; t - lane < r1; t += 32) f(t, t < r1 ? key_of(t) : 0u, t < r1);
-    }
-  };
-  // The keep-th largest key, digit by digit: among the keys that share the digits found
-  // so far, the bin that holds the rank still wanted.
-  unsigned prefix = 0, mask = 0;
-  int left = keep;
-#pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const unsigned digit = pass == 2 ? 1023u : 2047u;
-    for (int i = tid; i < kSelBins; i += kThreads) sh.hist[i] = 0;
-    __syncthreads();
-    each([&](int, unsigned k, bool in) {
-      if (in && (k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & digit], 1);
-    });
-    __syncthreads();
-    // Thread i holds kBins bins from the top down: an inclusive scan.
-    constexpr int kBins = kSelBins / kThreads;
-    int h[kBins], x = 0;
+      for (int g = g0; g < g1; g += kItems) {
+        if constexpr (kKeys == kInShared) {
 #pragma unroll
-    for (int j = 0; j < kBins; ++j) {
-      h[j] = sh.hist[kSelBins - 1 - (kBins * tid + j)];
-      x += h[j];
-    }
-    const int own = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sh.warp_a[warp] = x;
-    scan_warps<kThreads>(sh.warp_a);
-    int before = sh.warp_a[warp] + x - own;             // keys in higher bins
-    if (before < left && before + own >= left) {        // one thread
-#pragma unroll
-      for (int j = 0; j < kBins; ++j) {
-        if (before < left && before + h[j] >= left) {
-          sh.prefix = static_cast<unsigned>(kSelBins - 1 - (kBins * tid + j)) << shift;
-          sh.left = left - before;
+          for (int i = 0; i < kItems; ++i) keys[i] = g + i < g1 ? shared_keys[(g + i) * 32 + lane] : 0u;
+        } else {
+          load_keys(g, keys);
         }
-        before += h[j];
+        f(g, keys);
       }
     }
-    __syncthreads();
-    prefix |= sh.prefix;
-    mask |= digit << shift;
-    left = sh.left;
-  }
-  const unsigned bar = prefix;  // rows above stay, and the first `left` of those equal to it
-  const unsigned below = (1u << lane) - 1u;
-  int n_eq = 0;
-  each([&](int, unsigned k, bool in) { n_eq += __popc(__ballot_sync(0xffffffffu, in && k == bar)); });
-  __syncthreads();
-  if (lane == 0) sh.warp_a[warp] = n_eq;
-  scan_warps<kThreads>(sh.warp_a);
-  const int eq0 = sh.warp_a[warp];
-  int eq = eq0;
-  auto stays = [&](unsigned k, bool in) {  // warp-collective; eq: equal rows before these 32
-    const bool same = in && k == bar;
-    const unsigned m = __ballot_sync(0xffffffffu, same);
-    const bool stay = in && (k > bar || (same && eq + __popc(m & below) < left));
-    eq += __popc(m);
-    return stay;
   };
-  int holes = 0, movers = 0;
-  each([&](int t, unsigned k, bool in) {
-    const bool stay = stays(k, in);
-    holes += __popc(__ballot_sync(0xffffffffu, in && t < keep && !stay));
-    movers += __popc(__ballot_sync(0xffffffffu, t >= keep && stay));
+  // Sum over the CTA of a value per warp's lane 0 (`parity` alternates between calls).
+  auto cta_sum = [&](int warp_value, int parity) {
+    if (lane == 0) sh.count[parity][warp] = warp_value;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.count[parity][lane] : 0);
+  };
+  // Bits that all keys share.
+  unsigned lo = 0xffffffffu, hi = 0;
+  each([&](int, const unsigned (&k)[kItems]) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      hi = max(hi, k[i]);
+      lo = min(lo, k[i] != 0u ? k[i] : 0xffffffffu);
+    }
   });
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lane == 0) {
+    sh.warp_a[warp] = static_cast<int>(hi);
+    sh.warp_b[warp] = static_cast<int>(lo);
+  }
+  __syncthreads();
+  hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(sh.warp_a[lane]) : 0u);
+  lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<unsigned>(sh.warp_b[lane]) : 0xffffffffu);
+  const int top = hi == lo ? -1 : 31 - __clz(hi ^ lo);  // highest bit that differs
+  // bar: the largest value with the bits found so far that at least `keep` keys reach;
+  // reach: how many do. Without ties it is just `keep`.
+  unsigned bar = top < 0 ? hi : top == 31 ? 0u : hi & (0xffffffffu << (top + 1));
+  int reach = len, above = 0;  // above: keys known to be greater than any that share bar's bits
+#pragma unroll 1
+  for (int bit = top; bit >= 0 && reach != keep; --bit) {
+    const unsigned c = bar | (1u << bit);
+    int n = 0;
+    each([&](int, const unsigned (&k)[kItems]) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) n += k[i] >= c;
+    });
+    n = cta_sum(__reduce_add_sync(0xffffffffu, n), bit & 1);
+    if (n >= keep) {
+      bar = c;
+      reach = n;
+    } else {
+      above = n;
+    }
+  }
+  const bool ties = reach != keep;  // then bar is a key, and some of those equal to it leave
+  const int left = keep - above;    // how many of them stay
+  __syncthreads();
+  const unsigned below = (1u << lane) - 1u;
+  int eq = 0;  // keys equal to bar in earlier groups
+  if (ties) {
+    int n = 0;
+    each([&](int, const unsigned (&k)[kItems]) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) n += __popc(__ballot_sync(0xffffffffu, k[i] == bar));
+    });
+    if (lane == 0) sh.warp_a[warp] = n;
+    scan_warps<kThreads>(sh.warp_a);
+    eq = sh.warp_a[warp];
+  }
+  const int eq0 = eq;
+  // The rows of a load that stay: bit i of the result for the lane's own rows, and lane i's
+  // `group` for group i's 32 rows.
+  auto who_stays = [&](const unsigned (&k)[kItems], unsigned& group) {
+    unsigned own = 0;
+    group = 0;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      bool stay = k[i] >= bar && k[i] != 0u;
+      if (ties) {
+        const unsigned m = __ballot_sync(0xffffffffu, k[i] == bar);
+        if (k[i] == bar) stay = eq + __popc(m & below) < left;
+        eq += __popc(m);
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, stay);
+      if (lane == i) group = m;
+      own |= stay ? 1u << i : 0u;
+    }
+    return own;
+  };
+  // Of group g's rows that exist and lie below `keep` (lane's group: bit masks).
+  auto rows_below = [&](int row0, int end) {  // bits of rows row0 .. row0 + 31 below `end`
+    const int n = end - row0;
+    return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  };
+  int holes = 0, movers = 0;  // of the warp
+  each([&](int g, const unsigned (&k)[kItems]) {
+    unsigned m;
+    who_stays(k, m);
+    const int row0 = (g + lane) * 32;
+    const unsigned low = lane < kItems && g + lane < g1 ? rows_below(row0, keep) : 0u;
+    holes += __popc(~m & low & rows_below(row0, len));
+    movers += lane < kItems ? __popc(m & ~rows_below(row0, keep)) : 0;
+  });
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
   __syncthreads();
   if (lane == 0) {
     sh.warp_a[warp] = holes;
@@ -212,24 +300,48 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict_select(cons
   scan_warps<kThreads>(sh.warp_a);
   scan_warps<kThreads>(sh.warp_b);
   int hole = sh.warp_a[warp], mover = sh.warp_b[warp];
+  if (warp == kWarps - 1 && lane == 0) a.n_moves[unit] = mover + movers;  // as many holes as movers
   int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves;
   int32_t* src = dst + a.max_moves;
-  const bool copy = a.score_out != a.score_in || a.pos_out != a.pos_in;
   eq = eq0;
-  each([&](int t, unsigned k, bool in) {
-    const bool stay = stays(k, in);
-    const bool is_hole = in && t < keep && !stay, is_mover = t >= keep && stay;
-    const unsigned mh = __ballot_sync(0xffffffffu, is_hole), mm = __ballot_sync(0xffffffffu, is_mover);
-    if (is_hole) dst[hole + __popc(mh & below)] = t;
-    if (is_mover) src[mover + __popc(mm & below)] = t;
-    hole += __popc(mh);
-    mover += __popc(mm);
-    if (copy && stay && t < keep) {
-      a.score_out[base + t] = score[t];
-      a.pos_out[base + t] = pos[t];
+  each([&](int g, const unsigned (&k)[kItems]) {
+    unsigned m;
+    const unsigned own = who_stays(k, m);
+    const int row0 = (g + lane) * 32;
+    const unsigned low = rows_below(row0, keep);
+    const bool mine = lane < kItems && g + lane < g1;
+    const unsigned mh = mine ? ~m & low & rows_below(row0, len) : 0u, mm = mine ? m & ~low : 0u;
+    // where each group's holes and movers start in the lists
+    int h = __popc(mh), v = __popc(mm);
+    const int oh = h, ov = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, h, o), z = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) {
+        h += y;
+        v += z;
+      }
+    }
+    const int h_all = __shfl_sync(0xffffffffu, h, 31), v_all = __shfl_sync(0xffffffffu, v, 31);
+    h += hole - oh;
+    v += mover - ov;
+    for (unsigned todo = __ballot_sync(0xffffffffu, (mh | mm) != 0u); todo != 0u; todo &= todo - 1u) {
+      const int i = __ffs(todo) - 1, t = (g + i) * 32 + lane;
+      const unsigned gh = __shfl_sync(0xffffffffu, mh, i), gm = __shfl_sync(0xffffffffu, mm, i);
+      const int bh = __shfl_sync(0xffffffffu, h, i), bm = __shfl_sync(0xffffffffu, v, i);
+      if ((gh >> lane) & 1u) dst[bh + __popc(gh & below)] = t;
+      if ((gm >> lane) & 1u) src[bm + __popc(gm & below)] = t;
+    }
+    hole += h_all;
+    mover += v_all;
+    if (copy) {
+      unsigned in_place = own;  // the lane's rows that stay below `keep`
+#pragma unroll
+      for (int i = 0; i < kItems; ++i)
+        if ((g + i) * 32 + lane >= keep) in_place &= ~(1u << i);
+      copy_rows(g * 32, in_place);
     }
   });
-  if (warp == kWarps - 1 && lane == 0) a.n_moves[unit] = mover;  // as many holes as movers
 }
 
 __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs a) {
@@ -372,12 +484,26 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
   const unsigned units = static_cast<unsigned>(d->n_layers * d->n_seqs * d->n_kv_heads);
   {
     ProfScope prof(s, RF_STAGE_EVICT_SELECT);
-    // Threads and keys a thread by the cache's capacity: small CTAs leave room for several on
-    // an SM, and a CTA of 1,024 threads has 64 registers a thread for 32 keys.
-    if (d->capacity <= 2048) k_evict_select<256, 8><<<units, 256, 0, s>>>(a);
-    else if (d->capacity <= 8192) k_evict_select<512, 16><<<units, 512, 0, s>>>(a);
-    else if (d->capacity <= 32768) k_evict_select<1024, 32><<<units, 1024, 0, s>>>(a);
-    else k_evict_select<1024, 0><<<units, 1024, 0, s>>>(a);
+    // By the cache's capacity: every warp pays for a step's sums and barrier, so few warps with
+    // many keys each, in registers while they fit (16,384 rows in 160 units: 47 us on 1,024
+    // threads; with keys in shared memory 54 us on 512 threads and 59 us on 1,024).
+    const size_t key_bytes = (static_cast<size_t>(d->capacity) + 31) / 32 * 128;
+    if (d->capacity <= 128 * 17) {
+      k_evict_select<128, 17, kInRegisters, 4><<<units, 128, 0, s>>>(a);
+    } else if (d->capacity <= 256 * 17) {
+      k_evict_select<256, 17, kInRegisters, 3><<<units, 256, 0, s>>>(a);
+    } else if (d->capacity <= 512 * 17) {
+      k_evict_select<512, 17, kInRegisters, 2><<<units, 512, 0, s>>>(a);
+    } else if (d->capacity <= 1024 * 17) {
+      k_evict_select<1024, 17, kInRegisters, 1><<<units, 1024, 0, s>>>(a);
+    } else if (key_bytes <= kSelKeyBytes) {
+      static uint64_t done = 0;
+      const void* fn = reinterpret_cast<const void*>(&k_evict_select<1024, 16, kInShared, 1>);
+      if ((st = set_smem_attr(fn, kSelKeyBytes, &done)) != RF_OK) return st;
+      k_evict_select<1024, 16, kInShared, 1><<<units, 1024, key_bytes, s>>>(a);
+    } else {
+      k_evict_select<1024, 16, kInMemory, 1><<<units, 1024, 0, s>>>(a);
+    }
   }
   if ((st = cuda_check(cudaGetLastError(), "k_evict_select launch")) != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_EVICT_MOVE);

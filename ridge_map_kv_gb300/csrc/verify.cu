@@ -9,12 +9,14 @@
 // the chain above gives from p and q at that token, so the walk itself reads three
 // numbers a node, fetched for every node at once beforehand. A whole row is read where a
 // sum Z is needed (a refused child with a sibling behind it) and once at the end, for
-// the lowest argmax of r / noise. What bounds a call is the latency of these steps at
-// small sizes and the last row's bytes at large ones.
+// the lowest argmax of r / noise. What bounds a call is the latency of these steps.
 //
 // One cluster of CTAs a sequence: every thread follows the same walk through shared
 // memory, each CTA sums or scans its share of the vocabulary, and the shares meet
-// through distributed shared memory, in a fixed order.
+// through distributed shared memory, in a fixed order. A thread keeps its tokens' r and
+// q of the current node in registers (up to 16: 131,072 tokens in a cluster), so a
+// refusal costs one division a token; larger vocabularies form r_k anew from p and q
+// each time.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -27,7 +29,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kVerifyThreads = 1024;
 constexpr int kVerifyCtas = 8;      // CTAs of a cluster (the portable limit)
-constexpr int kVerifyBatch = 8;     // values of each row that a thread has in flight
+constexpr int kVerifyBatch = 8;     // values of each row that a thread has in flight (long rows)
+constexpr int kVerifySlots = 16;    // tokens of a thread that stay in registers
 constexpr int kVerifyShare = 2048;  // least tokens of a CTA
 
 struct VerifyArgs {
@@ -45,6 +48,9 @@ struct VerifyArgs {
   int n, vocab;
 };
 
+// Tokens of a CTA: whole 16-byte groups.
+__host__ __device__ inline int verify_share(int vocab, int ctas) { return ((vocab + ctas - 1) / ctas + 3) & ~3; }
+
 struct VerifyShared {
   int up[RF_TREE_MAX_NODES];
   int token[RF_TREE_MAX_NODES];
@@ -60,12 +66,21 @@ struct VerifyShared {
   unsigned long long warp_best[kVerifyThreads / 32];
 };
 
+// x / z, correctly rounded, for many x and one z: with y the correctly rounded 1/z, the
+// remainder of x y corrects it (P. Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990). Quotients near the underflow limit may be off by
+// their last (denormal) bits.
+__device__ __forceinline__ float quotient(float x, float z, float y) {
+  const float q = __fmul_rn(x, y);
+  return __fmaf_rn(__fmaf_rn(-q, z, x), y, q);
+}
+
 // r_k(t) from p(t), q(t) and the refusals.
 template <bool kDraft>
 __device__ __forceinline__ float residual(const VerifyShared& sh, float p, float q, int t, int k) {
   float r = p;
   for (int j = 0; j < k; ++j) {
-    if constexpr (kDraft) r = fmaxf(__fsub_rn(__fdiv_rn(r, sh.z[j]), q), 0.0f);
+    if constexpr (kDraft) r = fmaxf(__fsub_rn(quotient(r, sh.z[j], __frcp_rn(sh.z[j])), q), 0.0f);
     else r = sh.token[sh.refused[j]] == t ? 0.0f : r;
   }
   return r;
@@ -92,24 +107,36 @@ __device__ __forceinline__ void scan_row(int v0, int v1, const float* __restrict
   }
 }
 
-template <bool kDraft>
-__global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant__ VerifyArgs a) {
+// kFit: a CTA's share fits in its threads' registers.
+template <bool kDraft, bool kFit>
+__global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_constant__ VerifyArgs a) {
   __shared__ VerifyShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = static_cast<int>(cl.block_rank()), ctas = static_cast<int>(cl.num_blocks());
   const long long b = blockIdx.x / static_cast<unsigned>(ctas);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.n;
+  const int share = verify_share(a.vocab, ctas);
+  const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
+  // The noise is read in any case; the root's rows more often than not.
+  for (int t = v0 + tid * 32; t < v1; t += kVerifyThreads * 32) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.noise + b * a.ld_noise + t));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.target + b * n * a.ld_target + t));
+    if (kDraft) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.draft + b * n * a.ld_draft + t));
+  }
   bool bad = false;
   for (int i = tid; i < n; i += kVerifyThreads) {
     const int p = a.parents[b * n + i];
+    const int t = i > 0 ? a.tokens[b * n + i] : 0;
     sh.up[i] = p;
-    bad |= i == 0 ? p != -1 : (p < 0 || p >= i);
-    if (i > 0) {
-      const int t = a.tokens[b * n + i];
-      sh.token[i] = t;
-      bad |= t < 0 || t >= a.vocab;
-      sh.u[i] = a.u[b * n + i];
+    sh.token[i] = t;
+    sh.u[i] = i > 0 ? a.u[b * n + i] : 0.0f;
+    const bool wrong = i == 0 ? p != -1 : (p < 0 || p >= i || t < 0 || t >= a.vocab);
+    bad |= wrong;
+    if (i > 0 && !wrong) {
+      const long long row = b * n + p;
+      sh.p[i] = a.target[row * a.ld_target + t];
+      sh.q[i] = kDraft ? a.draft[row * a.ld_draft + t] : 1.0f;
     }
   }
   bad = __syncthreads_or(bad);
@@ -124,24 +151,44 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
     }
     return;
   }
-  for (int i = 1 + tid; i < n; i += kVerifyThreads) {
-    const long long row = b * n + sh.up[i];
-    sh.p[i] = a.target[row * a.ld_target + sh.token[i]];
-    sh.q[i] = kDraft ? a.draft[row * a.ld_draft + sh.token[i]] : 1.0f;
-  }
-  const int share = ((a.vocab + ctas - 1) / ctas + 3) & ~3;
-  const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
-  // the noise is read in any case, and at the end
-  for (int t = v0 + tid * 32; t < v1; t += kVerifyThreads * 32)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.noise + b * a.ld_noise + t));
-  __syncthreads();
-
   int cur = 0, k = 0, n_acc = 1, turn = 0;
   if (tid == 0) {
     sh.path[0] = 0;
     sh.z[0] = 1.0f;
   }
   __syncthreads();
+
+  // The thread's tokens v0 + tid, v0 + tid + 1024, ...: r after `applied` refusals at `cur`
+  // (-1: not read yet), and q.
+  const int slots = (v1 - v0 + kVerifyThreads - 1) / kVerifyThreads;
+  float r[kFit ? kVerifySlots : 1], q[kFit && kDraft ? kVerifySlots : 1];
+  int applied = -1;
+  auto bring = [&] {
+    if constexpr (kFit) {
+      if (applied < 0 || applied > k) {
+        const float* p = a.target + (b * n + cur) * a.ld_target;
+        const float* d = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
+#pragma unroll
+        for (int i = 0; i < kVerifySlots; ++i) {
+          const int t = v0 + tid + i * kVerifyThreads;
+          r[i] = t < v1 ? __ldg(p + t) : 0.0f;
+          if constexpr (kDraft) q[i] = t < v1 ? __ldg(d + t) : 0.0f;
+        }
+        applied = 0;
+      }
+      for (; applied < k; ++applied) {
+        const float z = sh.z[applied], y = __frcp_rn(z);
+        const int gone = sh.token[sh.refused[applied]] - v0 - tid;
+#pragma unroll
+        for (int i = 0; i < kVerifySlots; ++i) {
+          if (i < slots) {
+            if constexpr (kDraft) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
+            else r[i] = gone == i * kVerifyThreads ? 0.0f : r[i];
+          }
+        }
+      }
+    }
+  };
   // The next child of `cur` after node `c`, or n: 32 nodes at a time.
   auto next_child = [&](int c) {
     for (int c0 = c + 1; c0 < n; c0 += 32) {
@@ -152,8 +199,8 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
   };
   int c = next_child(0);
   while (c < n) {
-    const float r = residual<kDraft>(sh, sh.p[c], sh.q[c], sh.token[c], k);
-    if (__fmul_rn(__fmul_rn(sh.u[c], sh.q[c]), sh.z[k]) < r) {
+    const float rx = residual<kDraft>(sh, sh.p[c], sh.q[c], sh.token[c], k);
+    if (__fmul_rn(__fmul_rn(sh.u[c], sh.q[c]), sh.z[k]) < rx) {
       __syncthreads();  // the refusals of the node left behind are read no more
       if (tid == 0) {
         sh.path[n_acc] = c;
@@ -162,6 +209,7 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
       ++n_acc;
       cur = c;
       k = 0;
+      applied = -1;
       c = next_child(c);
       __syncthreads();
       continue;
@@ -173,10 +221,16 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
     ++k;
     if (sibling < n) {
       // Z_k, this CTA's share, then the cluster's
-      const float* p = a.target + (b * n + cur) * a.ld_target;
-      const float* q = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
       float sum = 0.0f;
-      scan_row(v0, v1, p, q, nullptr, [&](int t, float pt, float qt, float) { sum += residual<kDraft>(sh, pt, qt, t, k); });
+      if constexpr (kFit) {
+        bring();
+#pragma unroll
+        for (int i = 0; i < kVerifySlots; ++i)
+          if (i < slots) sum += r[i];
+      } else {
+        scan_row(v0, v1, a.target + (b * n + cur) * a.ld_target, kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr,
+                 nullptr, [&](int t, float pt, float qt, float) { sum += residual<kDraft>(sh, pt, qt, t, k); });
+      }
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) sh.warp_sum[warp] = sum;
       __syncthreads();
@@ -186,8 +240,8 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
         if (lane == 0) sh.part_sum[turn & 1] = s;
       }
       cl.sync();
-      float z = 0.0f;
-      for (int j = 0; j < ctas; ++j) z += *cl.map_shared_rank(&sh.part_sum[turn & 1], j);
+      float z = lane < ctas ? *cl.map_shared_rank(&sh.part_sum[turn & 1], lane) : 0.0f;
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       ++turn;
       if (z > 0.0f) {
         if (tid == 0) sh.z[k] = z;
@@ -201,18 +255,32 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
 
   // The lowest argmax of r / noise: the score's bits (scores are >= 0) above the
   // complement of the token.
-  const float* p = a.target + (b * n + cur) * a.ld_target;
-  const float* q = kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr;
   const float* e = a.noise + b * a.ld_noise;
   int token = 0;
   while (true) {
     unsigned long long best = 0;
-    scan_row(v0, v1, p, q, e, [&](int t, float pt, float qt, float et) {
-      const float r = residual<kDraft>(sh, pt, qt, t, k);
-      const float score = r > 0.0f ? __fdiv_rn(r, et) : 0.0f;
+    auto look = [&](int t, float rt, float et) {
+      const float score = rt > 0.0f ? __fdiv_rn(rt, et) : 0.0f;
       best = max(best, (static_cast<unsigned long long>(__float_as_uint(score)) << 32) |
                            (0xffffffffu - static_cast<unsigned>(t)));
-    });
+    };
+    if constexpr (kFit) {
+      float ev[kVerifySlots];
+#pragma unroll
+      for (int i = 0; i < kVerifySlots; ++i) {
+        const int t = v0 + tid + i * kVerifyThreads;
+        ev[i] = t < v1 ? __ldg(e + t) : 1.0f;
+      }
+      bring();
+#pragma unroll
+      for (int i = 0; i < kVerifySlots; ++i) {
+        const int t = v0 + tid + i * kVerifyThreads;
+        if (t < v1) look(t, r[i], ev[i]);
+      }
+    } else {
+      scan_row(v0, v1, a.target + (b * n + cur) * a.ld_target, kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr, e,
+               [&](int t, float pt, float qt, float et) { look(t, residual<kDraft>(sh, pt, qt, t, k), et); });
+    }
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) sh.warp_best[warp] = best;
     __syncthreads();
@@ -222,8 +290,8 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify(const __grid_constant
       if (lane == 0) sh.part_best[turn & 1] = m;
     }
     cl.sync();
-    unsigned long long m = 0;
-    for (int j = 0; j < ctas; ++j) m = max(m, *cl.map_shared_rank(&sh.part_best[turn & 1], j));
+    unsigned long long m = lane < ctas ? *cl.map_shared_rank(&sh.part_best[turn & 1], lane) : 0ull;
+    for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     ++turn;
     token = static_cast<int>(0xffffffffu - static_cast<unsigned>(m & 0xffffffffu));
     // All zero: the last refusal's residual is empty, so the one before it stands.
@@ -375,8 +443,10 @@ extern "C" rf_status rf_verify_draft(const rf_verify_desc* d, const float* targe
   cfg.attrs = at;
   cfg.numAttrs = 1;
   ProfScope prof(s, RF_STAGE_VERIFY);
-  return cuda_check(draft != nullptr ? cudaLaunchKernelEx(&cfg, k_verify<true>, a)
-                                     : cudaLaunchKernelEx(&cfg, k_verify<false>, a),
+  const bool fit = verify_share(a.vocab, static_cast<int>(ctas)) <= kVerifyThreads * kVerifySlots;
+  void (*kernel)(VerifyArgs) = draft != nullptr ? (fit ? k_verify<true, true> : k_verify<true, false>)
+                                                : (fit ? k_verify<false, true> : k_verify<false, false>);
+  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, a),
                     "k_verify launch");
 }
 

@@ -49,7 +49,7 @@ def _run(par, target, draft, tokens, u, noise, V, stream=None):
 
 @pytest.mark.parametrize("with_draft", [True, False], ids=["draft-probabilities", "outright"])
 @pytest.mark.parametrize("B,n,V,reach,ld", [(1, 1, 5, 1, None), (4, 5, 1000, 1, None), (9, 17, 333, 5, 341),
-                                           (3, 64, 50257, 8, None), (2, 64, 4096, 64, None), (2, 130, 64, 3, 72)])
+                                           (3, 64, 50257, 8, None), (2, 64, 4096, 64, None), (2, 130, 64, 3, 72), (2, 6, 140001, 6, None)])
 def test_verify_walks_like_the_definition(B, n, V, reach, ld, with_draft):
     checked = 0
     for seed in range(4):
