@@ -196,12 +196,24 @@ def _p(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    # torch.cuda.current_stream().cuda_stream without the Python stream object, which takes
+    # 2.9 us to make: more than the launch of a small kernel
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()     # initialises CUDA
+        get, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        _raw_stream = lambda: get(dev())  # noqa: E731
+    return _raw_stream()
+
+
 def _s(stream):
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without the Python stream object, which takes
-        # 2.9 us to make: more than the launch of a small kernel
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

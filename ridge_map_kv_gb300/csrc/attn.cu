@@ -59,7 +59,7 @@ constexpr float kAtRescale = 8.0f;  // log2 of the growth of the maximum that is
 // What a CTA's share starts with; also what k_attn_combine needs of it.
 struct AttnPlan {
   long long item;  // linear index, -1: no share
-  int b, h, mt, t0, n_tiles, pad;
+  int b, h, mt, t0, n_tiles, len;  // len: rows in use of sequence b
 };
 
 struct AttnArgs {
@@ -69,7 +69,7 @@ struct AttnArgs {
   const __nv_bfloat16* v_draft;
   __nv_bfloat16* out;
   float* lse;
-  float* part_o;     // [2 * ctas][rows of an item][head_dim]
+  float4* part_o;    // [2 * ctas][head_dim / 4][rows of an item]
   float2* part_ml;   // [2 * ctas][rows of an item]
   AttnPlan* plan;    // [ctas]
   int32_t* dev_status;
@@ -101,13 +101,6 @@ struct AttnCfg {
   static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kStages) * kTileBytes + sizeof(AttnShared) + 64;
   static constexpr int kRows = (kDual ? 2 : 1) * kAtTile;  // of an item
 };
-
-// The value that lane 0 of a converged warp holds; every lane holds it, but only so does
-// the compiler know, and keep what depends on it in uniform registers.
-template <class T>
-__device__ __forceinline__ T uniform(T x) {
-  return __shfl_sync(0xffffffffu, x, 0);
-}
 
 // Cache and draft tiles of one item.
 struct ItemShape {
@@ -158,7 +151,9 @@ struct Walk {
     shape = ItemShape{0, 0, 0};
     t1 = 0;
     if (left > 0) {
-      look(a);
+      shape.len = same(sh->plan.len);
+      shape.cached = (shape.len + kAtTile - 1) / kAtTile;
+      shape.tiles = same(sh->plan.n_tiles);
       t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), t0 + left));
     }
   }
@@ -182,22 +177,23 @@ struct Walk {
 };
 
 // The start of share `cta` of `ctas`: one warp sums the sequences' units, then finds the
-// sequence, head, item and tile of its first unit.
+// sequence, head, item and tile of its first unit. Writes the share to shared memory, and
+// to `plan` what k_attn_combine needs.
 template <bool kDual>
 __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
-  auto units_of = [&](int b) -> long long {
-    if (b >= a.n_seqs) return 0;
-    const int len = length_of(a, b);
-    if (len < 0) {
-      record_status(a.dev_status, RF_ERR_INVALID_ARG);
-      return 0;
-    }
-    return static_cast<long long>(a.heads) *
-           (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile) + a.draft_sum);
+  auto units_of = [&](int len) -> long long {
+    return len < 0 ? 0ll
+                   : static_cast<long long>(a.heads) *
+                         (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile) + a.draft_sum);
   };
   long long total = 0;
-  for (int b = lane; b < a.n_seqs; b += 32) total += units_of(b);
+  int len = -1;  // of sequence `lane`, then of later ones
+  for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+    len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
+    if (len < 0 && b0 + lane < a.n_seqs) record_status(a.dev_status, RF_ERR_INVALID_ARG);
+    total += units_of(len);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long shares = min(static_cast<long long>(ctas), total);
@@ -208,7 +204,8 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
     units = total * (cta + 1) / shares - first;
     long long base = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-      const long long own = units_of(b0 + lane);
+      if (a.n_seqs > 32) len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
+      const long long own = units_of(len);
       long long x = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -219,20 +216,21 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
       if (hit) {
         const int at = __ffs(hit) - 1;
         p.b = b0 + at;
+        p.len = __shfl_sync(0xffffffffu, len, at);
+        const int cached = (p.len + kAtTile - 1) / kAtTile;
         long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
         const long long per_head = __shfl_sync(0xffffffffu, own, at) / a.heads;
         p.h = static_cast<int>(r / per_head);
         r -= p.h * per_head;
         p.mt = 0;
+        p.n_tiles = cached + draft_tiles<kDual>(a, 0);
         if (a.mask != nullptr) {
-          const int tiles = item_shape<kDual>(a, p.b, 0).tiles;
-          p.mt = static_cast<int>(r / tiles);
-          r -= static_cast<long long>(p.mt) * tiles;
-          p.n_tiles = tiles;
+          p.mt = static_cast<int>(r / p.n_tiles);
+          r -= static_cast<long long>(p.mt) * p.n_tiles;
         } else {
-          while (r >= (p.n_tiles = item_shape<kDual>(a, p.b, p.mt).tiles)) {
+          while (r >= p.n_tiles) {
             r -= p.n_tiles;
-            ++p.mt;
+            p.n_tiles = cached + draft_tiles<kDual>(a, ++p.mt);
           }
         }
         p.t0 = static_cast<int>(r);
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   volatile int* abort_flag = &sh->abort;
   const uint64_t timeout = a.timeout_ns;
 
-  pdl_launch_dependents();  // k_attn_combine's CTAs may take their places as this kernel's leave
+  pdl_launch_dependents();  // the next kernel's CTAs may take their places as this one's leave
   if (threadIdx.x == 0) {
     for (int i = 0; i < Cfg::kStages; ++i) {
       mbar_init(&sh->full[i], 1);
@@ -375,6 +373,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
   }
+  // All above is this kernel's own; from here on it reads what earlier ones wrote, and writes.
+  pdl_wait();
   if (warp == 0) find_share<kDual>(a, sh, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
   tc_fence_before();
   __syncthreads();
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         const bool write = row < rows;
         const int head = w.h * a.group + row % a.group;
         const long long slot = 2LL * blockIdx.x + (w.t0 > 0 ? 0 : 1);
-        const long long prow = slot * Cfg::kRows + (kDual ? s * kAtTile : 0) + row;
+        const int prow = (kDual ? s * kAtTile : 0) + row;
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         if (!idle) {
           constexpr int kCols = kDual ? kHD : kHD / 2;
@@ -762,15 +762,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
                 __nv_bfloat16* dst = a.out + w.b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + col0 + c;
                 st_global_v4(dst, pk[0], pk[1], pk[2], pk[3]);
                 st_global_v4(dst + 8, pk[4], pk[5], pk[6], pk[7]);
-              } else {
-                float4* dst = reinterpret_cast<float4*>(a.part_o + prow * kHD + col0 + c);
+              } else {  // rows side by side: a warp's store is 512 bytes in a row
+                float4* dst = a.part_o + (slot * (kHD / 4) + (col0 + c) / 4) * Cfg::kRows + prow;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                for (int e = 0; e < 4; ++e) dst[e * Cfg::kRows] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
               }
             }
           }
           if (write && (kDual || s == 0)) {
-            if (!whole) a.part_ml[prow] = make_float2(m, l);
+            if (!whole) a.part_ml[slot * Cfg::kRows + prow] = make_float2(m, l);
             else if (a.lse != nullptr)
               a.lse[(static_cast<long long>(w.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
                   l == 0.0f ? -INFINITY : m * a.scale + logf(l);
@@ -794,13 +794,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   }
 }
 
-// Joins the rows of items that were cut. Block x: the cut before share x + 1; the first
-// cut inside an item answers for it. A warp takes a row: its lanes read the parts' maxima
-// and totals side by side, then the row's sums part after part, eight loads at a time.
-// Launched as a dependent of k_attn: its CTAs wait in place for that one's end.
+// Joins the rows of items that were cut. Block (x, y): the cut before share x + 1, rows
+// 32 y .. 32 y + 31 of its item; the first cut inside an item answers for it. A lane is a
+// row, a warp 16 channels of it. Launched as a dependent of k_attn: its CTAs wait in place
+// for that one's end.
 struct CombineArgs {
   const AttnPlan* plan;
-  const float* part_o;
+  const float4* part_o;
   const float2* part_ml;
   __nv_bfloat16* out;
   float* lse;
@@ -808,88 +808,83 @@ struct CombineArgs {
   int n, heads, group, npt, tiles, ctas;  // tiles: row tiles of an item
   float scale;
 };
-constexpr int kCombineWarps = 16;
-constexpr int kCombineBatch = 8;  // parts whose sums are in flight together
 
-template <int kHD>
-__global__ void __launch_bounds__(32 * kCombineWarps, 2) k_attn_combine(const __grid_constant__ CombineArgs a) {
+// kBatch: parts in flight together. Few rows (of few items, cut into many parts): 8; else 4, so
+// that more CTAs fit an SM.
+template <int kHD, int kBatch>
+__global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant__ CombineArgs a) {
+  pdl_launch_dependents();
   pdl_wait();
-  const int c = blockIdx.x + 1, lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // lane i: the share c - 1 + i
-  const int mine = min(c - 1 + lane, a.ctas - 1);
-  const AttnPlan q = a.plan[mine];
+  const AttnPlan q = a.plan[min(c - 1 + lane, a.ctas - 1)];
   const long long item = __shfl_sync(0xffffffffu, q.item, 1);
-  const long long item_before = __shfl_sync(0xffffffffu, q.item, 0);
-  const int t_cut = __shfl_sync(0xffffffffu, q.t0, 1), t_before = __shfl_sync(0xffffffffu, q.t0, 0);
-  if (item < 0 || t_cut == 0) return;
-  if (item_before == item && t_before > 0) return;
-  const int pb = __shfl_sync(0xffffffffu, q.b, 1), ph = __shfl_sync(0xffffffffu, q.h, 1), pmt = __shfl_sync(0xffffffffu, q.mt, 1);
+  if (item < 0 || __shfl_sync(0xffffffffu, q.t0, 1) == 0) return;
+  if (__shfl_sync(0xffffffffu, q.item, 0) == item && __shfl_sync(0xffffffffu, q.t0, 0) > 0) return;
+  const int b = __shfl_sync(0xffffffffu, q.b, 1), h = __shfl_sync(0xffffffffu, q.h, 1), mt = __shfl_sync(0xffffffffu, q.mt, 1);
   // parts of the item: from share c - 1, and from every share from c on that starts inside it
-  int parts = 1;
-  for (int i0 = 0;; i0 += 32) {
-    const int i = c + i0 + lane;
+  const unsigned inside = __ballot_sync(0xffffffffu, lane == 0 || (c - 1 + lane < a.ctas && q.item == item && q.t0 > 0));
+  int parts = inside == 0xffffffffu ? 32 : __ffs(~inside) - 1;
+  while (parts % 32 == 0) {
+    const int i = c - 1 + parts + lane;
     const bool in = i < a.ctas && a.plan[i].item == item && a.plan[i].t0 > 0;
     const unsigned m = __ballot_sync(0xffffffffu, in);
-    if (m != 0xffffffffu) {
-      parts += __ffs(~m) - 1;
-      break;
-    }
-    parts += 32;
+    if (m == 0u) break;
+    parts += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
   }
   const int item_rows = a.tiles * kAtTile;
+  const int r = blockIdx.y * 32 + lane, in_tile = r % kAtTile;
+  const int node = (mt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
+  if (r >= item_rows || in_tile >= a.npt * a.group || node >= a.n) return;
+  const int head = h * a.group + in_tile % a.group;
   const float sc = a.scale * kAtLog2e;
-  constexpr int kPer = kHD / 32;
   auto slot_of = [&](int i) { return i == 0 ? 2LL * (c - 1) + 1 : 2LL * (c - 1 + i); };
-  for (int r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); r < item_rows; r += gridDim.y * kCombineWarps) {
-    const int in_tile = r % kAtTile;
-    if (in_tile >= a.npt * a.group) continue;
-    const int node = (pmt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
-    if (node >= a.n) continue;
-    const int head = ph * a.group + in_tile % a.group;
-    float v[kCombineBatch][kPer];
-    auto load = [&](int i0) {
+  float m = -INFINITY, l = 0.0f;
+  float4 x[4] = {};
+  for (int i0 = 0; i0 < parts; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch][4];
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
-        const long long at = slot_of(min(i0 + j, parts - 1)) * item_rows + r;
-        if constexpr (kPer == 4) *reinterpret_cast<float4*>(v[j]) = *reinterpret_cast<const float4*>(a.part_o + at * kHD + lane * 4);
-        else *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(a.part_o + at * kHD + lane * 2);
-      }
-    };
-    load(0);  // on its way before the statistics are looked at
-    float m = -INFINITY;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, a.part_ml[slot_of(i) * item_rows + r].x);
+    for (int j = 0; j < kBatch; ++j) {
+      if (i0 + j >= parts) break;
+      const long long slot = slot_of(i0 + j);
+      ml[j] = a.part_ml[slot * item_rows + r];
+      const float4* src = a.part_o + (slot * (kHD / 4) + warp * 4) * item_rows + r;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float l = 0.0f, x[kPer] = {};
-    for (int i0 = 0; i0 < parts; i0 += kCombineBatch) {
-      if (i0 > 0) load(i0);
-      float f = 0.0f, lp = 0.0f;
-      if (lane < kCombineBatch && i0 + lane < parts) {
-        const float2 ml = a.part_ml[slot_of(i0 + lane) * item_rows + r];
-        f = ml.x == -INFINITY ? 0.0f : m == INFINITY ? NAN : exp2f_ftz((ml.x - m) * sc);
-        lp = ml.y * f;
-      }
+      for (int e = 0; e < 4; ++e) v[j][e] = src[e * item_rows];
+    }
 #pragma unroll
-      for (int j = 0; j < kCombineBatch; ++j) {
-        const float g = __shfl_sync(0xffffffffu, f, j), gl = __shfl_sync(0xffffffffu, lp, j);
-        if (i0 + j < parts) {
-          l += gl;
+    for (int j = 0; j < kBatch; ++j) {
+      if (i0 + j >= parts) break;
+      // a running maximum: one pass over the parts
+      const float mx = fmaxf(m, ml[j].x);
+      const float f = m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc);
+      const float g = ml[j].x == -INFINITY ? 0.0f : exp2f_ftz((ml[j].x - mx) * sc);
+      m = mx;
+      l = l * f + ml[j].y * g;
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) x[e] = fmaf(v[j][e], g, x[e]);
-        }
+      for (int e = 0; e < 4; ++e) {
+        x[e].x = x[e].x * f + v[j][e].x * g;
+        x[e].y = x[e].y * f + v[j][e].y * g;
+        x[e].z = x[e].z * f + v[j][e].z * g;
+        x[e].w = x[e].w * f + v[j][e].w * g;
       }
     }
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    __nv_bfloat16* dst = a.out + pb * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + lane * kPer;
-    if constexpr (kPer == 4) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-    } else {
-      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(x[0] * inv, x[1] * inv);
-    }
-    if (lane == 0 && a.lse != nullptr)
-      a.lse[(static_cast<long long>(pb) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
-          l == 0.0f ? -INFINITY : m * a.scale + logf(l);
   }
+  if (m == INFINITY) l = NAN;  // inf - inf
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint32_t pk[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    pk[2 * e] = pack_bf16x2(x[e].x * inv, x[e].y * inv);
+    pk[2 * e + 1] = pack_bf16x2(x[e].z * inv, x[e].w * inv);
+  }
+  __nv_bfloat16* dst = a.out + b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + warp * 16;
+  st_global_v4(dst, pk[0], pk[1], pk[2], pk[3]);
+  st_global_v4(dst + 8, pk[4], pk[5], pk[6], pk[7]);
+  if (warp == 0 && a.lse != nullptr)
+    a.lse[(static_cast<long long>(b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
+        l == 0.0f ? -INFINITY : m * a.scale + logf(l);
 }
 
 rf_status check_attn_desc(const rf_attn_desc* d) {
@@ -918,7 +913,7 @@ rf_status check_attn_desc(const rf_attn_desc* d) {
 }
 
 struct AttnLayout {
-  float* part_o;
+  float4* part_o;
   float2* part_ml;
   AttnPlan* plan;
   int tiles;  // row tiles of an item
@@ -930,7 +925,7 @@ static AttnLayout attn_layout(const rf_attn_desc* d, void* ws) {
   l.tiles = d->n_nodes * (d->n_q_heads / d->n_kv_heads) > kAtTile ? 2 : 1;
   const size_t rows = static_cast<size_t>(2 * kAtMaxCtas) * l.tiles * kAtTile;
   Carve c(ws);
-  l.part_o = c.take<float>(rows * d->head_dim);
+  l.part_o = c.take<float4>(rows * d->head_dim / 4);
   l.part_ml = c.take<float2>(rows);
   l.plan = c.take<AttnPlan>(kAtMaxCtas);
   l.bytes = c.bytes();
@@ -945,8 +940,8 @@ static rf_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t s) {
   rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual>), Cfg::kSmem, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTENTION);
-  k_attn<kHD, kDual><<<ctas, kAtThreads, Cfg::kSmem, s>>>(a);
-  return cuda_check(cudaGetLastError(), "k_attn launch");
+  return cuda_check(launch_dependent(k_attn<kHD, kDual>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, a),
+                    "k_attn launch");
 }
 
 }  // namespace rf
@@ -1050,9 +1045,13 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   c.tiles = lay.tiles;
   c.ctas = ctas;
   c.scale = a.scale;
-  const int rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, lay.tiles * kAtTile));
-  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>(std::min((rows + kCombineWarps - 1) / kCombineWarps, 4)));
+  // rows of an item that exist, in a tile's numbering (the first tile's are followed by a gap)
+  const int tile_rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, a.npt * group));
+  const int rows = lay.tiles == 2 ? 2 * kAtTile : tile_rows;
+  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + 31) / 32));
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
-  return cuda_check(launch_dependent(hd == 128 ? k_attn_combine<128> : k_attn_combine<64>, grid, dim3(32 * kCombineWarps), 0, s, c),
+  void (*combine)(CombineArgs) = hd == 128 ? (rows <= 32 ? k_attn_combine<128, 8> : k_attn_combine<128, 4>)
+                                           : (rows <= 32 ? k_attn_combine<64, 8> : k_attn_combine<64, 4>);
+  return cuda_check(launch_dependent(combine, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, c),
                     "k_attn_combine launch");
 }

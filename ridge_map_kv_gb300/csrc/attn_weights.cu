@@ -5,7 +5,7 @@
 // The statistics are known, so a key's sum needs no other key: each key tile is read
 // once, and what is written is one number a key. The product is taken as S = K Qᵀ, keys
 // along the TMEM lanes: a thread owns a key and sums over its columns, so there is no
-// reduction across threads but that of the two warps that share a key's columns.
+// reduction across threads but that of two warps where they share a key's columns.
 //
 // Bound: the keys' bytes up to a few hundred queries (2 hd bytes a key against 2 R hd
 // flops and R exponentials); beyond, the exponentials and the product.
@@ -16,8 +16,11 @@
 // launches. Units (128-key tiles) of all sequences and heads are cut into equal shares,
 // one per CTA.
 //
-//   warps 0-3, 4-7   sums: a thread is a key; the first four warps take a step's first
-//                    half of the columns, the others the second
+//   warps 0-3, 4-7   sums: a thread is a key. Where a tile takes one step, the two groups
+//                    of warps take alternate tiles (a tile's work is a chain of waits and
+//                    few instructions then, and two chains run side by side); else the
+//                    first group takes a step's first half of the columns, the other the
+//                    second, and the halves meet in shared memory
 //   warp 8           TMA: key tiles, in 64-channel slabs
 //   warp 9           MMA
 //   warps 10-13      the queries of the next (sequence, head), gathered along the path into
@@ -70,17 +73,28 @@ struct WeightShared {
   int abort;
 };
 
-template <int kHD>
+// A CTA's share, unit by unit; a thread alone or (kWarp) a converged warp walks it.
+template <bool kWarp>
 struct WeightWalk {
   const int *len, *cnt;
-  int b, h, t, tiles;
+  int b, h, t, tiles, queries;  // queries: path positions of the sequence
   long long left;
+  template <class T>
+  static __device__ __forceinline__ T same(T x) {
+    if constexpr (kWarp) return uniform(x);
+    else return x;
+  }
+  __device__ __forceinline__ void look() {
+    tiles = same((len[b] + kWtTile - 1) / kWtTile);
+    queries = same(cnt[b]);
+  }
   __device__ __forceinline__ WeightWalk(const WeightShared* sh, const int* len_, const int* cnt_) : len(len_), cnt(cnt_) {
-    b = sh->b;
-    h = sh->h;
-    t = sh->t;
-    left = sh->units;
-    tiles = left > 0 ? (len[b] + kWtTile - 1) / kWtTile : 0;
+    b = same(sh->b);
+    h = same(sh->h);
+    t = same(sh->t);
+    left = same(sh->units);
+    tiles = queries = 0;
+    if (left > 0) look();
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   // True when the next unit belongs to another sequence or head.
@@ -92,18 +106,32 @@ struct WeightWalk {
     if (++h == a.heads) {
       h = 0;
       do ++b;
-      while (len[b] <= 0);
-      tiles = (len[b] + kWtTile - 1) / kWtTile;
+      while (same(len[b]) <= 0);
+      look();
     }
   }
   // Query rows of the item in this launch, and the columns and number of its steps.
-  __device__ __forceinline__ int rows(const WeightArgs& a) const { return min(max(cnt[b] - a.j0, 0), a.j_max) * a.group; }
+  __device__ __forceinline__ int rows(const WeightArgs& a) const { return min(max(queries - a.j0, 0), a.j_max) * a.group; }
 };
 __device__ __forceinline__ int weight_steps(int rows) { return max(1, (rows + kWtStep - 1) / kWtStep); }
 // Columns of a step: equal shares, multiples of 16.
 __device__ __forceinline__ int weight_cols(int rows) {
   const int s = weight_steps(rows);
   return max(16, ((rows + s - 1) / s + 15) & ~15);
+}
+
+// Adds the weights 2^(s sc + nl) of N columns.
+template <int N>
+__device__ __forceinline__ void add_weights(const uint32_t (&r)[N], const float* nl, float sc, float2& s0, float2& s1) {
+  const float2 sc2 = make_float2(sc, sc);
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(nl + i);
+    const float2 x = fma_x2(make_float2(u2f(r[i]), u2f(r[i + 1])), sc2, make_float2(l.x, l.y));
+    const float2 y = fma_x2(make_float2(u2f(r[i + 2]), u2f(r[i + 3])), sc2, make_float2(l.z, l.w));
+    s0 = add_x2(s0, make_float2(exp2f_ftz(x.x), exp2f_ftz(x.y)));
+    s1 = add_x2(s1, make_float2(exp2f_ftz(y.x), exp2f_ftz(y.y)));
+  }
 }
 
 template <int kHD>
@@ -118,10 +146,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
   int* len = reinterpret_cast<int*>(neg_lse + a.bufs * a.rows_cap);
   int* cnt = len + a.n_seqs;
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + a.bufs * kSlabs * q_slab;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
   const uint64_t timeout = a.timeout_ns;
 
+  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sh->full[i], 1);
@@ -145,6 +174,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
   }
+  pdl_wait();
   // Lengths and counts, one warp a sequence: -1 for what may not be touched.
   for (int b = warp; b < a.n_seqs; b += kWtThreads / 32) {
     const int m = a.lens[b], c = a.n_path != nullptr ? a.n_path[b] : a.n;
@@ -208,14 +238,14 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     }
   }
   __syncthreads();
-  const uint32_t tmem = sh->tmem;
+  const uint32_t tmem = uniform(sh->tmem);
 
   if (warp == 8) {
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0;
       long long issued = 0;
-      for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a)) {
+      for (WeightWalk<false> w(sh, len, cnt); w.more(); w.next(a)) {
 #pragma unroll
         for (int c = 0; c < kSlabs; ++c) {
           if (!mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, timeout)) goto load_done;
@@ -234,96 +264,129 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
         mbar_wait(&sh->full[i % a.stages], static_cast<uint32_t>((i / a.stages) & 1), &dummy, timeout);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, step = 0, item = 0;
-      int qb = 0;         // query buffer of the item
-      bool fresh = true;  // the next unit starts an item
-      for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a)) {
-        if (fresh) {
-          qb = a.bufs == 2 ? item & 1u : 0;
-          const uint32_t par = (a.bufs == 2 ? item >> 1 : item) & 1u;
-          if (!mbar_wait(&sh->q_full[qb], par, abort_flag, timeout)) goto mma_done;
-          ++item;
-          tc_fence_after();
-        }
-        const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
-        const uint32_t idesc = make_idesc_bf16(kWtTile, cols, 0, 0);
-        int st[kSlabs];
-#pragma unroll
-        for (int c = 0; c < kSlabs; ++c) {
-          st[c] = stage;
-          if (!mbar_wait(&sh->full[stage], phase, abort_flag, timeout)) goto mma_done;
-          if (++stage == a.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-        for (int i = 0; i < steps; ++i, ++step) {
-          const uint32_t buf = step & 1u;
-          if (!mbar_wait(&sh->t_empty[buf], ((step >> 1) & 1u) ^ 1u, abort_flag, timeout)) goto mma_done;
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < kHD / 16; ++k)
-            tc_mma_bf16(tmem + buf * kWtStep, make_sdesc_sw128(s_ring + st[k / 4] * kWtSlab + (k % 4) * 32, 16, 1024),
-                        make_sdesc_sw128(s_q + (qb * kSlabs + k / 4) * q_slab + i * cols * 128 + (k % 4) * 32, 16, 1024), idesc,
-                        k > 0 ? 1u : 0u);
-          tc_commit(&sh->t_full[buf]);
-        }
-#pragma unroll
-        for (int c = 0; c < kSlabs; ++c) tc_commit(&sh->empty[st[c]]);
-        fresh = w.last_of_item();
-        if (fresh) tc_commit(&sh->q_empty[qb]);
+    const uint32_t issue = lane == 0;
+    int stage = 0;
+    uint32_t phase = 0, step = 0, item = 0;
+    int qb = 0;         // query buffer of the item
+    int steps = 0, cols = 0;
+    uint32_t idesc = 0;
+    bool fresh = true;  // the next unit starts an item
+    auto wait = [&](uint64_t* bar, uint32_t par) {  // whole warp
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, timeout));
+      if (ok) tc_fence_after();
+      return ok;
+    };
+    for (WeightWalk<true> w(sh, len, cnt); w.more(); w.next(a)) {
+      if (fresh) {
+        qb = a.bufs == 2 ? item & 1u : 0;
+        if (!wait(&sh->q_full[qb], (a.bufs == 2 ? item >> 1 : item) & 1u)) goto mma_done;
+        ++item;
+        steps = weight_steps(w.rows(a));
+        cols = weight_cols(w.rows(a));
+        idesc = make_idesc_bf16(kWtTile, cols, 0, 0);
       }
-    mma_done:
-      tc_commit(&sh->mma_done);
+      int st[kSlabs];
+#pragma unroll
+      for (int c = 0; c < kSlabs; ++c) {
+        st[c] = stage;
+        if (!wait(&sh->full[stage], phase)) goto mma_done;
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      for (int i = 0; i < steps; ++i, ++step) {
+        const uint32_t buf = step & 1u;
+        if (!wait(&sh->t_empty[buf], ((step >> 1) & 1u) ^ 1u)) goto mma_done;
+#pragma unroll
+        for (int k = 0; k < kHD / 16; ++k)
+          tc_mma_bf16_warp(tmem + buf * kWtStep, make_sdesc_sw128(s_ring + st[k / 4] * kWtSlab + (k % 4) * 32, 16, 1024),
+                           make_sdesc_sw128(s_q + (qb * kSlabs + k / 4) * q_slab + i * cols * 128 + (k % 4) * 32, 16, 1024),
+                           idesc, k > 0 ? 1u : 0u, issue);
+        tc_commit_warp(&sh->t_full[buf], issue);
+      }
+#pragma unroll
+      for (int c = 0; c < kSlabs; ++c) tc_commit_warp(&sh->empty[st[c]], issue);
+      fresh = w.last_of_item();
+      if (fresh) tc_commit_warp(&sh->q_empty[qb], issue);
+    }
+  mma_done:
+    tc_commit_warp(&sh->mma_done, issue);
+    if (lane == 0) {
       int dummy = 0;
       mbar_wait(&sh->mma_done, 0, &dummy, timeout);
     }
     __syncwarp();
   } else if (warp >= 10) {
-    // Warp w of the four takes rows 32 w .. 32 w + 31 of every 128: first their statistics and
-    // addresses (a lane a row), then their pieces, in asynchronous copies.
+    // Warp w of the four takes rows 32 w .. 32 w + 31 of every 128. A lane looks up one row's
+    // address; the copies of all rows are on their way before the statistics are looked at.
     const int w0 = (warp - 10) * 32;
     uint32_t item = 0;
-    constexpr int kPieces = kHD / 8, kRowsAtOnce = 32 / kPieces;
-    for (WeightWalk<kHD> w(sh, len, cnt); w.more(); ++item) {
+    constexpr int kPieces = kHD / 8, kRowsAtOnce = 32 / kPieces, kGroups = kWtQBytes / (2 * kHD) / kWtLoaders + 1;
+    for (WeightWalk<true> w(sh, len, cnt); w.more(); ++item) {
       const int qb = a.bufs == 2 ? item & 1u : 0;
       const uint32_t par = ((a.bufs == 2 ? item >> 1 : item) & 1u) ^ 1u;
       if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty[qb], par, abort_flag, timeout))) break;
       const int rows = w.rows(a), cols = weight_cols(rows) * weight_steps(rows);
-      const long long q_heads = static_cast<long long>(a.heads) * a.group;
       const uint32_t q0 = s_q + qb * kSlabs * q_slab;
-      for (int r0 = w0; r0 < cols; r0 += kWtLoaders) {
-        const int r = r0 + lane;
-        float x = -INFINITY;  // a column that adds nothing; its row is 0, whatever the query's bits are
-        const __nv_bfloat16* src = nullptr;
+      int node[kGroups];  // -1: a row beyond the queries
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int r = w0 + g * kWtLoaders + lane;
+        node[g] = -1;
         if (r < rows) {
           const int j = a.j0 + r / a.group;
-          const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
-          const long long head = static_cast<long long>(w.h) * a.group + r % a.group;
-          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node) * q_heads + head];
-          if (l != -INFINITY) {
-            x = -l * kWtLog2e;
-            src = a.q + w.b * a.q_seq + node * a.q_row + head * kHD;
-          }
+          node[g] = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
         }
-        if (r < cols) neg_lse[qb * a.rows_cap + r] = x;
-        const unsigned long long mine = reinterpret_cast<unsigned long long>(src);
-#pragma unroll 4
+      }
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int r0 = w0 + g * kWtLoaders;
+        if (r0 >= cols) break;
+        const long long head = static_cast<long long>(w.h) * a.group + (r0 + lane) % a.group;
+        const unsigned long long mine =
+            node[g] < 0 ? 0ull
+                        : reinterpret_cast<unsigned long long>(a.q + w.b * a.q_seq + node[g] * a.q_row + head * kHD);
+#pragma unroll
         for (int i = 0; i < 32; i += kRowsAtOnce) {
           const int ri = i + lane / kPieces, pc = lane % kPieces;
           const unsigned long long from = __shfl_sync(0xffffffffu, mine, ri);
           const int rr = r0 + ri;
-          if (rr < cols) {
-            const uint32_t dst = q0 + (pc / 8) * q_slab + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-            if (from != 0ull)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + pc * 16ull) : "memory");
-            else st_shared_v4(dst, 0, 0, 0, 0);
-          }
+          const uint32_t dst = q0 + (pc / 8) * q_slab + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
+          // a row beyond the queries is filled with zeros (a copy of 0 bytes)
+          if (rr < cols)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                         "l"((from != 0ull ? from : reinterpret_cast<unsigned long long>(a.q)) + pc * 16ull),
+                         "r"(from != 0ull ? 16 : 0)
+                         : "memory");
         }
       }
+      // Statistics. A query that sees nothing (-inf) adds nothing: its row becomes 0, whatever
+      // its bits are, and its column -inf.
+      unsigned empty = 0;  // bit g: the lane's row of group g
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        const int r = w0 + g * kWtLoaders + lane;
+        float x = -INFINITY;
+        if (node[g] >= 0) {
+          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node[g]) * (static_cast<long long>(a.heads) * a.group) +
+                                w.h * a.group + r % a.group];
+          if (l != -INFINITY) x = -l * kWtLog2e;
+          else empty |= 1u << g;
+        }
+        if (r < cols) neg_lse[qb * a.rows_cap + r] = x;
+      }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (__any_sync(0xffffffffu, empty != 0u)) {  // the copies of a row are other lanes', complete after this
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
+          if ((empty >> g) & 1u) {
+            const int r = w0 + g * kWtLoaders + lane;
+            for (int pc = 0; pc < kPieces; ++pc)
+              st_shared_v4(q0 + (pc / 8) * q_slab + r * 128 + ((pc & 7) << 4), 0, 0, 0, 0);
+          }
+      }
       fence_proxy_async_shared();
       mbar_arrive(&sh->q_full[qb]);
       // on to the next item
@@ -335,74 +398,110 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sc = a.scale * kWtLog2e;
-    uint32_t step = 0, unit = 0, item = 0;
-    int qb = 0;
+    uint32_t step = 0, halves = 0, item = 0;
+    int qb = 0, rows = 0, steps = 0, cols = 0, c0 = 0, c1 = 0, m = 0, c = 0;
+    const float* item_lse = neg_lse;
     bool fresh = true;
-    for (WeightWalk<kHD> w(sh, len, cnt); w.more(); w.next(a), ++unit) {
+    // The scores so far come from memory a unit ahead.
+    auto place = [&](const WeightWalk<true>& w) {
+      return (static_cast<long long>(w.b) * a.heads + w.h) * a.capacity + w.t * kWtTile + row;
+    };
+    auto old_score = [&](const WeightWalk<true>& w) {
+      return a.score_in != nullptr && w.more() && w.t * kWtTile + row < len[w.b] ? a.score_in[place(w)] : 0.0f;
+    };
+    WeightWalk<true> ahead(sh, len, cnt);
+    float old_next = old_score(ahead);
+    for (WeightWalk<true> w(sh, len, cnt); w.more(); w.next(a)) {
+      const float old = old_next;
+      ahead.next(a);
+      old_next = old_score(ahead);
       if (fresh) {
         qb = a.bufs == 2 ? item & 1u : 0;
         const uint32_t par = (a.bufs == 2 ? item >> 1 : item) & 1u;
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_full[qb], par, abort_flag, timeout))) goto sum_done;
         ++item;
-      }
-      const int rows = w.rows(a), steps = weight_steps(rows), cols = weight_cols(rows);
-      const int m = len[w.b], c = cnt[w.b];
-      const int key = w.t * kWtTile + row;
-      const long long at = (static_cast<long long>(w.b) * a.heads + w.h) * a.capacity + key;
-      float base = 0.0f;
-      if (part == 0 && key < m && a.score_in != nullptr) base = a.score_in[at] * a.decay;
-      // The first query sees rows up to m - c; the j-th up to m - c + j.
-      const bool masked = rows == 0 || (w.t + 1) * kWtTile > m - c + a.j0 + 1;
-      const int half = ((cols / 16 + 1) / 2) * 16;  // columns of the first warps
-      const int c0 = part == 0 ? 0 : half, c1 = part == 0 ? half : cols;
-      const float* item_lse = neg_lse + qb * a.rows_cap;
-      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
-      for (int i = 0; i < steps; ++i, ++step) {
-        const uint32_t buf = step & 1u;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->t_full[buf], (step >> 1) & 1u, abort_flag, timeout))) goto sum_done;
-        tc_fence_after();
-        for (int x = c0; x < c1; x += 16) {
-          uint32_t r[16];
-          tmem_ld16(tmem + lanes + buf * kWtStep + x, r);
-          tmem_wait_ld16(r);
-          const float4* nl = reinterpret_cast<const float4*>(item_lse + i * cols + x);
-          if (!masked) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float4 l = nl[e];
-              s0 += exp2f_ftz(fmaf(u2f(r[4 * e]), sc, l.x));
-              s1 += exp2f_ftz(fmaf(u2f(r[4 * e + 1]), sc, l.y));
-              s2 += exp2f_ftz(fmaf(u2f(r[4 * e + 2]), sc, l.z));
-              s3 += exp2f_ftz(fmaf(u2f(r[4 * e + 3]), sc, l.w));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int col = i * cols + x + e;
-              const int last = m - c + a.j0 + col / a.group;
-              const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, item_lse[col]));
-              s0 += col < rows && key <= last ? y : 0.0f;
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->t_empty[buf]);
+        rows = w.rows(a);
+        steps = weight_steps(rows);
+        cols = weight_cols(rows);
+        const int first = ((cols / 16 + 1) / 2) * 16;  // columns of the first warps
+        c0 = steps == 1 || part == 0 ? 0 : first;
+        c1 = steps == 1 || part == 1 ? cols : first;
+        m = len[w.b];
+        c = w.queries;
+        item_lse = neg_lse + qb * a.rows_cap;
       }
       fresh = w.last_of_item();
+      const bool mine = steps > 1 || (step & 1u) == static_cast<uint32_t>(part);
+      const int key = w.t * kWtTile + row;
+      float2 s0 = make_float2(0.0f, 0.0f), s1 = s0;
+      if (mine) {
+        // The first query sees rows up to m - c; the j-th up to m - c + j.
+        const bool masked = rows == 0 || (w.t + 1) * kWtTile > m - c + a.j0 + 1;
+        for (int i = 0; i < steps; ++i) {
+          const uint32_t buf = (step + i) & 1u;
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh->t_full[buf], ((step + i) >> 1) & 1u, abort_flag, timeout)))
+            goto sum_done;
+          tc_fence_after();
+          const uint32_t from = tmem + lanes + buf * kWtStep;
+          const float* lse0 = item_lse + i * cols;
+          if (!masked) {
+            int x = c0;
+            for (; x + 32 <= c1; x += 32) {
+              uint32_t r[32];
+              tmem_ld32(from + x, r);
+              tmem_wait_ld32(r);
+              add_weights(r, lse0 + x, sc, s0, s1);
+            }
+            if (x < c1) {
+              uint32_t r[16];
+              tmem_ld16(from + x, r);
+              tmem_wait_ld16(r);
+              add_weights(r, lse0 + x, sc, s0, s1);
+            }
+          } else {
+            for (int x = c0; x < c1; x += 16) {
+              uint32_t r[16];
+              tmem_ld16(from + x, r);
+              tmem_wait_ld16(r);
+              // path position (relative to j0) and query head of the first column
+              int j = (i * cols + x) / a.group, g = (i * cols + x) - j * a.group;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, lse0[x + e]));
+                s0.x += i * cols + x + e < rows && key <= m - c + a.j0 + j ? y : 0.0f;
+                if (++g == a.group) {
+                  g = 0;
+                  ++j;
+                }
+              }
+            }
+          }
+          // Eight arrivals hand a step's columns back: one a warp, or two where four warps read it.
+          tc_fence_before();
+          __syncwarp();
+          if (lane < (steps > 1 ? 1 : 2)) mbar_arrive(&sh->t_empty[buf]);
+        }
+      }
+      step += steps;
       if (fresh && lane == 0) mbar_arrive(&sh->q_empty[qb]);  // neg_lse is read no more
-      const float sum = (s0 + s1) + (s2 + s3);
-      // The two warps of a key meet. The second ones reach unit u + 4 only after the first
-      // ones have handed back a step of unit u + 2, hence are done with slot and barrier of
-      // unit u.
-      float* slot = sh->half[unit & 3u];
-      if (part == 1) {
-        slot[row] = sum;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->half_full[unit & 3u]);
+      const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+      if (steps == 1) {
+        if (mine && key < m) a.score_out[place(w)] = old * a.decay + sum;
       } else {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->half_full[unit & 3u], (unit >> 2) & 1u, abort_flag, timeout))) goto sum_done;
-        if (key < m) a.score_out[at] = base + (sum + slot[row]);
+        // The two warps of a key meet. The second ones reach their fourth next meeting only after
+        // the first ones have handed back a step of the second next, hence are done with slot and
+        // barrier of this one.
+        float* slot = sh->half[halves & 3u];
+        if (part == 1) {
+          slot[row] = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->half_full[halves & 3u]);
+        } else {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh->half_full[halves & 3u], (halves >> 2) & 1u, abort_flag, timeout)))
+            goto sum_done;
+          if (key < m) a.score_out[place(w)] = old * a.decay + (sum + slot[row]);
+        }
+        ++halves;
       }
     }
   sum_done:;
@@ -423,8 +522,8 @@ static rf_status launch_weights(WeightArgs a, int ctas, size_t smem, cudaStream_
   rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn_weights<kHD>), 227 * 1024, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTN_WEIGHTS);
-  k_attn_weights<kHD><<<ctas, kWtThreads, smem, s>>>(a);
-  return cuda_check(cudaGetLastError(), "k_attn_weights launch");
+  return cuda_check(launch_dependent(k_attn_weights<kHD>, dim3(static_cast<unsigned>(ctas)), dim3(kWtThreads), smem, s, a),
+                    "k_attn_weights launch");
 }
 
 static rf_status check_weights(const rf_attn_desc* d) {
