@@ -940,7 +940,7 @@ static rf_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t s) {
   rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual>), Cfg::kSmem, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTENTION);
-  return cuda_check(launch_dependent(k_attn<kHD, kDual>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, a),
+  return cuda_check(launch_dependent(k_attn<kHD, kDual>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, 1, a),
                     "k_attn launch");
 }
 
@@ -1052,6 +1052,6 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
   void (*combine)(CombineArgs) = hd == 128 ? (rows <= 32 ? k_attn_combine<128, 8> : k_attn_combine<128, 4>)
                                            : (rows <= 32 ? k_attn_combine<64, 8> : k_attn_combine<64, 4>);
-  return cuda_check(launch_dependent(combine, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, c),
+  return cuda_check(launch_dependent(combine, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, 1, c),
                     "k_attn_combine launch");
 }

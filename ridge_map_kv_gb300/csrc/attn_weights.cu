@@ -522,7 +522,7 @@ static rf_status launch_weights(WeightArgs a, int ctas, size_t smem, cudaStream_
   rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn_weights<kHD>), 227 * 1024, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTN_WEIGHTS);
-  return cuda_check(launch_dependent(k_attn_weights<kHD>, dim3(static_cast<unsigned>(ctas)), dim3(kWtThreads), smem, s, a),
+  return cuda_check(launch_dependent(k_attn_weights<kHD>, dim3(static_cast<unsigned>(ctas)), dim3(kWtThreads), smem, s, 1, a),
                     "k_attn_weights launch");
 }
 

@@ -9,12 +9,13 @@
 //   k_evict_select  one CTA a unit, a warp a contiguous run of rows and a lane one row of
 //                   each 32. Rank keys stay in registers or shared memory (beyond 49,152
 //                   rows they are formed anew from memory in every pass). The keep-th
-//                   largest is searched bit by bit, by counting the keys that reach a
-//                   candidate: two instructions a key and one barrier a step, from the
-//                   highest bit in which keys differ until a candidate is reached by just
-//                   `keep`, about 18 steps for 4,000 different scores. (Histograms of 8-bit
-//                   digits take 3 passes, but shared-memory atomics ran at about a lane a
-//                   cycle: 35 us for 16,384 rows.) Ranks among equals and the places of
+//                   largest is searched by counting the keys that reach a candidate, two
+//                   instructions a key and one barrier a step, bit by bit from the
+//                   highest bit in which keys differ until just `keep` keys reach one, about
+//                   20 steps for 4,000 different scores. (Interpolating on the counts took
+//                   more steps, since rows that are sure to stay lie far off; histograms of
+//                   8-bit digits take 3 passes, but their shared-memory atomics took 35 us
+//                   for 16,384 rows.) Ranks among equals and the places of
 //                   holes and movers come from ballots. It also writes the scores and
 //                   positions of the rows that stay in place.
 //   k_evict_move    the listed rows of K and V, their scores and positions.
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
   constexpr int kWarps = kThreads / 32;
   constexpr int kSelBatch = kItems < 8 ? kItems : 8;  // rows of a thread whose loads are in flight together
   __shared__ SelShared<kThreads> sh;
-  pdl_launch_dependents();
+  pdl_wait();  // (no early release: waiting CTAs of the next kernel would take this one's places)
   const int unit = blockIdx.x;
   const int b = (unit / a.heads) % a.n_seqs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
     __syncthreads();
     return __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.count[parity][lane] : 0);
   };
-  // Bits that all keys share.
+  // The smallest and the largest key.
   unsigned lo = 0xffffffffu, hi = 0;
   each([&](int, const unsigned (&k)[kItems]) {
 #pragma unroll
@@ -281,10 +282,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
     const int n = end - row0;
     return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
   };
-  int holes = 0, movers = 0;  // of the warp
+  int holes = 0, movers = 0;       // of the warp
+  unsigned own_first = 0, m_first = 0;  // of its one load (kInRegisters)
   each([&](int g, const unsigned (&k)[kItems]) {
     unsigned m;
-    who_stays(k, m);
+    own_first = who_stays(k, m);
+    m_first = m;
     const int row0 = (g + lane) * 32;
     const unsigned low = lane < kItems && g + lane < g1 ? rows_below(row0, keep) : 0u;
     holes += __popc(~m & low & rows_below(row0, len));
@@ -305,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
   int32_t* src = dst + a.max_moves;
   eq = eq0;
   each([&](int g, const unsigned (&k)[kItems]) {
-    unsigned m;
-    const unsigned own = who_stays(k, m);
+    unsigned m = m_first;
+    const unsigned own = kKeys == kInRegisters ? own_first : who_stays(k, m);
     const int row0 = (g + lane) * 32;
     const unsigned low = rows_below(row0, keep);
     const bool mine = lane < kItems && g + lane < g1;
@@ -487,26 +490,27 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
     // By the cache's capacity: every warp pays for a step's sums and barrier, so few warps with
     // many keys each, in registers while they fit (16,384 rows in 160 units: 47 us on 1,024
     // threads; with keys in shared memory 54 us on 512 threads and 59 us on 1,024).
+    cudaError_t e = cudaSuccess;
     const size_t key_bytes = (static_cast<size_t>(d->capacity) + 31) / 32 * 128;
     if (d->capacity <= 128 * 17) {
-      k_evict_select<128, 17, kInRegisters, 4><<<units, 128, 0, s>>>(a);
+      e = launch_dependent(k_evict_select<128, 17, kInRegisters, 4>, dim3(units), dim3(128), 0, s, 1, a);
     } else if (d->capacity <= 256 * 17) {
-      k_evict_select<256, 17, kInRegisters, 3><<<units, 256, 0, s>>>(a);
+      e = launch_dependent(k_evict_select<256, 17, kInRegisters, 3>, dim3(units), dim3(256), 0, s, 1, a);
     } else if (d->capacity <= 512 * 17) {
-      k_evict_select<512, 17, kInRegisters, 2><<<units, 512, 0, s>>>(a);
+      e = launch_dependent(k_evict_select<512, 17, kInRegisters, 2>, dim3(units), dim3(512), 0, s, 1, a);
     } else if (d->capacity <= 1024 * 17) {
-      k_evict_select<1024, 17, kInRegisters, 1><<<units, 1024, 0, s>>>(a);
+      e = launch_dependent(k_evict_select<1024, 17, kInRegisters, 1>, dim3(units), dim3(1024), 0, s, 1, a);
     } else if (key_bytes <= kSelKeyBytes) {
       static uint64_t done = 0;
       const void* fn = reinterpret_cast<const void*>(&k_evict_select<1024, 16, kInShared, 1>);
       if ((st = set_smem_attr(fn, kSelKeyBytes, &done)) != RF_OK) return st;
-      k_evict_select<1024, 16, kInShared, 1><<<units, 1024, key_bytes, s>>>(a);
+      e = launch_dependent(k_evict_select<1024, 16, kInShared, 1>, dim3(units), dim3(1024), key_bytes, s, 1, a);
     } else {
-      k_evict_select<1024, 16, kInMemory, 1><<<units, 1024, 0, s>>>(a);
+      e = launch_dependent(k_evict_select<1024, 16, kInMemory, 1>, dim3(units), dim3(1024), 0, s, 1, a);
     }
+    if ((st = cuda_check(e, "k_evict_select launch")) != RF_OK) return st;
   }
-  if ((st = cuda_check(cudaGetLastError(), "k_evict_select launch")) != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_EVICT_MOVE);
   const unsigned chunks = static_cast<unsigned>(std::max<int64_t>((lay.max_moves + kMoveRows - 1) / kMoveRows, 1));
-  return cuda_check(launch_dependent(k_evict_move, dim3(chunks, units), dim3(256), 0, s, a), "k_evict_move launch");
+  return cuda_check(launch_dependent(k_evict_move, dim3(chunks, units), dim3(256), 0, s, 1, a), "k_evict_move launch");
 }

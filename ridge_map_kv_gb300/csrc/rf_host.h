@@ -105,18 +105,24 @@ rf_status check_attn_desc(const rf_attn_desc* d);
 // running, once that one's CTAs have all exited or called pdl_launch_dependents(); the
 // kernel itself calls pdl_wait() (rf_device.cuh) before it touches what the previous one
 // writes, which returns when that one has finished and its writes are visible.
+// `cluster`: CTAs of a cluster along x.
 template <class... A>
-cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, unsigned cluster,
+                             const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 

@@ -83,6 +83,8 @@ constexpr int kRopeHeads = 4;  // heads whose loads are in flight together
 template <class T, bool kWide, bool kHalf>
 __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTable tab) {
   using S = RopeShape<T, kWide, kHalf>;
+  pdl_launch_dependents();
+  pdl_wait();
   const unsigned idx = blockIdx.x * 256u + threadIdx.x;
   if (idx >= static_cast<unsigned>(a.n_rows) * static_cast<unsigned>(a.items)) return;
   const int row = static_cast<int>(idx / static_cast<unsigned>(a.items));
@@ -213,7 +215,7 @@ static rf_status check_rope(const rf_rope_desc* d) {
 }
 
 template <class T, bool kWide, bool kHalf>
-static void launch_rope(RopeArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
+static cudaError_t launch_rope(RopeArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
   a.items = a.head_dim / RopeShape<T, kWide, kHalf>::kChannels;
   // Heads per thread: as many (multiples of the four that are loaded together) as still
   // leave two waves of threads; all of them one by one in the smallest calls.
@@ -221,19 +223,19 @@ static void launch_rope(RopeArgs& a, const RopeTable& t, int sms, cudaStream_t s
   a.hpt = 1;
   while (a.hpt < 16 && threads1 * a.n_heads / (2 * a.hpt) >= 4096LL * sms) a.hpt *= 2;
   const dim3 grid(static_cast<unsigned>((threads1 + 255) / 256), static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
-  k_rope<T, kWide, kHalf><<<grid, 256, 0, s>>>(a, t);
+  return launch_dependent(k_rope<T, kWide, kHalf>, grid, dim3(256), 0, s, 1, a, t);
 }
 template <class T>
-static void launch_rope(RopeArgs& a, const RopeTable& t, bool half, int sms, cudaStream_t s) {
+static cudaError_t launch_rope(RopeArgs& a, const RopeTable& t, bool half, int sms, cudaStream_t s) {
   constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   const int unit = half ? 2 * kVec : kVec;  // channels of a thread and head
   const bool wide = a.rot % unit == 0 && a.head_dim % unit == 0;
   if (half) {
-    if (wide) launch_rope<T, true, true>(a, t, sms, s);
-    else launch_rope<T, false, true>(a, t, sms, s);
+    if (wide) return launch_rope<T, true, true>(a, t, sms, s);
+    return launch_rope<T, false, true>(a, t, sms, s);
   } else {
-    if (wide) launch_rope<T, true, false>(a, t, sms, s);
-    else launch_rope<T, false, false>(a, t, sms, s);
+    if (wide) return launch_rope<T, true, false>(a, t, sms, s);
+    return launch_rope<T, false, false>(a, t, sms, s);
   }
 }
 
@@ -245,6 +247,8 @@ __global__ void __launch_bounds__(1024) k_tree_build(int n, int words, const int
                                                      unsigned long long* __restrict__ mask,
                                                      int32_t* __restrict__ positions, int32_t* dev_status) {
   __shared__ int up[RF_TREE_MAX_NODES];
+  pdl_launch_dependents();
+  pdl_wait();
   const int b = blockIdx.x, i = threadIdx.x;
   bool bad = false;
   if (i < n) {
@@ -304,9 +308,9 @@ extern "C" rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out
   a.sign = desc->transpose ? -1.0f : 1.0f;
   const bool half = desc->layout == RF_ROPE_HALF;
   ProfScope prof(s, RF_STAGE_ROPE);
-  if (desc->dtype == RF_BF16) launch_rope<__nv_bfloat16>(a, tab, half, sms, s);
-  else launch_rope<float>(a, tab, half, sms, s);
-  return cuda_check(cudaGetLastError(), "k_rope launch");
+  return cuda_check(desc->dtype == RF_BF16 ? launch_rope<__nv_bfloat16>(a, tab, half, sms, s)
+                                           : launch_rope<float>(a, tab, half, sms, s),
+                    "k_rope launch");
 }
 
 extern "C" rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_t* parents, const int32_t* next_pos,
@@ -325,8 +329,9 @@ extern "C" rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_
   if (st != RF_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope prof(s, RF_STAGE_TREE_BUILD);
-  k_tree_build<<<static_cast<unsigned>(n_seqs), static_cast<unsigned>((n_nodes + 31) / 32 * 32), 0, s>>>(
-      static_cast<int>(n_nodes), static_cast<int>(RF_TREE_WORDS(n_nodes)), parents, next_pos,
-      reinterpret_cast<unsigned long long*>(mask), positions, dev_status);
-  return cuda_check(cudaGetLastError(), "k_tree_build launch");
+  return cuda_check(launch_dependent(k_tree_build, dim3(static_cast<unsigned>(n_seqs)),
+                                     dim3(static_cast<unsigned>((n_nodes + 31) / 32 * 32)), 0, s, 1,
+                                     static_cast<int>(n_nodes), static_cast<int>(RF_TREE_WORDS(n_nodes)), parents, next_pos,
+                                     reinterpret_cast<unsigned long long*>(mask), positions, dev_status),
+                    "k_tree_build launch");
 }

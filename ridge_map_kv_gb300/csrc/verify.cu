@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
   const int n = a.n;
   const int share = verify_share(a.vocab, ctas);
   const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
+  pdl_launch_dependents();
+  pdl_wait();
   // The noise is read in any case; the root's rows more often than not.
   for (int t = v0 + tid * 32; t < v1; t += kVerifyThreads * 32) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(a.noise + b * a.ld_noise + t));
@@ -348,6 +350,7 @@ __device__ __forceinline__ void write_lens(const CommitArgs& a, int b, bool ok, 
 // Layer blockIdx.x, sequence blockIdx.y.
 __global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitArgs a) {
   pdl_launch_dependents();
+  pdl_wait();
   const int l = blockIdx.x, b = blockIdx.y;
   const int cnt = a.n_path[b], len = a.lens[b];
   const bool ok = commit_ok(a, b, cnt, len);
@@ -375,11 +378,11 @@ __global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitAr
 // Where new_lens is lens (or new_next_pos next_pos) the lengths are written behind all of
 // k_commit's reads: by a dependent launch, one CTA a sequence.
 __global__ void __launch_bounds__(64) k_commit_lens(const __grid_constant__ CommitArgs a) {
+  pdl_wait();
   const int b = blockIdx.x;
   const int cnt = a.n_path[b], len = a.lens[b];
   const int next = a.next_pos != nullptr ? a.next_pos[b] : 0;
   const bool ok = commit_ok(a, b, cnt, len);
-  pdl_wait();
   if (threadIdx.x == 0) write_lens(a, b, ok, cnt, len, next);
 }
 
@@ -428,25 +431,14 @@ extern "C" rf_status rf_verify_draft(const rf_verify_desc* d, const float* targe
   a.ld_noise = d->ld_noise;
   a.n = static_cast<int>(d->n_nodes);
   a.vocab = static_cast<int>(d->vocab);
-  cudaLaunchConfig_t cfg = {};
   // a power of two of CTAs, so many that each has a few tokens a thread
   unsigned ctas = 1;
   while (ctas < kVerifyCtas && static_cast<int64_t>(ctas) * kVerifyShare < d->vocab) ctas *= 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(d->n_seqs) * ctas);
-  cfg.blockDim = dim3(kVerifyThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   ProfScope prof(s, RF_STAGE_VERIFY);
   const bool fit = verify_share(a.vocab, static_cast<int>(ctas)) <= kVerifyThreads * kVerifySlots;
   void (*kernel)(VerifyArgs) = draft != nullptr ? (fit ? k_verify<true, true> : k_verify<true, false>)
                                                 : (fit ? k_verify<false, true> : k_verify<false, false>);
-  return cuda_check(cudaLaunchKernelEx(&cfg, kernel, a),
+  return cuda_check(launch_dependent(kernel, dim3(static_cast<unsigned>(d->n_seqs) * ctas), dim3(kVerifyThreads), 0, s, ctas, a),
                     "k_verify launch");
 }
 
@@ -509,11 +501,13 @@ extern "C" rf_status rf_commit_draft(const rf_cache_desc* d, int64_t n_nodes, in
   a.lens_here = d->n_layers > 0 && new_lens != lens && (new_next_pos == nullptr || new_next_pos != next_pos);
   if (d->n_layers > 0) {
     ProfScope prof(s, RF_STAGE_COMMIT);
-    k_commit<<<dim3(static_cast<unsigned>(d->n_layers), static_cast<unsigned>(d->n_seqs)), 256, 0, s>>>(a);
-    if ((st = cuda_check(cudaGetLastError(), "k_commit launch")) != RF_OK) return st;
+    st = cuda_check(launch_dependent(k_commit, dim3(static_cast<unsigned>(d->n_layers), static_cast<unsigned>(d->n_seqs)),
+                                     dim3(256), 0, s, 1, a),
+                    "k_commit launch");
+    if (st != RF_OK) return st;
   }
   if (a.lens_here) return RF_OK;
   ProfScope prof(s, RF_STAGE_COMMIT);
-  return cuda_check(launch_dependent(k_commit_lens, dim3(static_cast<unsigned>(d->n_seqs)), dim3(64), 0, s, a),
+  return cuda_check(launch_dependent(k_commit_lens, dim3(static_cast<unsigned>(d->n_seqs)), dim3(64), 0, s, 1, a),
                     "k_commit_lens launch");
 }
