@@ -167,7 +167,10 @@ struct Walk {
         mt = 0;
         if (++h == a.heads) {
           h = 0;
-          ++b;
+          if (++b >= a.n_seqs) {  // lengths that changed under the kernel: no sequence is left
+            left = 0;
+            return;
+          }
         }
       }
       look(a);
@@ -200,8 +203,8 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
   AttnPlan p{-1, 0, 0, 0, 0, 0, 0};
   long long units = 0;
   if (cta < shares) {
-    const long long first = total * cta / shares;
-    units = total * (cta + 1) / shares - first;
+    const long long first = share_start(total, cta, static_cast<int>(shares));
+    units = share_start(total, cta + 1, static_cast<int>(shares)) - first;
     long long base = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
       if (a.n_seqs > 32) len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
@@ -219,13 +222,13 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
         p.len = __shfl_sync(0xffffffffu, len, at);
         const int cached = (p.len + kAtTile - 1) / kAtTile;
         long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
-        const long long per_head = __shfl_sync(0xffffffffu, own, at) / a.heads;
-        p.h = static_cast<int>(r / per_head);
+        const long long per_head = quick_div(__shfl_sync(0xffffffffu, own, at), a.heads);
+        p.h = static_cast<int>(quick_div(r, per_head));
         r -= p.h * per_head;
         p.mt = 0;
         p.n_tiles = cached + draft_tiles<kDual>(a, 0);
         if (a.mask != nullptr) {
-          p.mt = static_cast<int>(r / p.n_tiles);
+          p.mt = static_cast<int>(quick_div(r, p.n_tiles));
           r -= static_cast<long long>(p.mt) * p.n_tiles;
         } else {
           while (r >= p.n_tiles) {

@@ -41,6 +41,7 @@ constexpr int kWtStep = 256;         // columns of a step
 constexpr int kWtMaxStages = 12;
 constexpr int kWtSlab = kWtTile * 128;
 constexpr int kWtQBytes = 640 * 128 * 2;  // the most that queries may take
+constexpr int kWtNever = INT32_MIN;       // position of a column that no key is seen from
 constexpr float kWtLog2e = 1.4426950408889634f;
 
 struct WeightArgs {
@@ -143,7 +144,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
   uint8_t* p = smem + a.bufs * kSlabs * q_slab + a.stages * kWtSlab;
   WeightShared* sh = reinterpret_cast<WeightShared*>(p);
   float* neg_lse = reinterpret_cast<float*>(p + ((sizeof(WeightShared) + 15) & ~size_t(15)));  // -lse log2 e, a column each
-  int* len = reinterpret_cast<int*>(neg_lse + a.bufs * a.rows_cap);
+  int* position = reinterpret_cast<int*>(neg_lse + a.bufs * a.rows_cap);  // a column's path position, from j0
+  int* len = position + a.bufs * a.rows_cap;
   int* cnt = len + a.n_seqs;
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + a.bufs * kSlabs * q_slab;
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -206,8 +208,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     long long units = 0;
     int fb = 0, fh = 0, ft = 0;
     if (blockIdx.x < shares) {
-      const long long first = total * blockIdx.x / shares;
-      units = total * (blockIdx.x + 1) / shares - first;
+      const long long first = share_start(total, static_cast<int>(blockIdx.x), static_cast<int>(shares));
+      units = share_start(total, static_cast<int>(blockIdx.x) + 1, static_cast<int>(shares)) - first;
       long long base = 0;
       for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
         const long long own = units_of(b0 + lane);
@@ -222,8 +224,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
           const int at = __ffs(hit) - 1;
           fb = b0 + at;
           const long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
-          const long long per_head = __shfl_sync(0xffffffffu, own, at) / a.heads;
-          fh = static_cast<int>(r / per_head);
+          const long long per_head = quick_div(__shfl_sync(0xffffffffu, own, at), a.heads);
+          fh = static_cast<int>(quick_div(r, per_head));
           ft = static_cast<int>(r - fh * per_head);
           break;
         }
@@ -329,52 +331,53 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
       if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty[qb], par, abort_flag, timeout))) break;
       const int rows = w.rows(a), cols = weight_cols(rows) * weight_steps(rows);
       const uint32_t q0 = s_q + qb * kSlabs * q_slab;
-      int node[kGroups];  // -1: a row beyond the queries
+      // Row of the lane in each group: its statistic, and its query's address (0: a row beyond the
+      // queries, to be filled with zeros).
+      float stat[kGroups];
+      unsigned long long row_at[kGroups];
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int r = w0 + g * kWtLoaders + lane;
-        node[g] = -1;
+        stat[g] = -INFINITY;
+        row_at[g] = 0ull;
         if (r < rows) {
           const int j = a.j0 + r / a.group;
-          node[g] = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
+          const int node = a.path != nullptr ? a.path[static_cast<long long>(w.b) * a.n + j] : j;
+          const long long head = static_cast<long long>(w.h) * a.group + r % a.group;
+          stat[g] = a.lse[(static_cast<long long>(w.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head];
+          row_at[g] = reinterpret_cast<unsigned long long>(a.q + w.b * a.q_seq + node * a.q_row + head * kHD);
         }
       }
+      const int pc = lane % kPieces;
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int r0 = w0 + g * kWtLoaders;
         if (r0 >= cols) break;
-        const long long head = static_cast<long long>(w.h) * a.group + (r0 + lane) % a.group;
-        const unsigned long long mine =
-            node[g] < 0 ? 0ull
-                        : reinterpret_cast<unsigned long long>(a.q + w.b * a.q_seq + node[g] * a.q_row + head * kHD);
+        unsigned long long from[kPieces];  // all shuffles before the first copy, which none would pass
 #pragma unroll
-        for (int i = 0; i < 32; i += kRowsAtOnce) {
-          const int ri = i + lane / kPieces, pc = lane % kPieces;
-          const unsigned long long from = __shfl_sync(0xffffffffu, mine, ri);
-          const int rr = r0 + ri;
+        for (int i = 0; i < kPieces; ++i) from[i] = __shfl_sync(0xffffffffu, row_at[g], i * kRowsAtOnce + lane / kPieces);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int rr = r0 + i * kRowsAtOnce + lane / kPieces;
           const uint32_t dst = q0 + (pc / 8) * q_slab + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-          // a row beyond the queries is filled with zeros (a copy of 0 bytes)
           if (rr < cols)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                         "l"((from != 0ull ? from : reinterpret_cast<unsigned long long>(a.q)) + pc * 16ull),
-                         "r"(from != 0ull ? 16 : 0)
+                         "l"((from[i] != 0ull ? from[i] : reinterpret_cast<unsigned long long>(a.q)) + pc * 16ull),
+                         "r"(from[i] != 0ull ? 16 : 0)
                          : "memory");
         }
       }
-      // Statistics. A query that sees nothing (-inf) adds nothing: its row becomes 0, whatever
-      // its bits are, and its column -inf.
+      // A query that sees nothing (-inf) adds nothing: its row becomes 0, whatever its bits are,
+      // and its column -inf.
       unsigned empty = 0;  // bit g: the lane's row of group g
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int r = w0 + g * kWtLoaders + lane;
-        float x = -INFINITY;
-        if (node[g] >= 0) {
-          const float l = a.lse[(static_cast<long long>(w.b) * a.n + node[g]) * (static_cast<long long>(a.heads) * a.group) +
-                                w.h * a.group + r % a.group];
-          if (l != -INFINITY) x = -l * kWtLog2e;
-          else empty |= 1u << g;
+        if (r < rows && stat[g] == -INFINITY) empty |= 1u << g;
+        if (r < cols) {
+          neg_lse[qb * a.rows_cap + r] = stat[g] == -INFINITY ? -INFINITY : -stat[g] * kWtLog2e;
+          position[qb * a.rows_cap + r] = r < rows ? r / a.group : kWtNever;
         }
-        if (r < cols) neg_lse[qb * a.rows_cap + r] = x;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       if (__any_sync(0xffffffffu, empty != 0u)) {  // the copies of a row are other lanes', complete after this
@@ -463,16 +466,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
               uint32_t r[16];
               tmem_ld16(from + x, r);
               tmem_wait_ld16(r);
-              // path position (relative to j0) and query head of the first column
-              int j = (i * cols + x) / a.group, g = (i * cols + x) - j * a.group;
+              const int* pos = position + qb * a.rows_cap + i * cols + x;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const float y = exp2f_ftz(fmaf(u2f(r[e]), sc, lse0[x + e]));
-                s0.x += i * cols + x + e < rows && key <= m - c + a.j0 + j ? y : 0.0f;
-                if (++g == a.group) {
-                  g = 0;
-                  ++j;
-                }
+                s0.x += key - (m - c + a.j0) <= pos[e] ? y : 0.0f;
               }
             }
           }
@@ -592,7 +590,7 @@ extern "C" rf_status rf_attn_weights(const rf_attn_desc* d, const rf_bf16* q, co
   // A second query buffer lets the next item's queries come in early; the ring keeps at
   // least five slabs (80 KB: more than the bytes in flight that hide memory's latency).
   auto fixed = [&](int bufs) {
-    return 1024 + static_cast<size_t>(bufs) * a.rows_cap * (hd * 2 + 4) + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
+    return 1024 + static_cast<size_t>(bufs) * a.rows_cap * (hd * 2 + 8) + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
            static_cast<size_t>(B) * 8;
   };
   constexpr size_t kMost = 227 * 1024;

@@ -25,6 +25,18 @@ __device__ __forceinline__ T uniform(T x) {
   return __shfl_sync(0xffffffffu, x, 0);
 }
 
+// First of share `i` of `shares` (at most 255) when `total` units are cut into equal shares; and a / b of
+// sizes that are small as a rule. 64-bit division takes a few hundred cycles, so it is kept for
+// what needs it.
+__device__ __forceinline__ long long share_start(long long total, int i, int shares) {
+  if (total < (1ll << 24)) return static_cast<unsigned>(total) * static_cast<unsigned>(i) / static_cast<unsigned>(shares);
+  return total * i / shares;
+}
+__device__ __forceinline__ long long quick_div(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
