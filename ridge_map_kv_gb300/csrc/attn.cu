@@ -9,12 +9,13 @@
 // about R = 275 (the ratio of the measured rates) the cache's bytes are the floor, above
 // it the two matrix products.
 //
-// Work split. A unit is one 128-key tile of one item (sequence, KV head, row tiles); the
-// units of all items are laid end to end and cut into equal shares, one per CTA and one
-// CTA per SM, whatever the lengths are (they are known on the device only). A CTA works
-// through at most a few segments of items; the rows of an item that was cut leave
-// unnormalised sums, maxima and totals in the workspace, and k_attn_combine joins them in
-// the order of the cuts.
+// Work split. The 128-key tiles of all items (sequence, KV head, row tiles) are laid end to
+// end and cut into equal shares, one per CTA and one CTA per SM, whatever the lengths are
+// (they are known on the device only). An item weighs four tiles more than it has: its
+// queries, first scores and epilogue take about that long, and a share of many short items
+// would finish last (16 trees over 912 to 16,384 rows: 156 us without, 134 with). The rows
+// of an item that was cut leave unnormalised sums, maxima and totals in the workspace, and
+// k_attn_combine joins them in the order of the cuts.
 //
 // Two streams per CTA, each with its own score tile S_s and accumulator O_s in TMEM and
 // its own four softmax warps, so that one stream's matrix products run while the other's
@@ -51,15 +52,23 @@ constexpr int kAtThreads = 384;
 constexpr int kAtRegsSoftmax = 208, kAtRegsOther = 88;
 static_assert(256 * kAtRegsSoftmax + 128 * kAtRegsOther <= kAtThreads * 168, "more registers than the launch has");
 constexpr int kAtFirst = 96;      // keys of the first part in which a tile's weights are handed over
+constexpr int kAtItemCost = 4;    // tiles that an item weighs beyond its own
 constexpr int kAtMaxCtas = 160;   // bounds the workspace
 constexpr int kAtMaxStages = 8;
 constexpr float kAtLog2e = 1.4426950408889634f;
 constexpr float kAtRescale = 8.0f;  // log2 of the growth of the maximum that is let pass
 
-// What a CTA's share starts with; also what k_attn_combine needs of it.
+// The first tiles of a CTA's share, for k_attn_combine.
 struct AttnPlan {
-  long long item;  // linear index, -1: no share
-  int b, h, mt, t0, n_tiles, len;  // len: rows in use of sequence b
+  long long item;  // linear index, -1: no tiles
+  int b, h, mt, t0;
+};
+// Where a share starts: `at` in the weight of item (b, h, mt), whose tiles come behind
+// kAtItemCost of it.
+struct AttnShare {
+  long long weight;  // of the share
+  int b, h, mt, at;
+  int len, n_tiles;  // rows in use of sequence b, tiles of the item
 };
 
 struct AttnArgs {
@@ -85,20 +94,22 @@ struct AttnArgs {
 struct AttnShared {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean, mma_done[2];
-  AttnPlan plan;
-  long long units;
-  float2 ml[2][2][kAtTile];  // [segment parity][stream][row]: maximum and total
+  AttnShare share;
   int bad[2];                // a drafted V row of the segment is not finite
   uint32_t tmem;
   int abort;
 };
 
+// With one row tile the streams exchange maxima and totals: [segment parity][stream][row].
+using AttnExchange = float2[2][2][kAtTile];
+
 template <int kHD, bool kDual>
 struct AttnCfg {
   static constexpr int kTileBytes = kAtTile * kHD * 2;
   static constexpr int kQBytes = (kDual ? 2 : 1) * kTileBytes;
-  static constexpr int kStages = kHD == 128 ? (kDual ? 4 : 5) : 8;
-  static constexpr size_t kSmem = 1024 + kQBytes + static_cast<size_t>(kStages) * kTileBytes + sizeof(AttnShared) + 64;
+  static constexpr int kStages = kHD == 128 ? 5 : 8;
+  static constexpr size_t kSmem =
+      1024 + kQBytes + static_cast<size_t>(kStages) * kTileBytes + sizeof(AttnShared) + (kDual ? 0 : sizeof(AttnExchange));
   static constexpr int kRows = (kDual ? 2 : 1) * kAtTile;  // of an item
 };
 
@@ -128,40 +139,49 @@ __device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt
 // converged warp.
 template <bool kDual, bool kWarp>
 struct Walk {
-  int b, h, mt, t0, t1;
-  long long left;
+  int b, h, mt, t0, t1;  // an item and the tiles of it that are the share's
+  int at;                // where the share stands in the item's weight
+  long long left;        // weight
   ItemShape shape;
   template <class T>
   static __device__ __forceinline__ T same(T x) {
     if constexpr (kWarp) return uniform(x);
     else return x;
   }
-  __device__ __forceinline__ void look(const AttnArgs& a) {
-    shape = item_shape<kDual>(a, b, mt);
-    shape.len = same(shape.len);
-    shape.cached = same(shape.cached);
-    shape.tiles = same(shape.tiles);
-  }
   __device__ __forceinline__ Walk(const AttnArgs& a, const AttnShared* sh) {
-    b = same(sh->plan.b);
-    h = same(sh->plan.h);
-    mt = same(sh->plan.mt);
-    t0 = same(sh->plan.t0);
-    left = same(sh->units);
-    shape = ItemShape{0, 0, 0};
-    t1 = 0;
-    if (left > 0) {
-      shape.len = same(sh->plan.len);
-      shape.cached = (shape.len + kAtTile - 1) / kAtTile;
-      shape.tiles = same(sh->plan.n_tiles);
-      t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), t0 + left));
-    }
+    b = same(sh->share.b);
+    h = same(sh->share.h);
+    mt = same(sh->share.mt);
+    at = same(sh->share.at);
+    left = same(sh->share.weight);
+    shape.len = same(sh->share.len);
+    shape.cached = (shape.len + kAtTile - 1) / kAtTile;
+    shape.tiles = same(sh->share.n_tiles);
+    t0 = t1 = 0;
+    if (left > 0) settle(a);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ int end() const {
+    return static_cast<int>(min(static_cast<long long>(shape.tiles + kAtItemCost), at + left));
+  }
+  // The first tiles from here on (a share may end within an item's extra weight).
+  __device__ __forceinline__ void settle(const AttnArgs& a) {
+    while (true) {
+      t0 = max(at - kAtItemCost, 0);
+      t1 = max(end() - kAtItemCost, 0);
+      if (t1 > t0) return;
+      next_item(a);
+      if (left <= 0) return;
+    }
+  }
   __device__ __forceinline__ void next(const AttnArgs& a) {
-    left -= t1 - t0;
+    next_item(a);
+    if (left > 0) settle(a);
+  }
+  __device__ __forceinline__ void next_item(const AttnArgs& a) {
+    left -= end() - at;
     if (left <= 0) return;
-    t0 = 0;
+    at = 0;
     do {
       if (++mt == a.m_items) {
         mt = 0;
@@ -173,42 +193,43 @@ struct Walk {
           }
         }
       }
-      look(a);
+      shape = item_shape<kDual>(a, b, mt);
+      shape.len = same(shape.len);
+      shape.cached = same(shape.cached);
+      shape.tiles = same(shape.tiles);
     } while (shape.tiles == 0);
-    t1 = static_cast<int>(min(static_cast<long long>(shape.tiles), left));
   }
 };
 
-// The start of share `cta` of `ctas`: one warp sums the sequences' units, then finds the
-// sequence, head, item and tile of its first unit. Writes the share to shared memory, and
+// The start of share `cta` of `ctas`: one warp sums the sequences' weights, then finds the
+// sequence, head, item and place of its first one. Writes the share to shared memory, and
 // to `plan` what k_attn_combine needs.
 template <bool kDual>
 __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
-  auto units_of = [&](int len) -> long long {
+  auto weight_of = [&](int len) -> long long {
     return len < 0 ? 0ll
                    : static_cast<long long>(a.heads) *
-                         (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile) + a.draft_sum);
+                         (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile + kAtItemCost) + a.draft_sum);
   };
   long long total = 0;
   int len = -1;  // of sequence `lane`, then of later ones
   for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
     len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
     if (len < 0 && b0 + lane < a.n_seqs) record_status(a.dev_status, RF_ERR_INVALID_ARG);
-    total += units_of(len);
+    total += weight_of(len);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const long long shares = min(static_cast<long long>(ctas), total);
-  AttnPlan p{-1, 0, 0, 0, 0, 0, 0};
-  long long units = 0;
+  AttnShare p{};
   if (cta < shares) {
     const long long first = share_start(total, cta, static_cast<int>(shares));
-    units = share_start(total, cta + 1, static_cast<int>(shares)) - first;
+    p.weight = share_start(total, cta + 1, static_cast<int>(shares)) - first;
     long long base = 0;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
       if (a.n_seqs > 32) len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
-      const long long own = units_of(len);
+      const long long own = weight_of(len);
       long long x = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -228,26 +249,25 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
         p.mt = 0;
         p.n_tiles = cached + draft_tiles<kDual>(a, 0);
         if (a.mask != nullptr) {
-          p.mt = static_cast<int>(quick_div(r, p.n_tiles));
-          r -= static_cast<long long>(p.mt) * p.n_tiles;
+          p.mt = static_cast<int>(quick_div(r, p.n_tiles + kAtItemCost));
+          r -= static_cast<long long>(p.mt) * (p.n_tiles + kAtItemCost);
         } else {
-          while (r >= p.n_tiles) {
-            r -= p.n_tiles;
+          while (r >= p.n_tiles + kAtItemCost) {
+            r -= p.n_tiles + kAtItemCost;
             p.n_tiles = cached + draft_tiles<kDual>(a, ++p.mt);
           }
         }
-        p.t0 = static_cast<int>(r);
-        p.item = (static_cast<long long>(p.b) * a.heads + p.h) * a.m_items + p.mt;
+        p.at = static_cast<int>(r);
         break;
       }
       base += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  if (lane == 0) {
-    sh->plan = p;
-    sh->units = units;
-    a.plan[cta] = p;
-  }
+  if (lane == 0) sh->share = p;
+  __syncwarp();
+  const Walk<kDual, true> w(a, sh);
+  if (lane == 0)
+    a.plan[cta] = AttnPlan{w.more() ? (static_cast<long long>(w.b) * a.heads + w.h) * a.m_items + w.mt : -1ll, w.b, w.h, w.mt, w.t0};
 }
 
 // A row's 128 scores, from `ts`, and their maximum; keys that are not seen (kMasked) become
@@ -337,6 +357,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   AttnShared* sh = reinterpret_cast<AttnShared*>(smem + Cfg::kQBytes + Cfg::kStages * Cfg::kTileBytes);
+  AttnExchange& ml = *reinterpret_cast<AttnExchange*>(sh + 1);  // (one row tile)
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + Cfg::kQBytes;
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
@@ -386,20 +407,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
 
   if (warp == 8) {
     regs_dec<kAtRegsOther>();
-    if (lane == 0) {
+    {  // the whole warp waits, one lane issues
+      const auto wait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, timeout)) != 0; };
       int stage = 0;
       uint32_t phase = 0, q_phase = 0;
       long long issued = 0;
       bool ok = true, q_inflight = false;
-      auto load = [&](const Walk<kDual, false>& w, int t, bool v) {
-        if (!mbar_wait(&sh->empty[stage], phase ^ 1u, abort_flag, timeout)) return false;
-        mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
+      auto load = [&](const Walk<kDual, true>& w, int t, bool v) {
+        if (!wait(&sh->empty[stage], phase ^ 1u)) return false;
         const bool draft = t >= w.shape.cached;
         const CUtensorMap* tm = draft ? (v ? &a.tm_vd : &a.tm_kd) : (v ? &a.tm_v : &a.tm_k);
         const int row = (draft ? t - w.shape.cached : t) * kAtTile;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, w.b);
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, w.b);
+        }
+        __syncwarp();
         ++issued;
         if (++stage == Cfg::kStages) {
           stage = 0;
@@ -407,15 +432,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         return true;
       };
-      for (Walk<kDual, false> w(a, sh); w.more() && ok; w.next(a)) {
-        if (!mbar_wait(&sh->q_empty, q_phase ^ 1u, abort_flag, timeout)) break;
-        mbar_arrive_expect_tx(&sh->q_full, (kDual ? 2 : 1) * kChunks * 64 * 2 * a.group * a.npt);
+      for (Walk<kDual, true> w(a, sh); w.more() && ok; w.next(a)) {
+        if (!wait(&sh->q_empty, q_phase ^ 1u)) break;
         q_inflight = true;
-        for (int s = 0; s < (kDual ? 2 : 1); ++s)
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh->q_full, (kDual ? 2 : 1) * kChunks * 64 * 2 * a.group * a.npt);
+          for (int s = 0; s < (kDual ? 2 : 1); ++s)
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, &a.tm_q, smem_u32(&sh->q_full), c * 64, w.h * a.group,
-                        (w.mt * (kDual ? 2 : 1) + s) * a.npt, w.b);
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, &a.tm_q, smem_u32(&sh->q_full), c * 64, w.h * a.group,
+                          (w.mt * (kDual ? 2 : 1) + s) * a.npt, w.b);
+        }
+        __syncwarp();
         q_phase ^= 1u;
         // the order in which warp 9 takes them
         if (kDual) {
@@ -694,7 +722,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       }
       // Epilogue.
       if (!kDual) {
-        sh->ml[seg & 1][s][row] = make_float2(m, l);
+        ml[seg & 1][s][row] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ml_full);
         if (!__all_sync(0xffffffffu, mbar_wait(&sh->ml_full, f_phase, abort_flag, timeout))) goto softmax_done;
@@ -706,7 +734,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         // stream sums to join (one row tile): this warp takes half of the channels of both
         float f0 = 1.0f, f1 = 0.0f;
         if (!kDual) {
-          const float2 u = sh->ml[seg & 1][0][row], v = sh->ml[seg & 1][1][row];
+          const float2 u = ml[seg & 1][0][row], v = ml[seg & 1][1][row];
           m = fmaxf(u.x, v.x);
           f0 = u.x == -INFINITY ? 0.0f : exp2f_ftz((u.x - m) * sc);
           f1 = v.x == -INFINITY ? 0.0f : exp2f_ftz((v.x - m) * sc);
@@ -1028,7 +1056,8 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   }
   if (draft_sum >= (int64_t(1) << 31)) return fail(RF_ERR_SHAPE, "n_nodes is too large");
   a.draft_sum = static_cast<int>(draft_sum);
-  const int64_t most = static_cast<int64_t>(B * H) * (a.m_items * static_cast<int64_t>((cap + kAtTile - 1) / kAtTile) + draft_sum);
+  // no more CTAs than weight, which is at least the tiles
+  const int64_t most = static_cast<int64_t>(B * H) * (a.m_items * static_cast<int64_t>((cap + kAtTile - 1) / kAtTile + kAtItemCost) + draft_sum);
   const int ctas = static_cast<int>(std::min<int64_t>(most, std::min(sms, kAtMaxCtas)));
   if (hd == 128) st = lay.tiles == 2 ? launch_attn<128, true>(a, ctas, s) : launch_attn<128, false>(a, ctas, s);
   else st = lay.tiles == 2 ? launch_attn<64, true>(a, ctas, s) : launch_attn<64, false>(a, ctas, s);
