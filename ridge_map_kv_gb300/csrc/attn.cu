@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
 
   if (warp == 8) {
     regs_dec<kAtRegsOther>();
-    {  // the whole warp waits, one lane issues
+    {  // the whole warp waits, one lane issues: a lane's wait by itself takes twice as long
       const auto wait = [&](uint64_t* bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_wait(bar, par, abort_flag, timeout)) != 0; };
       int stage = 0;
       uint32_t phase = 0, q_phase = 0;
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
 
 // Joins the rows of items that were cut. Block (x, y): the cut before share x + 1, rows
 // 32 y .. 32 y + 31 of its item; the first cut inside an item answers for it. A lane is a
-// row, a warp 16 channels of it. Launched as a dependent of k_attn: its CTAs wait in place
+// row (or part of one), a warp 16 channels of it. Launched as a dependent of k_attn: its CTAs wait in place
 // for that one's end.
 struct CombineArgs {
   const AttnPlan* plan;
@@ -840,9 +840,12 @@ struct CombineArgs {
   float scale;
 };
 
-// kBatch: parts in flight together. Few rows (of few items, cut into many parts): 8; else 4, so
-// that more CTAs fit an SM.
-template <int kHD, int kBatch>
+// kBatch: parts in flight together; kSplit: lanes that share a row, each joining every kSplit-th
+// part. Few rows of few items, cut into 8 parts or more: 8 and 4, so that one round of loads
+// holds up to 32 parts. Else 4 and 1: more rows a CTA, more CTAs an SM. The whole call, one way
+// and the other: 25 rows in 19 parts 34.6 and 38.4 us, 20 rows in 2.4 parts 40.4 and 39.3,
+// 125 rows in 19 parts 24.0 and 21.8.
+template <int kHD, int kBatch, int kSplit>
 __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant__ CombineArgs a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -864,21 +867,23 @@ __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant_
     parts += m == 0xffffffffu ? 32 : __ffs(~m) - 1;
   }
   const int item_rows = a.tiles * kAtTile;
-  const int r = blockIdx.y * 32 + lane, in_tile = r % kAtTile;
+  constexpr int kLanes = 32 / kSplit;
+  const int r = blockIdx.y * kLanes + lane % kLanes, in_tile = r % kAtTile;
   const int node = (mt * a.tiles + r / kAtTile) * a.npt + in_tile / a.group;
-  if (r >= item_rows || in_tile >= a.npt * a.group || node >= a.n) return;
+  const bool live = r < item_rows && in_tile < a.npt * a.group && node < a.n;
+  if (kSplit == 1 && !live) return;
   const int head = h * a.group + in_tile % a.group;
   const float sc = a.scale * kAtLog2e;
   auto slot_of = [&](int i) { return i == 0 ? 2LL * (c - 1) + 1 : 2LL * (c - 1 + i); };
   float m = -INFINITY, l = 0.0f;
   float4 x[4] = {};
-  for (int i0 = 0; i0 < parts; i0 += kBatch) {
+  for (int i0 = live ? lane / kLanes : parts; i0 < parts; i0 += kBatch * kSplit) {
     float2 ml[kBatch];
     float4 v[kBatch][4];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (i0 + j >= parts) break;
-      const long long slot = slot_of(i0 + j);
+      if (i0 + j * kSplit >= parts) break;
+      const long long slot = slot_of(i0 + j * kSplit);
       ml[j] = a.part_ml[slot * item_rows + r];
       const float4* src = a.part_o + (slot * (kHD / 4) + warp * 4) * item_rows + r;
 #pragma unroll
@@ -886,7 +891,7 @@ __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant_
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (i0 + j >= parts) break;
+      if (i0 + j * kSplit >= parts) break;
       // a running maximum: one pass over the parts
       const float mx = fmaxf(m, ml[j].x);
       const float f = m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc);
@@ -901,6 +906,25 @@ __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant_
         x[e].w = x[e].w * f + v[j][e].w * g;
       }
     }
+  }
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) {
+      const float m1 = __shfl_xor_sync(0xffffffffu, m, o), l1 = __shfl_xor_sync(0xffffffffu, l, o);
+      const float mx = fmaxf(m, m1);
+      const float f = m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc);
+      const float g = m1 == -INFINITY ? 0.0f : exp2f_ftz((m1 - mx) * sc);
+      m = mx;
+      l = l * f + l1 * g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e].x = x[e].x * f + __shfl_xor_sync(0xffffffffu, x[e].x, o) * g;
+        x[e].y = x[e].y * f + __shfl_xor_sync(0xffffffffu, x[e].y, o) * g;
+        x[e].z = x[e].z * f + __shfl_xor_sync(0xffffffffu, x[e].z, o) * g;
+        x[e].w = x[e].w * f + __shfl_xor_sync(0xffffffffu, x[e].w, o) * g;
+      }
+    }
+    if (!live || lane >= kLanes) return;
   }
   if (m == INFINITY) l = NAN;  // inf - inf
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -1080,10 +1104,11 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   // rows of an item that exist, in a tile's numbering (the first tile's are followed by a gap)
   const int tile_rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, a.npt * group));
   const int rows = lay.tiles == 2 ? 2 * kAtTile : tile_rows;
-  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + 31) / 32));
+  const bool few = rows <= 32 && B * H * a.m_items * 8 <= ctas;
+  const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + (few ? 7 : 31)) / (few ? 8 : 32)));
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
-  void (*combine)(CombineArgs) = hd == 128 ? (rows <= 32 ? k_attn_combine<128, 8> : k_attn_combine<128, 4>)
-                                           : (rows <= 32 ? k_attn_combine<64, 8> : k_attn_combine<64, 4>);
+  void (*combine)(CombineArgs) = hd == 128 ? (few ? k_attn_combine<128, 8, 4> : k_attn_combine<128, 4, 1>)
+                                           : (few ? k_attn_combine<64, 8, 4> : k_attn_combine<64, 4, 1>);
   return cuda_check(launch_dependent(combine, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, 1, c),
                     "k_attn_combine launch");
 }
