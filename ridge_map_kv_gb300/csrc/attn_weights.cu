@@ -23,8 +23,9 @@
 //                    second, and the halves meet in shared memory
 //   warp 8           TMA: key tiles, in 64-channel slabs
 //   warp 9           MMA
-//   warps 10-13      the queries of the next (sequence, head), gathered along the path into
-//                    the other of two buffers (or, where two do not fit, once the one is free)
+//   warps 10-13      the queries of the next (sequence, head), into the other of two buffers
+//                    (or, where two do not fit, once the one is free): all nodes of a sequence
+//                    as one TMA box a slab, those of a path gathered row by row
 #include <algorithm>
 #include <cmath>
 
@@ -45,7 +46,7 @@ constexpr int kWtNever = INT32_MIN;       // position of a column that no key is
 constexpr float kWtLog2e = 1.4426950408889634f;
 
 struct WeightArgs {
-  CUtensorMap tm_k;
+  CUtensorMap tm_k, tm_q;  // tm_q: boxes of j_max nodes, if box
   const __nv_bfloat16* q;
   const float* lse;
   const int32_t* path;
@@ -58,6 +59,7 @@ struct WeightArgs {
   long long q_row, q_seq;
   int n_seqs, heads, group, n, capacity;
   int j0, j_max;   // this launch takes path positions j0 .. j0 + j_max - 1
+  bool box;        // queries come as boxes
   int rows_cap;    // query rows of one buffer (a multiple of 16)
   int bufs;        // query buffers: 2 where that leaves the ring its stages, else 1
   int stages;
@@ -66,7 +68,7 @@ struct WeightArgs {
 
 struct WeightShared {
   uint64_t full[kWtMaxStages], empty[kWtMaxStages];
-  uint64_t q_full[2], q_empty[2], t_full[2], t_empty[2], half_full[4], mma_done;
+  uint64_t q_full[2], q_empty[2], q_box[2], t_full[2], t_empty[2], half_full[4], mma_done;
   float half[4][kWtTile];  // the second warps' sums
   int b, h, t;             // first unit of the share
   long long units;
@@ -161,6 +163,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->q_full[i], kWtLoaders);
       mbar_init(&sh->q_empty[i], 9);
+      mbar_init(&sh->q_box[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->t_full[i], 1);
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
     fence_mbar_init();
   }
   if (warp == 8 && lane == 0) tma_prefetch_desc(&a.tm_k);
+  if (warp == 10 && lane == 0 && a.box) tma_prefetch_desc(&a.tm_q);
   if (warp == 9) {
     tmem_alloc(&sh->tmem, 512);
     tmem_relinquish();
@@ -331,6 +335,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
       if (!__all_sync(0xffffffffu, mbar_wait(&sh->q_empty[qb], par, abort_flag, timeout))) break;
       const int rows = w.rows(a), cols = weight_cols(rows) * weight_steps(rows);
       const uint32_t q0 = s_q + qb * kSlabs * q_slab;
+      const int boxed = a.box ? a.j_max * a.group : 0;  // rows that a box brings
+      if (a.box) {
+        if (warp == 10 && lane == 0) {
+          mbar_arrive_expect_tx(&sh->q_box[qb], kSlabs * boxed * 128);
+#pragma unroll
+          for (int c = 0; c < kSlabs; ++c) tma_load_4d(q0 + c * q_slab, &a.tm_q, smem_u32(&sh->q_box[qb]), c * 64, w.h * a.group, a.j0, w.b);
+        }
+        __syncwarp();
+      }
       // Row of the lane in each group: its statistic, and its query's address (0: a row beyond the
       // queries, to be filled with zeros).
       float stat[kGroups];
@@ -353,6 +366,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
       for (int g = 0; g < kGroups; ++g) {
         const int r0 = w0 + g * kWtLoaders;
         if (r0 >= cols) break;
+        if (r0 + kWtLoaders / 4 <= boxed) continue;
         unsigned long long from[kPieces];  // all shuffles before the first copy, which none would pass
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) from[i] = __shfl_sync(0xffffffffu, row_at[g], i * kRowsAtOnce + lane / kPieces);
@@ -360,7 +374,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
         for (int i = 0; i < kPieces; ++i) {
           const int rr = r0 + i * kRowsAtOnce + lane / kPieces;
           const uint32_t dst = q0 + (pc / 8) * q_slab + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4);
-          if (rr < cols)
+          if (rr >= boxed && rr < cols)
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                          "l"((from[i] != 0ull ? from[i] : reinterpret_cast<unsigned long long>(a.q)) + pc * 16ull),
                          "r"(from[i] != 0ull ? 16 : 0)
@@ -380,6 +394,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (a.box && !__all_sync(0xffffffffu, mbar_wait(&sh->q_box[qb], par ^ 1u, abort_flag, timeout))) {
+        int dummy = 0;  // the box lands before the CTA may exit
+        mbar_wait(&sh->q_box[qb], par ^ 1u, &dummy, timeout);
+        break;
+      }
       if (__any_sync(0xffffffffu, empty != 0u)) {  // the copies of a row are other lanes', complete after this
         __syncwarp();
 #pragma unroll
@@ -583,6 +602,12 @@ extern "C" rf_status rf_attn_weights(const rf_attn_desc* d, const rf_bf16* q, co
   // As many path positions a launch as their query rows fit in shared memory.
   const int64_t most = kWtQBytes / (2 * static_cast<int64_t>(hd));
   a.j_max = static_cast<int>(std::min<int64_t>(d->n_nodes, std::max<int64_t>(most / a.group, 1)));
+  // A box holds up to 256 nodes (fewer query heads a KV head than three: gathered).
+  a.box = path == nullptr && a.j_max <= 256;
+  if (a.box && (st = make_tmap_bf16_4d(&a.tm_q, q, {hd, (uint64_t)d->n_q_heads, (uint64_t)d->n_nodes, B},
+                                       {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
+                                       {64, (uint32_t)a.group, (uint32_t)a.j_max, 1})) != RF_OK)
+    return st;
   // Steps round a launch's rows up by at most 16 columns each.
   const int rows = a.j_max * a.group;
   const int steps = std::max(1, (rows + kWtStep - 1) / kWtStep);
