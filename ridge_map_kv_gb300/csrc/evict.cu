@@ -18,7 +18,8 @@
 //                   for 16,384 rows.) Ranks among equals and the places of
 //                   holes and movers come from ballots. It also writes the scores and
 //                   positions of the rows that stay in place.
-//   k_evict_move    the listed rows of K and V, their scores and positions.
+//   k_evict_move    the listed rows of K and V, their scores and positions. (No launch of its
+//                   own where the capacity leaves a unit 128 moves at most.)
 //
 // Bound: reading scores and positions and writing the kept ones (16 bytes a row) and the
 // moved rows' bytes twice; at a few rows a step, the latency of the selection.
@@ -29,7 +30,8 @@
 
 namespace rf {
 
-constexpr int kMoveRows = 64;                // moves of one CTA of k_evict_move
+constexpr int kMoveRows = 64;    // moves of one CTA of k_evict_move
+constexpr int kOwnMoves = 128;   // at most: k_evict_select moves the rows itself
 
 struct EvictArgs {
   const int32_t* lens;
@@ -46,6 +48,7 @@ struct EvictArgs {
   int32_t* dev_status;
   long long row_stride, seq_stride, layer_stride, max_moves;
   int n_seqs, heads, head_dim, capacity, keep, sink, recent;
+  bool moves_too;  // k_evict_select also moves the rows and writes new_lens
 };
 
 // Order-preserving integer of a rank: larger scores give larger keys, -0 equals 0, NaN
@@ -64,6 +67,7 @@ struct SelShared {
   int count[2][kThreads / 32];  // by the parity of the step
   int warp_a[kThreads / 32];
   int warp_b[kThreads / 32];
+  int n_moves;
 };
 
 // Exclusive scan over the CTA's warps of one value per warp, in shared memory.
@@ -81,6 +85,34 @@ __device__ __forceinline__ void scan_warps(int* v) {
     if (threadIdx.x < kThreads / 32) v[threadIdx.x] = x - own;
   }
   __syncthreads();
+}
+
+__device__ __forceinline__ int32_t length_after(const EvictArgs& a, int len) {
+  return len > a.keep && len <= a.capacity ? a.keep : len;
+}
+
+// Moves i0 .. i0 + m - 1 of a unit's list, by the whole CTA.
+template <int kThreads>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int unit, int i0, int m) {
+  const int h = unit % a.heads, lb = unit / a.heads, b = lb % a.n_seqs, l = lb / a.n_seqs;
+  const int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves + i0;
+  const int32_t* src = dst + a.max_moves;
+  const long long head = l * a.layer_stride + b * a.seq_stride + static_cast<long long>(h) * a.head_dim;
+  const int pieces = a.head_dim / 8;
+#pragma unroll 4
+  for (int x = threadIdx.x; x < m * pieces; x += kThreads) {
+    const int i = x / pieces, c = (x - i * pieces) * 8;
+    const long long from = head + static_cast<long long>(src[i]) * a.row_stride + c;
+    const long long to = head + static_cast<long long>(dst[i]) * a.row_stride + c;
+    const uint4 k = *reinterpret_cast<const uint4*>(a.k + from), v = *reinterpret_cast<const uint4*>(a.v + from);
+    *reinterpret_cast<uint4*>(a.k + to) = k;
+    *reinterpret_cast<uint4*>(a.v + to) = v;
+  }
+  const long long base = static_cast<long long>(unit) * a.capacity;
+  for (int i = threadIdx.x; i < m; i += kThreads) {
+    a.score_out[base + dst[i]] = a.score_in[base + src[i]];
+    a.pos_out[base + dst[i]] = a.pos_in[base + src[i]];
+  }
 }
 
 // Rows are taken in groups of 32, one a lane: warp w owns the groups from w * per_warp on,
@@ -102,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
   const long long base = static_cast<long long>(unit) * a.capacity;
   const float* score = a.score_in + base;
   const int32_t* pos = a.pos_in + base;
+  if (a.moves_too && tid == 0 && unit % a.heads == 0 && unit / a.heads < a.n_seqs) a.new_lens[b] = length_after(a, len);
   if (len < 0 || len > a.capacity) {
     if (tid == 0) {
       a.n_moves[unit] = 0;
@@ -303,7 +336,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
   scan_warps<kThreads>(sh.warp_a);
   scan_warps<kThreads>(sh.warp_b);
   int hole = sh.warp_a[warp], mover = sh.warp_b[warp];
-  if (warp == kWarps - 1 && lane == 0) a.n_moves[unit] = mover + movers;  // as many holes as movers
+  if (warp == kWarps - 1 && lane == 0) {
+    a.n_moves[unit] = mover + movers;  // as many holes as movers
+    sh.n_moves = mover + movers;
+  }
   int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves;
   int32_t* src = dst + a.max_moves;
   eq = eq0;
@@ -345,6 +381,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
       copy_rows(g * 32, in_place);
     }
   });
+  if (a.moves_too) {
+    __syncthreads();
+    move_rows<kThreads>(a, unit, 0, sh.n_moves);
+  }
 }
 
 __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ EvictArgs a) {
@@ -353,32 +393,10 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
   const int n = a.n_moves[unit];
   const int i0 = blockIdx.x * kMoveRows;
   if (unit == 0 && i0 == 0) {  // new_lens may be lens, which k_evict_select has read
-    for (int b = threadIdx.x; b < a.n_seqs; b += 256) {
-      const int len = a.lens[b];
-      a.new_lens[b] = len > a.keep && len <= a.capacity ? a.keep : len;
-    }
+    for (int b = threadIdx.x; b < a.n_seqs; b += 256) a.new_lens[b] = length_after(a, a.lens[b]);
   }
   const int m = min(n - i0, kMoveRows);
-  if (m <= 0) return;
-  const int h = unit % a.heads, lb = unit / a.heads, b = lb % a.n_seqs, l = lb / a.n_seqs;
-  const int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves + i0;
-  const int32_t* src = dst + a.max_moves;
-  const long long head = l * a.layer_stride + b * a.seq_stride + static_cast<long long>(h) * a.head_dim;
-  const int pieces = a.head_dim / 8;
-#pragma unroll 4
-  for (int x = threadIdx.x; x < m * pieces; x += 256) {
-    const int i = x / pieces, c = (x - i * pieces) * 8;
-    const long long from = head + static_cast<long long>(src[i]) * a.row_stride + c;
-    const long long to = head + static_cast<long long>(dst[i]) * a.row_stride + c;
-    const uint4 k = *reinterpret_cast<const uint4*>(a.k + from), v = *reinterpret_cast<const uint4*>(a.v + from);
-    *reinterpret_cast<uint4*>(a.k + to) = k;
-    *reinterpret_cast<uint4*>(a.v + to) = v;
-  }
-  const long long base = static_cast<long long>(unit) * a.capacity;
-  for (int i = threadIdx.x; i < m; i += 256) {
-    a.score_out[base + dst[i]] = a.score_in[base + src[i]];
-    a.pos_out[base + dst[i]] = a.pos_in[base + src[i]];
-  }
+  if (m > 0) move_rows<256>(a, unit, i0, m);
 }
 
 rf_status check_cache_desc(const rf_cache_desc* d) {
@@ -484,6 +502,12 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
   a.keep = static_cast<int>(std::min(keep, d->capacity));
   a.sink = static_cast<int>(n_sink);
   a.recent = static_cast<int>(n_recent);
+  // One launch where few rows can move, so that a unit's CTA moves them by itself (320 units of
+  // 4,096 rows, 64 moves each: 13.2 us, 15.0 in two launches; 128: 14.7 and 15.7; one layer's 8
+  // units of 2,000 rows, 64: 9.8 and 10.4; 256: 12.3 and 11.0); not where new_lens is written
+  // over lens, which every CTA reads.
+  const bool lens_apart = new_lens + d->n_seqs <= lens || lens + d->n_seqs <= new_lens;
+  a.moves_too = lens_apart && lay.max_moves <= kOwnMoves;
   const unsigned units = static_cast<unsigned>(d->n_layers * d->n_seqs * d->n_kv_heads);
   {
     ProfScope prof(s, RF_STAGE_EVICT_SELECT);
@@ -510,6 +534,7 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
     }
     if ((st = cuda_check(e, "k_evict_select launch")) != RF_OK) return st;
   }
+  if (a.moves_too) return RF_OK;
   ProfScope prof(s, RF_STAGE_EVICT_MOVE);
   const unsigned chunks = static_cast<unsigned>(std::max<int64_t>((lay.max_moves + kMoveRows - 1) / kMoveRows, 1));
   return cuda_check(launch_dependent(k_evict_move, dim3(chunks, units), dim3(256), 0, s, 1, a), "k_evict_move launch");

@@ -157,3 +157,31 @@ def test_evict_over_rounds_keeps_the_heavy_rows_and_their_positions():
             assert torch.equal(k[:m, h * hd].float(), pos[h, :m].to(torch.bfloat16).float())
             assert torch.equal(v[:m, h * hd].float(), -pos[h, :m].to(torch.bfloat16).float())
             assert torch.equal(score[h, :m], weight[h][pos[h, :m].long()])
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties"])
+@pytest.mark.parametrize("cap,keep", [(20, 19), (640, 513), (641, 513), (642, 513), (4224, 4096), (9000, 8901)])
+def test_evict_gives_the_same_wherever_lengths_and_scores_go(cap, keep, kind):
+    """New lengths over the old ones or apart, scores in place or apart: the same rows move, bit for bit."""
+    L, B, H, hd, W = 2, 2, 2, 16, 32
+    lens = [cap, (cap + keep) // 2]
+    d = rf.rf_cache_desc(n_layers=L, n_seqs=B, n_kv_heads=H, head_dim=hd, capacity=cap, row_stride=W, seq_stride=cap * W,
+                         layer_stride=B * cap * W)
+    wsb = rf.rf_evict_workspace_bytes(d, keep)
+    results = []
+    for lens_apart in (False, True):
+        for scores_apart in (False, True):
+            k, v = R.randn((L, B, cap, W), 1), R.randn((L, B, cap, W), 2)
+            score = _scores((L, B, H, cap), kind, 3)
+            pos = torch.arange(cap, dtype=torch.int32, device=DEV).expand(L, B, H, cap).contiguous()
+            so, po = (score.clone(), pos.clone()) if scores_apart else (score, pos)
+            ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+            nx, nl = ln.clone(), torch.zeros_like(ln) if lens_apart else ln
+            ws = torch.full((wsb,), 0xA5, dtype=torch.uint8, device=DEV)
+            st = torch.zeros(1, dtype=torch.int32, device=DEV)
+            rf.rf_evict(d, keep, 4, 8, ln, nx, k, v, score, pos, so, po, nl, st, ws, wsb)
+            torch.cuda.synchronize()
+            assert int(st.item()) == 0 and nl.tolist() == [min(n, keep) for n in lens]
+            results.append((k, v, so[..., :keep], po[..., :keep]))
+    for r in results[1:]:
+        assert all(_same(x, y) for x, y in zip(r, results[0]))
