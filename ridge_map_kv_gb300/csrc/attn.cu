@@ -13,7 +13,7 @@
 // end and cut into equal shares, one per CTA and one CTA per SM, whatever the lengths are
 // (they are known on the device only). An item weighs four tiles more than it has: its
 // queries, first scores and epilogue take about that long, and a share of many short items
-// would finish last (16 trees over 912 to 16,384 rows: 156 us without, 134 with). The rows
+// would finish last (16 trees over 913 to 16,384 rows: 156 us without, 134 with). The rows
 // of an item that was cut leave unnormalised sums, maxima and totals in the workspace, and
 // k_attn_combine joins them in the order of the cuts.
 //
@@ -30,13 +30,21 @@
 //                    a factor 2^8 (weights stay below 2^8 of the reference, which fp32
 //                    sums and bf16 weights hold without loss), so rarely after the first
 //                    tiles.
-//   (warps 10, 11)   fill the third warpgroup, which gives registers to the first two
 //   warp 8           TMA: query tiles, then K and V tiles through one ring
-//   warp 9           MMA: S_s = Q K^T, O_s += P_s V (P_s from TMEM). It also clears what
+//   warp 9           MMA: S_s = Q K^T, O_s += P_s V (P_s from TMEM); with two row tiles warp 10
+//                    issues the second one's, in turns with it. It also clears what
 //                    the second product must not see: V rows beyond a sequence's length
 //                    (any bits; their weights are 0, but 0 x NaN is NaN), and elements of
 //                    drafted V rows that are not finite. Rows that do see such an element
 //                    get it in the epilogue.
+//   warp 11          fills the third warpgroup, which gives registers to the first two
+//
+// Measured (128 channels): one token, 40 query heads on 8, over 32,767 rows: 33 us, 4.1 TB/s of
+// the cache's bytes (22 us of it in the tiles). 16 trees of 64 nodes, 32 heads on 8, over 913 to
+// 16,384 rows: 132 us, 4.7 TB/s and 1,150 TFLOP/s. 4,096 rows in order over 28,672, 40 heads on
+// 8: 1.86 ms, 1,390 TFLOP/s, 0.74 of the measured burst rate: a tile's chain of product, softmax
+// (about 1,100 cycles), product and three hand-overs (about 105 each) is longer than the
+// 2 x 1,028 cycles of products that the two streams have between them.
 #include <algorithm>
 #include <cmath>
 
@@ -135,28 +143,22 @@ __device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt
   return s;
 }
 
-// A CTA's share, segment by segment; every role walks it alike, a thread alone or (kWarp) a
-// converged warp.
-template <bool kDual, bool kWarp>
+// A CTA's share, segment by segment; every role walks it alike, a converged warp at a time.
+template <bool kDual>
 struct Walk {
   int b, h, mt, t0, t1;  // an item and the tiles of it that are the share's
   int at;                // where the share stands in the item's weight
   long long left;        // weight
   ItemShape shape;
-  template <class T>
-  static __device__ __forceinline__ T same(T x) {
-    if constexpr (kWarp) return uniform(x);
-    else return x;
-  }
   __device__ __forceinline__ Walk(const AttnArgs& a, const AttnShared* sh) {
-    b = same(sh->share.b);
-    h = same(sh->share.h);
-    mt = same(sh->share.mt);
-    at = same(sh->share.at);
-    left = same(sh->share.weight);
-    shape.len = same(sh->share.len);
+    b = uniform(sh->share.b);
+    h = uniform(sh->share.h);
+    mt = uniform(sh->share.mt);
+    at = uniform(sh->share.at);
+    left = uniform(sh->share.weight);
+    shape.len = uniform(sh->share.len);
     shape.cached = (shape.len + kAtTile - 1) / kAtTile;
-    shape.tiles = same(sh->share.n_tiles);
+    shape.tiles = uniform(sh->share.n_tiles);
     t0 = t1 = 0;
     if (left > 0) settle(a);
   }
@@ -194,9 +196,9 @@ struct Walk {
         }
       }
       shape = item_shape<kDual>(a, b, mt);
-      shape.len = same(shape.len);
-      shape.cached = same(shape.cached);
-      shape.tiles = same(shape.tiles);
+      shape.len = uniform(shape.len);
+      shape.cached = uniform(shape.cached);
+      shape.tiles = uniform(shape.tiles);
     } while (shape.tiles == 0);
   }
 };
@@ -265,7 +267,7 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
   }
   if (lane == 0) sh->share = p;
   __syncwarp();
-  const Walk<kDual, true> w(a, sh);
+  const Walk<kDual> w(a, sh);
   if (lane == 0)
     a.plan[cta] = AttnPlan{w.more() ? (static_cast<long long>(w.b) * a.heads + w.h) * a.m_items + w.mt : -1ll, w.b, w.h, w.mt, w.t0};
 }
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       uint32_t phase = 0, q_phase = 0;
       long long issued = 0;
       bool ok = true, q_inflight = false;
-      auto load = [&](const Walk<kDual, true>& w, int t, bool v) {
+      auto load = [&](const Walk<kDual>& w, int t, bool v) {
         if (!wait(&sh->empty[stage], phase ^ 1u)) return false;
         const bool draft = t >= w.shape.cached;
         const CUtensorMap* tm = draft ? (v ? &a.tm_vd : &a.tm_kd) : (v ? &a.tm_v : &a.tm_k);
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         return true;
       };
-      for (Walk<kDual, true> w(a, sh); w.more() && ok; w.next(a)) {
+      for (Walk<kDual> w(a, sh); w.more() && ok; w.next(a)) {
         if (!wait(&sh->q_empty, q_phase ^ 1u)) break;
         q_inflight = true;
         if (lane == 0) {
@@ -521,9 +523,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       advance();
       return st;
     };
-    auto to_clean = [&](const Walk<kDual, true>& w, int t) { return t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len; };
+    auto to_clean = [&](const Walk<kDual>& w, int t) { return t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len; };
     // Clears V elements of stage `st` that no product may see (whole warp).
-    auto clean = [&](const Walk<kDual, true>& w, int t, int st) {
+    auto clean = [&](const Walk<kDual>& w, int t, int st) {
       const uint32_t v0 = s_ring + st * Cfg::kTileBytes;
       if (t < w.shape.cached) {
         const int rows = w.shape.len - t * kAtTile;
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       fence_proxy_async_shared();
       __syncwarp();
     };
-    for (Walk<kDual, true> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
       if (warp == 9 && lane == 0) sh->bad[seg & 1] = 0;
       __syncwarp();
@@ -660,7 +662,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     const float sc = a.scale * kAtLog2e;
     uint32_t s_phase = 0, f_phase = 0;
     int seg = 0;
-    for (Walk<kDual, true> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
       const int node0 = (w.mt * (kDual ? 2 : 1) + (kDual ? s : 0)) * a.npt;
       const int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile

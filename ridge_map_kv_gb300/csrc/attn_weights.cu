@@ -8,7 +8,10 @@
 // reduction across threads but that of two warps where they share a key's columns.
 //
 // Bound: the keys' bytes up to a few hundred queries (2 hd bytes a key against 2 R hd
-// flops and R exponentials); beyond, the exponentials and the product.
+// flops and R exponentials); beyond, the exponentials and the product. Measured (128 channels):
+// 16 paths of up to 7 nodes, 32 heads on 8, over 913 to 16,384 rows: 62 us, 5.0 TB/s; the last 64
+// of 32,768 rows, 20 heads on 2: 24 us, of which 8 are launch and queries (27.5 us with the
+// queries gathered row by row); the exponentials of 672 columns a key fill most of the rest.
 //
 // The queries of a KV head (nodes of the path times query heads, R of them) stay in
 // shared memory, up to 640 rows of 128 channels; the product takes them in steps of up
