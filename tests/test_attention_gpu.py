@@ -219,3 +219,21 @@ def test_attention_in_a_cuda_graph_follows_new_lengths():
         torch.cuda.synchronize()
         want, _, bo, _ = R.attention(q, k, v, kd, vd, lens, None, 0.125)
         assert R.within(out, want, bo) <= 1.0
+
+
+@pytest.mark.parametrize("B,n,H,G,hd,lens", [
+    (200, 1, 1, 4, 64, [(13 * b) % 260 for b in range(200)]),      # more items than shares, some of one tile
+    (7, 2, 1, 2, 128, [0, 1, 0, 0, 129, 0, 2]),                    # shares that hold no tile
+    (1, 4, 2, 8, 128, [12000]),                                    # 32 rows in many parts
+    (1, 3, 1, 3, 64, [30000]),                                     # 9 rows, more parts than a round of loads joins
+    (2, 33, 1, 4, 128, [3000, 1]),                                 # two row tiles, the second of one node
+])
+def test_attention_however_the_work_is_shared(B, n, H, G, hd, lens):
+    cap = max(lens) + 1
+    q, k, v, kd, vd = _data(B, n, H, G, hd, cap, lens, 11 * n + B)
+    scale = hd ** -0.5
+    out, lse, st = _call(q, k, v, kd, vd, torch.tensor(lens, dtype=torch.int32, device=DEV), None, scale, H)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    want, wl, bo, bl = R.attention(q, k, v, kd, vd, lens, None, scale)
+    assert R.within(out, want, bo) <= 1.0 and R.within(lse, wl, bl) <= 1.0

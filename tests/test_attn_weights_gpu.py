@@ -146,3 +146,28 @@ def test_attention_then_weights_add_up_to_one_a_query(hd, G, n, m):
     total = score.double().sum(-1)
     # each weight is off by 2 eps (both scores) relatively, eps = hd 2^-22 scale sum |q||k| < hd^2 2^-22 x 0.09 x 40
     assert float((total / (n * G) - 1).abs().max()) <= 2 * hd * hd * 2.0 ** -22 * 0.09 * 40
+
+
+@pytest.mark.parametrize("n,G,hd,m", [(64, 10, 128, 700), (70, 10, 128, 300), (257, 1, 64, 600), (256, 2, 64, 257), (3, 128, 64, 40)])
+def test_weights_of_all_nodes_equal_those_along_the_path_of_all_nodes(n, G, hd, m):
+    """All nodes in order, given as such or as a path: the same bits. Queries are part of wider rows, the first
+    sequence shorter than the other; one query sees nothing and holds NaN."""
+    B, H, scale = 2, 2, hd ** -0.5
+    lens = [n, max(m, n)]
+    wide = R.randn((B, n, H * G + 3, hd), 1, std=2.0)
+    q, k = wide[:, :, 1:1 + H * G], R.randn((B, max(lens) + 2, H, hd), 2)
+    paths = [list(range(n))] * B
+    lse = _stats(q, k, lens, paths, scale, H)
+    q[1, n // 2, G - 1], lse[1, n // 2, G - 1] = math.nan, -math.inf
+    for b in range(B):
+        k[b, lens[b]:] = math.nan
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    path = torch.arange(n, dtype=torch.int32, device=DEV).expand(B, n).contiguous()
+    cnt = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    score = torch.rand((B, H, k.shape[1]), device=DEV)
+    out, along = torch.full_like(score, math.nan), torch.full_like(score, math.nan)
+    assert _call(q, lse, None, None, k, ln, 0.5, score, out, scale) == 0
+    assert _call(q, lse, path, cnt, k, ln, 0.5, score, along, scale) == 0
+    assert torch.equal(out.view(torch.int32), along.view(torch.int32))
+    want, bound = R.weights(q, lse, k, lens, paths, 0.5, score, scale)
+    assert R.within(out, want, bound) <= 1.0
