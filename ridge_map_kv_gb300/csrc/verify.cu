@@ -11,11 +11,12 @@
 // sum Z is needed (a refused child with a sibling behind it) and once at the end, for
 // the lowest argmax of r / noise. What bounds a call is the latency of these steps: with the
 // commit of 32 layers, a chain of 5 over 32,000 tokens takes 12 us, 16 trees of 64 nodes over
-// 131,072 tokens 31 us for 29 MB that must be read.
+// 131,072 tokens 27 us for 29 MB that must be read.
 //
 // One cluster of CTAs a sequence: every thread follows the same walk through shared
 // memory, each CTA sums or scans its share of the vocabulary, and the shares meet
-// through distributed shared memory, in a fixed order. A thread keeps its tokens' r and
+// through distributed shared memory, each CTA writing its own to all, and are joined in a
+// fixed order. A thread keeps its tokens' r and
 // q of the current node in registers (up to 16: 131,072 tokens in a cluster), so a
 // refusal costs one division a token; larger vocabularies form r_k anew from p and q
 // each time.
@@ -62,8 +63,8 @@ struct VerifyShared {
   float z[RF_TREE_MAX_NODES];      // Z_j of the refusals at the current node
   int refused[RF_TREE_MAX_NODES];  // their nodes
   int path[RF_TREE_MAX_NODES];
-  float part_sum[2];               // this CTA's share, by the parity of the exchange
-  unsigned long long part_best[2];
+  float part_sum[2][kVerifyCtas];  // the CTAs' shares, by the parity of the turn
+  unsigned long long part_best[2][kVerifyCtas];
   float warp_sum[kVerifyThreads / 32];
   unsigned long long warp_best[kVerifyThreads / 32];
 };
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
   const int share = verify_share(a.vocab, ctas);
   const int v0 = min(rank * share, a.vocab), v1 = min(v0 + share, a.vocab);
   pdl_launch_dependents();
+  cl.barrier_arrive();  // (waited for below: every CTA of the cluster runs before another writes to it)
   pdl_wait();
   // The noise is read in any case; the root's rows more often than not.
   for (int t = v0 + tid * 32; t < v1; t += kVerifyThreads * 32) {
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
     }
   }
   bad = __syncthreads_or(bad);
+  cl.barrier_wait();
   if (bad) {  // every CTA of the cluster sees the same
     if (rank == 0) {
       for (int i = tid; i < n; i += kVerifyThreads) a.path[b * n + i] = -1;
@@ -219,9 +222,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       continue;
     }
     const int sibling = next_child(c);
-    __syncthreads();
-    if (tid == 0) sh.refused[k] = c;
-    __syncthreads();
+    if constexpr (!kDraft) {
+      if (tid == 0) sh.refused[k] = c;
+      __syncthreads();
+    }
     ++k;
     if (sibling < n) {
       // Z_k, this CTA's share, then the cluster's
@@ -241,10 +245,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       if (warp == 0) {
         float s = lane < kVerifyThreads / 32 ? sh.warp_sum[lane] : 0.0f;
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) sh.part_sum[turn & 1] = s;
+        if (lane < ctas) *cl.map_shared_rank(&sh.part_sum[turn & 1][rank], lane) = s;
       }
       cl.sync();
-      float z = lane < ctas ? *cl.map_shared_rank(&sh.part_sum[turn & 1], lane) : 0.0f;
+      float z = lane < ctas ? sh.part_sum[turn & 1][lane] : 0.0f;
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       ++turn;
       if (z > 0.0f) {
@@ -291,10 +295,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
     if (warp == 0) {
       unsigned long long m = lane < kVerifyThreads / 32 ? sh.warp_best[lane] : 0ull;
       for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane == 0) sh.part_best[turn & 1] = m;
+      if (lane < ctas) *cl.map_shared_rank(&sh.part_best[turn & 1][rank], lane) = m;
     }
     cl.sync();
-    unsigned long long m = lane < ctas ? *cl.map_shared_rank(&sh.part_best[turn & 1], lane) : 0ull;
+    unsigned long long m = lane < ctas ? sh.part_best[turn & 1][lane] : 0ull;
     for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     ++turn;
     token = static_cast<int>(0xffffffffu - static_cast<unsigned>(m & 0xffffffffu));
@@ -310,7 +314,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       a.next_token[b] = token;
     }
   }
-  cl.sync();  // no CTA leaves while another may read its share
 }
 
 struct CommitArgs {
