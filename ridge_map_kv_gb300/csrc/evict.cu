@@ -23,7 +23,7 @@
 //
 // Bound: reading scores and positions and writing the kept ones (16 bytes a row) and the
 // moved rows' bytes twice; at a few rows a step, the latency of the selection. Measured (heads of
-// 128 channels): half of 320 units at 4,103 rows with 4,096 to stay 10 us, of which the counting
+// 128 channels): half of 320 units at 4,103 rows with 4,096 to stay 9.8 us, of which the counting
 // steps are most; 160 units of 16,384 rows with 4,096 to stay 121 us, of which the moves take 81
 // (at the memory's rate) and the selection 42 (instructions, and a second wave of 8 CTAs).
 #include <algorithm>
@@ -71,6 +71,7 @@ struct SelShared {
   int warp_a[kThreads / 32];
   int warp_b[kThreads / 32];
   int n_moves;
+  int32_t moves[2][kOwnMoves];  // destinations and sources, where the CTA moves the rows itself
 };
 
 // Exclusive scan over the CTA's warps of one value per warp, in shared memory.
@@ -94,12 +95,10 @@ __device__ __forceinline__ int32_t length_after(const EvictArgs& a, int len) {
   return len > a.keep && len <= a.capacity ? a.keep : len;
 }
 
-// Moves i0 .. i0 + m - 1 of a unit's list, by the whole CTA.
+// m moves of a unit, by the whole CTA.
 template <int kThreads>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, int unit, int i0, int m) {
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int unit, const int32_t* dst, const int32_t* src, int m) {
   const int h = unit % a.heads, lb = unit / a.heads, b = lb % a.n_seqs, l = lb / a.n_seqs;
-  const int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves + i0;
-  const int32_t* src = dst + a.max_moves;
   const long long head = l * a.layer_stride + b * a.seq_stride + static_cast<long long>(h) * a.head_dim;
   const int pieces = a.head_dim / 8;
 #pragma unroll 4
@@ -343,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
     a.n_moves[unit] = mover + movers;  // as many holes as movers
     sh.n_moves = mover + movers;
   }
-  int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves;
-  int32_t* src = dst + a.max_moves;
+  int32_t* dst = a.moves_too ? sh.moves[0] : a.moves + static_cast<long long>(unit) * 2 * a.max_moves;
+  int32_t* src = a.moves_too ? sh.moves[1] : dst + a.max_moves;
   eq = eq0;
   each([&](int g, const unsigned (&k)[kItems]) {
     unsigned m = m_first;
@@ -386,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) k_evict_select(const __grid_
   });
   if (a.moves_too) {
     __syncthreads();
-    move_rows<kThreads>(a, unit, 0, sh.n_moves);
+    move_rows<kThreads>(a, unit, dst, src, sh.n_moves);
   }
 }
 
@@ -399,7 +398,8 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
     for (int b = threadIdx.x; b < a.n_seqs; b += 256) a.new_lens[b] = length_after(a, a.lens[b]);
   }
   const int m = min(n - i0, kMoveRows);
-  if (m > 0) move_rows<256>(a, unit, i0, m);
+  const int32_t* dst = a.moves + static_cast<long long>(unit) * 2 * a.max_moves + i0;
+  if (m > 0) move_rows<256>(a, unit, dst, dst + a.max_moves, m);
 }
 
 rf_status check_cache_desc(const rf_cache_desc* d) {

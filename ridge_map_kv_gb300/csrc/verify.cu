@@ -14,12 +14,10 @@
 // 131,072 tokens 27 us for 29 MB that must be read.
 //
 // One cluster of CTAs a sequence: every thread follows the same walk through shared
-// memory, each CTA sums or scans its share of the vocabulary, and the shares meet
-// through distributed shared memory, each CTA writing its own to all, and are joined in a
-// fixed order. A thread keeps its tokens' r and
-// q of the current node in registers (up to 16: 131,072 tokens in a cluster), so a
-// refusal costs one division a token; larger vocabularies form r_k anew from p and q
-// each time.
+// memory, each CTA sums or scans its share of the vocabulary and writes the result into the
+// shared memory of all, and all join the shares in a fixed order. A thread keeps its tokens' r
+// and q of the current node in registers (up to 16: 131,072 tokens in a cluster), so a refusal
+// costs one division a token; larger vocabularies form r_k anew from p and q each time.
 #include <cooperative_groups.h>
 
 #include <algorithm>
