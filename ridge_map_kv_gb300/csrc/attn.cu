@@ -42,9 +42,12 @@
 // Measured (128 channels): one token, 40 query heads on 8, over 32,767 rows: 33 us, 4.1 TB/s of
 // the cache's bytes (22 us of it in the tiles). 16 trees of 64 nodes, 32 heads on 8, over 913 to
 // 16,384 rows: 132 us, 4.7 TB/s and 1,150 TFLOP/s. 4,096 rows in order over 28,672, 40 heads on
-// 8: 1.86 ms, 1,390 TFLOP/s, 0.74 of the measured burst rate: a tile's chain of product, softmax
-// (about 1,100 cycles), product and three hand-overs (about 105 each) is longer than the
-// 2 x 1,028 cycles of products that the two streams have between them.
+// 8: 1.86 ms, 1,390 TFLOP/s, 0.74 of the measured burst rate. A stream's turn at the tensor
+// cores, for 16 products that take 1,030 cycles back to back, lasts about 1,400: the wait between
+// the two parts of the weights, the issue beside eight busy warps, and the hand-over to the other
+// stream. A shorter softmax does not change that (weights formed against the last maximum while
+// the tile's own is taken: 1.87 ms), nor do sums behind the hand-over (1.89 ms) or streams
+// without turns (2.33 ms).
 #include <algorithm>
 #include <cmath>
 
@@ -829,8 +832,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
 
 // Joins the rows of items that were cut. Block (x, y): the cut before share x + 1, rows
 // 32 y .. 32 y + 31 of its item; the first cut inside an item answers for it. A lane is a
-// row (or part of one), a warp 16 channels of it. Launched as a dependent of k_attn: its CTAs wait in place
-// for that one's end.
+// row (or part of one), a warp 16 channels of it. Launched as a dependent of k_attn: its CTAs
+// wait in place for that one's end.
 struct CombineArgs {
   const AttnPlan* plan;
   const float4* part_o;
