@@ -104,7 +104,7 @@ struct AttnArgs {
 
 struct AttnShared {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
-  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean, mma_done[2];
+  uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean[2], mma_done[2];
   AttnShare share;
   int bad[2];                // a drafted V row of the segment is not finite
   uint32_t tmem;
@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     mbar_init(&sh->o_final, kMmaWarps + 1);
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->ml_full, 8);
-    mbar_init(&sh->v_clean, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->v_clean[i], 1);
       mbar_init(&sh->turn[i], 1);
       mbar_init(&sh->mma_done[i], 1);
     }
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     constexpr uint32_t idesc_o = make_idesc_bf16(kAtTile, kHD, 0, 1);
     const uint32_t issue = lane == 0;
     int stage = 0;
-    uint32_t phase = 0, q_phase = 0, o_phase = 0, c_phase = 0, turn_phase = warp == 9 ? 1 : 0, p_phase[2] = {0, 0};
+    uint32_t phase = 0, q_phase = 0, o_phase = 0, cleaned = 0, turn_phase = warp == 9 ? 1 : 0, p_phase[2] = {0, 0};
     int seg = 0;
     auto advance = [&] {
       if (++stage == Cfg::kStages) {
@@ -593,13 +593,16 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           const int v = take();
           if (v < 0) goto mma_done;
           if (to_clean(w, w.t0 + i)) {
+            // Two barriers in turns: warp 9 may clean the next tile before warp 10 has looked at this
+            // one's barrier, but not the one after that, which lies behind a turn that warp 10 gives
+            // back after its wait. With one barrier the phase could wrap under that wait.
             if (s == 0) {
               clean(w, w.t0 + i, v);
-              if (lane == 0) mbar_arrive(&sh->v_clean);
+              if (lane == 0) mbar_arrive(&sh->v_clean[cleaned & 1u]);
             } else {
-              if (!wait(&sh->v_clean, c_phase)) goto mma_done;
-              c_phase ^= 1u;
+              if (!wait(&sh->v_clean[cleaned & 1u], (cleaned >> 1) & 1u)) goto mma_done;
             }
+            ++cleaned;
           }
           k = more ? take() : 0;
           if (k < 0) goto mma_done;

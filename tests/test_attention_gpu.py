@@ -237,3 +237,19 @@ def test_attention_however_the_work_is_shared(B, n, H, G, hd, lens):
     assert int(st.item()) == 0
     want, wl, bo, bl = R.attention(q, k, v, kd, vd, lens, None, scale)
     assert R.within(out, want, bo) <= 1.0 and R.within(lse, wl, bl) <= 1.0
+
+
+def test_attention_many_drafted_tiles_in_a_row_for_two_row_tiles():
+    """Every drafted tile is looked through for what is not finite, by one of the two issuing warps for both: a dozen
+    of them one after another, many times over, with the same bits every time."""
+    n, H, G, hd, lens = 1500, 2, 2, 128, [130, 0]
+    q, k, v, kd, vd = _data(2, n, H, G, hd, 140, lens, 12)
+    ln = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    out, lse, st = _call(q, k, v, kd, vd, ln, None, 0.09, H)
+    for _ in range(30):
+        again, lse2, _ = _call(q, k, v, kd, vd, ln, None, 0.09, H, status=st)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+    assert int(st.item()) == 0
+    want, wl, bo, bl = R.attention(q, k, v, kd, vd, lens, None, 0.09)
+    assert R.within(out, want, bo) <= 1.0 and R.within(lse, wl, bl) <= 1.0
