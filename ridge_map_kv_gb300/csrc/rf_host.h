@@ -105,6 +105,8 @@ rf_status check_attn_desc(const rf_attn_desc* d);
 // running, once that one's CTAs have all exited or called pdl_launch_dependents(); the
 // kernel itself calls pdl_wait() (rf_device.cuh) before it touches what the previous one
 // writes, which returns when that one has finished and its writes are visible.
+// Such a kernel reads by plain loads: read-only ones (__ldg, const __restrict__) want data that
+// nothing writes from the kernel's first instruction on, which is before the wait.
 // `cluster`: CTAs of a cluster along x.
 template <class... A>
 cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, unsigned cluster,

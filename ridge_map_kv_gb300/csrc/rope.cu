@@ -244,10 +244,9 @@ static cudaError_t launch_rope(RopeArgs& a, const RopeTable& t, bool half, int s
 // Masks and positions of drafted trees, one CTA a sequence. A thread per node climbs its
 // ancestors through the parents in shared memory; indices fall on the way up, so its
 // mask words come out one after another, the highest first.
-__global__ void __launch_bounds__(1024) k_tree_build(int n, int words, const int32_t* __restrict__ parents,
-                                                     const int32_t* __restrict__ next_pos,
-                                                     unsigned long long* __restrict__ mask,
-                                                     int32_t* __restrict__ positions, int32_t* dev_status) {
+__global__ void __launch_bounds__(1024) k_tree_build(int n, int words, const int32_t* parents,
+                                                     const int32_t* next_pos, unsigned long long* mask,
+                                                     int32_t* positions, int32_t* dev_status) {
   __shared__ int up[RF_TREE_MAX_NODES];
   pdl_launch_dependents();
   pdl_wait();

@@ -89,16 +89,15 @@ __device__ __forceinline__ float residual(const VerifyShared& sh, float p, float
 
 // f(t, p(t), q(t), e(t)) for the tokens v0 <= t < v1 of this thread; q and e may be NULL.
 template <class F>
-__device__ __forceinline__ void scan_row(int v0, int v1, const float* __restrict__ p, const float* __restrict__ q,
-                                         const float* __restrict__ e, F f) {
+__device__ __forceinline__ void scan_row(int v0, int v1, const float* p, const float* q, const float* e, F f) {
   for (int t0 = v0 + static_cast<int>(threadIdx.x); t0 < v1; t0 += kVerifyThreads * kVerifyBatch) {
     float pv[kVerifyBatch], qv[kVerifyBatch], ev[kVerifyBatch];
 #pragma unroll
     for (int i = 0; i < kVerifyBatch; ++i) {
       const int t = t0 + i * kVerifyThreads;
-      pv[i] = t < v1 ? __ldg(p + t) : 0.0f;
-      qv[i] = q != nullptr && t < v1 ? __ldg(q + t) : 0.0f;
-      ev[i] = e != nullptr && t < v1 ? __ldg(e + t) : 1.0f;
+      pv[i] = t < v1 ? p[t] : 0.0f;
+      qv[i] = q != nullptr && t < v1 ? q[t] : 0.0f;
+      ev[i] = e != nullptr && t < v1 ? e[t] : 1.0f;
     }
 #pragma unroll
     for (int i = 0; i < kVerifyBatch; ++i) {
@@ -176,8 +175,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
 #pragma unroll
         for (int i = 0; i < kVerifySlots; ++i) {
           const int t = v0 + tid + i * kVerifyThreads;
-          r[i] = t < v1 ? __ldg(p + t) : 0.0f;
-          if constexpr (kDraft) q[i] = t < v1 ? __ldg(d + t) : 0.0f;
+          r[i] = t < v1 ? p[t] : 0.0f;
+          if constexpr (kDraft) q[i] = t < v1 ? d[t] : 0.0f;
         }
         applied = 0;
       }
@@ -275,7 +274,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
 #pragma unroll
       for (int i = 0; i < kVerifySlots; ++i) {
         const int t = v0 + tid + i * kVerifyThreads;
-        ev[i] = t < v1 ? __ldg(e + t) : 1.0f;
+        ev[i] = t < v1 ? e[t] : 1.0f;
       }
       bring();
 #pragma unroll
