@@ -52,14 +52,21 @@ struct VerifyArgs {
 // Tokens of a CTA: whole 16-byte groups.
 __host__ __device__ inline int verify_share(int vocab, int ctas) { return ((vocab + ctas - 1) / ctas + 3) & ~3; }
 
-struct VerifyShared {
+// What only the form without draft probabilities has, so that the other cannot read it.
+template <bool kDraft>
+struct VerifyRefused {};
+template <>
+struct VerifyRefused<false> {
+  int refused[RF_TREE_MAX_NODES];  // nodes of the refusals at the current node
+};
+template <bool kDraft>
+struct VerifyShared : VerifyRefused<kDraft> {
   int up[RF_TREE_MAX_NODES];
   int token[RF_TREE_MAX_NODES];
   float u[RF_TREE_MAX_NODES];
   float p[RF_TREE_MAX_NODES];  // target probability of the node's token at its parent
   float q[RF_TREE_MAX_NODES];
-  float z[RF_TREE_MAX_NODES];      // Z_j of the refusals at the current node
-  int refused[RF_TREE_MAX_NODES];  // their nodes
+  float z[RF_TREE_MAX_NODES];  // Z_j of the refusals at the current node
   int path[RF_TREE_MAX_NODES];
   float part_sum[2][kVerifyCtas];  // the CTAs' shares, by the parity of the turn
   unsigned long long part_best[2][kVerifyCtas];
@@ -78,7 +85,7 @@ __device__ __forceinline__ float quotient(float x, float z, float y) {
 
 // r_k(t) from p(t), q(t) and the refusals.
 template <bool kDraft>
-__device__ __forceinline__ float residual(const VerifyShared& sh, float p, float q, int t, int k) {
+__device__ __forceinline__ float residual(const VerifyShared<kDraft>& sh, float p, float q, int t, int k) {
   float r = p;
   for (int j = 0; j < k; ++j) {
     if constexpr (kDraft) r = fmaxf(__fsub_rn(quotient(r, sh.z[j], __frcp_rn(sh.z[j])), q), 0.0f);
@@ -110,7 +117,7 @@ __device__ __forceinline__ void scan_row(int v0, int v1, const float* p, const f
 // kFit: a CTA's share fits in its threads' registers.
 template <bool kDraft, bool kFit>
 __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_constant__ VerifyArgs a) {
-  __shared__ VerifyShared sh;
+  __shared__ VerifyShared<kDraft> sh;
   cg::cluster_group cl = cg::this_cluster();
   const int rank = static_cast<int>(cl.block_rank()), ctas = static_cast<int>(cl.num_blocks());
   const long long b = blockIdx.x / static_cast<unsigned>(ctas);
@@ -181,14 +188,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
         applied = 0;
       }
       for (; applied < k; ++applied) {
-        const float z = sh.z[applied], y = __frcp_rn(z);
-        const int gone = sh.token[sh.refused[applied]] - v0 - tid;
+        if constexpr (kDraft) {
+          const float z = sh.z[applied], y = __frcp_rn(z);
 #pragma unroll
-        for (int i = 0; i < kVerifySlots; ++i) {
-          if (i < slots) {
-            if constexpr (kDraft) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
-            else r[i] = gone == i * kVerifyThreads ? 0.0f : r[i];
-          }
+          for (int i = 0; i < kVerifySlots; ++i)
+            if (i < slots) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
+        } else {
+          const int gone = sh.token[sh.refused[applied]] - v0 - tid;
+#pragma unroll
+          for (int i = 0; i < kVerifySlots; ++i)
+            if (i < slots) r[i] = gone == i * kVerifyThreads ? 0.0f : r[i];
         }
       }
     }
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
   };
   int c = next_child(0);
   while (c < n) {
-    const float rx = residual<kDraft>(sh, sh.p[c], sh.q[c], sh.token[c], k);
+    const float rx = residual(sh, sh.p[c], sh.q[c], sh.token[c], k);
     if (__fmul_rn(__fmul_rn(sh.u[c], sh.q[c]), sh.z[k]) < rx) {
       __syncthreads();  // the refusals of the node left behind are read no more
       if (tid == 0) {
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
           if (i < slots) sum += r[i];
       } else {
         scan_row(v0, v1, a.target + (b * n + cur) * a.ld_target, kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr,
-                 nullptr, [&](int t, float pt, float qt, float) { sum += residual<kDraft>(sh, pt, qt, t, k); });
+                 nullptr, [&](int t, float pt, float qt, float) { sum += residual(sh, pt, qt, t, k); });
       }
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       if (lane == 0) sh.warp_sum[warp] = sum;
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       }
     } else {
       scan_row(v0, v1, a.target + (b * n + cur) * a.ld_target, kDraft ? a.draft + (b * n + cur) * a.ld_draft : nullptr, e,
-               [&](int t, float pt, float qt, float et) { look(t, residual<kDraft>(sh, pt, qt, t, k), et); });
+               [&](int t, float pt, float qt, float et) { look(t, residual(sh, pt, qt, t, k), et); });
     }
     for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
     if (lane == 0) sh.warp_best[warp] = best;
