@@ -731,7 +731,7 @@ rf_status rf_attn_weights(const rf_attn_desc* desc, const rf_bf16* q, const floa
  * holds each row's position.
  *   score_in, pos_in, score_out, pos_out  [n_layers][n_seqs][n_kv_heads][capacity]; out
  *       may be in; entries beyond new_lens[b] are not written
- *   new_lens [n_seqs] int32 (may be lens)
+ *   new_lens [n_seqs] int32: lens itself (or next_pos), or apart from lens
  * A length outside [0, capacity] records RF_ERR_INVALID_ARG and that sequence stays as
  * it is. keep >= 1. */
 size_t rf_evict_workspace_bytes(const rf_cache_desc* desc, int64_t keep);

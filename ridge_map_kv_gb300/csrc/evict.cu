@@ -475,6 +475,8 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
                          reinterpret_cast<uintptr_t>(score_out) | reinterpret_cast<uintptr_t>(pos_out) |
                          reinterpret_cast<uintptr_t>(new_lens);
   if (bits & 3u) return fail(RF_ERR_ALIGN, "arrays must be 4-byte aligned");
+  if (new_lens != lens && overlap(new_lens, d->n_seqs, lens, d->n_seqs))
+    return fail(RF_ERR_INVALID_ARG, "new_lens must be lens or lie apart from it");
   const EvictLayout lay = evict_layout(d, keep, workspace);
   if (workspace == nullptr || workspace_bytes < lay.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
@@ -508,9 +510,9 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
   // One launch where few rows can move, so that a unit's CTA moves them by itself (half of 320
   // units over the 4,096 rows that stay, by 64 rows: 13.2 us, 15.0 in two launches; by 128: 14.7
   // and 15.7; 8 units over 2,000 rows by 64: 9.8 and 10.4; by 256: 12.3 and 11.0); not where
-  // new_lens is written over lens, which every CTA reads.
-  const bool lens_apart = new_lens + d->n_seqs <= lens || lens + d->n_seqs <= new_lens;
-  a.moves_too = lens_apart && lay.max_moves <= kOwnMoves;
+  // new_lens is written over lens or next_pos, which every CTA reads.
+  const bool apart = !overlap(new_lens, d->n_seqs, lens, d->n_seqs) && !overlap(new_lens, d->n_seqs, next_pos, d->n_seqs);
+  a.moves_too = apart && lay.max_moves <= kOwnMoves;
   const unsigned units = static_cast<unsigned>(d->n_layers * d->n_seqs * d->n_kv_heads);
   {
     ProfScope prof(s, RF_STAGE_EVICT_SELECT);

@@ -95,6 +95,14 @@ rf_status chol_inv_block(float* A, long long lda, long long sA, float* W, long l
 rf_status spd_inverse(float* H, int n, float* Linv, float* Hinv, float* ctmp, __nv_bfloat16* planes, bool pair,
                       int32_t* dev_status, int sms, cudaStream_t s);
 
+// Whether n elements at a and m at b have memory in common (NULL has none).
+template <class A, class B>
+bool overlap(const A* a, int64_t n, const B* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + static_cast<uintptr_t>(m) * sizeof(B) &&
+         y < x + static_cast<uintptr_t>(n) * sizeof(A);
+}
+
 // Checks of an rf_cache_desc that the calls writing to a cache share (evict.cu).
 rf_status check_cache_desc(const rf_cache_desc* d);
 

@@ -219,3 +219,10 @@ def test_constants_and_stage_names_match_the_header():
         assert rf.rf_stage_name(int(val)) != "unknown", name
     assert [rf.rf_stage_name(i) for i in (22, 24, 26, 28, 29)] == ["rope", "attention", "verify", "attention_weights",
                                                                   "evict_select"]
+
+
+def test_evict_refuses_lengths_that_overlap_in_part():
+    d = _cache()
+    need = rf.rf_evict_workspace_bytes(d, 10)
+    for shift in (-4, 4):                       # two sequences: 8 bytes
+        _refused(INV, rf.rf_evict, d, 10, 0, 0, P, 2 * P, *[P] * 6, P + shift, None, P, need)

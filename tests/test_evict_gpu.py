@@ -185,3 +185,30 @@ def test_evict_gives_the_same_wherever_lengths_and_scores_go(cap, keep, kind):
             results.append((k, v, so[..., :keep], po[..., :keep]))
     for r in results[1:]:
         assert all(_same(x, y) for x, y in zip(r, results[0]))
+
+
+@pytest.mark.parametrize("cap,keep", [(100, 64), (300, 100)])
+def test_evict_writes_lengths_over_the_next_positions(cap, keep):
+    """new_lens may be next_pos. Thousands of heads of one sequence, so that some are selected long after the first: all
+    read the position that was there before the call. (36 rows can move, which takes one launch, and 100, which takes
+    two.)"""
+    L, B, H, hd = 500, 1, 8, 8
+    W = H * hd
+    d = rf.rf_cache_desc(n_layers=L, n_seqs=B, n_kv_heads=H, head_dim=hd, capacity=cap, row_stride=W, seq_stride=cap * W,
+                         layer_stride=cap * W)
+    wsb = rf.rf_evict_workspace_bytes(d, keep)
+    results = []
+    for over in (False, True):
+        k, v = R.randn((L, B, cap, W), 1), R.randn((L, B, cap, W), 2)
+        score = _scores((L, B, H, cap), "plain", 3)
+        pos = torch.arange(cap, dtype=torch.int32, device=DEV).flip(0).expand(L, B, H, cap).contiguous()
+        ln, nx = torch.full((B,), cap, dtype=torch.int32, device=DEV), torch.full((B,), cap, dtype=torch.int32, device=DEV)
+        nl = nx if over else torch.zeros_like(ln)
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        ws = torch.full((wsb,), 0xA5, dtype=torch.uint8, device=DEV)
+        rf.rf_evict(d, keep, 2, 20, ln, nx, k, v, score, pos, score, pos, nl, st, ws, wsb)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0 and nl.tolist() == [keep] and ln.tolist() == [cap]
+        assert bool(((pos[..., :keep] >= cap - 20).sum(-1) == 20).all())      # the newest twenty of every head
+        results.append((k, v, score[..., :keep], pos[..., :keep]))
+    assert all(_same(x, y) for x, y in zip(*results))
