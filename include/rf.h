@@ -691,8 +691,9 @@ typedef struct rf_cache_desc {
  *   new_lens[b] = lens[b] + n_path[b], new_next_pos[b] = next_pos[b] + n_path[b].
  * score, pos [n_layers][n_seqs][n_kv_heads][capacity] (either may be NULL); k_draft,
  * v_draft: element l*draft_layer_stride + b*draft_seq_stride + i*draft_row_stride +
- * h*head_dim + c. new_lens may be lens, new_next_pos may be next_pos, which may be NULL
- * together with new_next_pos and pos. A sequence whose rows do not fit, or whose path or
+ * h*head_dim + c. new_lens may be lens and new_next_pos next_pos; either may be any of lens,
+ * next_pos and n_path, but not overlap them in part, nor path. next_pos may be NULL together
+ * with new_next_pos and pos. A sequence whose rows do not fit, or whose path or
  * counts are out of range, records RF_ERR_INVALID_ARG and keeps its lengths and rows. */
 rf_status rf_commit_draft(const rf_cache_desc* desc, int64_t n_nodes, int64_t draft_row_stride,
                           int64_t draft_seq_stride, int64_t draft_layer_stride,

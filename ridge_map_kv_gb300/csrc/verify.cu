@@ -338,7 +338,7 @@ struct CommitArgs {
   int32_t* dev_status;
   long long row_stride, seq_stride, layer_stride, draft_row, draft_seq, draft_layer;
   int n_seqs, heads, width, capacity, n;  // width = heads * head_dim
-  int lens_here;  // k_commit itself writes the lengths (new ones lie apart from the old)
+  int lens_here;  // k_commit itself writes the lengths (new ones lie apart from its inputs)
 };
 
 // Whether sequence b's rows may be appended (whole CTA).
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(256) k_commit(const __grid_constant__ CommitAr
   }
 }
 
-// Where new_lens is lens (or new_next_pos next_pos) the lengths are written behind all of
-// k_commit's reads: by a dependent launch, one CTA a sequence.
+// Where new lengths or positions are written over lens, next_pos or n_path, they are written behind
+// all of k_commit's reads: by a dependent launch, one CTA a sequence.
 __global__ void __launch_bounds__(64) k_commit_lens(const __grid_constant__ CommitArgs a) {
   pdl_wait();
   const int b = blockIdx.x;
@@ -481,6 +481,18 @@ extern "C" rf_status rf_commit_draft(const rf_cache_desc* d, int64_t n_nodes, in
                          reinterpret_cast<uintptr_t>(score) | reinterpret_cast<uintptr_t>(pos) |
                          reinterpret_cast<uintptr_t>(new_lens) | reinterpret_cast<uintptr_t>(new_next_pos);
   if (bits & 3u) return fail(RF_ERR_ALIGN, "arrays must be 4-byte aligned");
+  // Lengths written over an input, element by element, wait for all of k_commit's reads; no order
+  // would be right where arrays overlap otherwise.
+  bool over_inputs = false;
+  for (const int32_t* w : {new_lens, new_next_pos}) {
+    if (overlap(w, d->n_seqs, path, d->n_seqs * n_nodes))
+      return fail(RF_ERR_INVALID_ARG, "new_lens and new_next_pos must lie apart from path");
+    for (const int32_t* r : {lens, next_pos, n_path}) {
+      if (!overlap(w, d->n_seqs, r, d->n_seqs)) continue;
+      if (w != r) return fail(RF_ERR_INVALID_ARG, "new_lens and new_next_pos must not overlap an input in part");
+      over_inputs = true;
+    }
+  }
   int sms = 0;
   if ((st = current_device(&sms)) != RF_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -509,7 +521,7 @@ extern "C" rf_status rf_commit_draft(const rf_cache_desc* d, int64_t n_nodes, in
   a.width = static_cast<int>(width);
   a.capacity = static_cast<int>(d->capacity);
   a.n = static_cast<int>(n_nodes);
-  a.lens_here = d->n_layers > 0 && new_lens != lens && (new_next_pos == nullptr || new_next_pos != next_pos);
+  a.lens_here = d->n_layers > 0 && !over_inputs;
   if (d->n_layers > 0) {
     ProfScope prof(s, RF_STAGE_COMMIT);
     st = cuda_check(launch_dependent(k_commit, dim3(static_cast<unsigned>(d->n_layers), static_cast<unsigned>(d->n_seqs)),

@@ -226,3 +226,12 @@ def test_evict_refuses_lengths_that_overlap_in_part():
     need = rf.rf_evict_workspace_bytes(d, 10)
     for shift in (-4, 4):                       # two sequences: 8 bytes
         _refused(INV, rf.rf_evict, d, 10, 0, 0, P, 2 * P, *[P] * 6, P + shift, None, P, need)
+
+
+def test_commit_refuses_lengths_that_overlap_in_part():
+    d = _cache()
+    far = [P << 4, P << 5, P << 6, P << 7]      # path, n_path, lens, next_pos
+    for i in range(4):                          # two sequences: 8 bytes; the path: 32
+        for shift in (-4, 4) if i else (-4, 0, 28):
+            for out in ([far[i] + shift, P << 8], [P << 8, far[i] + shift]):
+                _refused(INV, rf.rf_commit_draft, d, 4, 128, 512, 1024, *far, *[P] * 6, *out)

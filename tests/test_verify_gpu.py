@@ -206,3 +206,39 @@ def test_commit_refuses_what_does_not_fit_and_goes_on_with_the_rest(what):
     assert torch.equal(k[:, 1], k0[:, 1]) and torch.equal(v[:, 1], k0[:, 1])
     for b in (0, 2):
         assert torch.equal(k[:, b, 3:5], kd[:, b, [0, 2]])
+
+
+@pytest.mark.parametrize("where", ["apart", "lens over next_pos", "one array for all", "over n_path", "next_pos over lens"])
+def test_commit_reads_its_inputs_before_it_writes_over_them(where):
+    """New lengths and positions over any input of their size: every layer still sees what was there before. More
+    layers and sequences than the GPU takes at once."""
+    L, B, n, H, hd, cap = 60, 100, 3, 1, 8, 40
+    k, v = torch.zeros((L, B, cap, H * hd), dtype=torch.bfloat16, device=DEV), torch.zeros((L, B, cap, H * hd),
+                                                                                      dtype=torch.bfloat16, device=DEV)
+    kd, vd = R.randn((L, B, n, H * hd), 1), R.randn((L, B, n, H * hd), 2)
+    pos = torch.full((L, B, H, cap), -5, dtype=torch.int32, device=DEV)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    lens, cnt = [b % 30 for b in range(B)], [b % (n + 1) for b in range(B)]
+    nxt = lens if where == "one array for all" else [x + 7 for x in lens]
+    path = ints([[0, 1, 2]] * B)
+    a_len, a_cnt = ints(lens), ints(cnt)
+    a_nxt = a_len if where == "one array for all" else ints(nxt)
+    nl, nn = {"apart": (ints([0] * B), ints([0] * B)), "lens over next_pos": (a_nxt, None), "one array for all": (a_len, a_len),
+              "over n_path": (a_cnt, ints([0] * B)), "next_pos over lens": (None, a_len)}[where]
+    d = rf.rf_cache_desc(n_layers=L, n_seqs=B, n_kv_heads=H, head_dim=hd, capacity=cap, row_stride=H * hd,
+                         seq_stride=cap * H * hd, layer_stride=B * cap * H * hd)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    rf.rf_commit_draft(d, n, kd.stride(2), kd.stride(1), kd.stride(0), path, a_cnt, a_len, a_nxt, kd, vd, k, v, None, pos,
+                       nl, nn, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    wk, wp = torch.zeros_like(k), torch.full_like(pos, -5)
+    for b in range(B):
+        for j in range(cnt[b]):
+            wk[:, b, lens[b] + j] = kd[:, b, j]
+            wp[:, b, :, lens[b] + j] = nxt[b] + j
+    assert torch.equal(k, wk) and torch.equal(pos, wp)
+    if nl is not None:
+        assert nl.tolist() == [x + c for x, c in zip(lens, cnt)]
+    if nn is not None:
+        assert nn.tolist() == [x + c for x, c in zip(nxt, cnt)]
