@@ -673,7 +673,8 @@ rf_status rf_verify_draft(const rf_verify_desc* desc, const float* target, const
                           int32_t* path, int32_t* n_path, int32_t* next_token, int32_t* dev_status,
                           rf_stream_t stream);
 
-/* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c. */
+/* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c.
+ * Layers, sequences and rows may be nested in any order; no two rows may overlap. */
 typedef struct rf_cache_desc {
   int64_t n_layers;
   int64_t n_seqs;

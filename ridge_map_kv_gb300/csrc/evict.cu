@@ -402,6 +402,40 @@ __global__ void __launch_bounds__(256) k_evict_move(const __grid_constant__ Evic
   if (m > 0) move_rows<256>(a, unit, dst, dst + a.max_moves, m);
 }
 
+// Whether no two rows of a cache, to all of which the calls write, lie on one another. As a rule
+// layers, sequences and rows are nested, in any order: each stride spans all that lies inside it.
+// Otherwise all differences of two places are looked at (up to 2^20 of them).
+static bool rows_apart(const rf_cache_desc* d) {
+  using Wide = __int128;
+  struct Dim {
+    int64_t n, stride;
+  } dim[3] = {{d->capacity, d->row_stride}, {d->n_seqs, d->seq_stride}, {d->n_layers, d->layer_stride}};
+  const Wide row = d->n_kv_heads * d->head_dim;
+  std::sort(dim, dim + 3, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  Wide span = row;
+  bool nested = true;
+  for (const Dim& x : dim) {
+    if (x.n <= 1) continue;
+    nested &= x.stride >= span;
+    span += static_cast<Wide>(x.n - 1) * x.stride;
+  }
+  if (nested) return true;
+  std::sort(dim, dim + 3, [](const Dim& x, const Dim& y) { return x.n > y.n; });
+  for (const Dim& x : dim)
+    if (x.n > 1 && x.stride < row) return false;
+  if (dim[1].n * dim[2].n > (int64_t(1) << 20)) return false;
+  const Wide most = dim[0].n - 1, step = dim[0].stride;
+  for (int64_t i = 0; i < dim[1].n; ++i)
+    for (int64_t j = i == 0 ? 1 : 1 - dim[2].n; j < dim[2].n; ++j) {
+      const Wide x = static_cast<Wide>(i) * dim[1].stride + static_cast<Wide>(j) * dim[2].stride;
+      for (int near = -1; near <= 1; ++near) {  // places of the first dimension around -x
+        const Wide y = x + std::min(std::max(near - x / step, -most), most) * step;
+        if (y < row && -y < row) return false;
+      }
+    }
+  return true;
+}
+
 rf_status check_cache_desc(const rf_cache_desc* d) {
   if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_layers < 0 || d->n_seqs < 0 || d->n_kv_heads <= 0 || d->head_dim <= 0 || d->capacity <= 0)
@@ -412,11 +446,7 @@ rf_status check_cache_desc(const rf_cache_desc* d) {
   if (d->row_stride < d->n_kv_heads * d->head_dim || d->row_stride % 8 || d->seq_stride % 8 || d->layer_stride % 8 ||
       d->seq_stride < 0 || d->layer_stride < 0)
     return fail(RF_ERR_ALIGN, "cache strides must be multiples of 8, the row stride >= n_kv_heads*head_dim");
-  // rows of one cache must not lie on one another: the calls write to them
-  const int64_t span = (d->capacity - 1) * d->row_stride + d->n_kv_heads * d->head_dim;
-  if ((d->n_seqs > 1 && d->seq_stride < span && d->layer_stride < span) ||
-      (d->n_seqs > 1 && d->seq_stride == 0) || (d->n_layers > 1 && d->layer_stride == 0))
-    return fail(RF_ERR_ALIGN, "layers and sequences must not overlap");
+  if (!rows_apart(d)) return fail(RF_ERR_ALIGN, "rows, sequences and layers must not overlap");
   return RF_OK;
 }
 

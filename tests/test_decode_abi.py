@@ -1,6 +1,7 @@
 """Refusals of the decoding operators: all on the host, before any launch, so no GPU is
 touched. Pointers are aligned numbers that nothing dereferences."""
 import os
+import random
 import re
 
 import pytest
@@ -235,3 +236,46 @@ def test_commit_refuses_lengths_that_overlap_in_part():
         for shift in (-4, 4) if i else (-4, 0, 28):
             for out in ([far[i] + shift, P << 8], [P << 8, far[i] + shift]):
                 _refused(INV, rf.rf_commit_draft, d, 4, 128, 512, 1024, *far, *[P] * 6, *out)
+
+
+W = 128          # elements of a row of _cache(): 2 heads of 64 channels; 50 rows, 2 sequences, 2 layers
+
+
+@pytest.mark.parametrize("strides,legal", [
+    # (row, sequence, layer), and whether rows of the whole cache lie apart
+    ((W, 50 * W, 100 * W), True), ((W, 100 * W, 50 * W), True),          # layers of sequences, sequences of layers
+    ((2 * W, W, 100 * W), True), ((4 * W, W, 2 * W), True), ((4 * W, 2 * W, W), True),     # rows of both, between and outside
+    ((2 * W, 100 * W, W), True), ((3 * W, 200 * W, 3 * 49 * W + W), True),
+    ((W, 50 * W, 50 * W), False), ((W, 50 * W, 99 * W), False), ((W, 49 * W, 100 * W), False), ((W, 100 * W, 49 * W), False),
+    ((2 * W, W, 99 * W), False), ((2 * W, W - 8, 100 * W), False), ((3 * W, W, 2 * W), False), ((4 * W, W, W), False)])
+def test_caches_may_be_nested_in_any_order_but_not_overlap(strides, legal):
+    names = ("row_stride", "seq_stride", "layer_stride")
+    d = _cache(**dict(zip(names, strides)))
+    assert (rf.rf_evict_workspace_bytes(d, 10) > 0) == legal
+    at = {r * strides[0] + b * strides[1] + l * strides[2] for r in range(50) for b in range(2) for l in range(2)}
+    places = sorted(at)
+    apart = len(places) == 200 and all(y - x >= W for x, y in zip(places, places[1:]))
+    assert apart == legal                                                # the parameters themselves
+    if not legal:
+        _refused(ALIGN, rf.rf_evict, d, 10, 0, 0, *[P] * 9, None, P, 1 << 40)
+        _refused(ALIGN, rf.rf_commit_draft, d, 4, 128, 512, 1024, *[P] * 12)
+
+
+@pytest.mark.parametrize("stride,legal", [(50 * W, True), (50 * W - 8, False), (8, False)])
+def test_layers_of_a_single_sequence_may_not_overlap(stride, legal):
+    d = _cache(n_seqs=1, layer_stride=stride, seq_stride=0)
+    assert (rf.rf_evict_workspace_bytes(d, 10) > 0) == legal
+    assert rf.rf_evict_workspace_bytes(_cache(n_layers=1, n_seqs=1, layer_stride=0, seq_stride=0), 10) > 0
+    # strides whose spans pass 64 bits
+    assert rf.rf_evict_workspace_bytes(_cache(n_layers=65535, layer_stride=1 << 61, seq_stride=1 << 61), 10) == 0
+
+
+def test_small_caches_are_accepted_exactly_where_no_two_rows_overlap():
+    r = random.Random(1)
+    for _ in range(3000):
+        n_layers, n_seqs, rows, w = r.randint(1, 4), r.randint(1, 4), r.randint(1, 5), r.choice([8, 16])
+        row, seq, layer = r.randint(w // 8, 14) * 8, r.randint(0, 14) * 8, r.randint(0, 14) * 8
+        d = rf.rf_cache_desc(n_layers=n_layers, n_seqs=n_seqs, n_kv_heads=1, head_dim=w, capacity=rows, row_stride=row,
+                             seq_stride=seq, layer_stride=layer)
+        at = sorted(t * row + b * seq + l * layer for t in range(rows) for b in range(n_seqs) for l in range(n_layers))
+        assert (rf.rf_evict_workspace_bytes(d, 3) > 0) == all(y - x >= w for x, y in zip(at, at[1:]))
