@@ -260,7 +260,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       if (z > 0.0f) {
         if (tid == 0) sh.z[k] = z;
       } else {
-        --k;  // nothing would be left: the residual stays
+        --k;  // nothing would be left: the residual stays, and is read anew
+        applied = -1;
       }
       __syncthreads();
     }

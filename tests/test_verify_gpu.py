@@ -242,3 +242,27 @@ def test_commit_reads_its_inputs_before_it_writes_over_them(where):
         assert nl.tolist() == [x + c for x, c in zip(lens, cnt)]
     if nn is not None:
         assert nn.tolist() == [x + c for x, c in zip(nxt, cnt)]
+
+
+@pytest.mark.parametrize("V", [8, 140001], ids=["registers", "memory"])
+@pytest.mark.parametrize("with_draft", [False, True], ids=["outright", "draft-probabilities"])
+def test_verify_goes_on_from_the_row_that_an_empty_residual_leaves(V, with_draft):
+    """A refusal that would leave nothing is undone; the next refusal works on the row before it, not on nothing."""
+    par = [[-1, 0, 0, 0, 3]]
+    n = len(par[0])
+    target = torch.zeros((1, n, V), device=DEV)
+    target[0, 0, 2] = 0.5                       # half of a row: token 2 alone
+    target[0, 3, 5] = target[0, 4, 6] = 1.0
+    draft = None
+    if with_draft:                              # r/Z - q is empty each time: r = 0.5 at token 2 stays, Z = 1
+        draft = torch.zeros((1, n, V), device=DEV)
+        draft[0, 0, 2] = 1.0
+    tokens = torch.tensor([[0, 2, 1, 2, 5]], dtype=torch.int32, device=DEV)
+    # outright: token 2 refused (0.9 >= 0.5, nothing is left), token 1 refused (leaves token 2, Z = 0.5), token 2
+    # accepted (0.9 0.5 < 0.5); with draft probabilities: 0.9, then q(1) = 0 against r(1) = 0, then 0.4 < 0.5
+    u = torch.tensor([[0.0, 0.9, 0.9, 0.4 if with_draft else 0.9, 0.5]], device=DEV)
+    noise = torch.ones((1, V), device=DEV)
+    want, token, near = R.verify(target[0], None if draft is None else draft[0], tokens[0], par[0], u[0], noise[0])
+    assert want == [0, 3, 4] and token == 6
+    path, cnt, tok, st = _run(par, target, draft, tokens, u, noise, V)
+    assert st == 0 and path.tolist() == [[0, 3, 4, -1, -1]] and cnt.tolist() == [3] and tok.tolist() == [6]
