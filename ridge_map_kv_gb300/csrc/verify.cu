@@ -76,20 +76,31 @@ struct VerifyShared : VerifyRefused<kDraft> {
 
 // x / z, correctly rounded, for many x and one z: with y the correctly rounded 1/z, the
 // remainder of x y corrects it (P. Markstein, "Computation of elementary functions on the
-// IBM RISC System/6000 processor", 1990). Quotients near the underflow limit may be off by
-// their last (denormal) bits.
+// IBM RISC System/6000 processor", 1990). For significands that was checked one by one: every
+// divisor with all dividends whose quotient lies within 24 / 2z units of a rounding boundary,
+// 535 million pairs. It takes 1/z, the quotient and the remainder to be normal numbers:
+// divisors from 2^-100 to 2^16 and dividends from 2^-100 on (or 0; a divisor of 1 takes any).
+// The others, of rows that are nearly empty or hold almost nothing, are divided.
 __device__ __forceinline__ float quotient(float x, float z, float y) {
   const float q = __fmul_rn(x, y);
   return __fmaf_rn(__fmaf_rn(-q, z, x), y, q);
 }
+constexpr float kQuotientLeast = 0x1p-100f, kQuotientMost = 0x1p16f;
+__device__ __forceinline__ bool quotient_takes(float z) { return z >= kQuotientLeast && z <= kQuotientMost; }
+// The bits of x - 1, so that 0 is larger than any: quotient() takes x whose order is not below this.
+__device__ __forceinline__ unsigned quotient_order(float x) { return __float_as_uint(x) - 1u; }
+constexpr unsigned kQuotientOrder = (27u << 23) - 1u;  // of 2^-100
 
 // r_k(t) from p(t), q(t) and the refusals.
 template <bool kDraft>
 __device__ __forceinline__ float residual(const VerifyShared<kDraft>& sh, float p, float q, int t, int k) {
   float r = p;
   for (int j = 0; j < k; ++j) {
-    if constexpr (kDraft) r = fmaxf(__fsub_rn(quotient(r, sh.z[j], __frcp_rn(sh.z[j])), q), 0.0f);
-    else r = sh.token[sh.refused[j]] == t ? 0.0f : r;
+    if constexpr (kDraft) {
+      const float z = sh.z[j];
+      const bool quick = z == 1.0f || (quotient_takes(z) && quotient_order(r) >= kQuotientOrder);
+      r = fmaxf(__fsub_rn(quick ? quotient(r, z, __frcp_rn(z)) : __fdiv_rn(r, z), q), 0.0f);
+    } else r = sh.token[sh.refused[j]] == t ? 0.0f : r;
   }
   return r;
 }
@@ -189,10 +200,23 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       }
       for (; applied < k; ++applied) {
         if constexpr (kDraft) {
-          const float z = sh.z[applied], y = __frcp_rn(z);
+          const float z = sh.z[applied];
+          unsigned least = kQuotientOrder;
+          if (z != 1.0f) {
 #pragma unroll
-          for (int i = 0; i < kVerifySlots; ++i)
-            if (i < slots) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
+            for (int i = 0; i < kVerifySlots; ++i) least = min(least, quotient_order(r[i]));
+            if (!quotient_takes(z)) least = 0;
+          }
+          if (least >= kQuotientOrder) {
+            const float y = __frcp_rn(z);
+#pragma unroll
+            for (int i = 0; i < kVerifySlots; ++i)
+              if (i < slots) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kVerifySlots; ++i)
+              if (i < slots) r[i] = fmaxf(__fsub_rn(__fdiv_rn(r[i], z), q[i]), 0.0f);
+          }
         } else {
           const int gone = sh.token[sh.refused[applied]] - v0 - tid;
 #pragma unroll

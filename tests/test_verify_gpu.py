@@ -2,6 +2,7 @@
 to equal those of the definition in 64 bits. Decisions that a rounding could turn are
 counted by the reference: their margins are kept above 1e-4 (a chain of refusals rounds
 each number a few times, 1e-6 at most, and its sums by 1e-5 at most)."""
+import numpy as np
 import pytest
 import torch
 
@@ -266,3 +267,55 @@ def test_verify_goes_on_from_the_row_that_an_empty_residual_leaves(V, with_draft
     assert want == [0, 3, 4] and token == 6
     path, cnt, tok, st = _run(par, target, draft, tokens, u, noise, V)
     assert st == 0 and path.tolist() == [[0, 3, 4, -1, -1]] and cnt.tolist() == [3] and tok.tolist() == [6]
+
+
+def _quotient_rows(B, seed, orders):
+    """float32 (r, c, Z, Q): Z = r + c and Q = r / Z as IEEE rounds them, r <= Z and Q <= r. orders: the powers of two
+    below which r lies, in turns."""
+    g = np.random.default_rng(seed)
+    r = np.ldexp(g.uniform(0.5, 1.0, B).astype(np.float32), np.array(orders)[np.arange(B) % len(orders)]).astype(np.float32)
+    r = np.maximum(r, np.float32(1e-44))
+    c = np.exp2(g.uniform(0.5, 6.0, B)).astype(np.float32)
+    if max(orders) > 20:
+        c = c * r
+    z = r + c
+    return r, c, z, r / z
+
+
+@pytest.mark.parametrize("orders", [(0, -1, -5), (-90, -99, -100, -101, -110), (-120, -125, -127, -135, -140, -146), (30, 60)],
+                         ids=["usual", "small", "denormal", "large"])
+@pytest.mark.parametrize("B,V", [(20000, 4), (120, 131080)], ids=["registers", "memory"])
+def test_verify_rounds_quotients_as_ieee_does(B, V, orders):
+    """Two refusals leave r/Z - q at token 1, where q is the quotient or the number below it: the token is drawn if and
+    only if the kernel's quotient is larger than q, and token 2 otherwise."""
+    r, c, z, quot = _quotient_rows(B, 7, orders)
+    for below in (False, True):
+        q = np.nextafter(quot, np.float32(0.0)) if below else quot
+        p = q + r
+        use = (p - q == r) & (quot > 0)         # what the first refusal leaves is r itself
+        assert use.sum() >= B // 4
+        target, draft = torch.zeros((B, 3, V)), torch.zeros((B, 3, V))
+        target[:, 0, 0], draft[:, 0, 0] = 0.25, 0.5
+        target[:, 0, 1], draft[:, 0, 1] = torch.from_numpy(p), torch.from_numpy(q)
+        target[:, 0, 2] = torch.from_numpy(c)
+        noise = torch.ones((B, V))
+        noise[:, 1], noise[:, 2] = 1e-30, 1e30
+        u = torch.full((B, 3), 0.99, device=DEV)
+        tokens = torch.zeros((B, 3), dtype=torch.int32, device=DEV)
+        path, cnt, tok, st = _run([[-1, 0, 0]] * B, target.cuda(), draft.cuda(), tokens, u, noise.cuda(), V)
+        assert st == 0 and bool((cnt == 1).all())
+        assert np.array_equal(tok.numpy()[use], np.full(use.sum(), 1 if below else 2))
+
+
+@pytest.mark.parametrize("V", [40, 140001], ids=["registers", "memory"])
+def test_verify_divides_by_sums_whose_reciprocal_is_infinite(V):
+    """The first refusal leaves 8e-40 in all; the second one's residual is that over itself, less nothing."""
+    target, draft = torch.zeros((1, 3, V), device=DEV), torch.zeros((1, 3, V), device=DEV)
+    target[0, 0, 0], draft[0, 0, 0] = 0.9, 0.95
+    target[0, 0, 20], target[0, 0, 30] = 3e-40, 5e-40
+    noise = torch.full((1, V), 1e10, device=DEV)    # under which 5e-40 itself would vanish
+    u = torch.full((1, 3), 0.99, device=DEV)
+    path, cnt, tok, st = _run([[-1, 0, 0]], target, draft, torch.zeros((1, 3), dtype=torch.int32, device=DEV), u, noise, V)
+    want, token, _ = R.verify(target[0], draft[0], [0, 0, 0], [-1, 0, 0], u[0], noise[0])
+    assert (want, token) == ([0], 30)
+    assert st == 0 and path.tolist() == [[0, -1, -1]] and tok.tolist() == [30]
