@@ -52,12 +52,17 @@ struct VerifyArgs {
 // Tokens of a CTA: whole 16-byte groups.
 __host__ __device__ inline int verify_share(int vocab, int ctas) { return ((vocab + ctas - 1) / ctas + 3) & ~3; }
 
-// What only the form without draft probabilities has, so that the other cannot read it.
+// What one form has, so that the other cannot read it. With draft probabilities, for each refusal
+// at the current node: 1 / Z_j and the least order (quotient_order) of what is divided by it quickly.
 template <bool kDraft>
-struct VerifyRefused {};
+struct VerifyRefused {
+  float inverse[RF_TREE_MAX_NODES];
+  unsigned least[RF_TREE_MAX_NODES];
+};
+// Without: its node.
 template <>
 struct VerifyRefused<false> {
-  int refused[RF_TREE_MAX_NODES];  // nodes of the refusals at the current node
+  int refused[RF_TREE_MAX_NODES];
 };
 template <bool kDraft>
 struct VerifyShared : VerifyRefused<kDraft> {
@@ -85,11 +90,12 @@ __device__ __forceinline__ float quotient(float x, float z, float y) {
   const float q = __fmul_rn(x, y);
   return __fmaf_rn(__fmaf_rn(-q, z, x), y, q);
 }
-constexpr float kQuotientLeast = 0x1p-100f, kQuotientMost = 0x1p16f;
-__device__ __forceinline__ bool quotient_takes(float z) { return z >= kQuotientLeast && z <= kQuotientMost; }
-// The bits of x - 1, so that 0 is larger than any: quotient() takes x whose order is not below this.
+// The bits of x less 1, so that 0 is larger than any; and the least of them that quotient() takes
+// for a divisor.
 __device__ __forceinline__ unsigned quotient_order(float x) { return __float_as_uint(x) - 1u; }
-constexpr unsigned kQuotientOrder = (27u << 23) - 1u;  // of 2^-100
+__device__ __forceinline__ unsigned quotient_least(float z) {
+  return z == 1.0f ? 0u : z >= 0x1p-100f && z <= 0x1p16f ? __float_as_uint(0x1p-100f) - 1u : 0xffffffffu;
+}
 
 // r_k(t) from p(t), q(t) and the refusals.
 template <bool kDraft>
@@ -97,9 +103,8 @@ __device__ __forceinline__ float residual(const VerifyShared<kDraft>& sh, float 
   float r = p;
   for (int j = 0; j < k; ++j) {
     if constexpr (kDraft) {
-      const float z = sh.z[j];
-      const bool quick = z == 1.0f || (quotient_takes(z) && quotient_order(r) >= kQuotientOrder);
-      r = fmaxf(__fsub_rn(quick ? quotient(r, z, __frcp_rn(z)) : __fdiv_rn(r, z), q), 0.0f);
+      const float x = quotient_order(r) >= sh.least[j] ? quotient(r, sh.z[j], sh.inverse[j]) : __fdiv_rn(r, sh.z[j]);
+      r = fmaxf(__fsub_rn(x, q), 0.0f);
     } else r = sh.token[sh.refused[j]] == t ? 0.0f : r;
   }
   return r;
@@ -173,10 +178,17 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
     }
     return;
   }
+  auto set_z = [&](int j, float z) {
+    sh.z[j] = z;
+    if constexpr (kDraft) {
+      sh.inverse[j] = __frcp_rn(z);
+      sh.least[j] = quotient_least(z);
+    }
+  };
   int cur = 0, k = 0, n_acc = 1, turn = 0;
   if (tid == 0) {
     sh.path[0] = 0;
-    sh.z[0] = 1.0f;
+    set_z(0, 1.0f);
   }
   __syncthreads();
 
@@ -200,15 +212,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       }
       for (; applied < k; ++applied) {
         if constexpr (kDraft) {
-          const float z = sh.z[applied];
-          unsigned least = kQuotientOrder;
-          if (z != 1.0f) {
+          const float z = sh.z[applied], y = sh.inverse[applied];
+          unsigned order = 0xffffffffu;
 #pragma unroll
-            for (int i = 0; i < kVerifySlots; ++i) least = min(least, quotient_order(r[i]));
-            if (!quotient_takes(z)) least = 0;
-          }
-          if (least >= kQuotientOrder) {
-            const float y = __frcp_rn(z);
+          for (int i = 0; i < kVerifySlots; ++i) order = min(order, quotient_order(r[i]));
+          if (order >= sh.least[applied]) {
 #pragma unroll
             for (int i = 0; i < kVerifySlots; ++i)
               if (i < slots) r[i] = fmaxf(__fsub_rn(quotient(r[i], z, y), q[i]), 0.0f);
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       __syncthreads();  // the refusals of the node left behind are read no more
       if (tid == 0) {
         sh.path[n_acc] = c;
-        sh.z[0] = 1.0f;
+        set_z(0, 1.0f);
       }
       ++n_acc;
       cur = c;
@@ -282,7 +290,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 1) k_verify(const __grid_const
       for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
       ++turn;
       if (z > 0.0f) {
-        if (tid == 0) sh.z[k] = z;
+        if (tid == 0) set_z(k, z);
       } else {
         --k;  // nothing would be left: the residual stays, and is read anew
         applied = -1;
