@@ -45,7 +45,7 @@ constexpr int kWtStep = 256;         // columns of a step
 constexpr int kWtMaxStages = 12;
 constexpr int kWtSlab = kWtTile * 128;
 constexpr int kWtQBytes = 640 * 128 * 2;  // the most that queries may take
-constexpr int kWtNever = INT32_MIN;       // position of a column that no key is seen from
+constexpr int kWtNever = INT32_MIN;       // position of a column that counts for no key
 constexpr float kWtLog2e = 1.4426950408889634f;
 
 struct WeightArgs {
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
         if (r < rows && stat[g] == -INFINITY) empty |= 1u << g;
         if (r < cols) {
           neg_lse[qb * a.rows_cap + r] = stat[g] == -INFINITY ? -INFINITY : -stat[g] * kWtLog2e;
-          position[qb * a.rows_cap + r] = r < rows ? r / a.group : kWtNever;
+          position[qb * a.rows_cap + r] = r < rows && stat[g] != -INFINITY ? r / a.group : kWtNever;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -469,7 +469,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
           tc_fence_after();
           const uint32_t from = tmem + lanes + buf * kWtStep;
           const float* lse0 = item_lse + i * cols;
+          bool by_column = masked;
           if (!masked) {
+            const float2 b0 = s0, b1 = s1;
             int x = c0;
             for (; x + 32 <= c1; x += 32) {
               uint32_t r[32];
@@ -483,7 +485,16 @@ __global__ void __launch_bounds__(kWtThreads, 1) k_attn_weights(const __grid_con
               tmem_wait_ld16(r);
               add_weights(r, lse0 + x, sc, s0, s1);
             }
-          } else {
+            // A key with an infinity gives NaN in the columns of zeros (beyond the queries, or of one
+            // that sees nothing), which do not count: its warp takes the step again without them.
+            const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+            if (__any_sync(0xffffffffu, sum != sum)) {
+              s0 = b0;
+              s1 = b1;
+              by_column = true;
+            }
+          }
+          if (by_column) {
             for (int x = c0; x < c1; x += 16) {
               uint32_t r[16];
               tmem_ld16(from + x, r);

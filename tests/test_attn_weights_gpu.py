@@ -171,3 +171,36 @@ def test_weights_of_all_nodes_equal_those_along_the_path_of_all_nodes(n, G, hd, 
     assert torch.equal(out.view(torch.int32), along.view(torch.int32))
     want, bound = R.weights(q, lse, k, lens, paths, 0.5, score, scale)
     assert R.within(out, want, bound) <= 1.0
+
+
+@pytest.mark.parametrize("B,n,H,G,hd,m,take", [
+    (1, 7, 2, 4, 128, 400, 7),         # 28 queries in 32 columns
+    (2, 9, 1, 3, 64, 300, 5),          # 15 in 16, two sequences
+    (1, 64, 1, 10, 128, 300, 64),      # 640 in 672, three steps
+    (1, 16, 1, 16, 64, 500, 16),       # 256: no column is spare but that of a query that sees nothing
+])
+def test_weights_of_keys_with_infinities_are_those_of_the_queries_alone(B, n, H, G, hd, m, take):
+    """A key with an infinity whose product with every query is -inf receives nothing: spare columns, and the query that
+    sees nothing, do not make it NaN. A key that is NaN makes its own sum NaN and no other."""
+    q = R.randn((B, n, H * G, hd), 1)
+    q[..., 3] = -q[..., 3].abs() - 0.125
+    k = R.randn((B, m, H, hd), 2)
+    paths = [list(range(n - take, n)) for _ in range(B)]
+    path = torch.full((B, n), -1, dtype=torch.int32)
+    path[:, :take] = torch.arange(n - take, n)
+    args = (None, None) if take == n else (path.cuda(), torch.full((B,), take, dtype=torch.int32, device=DEV))
+    lse = _stats(q, k, [m] * B, paths, 0.1, H)
+    lse[:, n - 2, 0] = -math.inf
+    score = torch.rand((B, H, m), device=DEV)
+    ln = torch.full((B,), m, dtype=torch.int32, device=DEV)
+    plain, out = torch.full_like(score, -3.0), torch.full_like(score, -3.0)
+    assert _call(q, lse, *args, k, ln, 0.5, score, plain, 0.1) == 0
+    assert bool(torch.isfinite(plain).all())
+    odd, bad = [0, 50, 127, 130, m - take, m - 1], 77
+    k[:, odd, :, 3] = math.inf
+    k[:, bad] = math.nan
+    assert _call(q, lse, *args, k, ln, 0.5, score, out, 0.1) == 0
+    assert torch.equal(out[..., odd], score[..., odd] * 0.5)
+    assert bool(torch.isnan(out[..., bad]).all())
+    rest = [t for t in range(m) if t not in odd + [bad]]
+    assert R.within(out[..., rest], plain[..., rest].double(), 8 * take * G * R.U24 * plain[..., rest].double() + 1e-30) <= 1.0
