@@ -615,7 +615,7 @@ typedef struct rf_attn_desc {
   int64_t cache_seq_stride;
   int64_t out_row_stride;   /* out, likewise                                            */
   int64_t out_seq_stride;
-  double scale;             /* scores are scale * q.k (scale > 0)                       */
+  double scale;             /* scores are scale * q.k; > 0, scale / ln 2 finite in fp32 */
   uint64_t flags;           /* 0                                                        */
 } rf_attn_desc;
 

@@ -954,8 +954,10 @@ rf_status check_attn_desc(const rf_attn_desc* d) {
   if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_seqs < 0 || d->n_q_heads <= 0 || d->n_kv_heads <= 0 || d->n_nodes <= 0 || d->capacity <= 0)
     return fail(RF_ERR_INVALID_ARG, "need n_seqs >= 0, n_q_heads, n_kv_heads, n_nodes, capacity > 0");
-  if (!(d->scale > 0.0) || !std::isfinite(static_cast<float>(d->scale)) || !(static_cast<float>(d->scale) > 0.0f))
-    return fail(RF_ERR_INVALID_ARG, "scale must be a finite fp32 number > 0");
+  // (exponents are formed in base 2)
+  const float scale = static_cast<float>(d->scale);
+  if (!(d->scale > 0.0) || !(scale > 0.0f) || !std::isfinite(scale * kAtLog2e))
+    return fail(RF_ERR_INVALID_ARG, "scale must be > 0 and scale / ln 2 finite in fp32");
   if (d->flags != 0) return fail(RF_ERR_INVALID_ARG, "flags must be 0");
   if (d->head_dim != 64 && d->head_dim != 128) return fail(RF_ERR_SHAPE, "head_dim must be 64 or 128");
   if (d->n_q_heads % d->n_kv_heads != 0 || d->n_q_heads / d->n_kv_heads > 128)

@@ -279,3 +279,13 @@ def test_small_caches_are_accepted_exactly_where_no_two_rows_overlap():
                              seq_stride=seq, layer_stride=layer)
         at = sorted(t * row + b * seq + l * layer for t in range(rows) for b in range(n_seqs) for l in range(n_layers))
         assert (rf.rf_evict_workspace_bytes(d, 3) > 0) == all(y - x >= w for x, y in zip(at, at[1:]))
+
+
+def test_scales_whose_base_2_form_overflows_are_refused():
+    """Scores are taken to base 2, where the largest fp32 numbers turn infinite (and 0 times that NaN)."""
+    for scale, legal in ((2.3e38, True), (2.4e38, False), (3.4e38, False)):
+        d = _attn(scale=scale)
+        assert (rf.rf_attn_workspace_bytes(d) > 0) == legal
+        if not legal:
+            _refused(INV, rf.rf_tree_attention, d, P, P, P, P, P, P, P, P, P, None, P, 1 << 40)
+            _refused(INV, rf.rf_attn_weights, d, P, P, P, P, P, P, 1.0, P, P, None, P, 1 << 40)
