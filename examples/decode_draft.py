@@ -174,35 +174,44 @@ class Decoder:
         return path, self.n_path, self.token
 
 
-def draft(table, last, n: int):
-    """A tree of n nodes for each sequence: what followed each token before, breadth first, the most recent first;
+def tree(table, token: int, n: int, vocab: int):
+    """Tokens and parents of a tree of n nodes: what followed each token before, breadth first, the most recent first;
     other tokens where nothing is known."""
-    tokens, parents = [], []
-    for t in last:
-        tok, par = [int(t)], [-1]
-        at = 0
-        while len(tok) < n:
-            known = table.get(tok[at], [])[-2:][::-1] or [(tok[at] * 7 + 3) % 97]
-            for x in known[: n - len(tok)]:
-                tok.append(int(x))
-                par.append(at)
-            at += 1
-        tokens.append(tok)
-        parents.append(par)
+    tok, par = [int(token)], [-1]
+    at = 0
+    while len(tok) < n:
+        known = table.get(tok[at], [])[-2:][::-1] or [(tok[at] * 7 + 3) % min(97, vocab)]
+        for x in known[: n - len(tok)]:
+            tok.append(int(x))
+            par.append(at)
+        at += 1
+    return tok, par
+
+
+def draft(table, last, n: int, vocab: int):
+    """A tree of n nodes for each sequence."""
+    tokens, parents = zip(*(tree(table, int(t), n, vocab) for t in last))
     return (torch.tensor(tokens, dtype=torch.int32, device="cuda"), torch.tensor(parents, dtype=torch.int32, device="cuda"))
+
+
+def capacity(n0: int, n_tokens: int, nodes: int, budget: int) -> int:
+    """Cache rows that any sequence may need. Every step gives the slowest sequence a token at least, so there are fewer
+    than n_tokens; each may add all nodes to the fastest, of which a budget leaves its rows until the next step."""
+    most = n0 + n_tokens * nodes
+    return min(most, max(n0, budget + nodes)) if budget else most
 
 
 def generate(model: Model, prompts, n_tokens: int, nodes: int, budget: int = 0, sample: bool = False, seed: int = 1):
     """Decodes n_tokens (or a few more) for every prompt; returns lists of tokens, the steps taken and the decoder."""
     B, n0 = prompts.shape
-    dec = Decoder(model, B, n0 + n_tokens + 2 * nodes, max(nodes, n0), budget)
+    dec = Decoder(model, B, capacity(n0, n_tokens, nodes, budget), max(nodes, n0), budget)
     g = torch.Generator(device="cuda").manual_seed(seed)
     last = dec.prompt(prompts)
     out = [[int(x)] for x in last]
     table: dict[int, list[int]] = {}
     steps = 0
     while min(len(o) for o in out) < n_tokens:
-        tokens, parents = draft(table, last, nodes)
+        tokens, parents = draft(table, last, nodes, model.cfg.vocab)
         path, n_path, nxt = dec.step(tokens, parents, g, sample)
         steps += 1
         tok, pth, cnt, last = tokens.tolist(), path.tolist(), n_path.tolist(), nxt.clone()

@@ -127,3 +127,41 @@ def test_sampled_decoding_repeats_with_its_seed(ex):
     a = ex.generate(model, prompts, 12, 7, sample=True, seed=3)
     b = ex.generate(model, prompts, 12, 7, sample=True, seed=3)
     assert a[0] == b[0] and a[1] == b[1] and rf.rf_last_error() == ""
+
+
+@pytest.mark.parametrize("budget", [0, 32])
+def test_sequences_that_accept_unevenly_fit_the_cache(ex, monkeypatch, budget):
+    """Sequence 0 accepts every node of every step, sequence 1 only its last token: the model's logits are replaced, the
+    rows are its own. The cache holds both until the slow one is done."""
+    nodes, n0, n_tokens = 8, 40, 24
+    forward = ex.Decoder.forward
+
+    def steered(self, tokens, parents):
+        logits = torch.zeros_like(forward(self, tokens, parents))
+        follow = torch.cat([tokens[0, 1:], tokens.new_zeros(1)]).long()
+        logits[0, torch.arange(tokens.shape[1]), follow] = 10.0
+        logits[1, :, 200] = 10.0                    # never drafted
+        return logits
+
+    def chain(table, last, n, vocab):
+        tokens = [[int(t)] + list(range(1, n)) for t in last]
+        parents = [list(range(-1, n - 1))] * len(tokens)
+        return torch.tensor(tokens, dtype=torch.int32).cuda(), torch.tensor(parents, dtype=torch.int32).cuda()
+
+    monkeypatch.setattr(ex.Decoder, "forward", steered)
+    monkeypatch.setattr(ex, "draft", chain)
+    model = ex.Model(ex.Config())
+    prompts = torch.randint(0, 200, (2, n0), generator=torch.Generator().manual_seed(8)).to(torch.int32).cuda()
+    out, steps, dec = ex.generate(model, prompts, n_tokens, nodes, budget)
+    assert steps == n_tokens - 1
+    assert out[0] == ([0] + (list(range(1, nodes)) + [0]) * n_tokens)[:n_tokens]
+    assert out[1] == [200] * n_tokens
+    rows = [n0 + steps * nodes, n0 + steps]
+    assert dec.next_pos.tolist() == rows and dec.lens.tolist() == ([budget, budget] if budget else rows)
+
+
+def test_a_small_vocabulary_decodes(ex):
+    model = ex.Model(ex.Config(vocab=23))
+    prompts = torch.randint(0, 23, (2, 10), generator=torch.Generator().manual_seed(9)).to(torch.int32).cuda()
+    out, _, dec = ex.generate(model, prompts, 12, 9, sample=True)
+    assert all(0 <= t < 23 for o in out for t in o) and int(dec.status.item()) == 0
