@@ -212,3 +212,19 @@ def test_evict_writes_lengths_over_the_next_positions(cap, keep):
         assert bool(((pos[..., :keep] >= cap - 20).sum(-1) == 20).all())      # the newest twenty of every head
         results.append((k, v, score[..., :keep], pos[..., :keep]))
     assert all(_same(x, y) for x, y in zip(*results))
+
+
+@pytest.mark.parametrize("inplace", [False, True], ids=["apart", "in-place"])
+@pytest.mark.parametrize("kind", ["plain", "ties", "odd"])
+@pytest.mark.parametrize("cap,keep", [(17408, 5000), (17409, 5000), (17409, 17300), (32768, 8192), (32768, 32700),
+                                      (49152, 100), (49152, 49152), (49153, 20000), (49153, 49050)])
+def test_evict_of_long_caches(cap, keep, kind, inplace):
+    """Either side of the capacities at which ranks leave registers and shared memory, with more and with fewer moves
+    than one launch makes (the latter where the new lengths lie apart), whole and ragged."""
+    B, H, hd, sink, recent = 2, 1, 8, 4, 300
+    lens = [cap, max(1, cap - 77)]
+    r = _run(1, B, H, hd, cap, keep, sink, recent, lens, kind, inplace, seed=keep)
+    assert r["st"] == 0 and r["nl"].tolist() == [min(n, keep) for n in lens]
+    wk, wv, ws, wp = _expect(r, 1, B, H, hd, cap, keep, sink, recent, lens, inplace)
+    assert _same(r["k"], wk) and _same(r["v"], wv)
+    assert _same(r["so"], ws) and torch.equal(r["po"], wp)
