@@ -550,6 +550,7 @@ rf_status rf_select_sources(const rf_select_desc* desc, const rf_calib_stats* st
 typedef struct rf_rope_desc {
   int64_t n_rows;       /* tokens, at most 2^24                                         */
   int64_t n_heads;      /* heads of a row, head_dim channels each, one after another    */
+                        /* (at most 65535)                                              */
   int64_t head_dim;     /* a multiple of 8, at most 256                                 */
   int64_t rot_dim;      /* the first rot_dim channels of a head turn (even, at most     */
                         /* head_dim); the others are copied                             */
@@ -600,13 +601,13 @@ rf_status rf_tree_build(int64_t n_seqs, int64_t n_nodes, const int32_t* parents,
                         uint64_t* mask, int32_t* positions, int32_t* dev_status, rf_stream_t stream);
 
 typedef struct rf_attn_desc {
-  int64_t n_seqs;           /* sequences                                                */
+  int64_t n_seqs;           /* sequences, at most 2^20                                  */
   int64_t n_q_heads;        /* query heads, a multiple of n_kv_heads; query head i reads */
                             /* KV head i / (n_q_heads/n_kv_heads); at most 128 per KV head */
   int64_t n_kv_heads;
   int64_t head_dim;         /* 64 or 128                                                */
   int64_t n_nodes;          /* queries (drafted rows) per sequence                      */
-  int64_t capacity;         /* cache rows per sequence, 0 <= lens[b] <= capacity        */
+  int64_t capacity;         /* cache rows per sequence, 0 <= lens[b] <= capacity <= 2^30 */
   int64_t q_row_stride;     /* q: element b*q_seq_stride + i*q_row_stride + head*head_dim + c */
   int64_t q_seq_stride;
   int64_t draft_row_stride; /* k_draft, v_draft, likewise                               */
@@ -625,7 +626,8 @@ typedef struct rf_attn_desc {
  *   lse = ln sum_{j in S} exp(scale q.k_j),  out = sum_{j in S} exp(scale q.k_j - lse) v_j.
  *   tree_mask  [n_seqs][n_nodes][RF_TREE_WORDS(n_nodes)] uint64 (device), any bits (n_nodes
  *              <= RF_TREE_MAX_NODES; bits beyond n_nodes are ignored), or NULL: node i
- *              sees drafted rows j <= i (rows in order, n_nodes <= 2^20)
+ *              sees drafted rows j <= i (rows in order, n_nodes <= 2^20; < 2^20 with more
+ *              than 64 query heads per KV head)
  *   lens       [n_seqs] int32 (device); a length outside [0, capacity] records
  *              RF_ERR_INVALID_ARG in *dev_status and that sequence is not written
  *   out bf16;  lse [n_seqs][n_nodes][n_q_heads] fp32 (may be NULL)
@@ -641,7 +643,7 @@ rf_status rf_tree_attention(const rf_attn_desc* desc, const rf_bf16* q,
                             void* workspace, size_t workspace_bytes, rf_stream_t stream);
 
 typedef struct rf_verify_desc {
-  int64_t n_seqs;
+  int64_t n_seqs;     /* at most 2^24                                                  */
   int64_t n_nodes;    /* 1 .. RF_TREE_MAX_NODES                                        */
   int64_t vocab;      /* V <= 2^31 - 65536                                             */
   int64_t ld_target;  /* row strides, >= vocab (any value)                              */
@@ -676,7 +678,7 @@ rf_status rf_verify_draft(const rf_verify_desc* desc, const float* target, const
 /* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c.
  * Layers, sequences and rows may be nested in any order; no two rows may overlap. */
 typedef struct rf_cache_desc {
-  int64_t n_layers;
+  int64_t n_layers;     /* at most 65535, as n_seqs and n_kv_heads                      */
   int64_t n_seqs;
   int64_t n_kv_heads;
   int64_t head_dim;     /* a multiple of 8, at most 256                                 */
@@ -711,12 +713,13 @@ rf_status rf_commit_draft(const rf_cache_desc* desc, int64_t n_nodes, int64_t dr
  *   score_out[b][h][t] = decay score_in[b][h][t]
  *       + sum over j with t <= lens[b] - n + j, and the KV head's query heads a, of
  *         exp(scale q[path[j]][a].k_t - lse[path[j]][a]),   n = n_path[b] or n_nodes.
- * q, lse, desc as for rf_tree_attention; score [n_seqs][n_kv_heads][capacity] fp32,
- * score_out may be score_in; entries t >= lens[b] are not written. A query whose lse is
- * -inf adds nothing. decay 0 does not read score_in (which may be NULL then). A sequence
- * with a length, count or path out of range records RF_ERR_INVALID_ARG and is not
- * written (n <= lens[b] is required). Sums are fp32, in an order that depends on the
- * sizes alone. */
+ * q, lse, desc as for rf_tree_attention, with n_seqs <= 1024; score
+ * [n_seqs][n_kv_heads][capacity] fp32, score_out may be score_in; entries t >= lens[b] are
+ * not written. A query whose lse is -inf adds nothing. decay 0 does not read score_in (which
+ * may be NULL then). A sequence with a length, count or path out of range records
+ * RF_ERR_INVALID_ARG and is not written (n <= lens[b] is required). Sums are fp32, in an
+ * order that depends on the sizes alone. The workspace (256 bytes) is required, though
+ * nothing is kept in it at present. */
 size_t rf_attn_weights_workspace_bytes(const rf_attn_desc* desc);
 rf_status rf_attn_weights(const rf_attn_desc* desc, const rf_bf16* q, const float* lse,
                           const int32_t* path, const int32_t* n_path,
@@ -735,7 +738,7 @@ rf_status rf_attn_weights(const rf_attn_desc* desc, const rf_bf16* q, const floa
  *       may be in; entries beyond new_lens[b] are not written
  *   new_lens [n_seqs] int32: lens itself (or next_pos), or apart from lens
  * A length outside [0, capacity] records RF_ERR_INVALID_ARG and that sequence stays as
- * it is. keep >= 1. */
+ * it is. keep >= 1, n_layers * n_seqs * n_kv_heads <= 65535. */
 size_t rf_evict_workspace_bytes(const rf_cache_desc* desc, int64_t keep);
 rf_status rf_evict(const rf_cache_desc* desc, int64_t keep, int64_t n_sink, int64_t n_recent,
                    const int32_t* lens, const int32_t* next_pos, rf_bf16* k_cache, rf_bf16* v_cache,

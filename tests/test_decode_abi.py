@@ -289,3 +289,14 @@ def test_scales_whose_base_2_form_overflows_are_refused():
         if not legal:
             _refused(INV, rf.rf_tree_attention, d, P, P, P, P, P, P, P, P, P, None, P, 1 << 40)
             _refused(INV, rf.rf_attn_weights, d, P, P, P, P, P, P, 1.0, P, P, None, P, 1 << 40)
+
+
+def test_the_header_states_the_limits_of_the_decoding_calls():
+    """What the calls refuse by size alone is found in the header beside them."""
+    text = re.sub(r"\n \* ?", " ", open(os.path.join(ROOT, "include", "rf.h")).read())
+    assert "n_layers * n_seqs * n_kv_heads <= 65535" in text and "with n_seqs <= 1024" in text
+    ok = dict(n_kv_heads=15, row_stride=960, seq_stride=48000, layer_stride=96000)
+    assert rf.rf_evict_workspace_bytes(_cache(n_layers=2184, **ok), 10) > 0
+    assert rf.rf_evict_workspace_bytes(_cache(n_layers=2185, **ok), 10) == 0            # 65,550
+    assert rf.rf_attn_weights_workspace_bytes(_attn(n_seqs=1024)) == 256
+    assert rf.rf_attn_weights_workspace_bytes(_attn(n_seqs=1025)) == 0
