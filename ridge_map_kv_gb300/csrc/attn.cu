@@ -41,8 +41,11 @@
 //
 // Measured (128 channels): one token, 40 query heads on 8, over 32,767 rows: 33 us, 4.1 TB/s of
 // the cache's bytes (22 us of it in the tiles). 16 trees of 64 nodes, 32 heads on 8, over 913 to
-// 16,384 rows: 132 us, 4.7 TB/s and 1,150 TFLOP/s. 4,096 rows in order over 28,672, 40 heads on
-// 8: 1.86 ms, 1,390 TFLOP/s, 0.74 of the measured burst rate. A stream's turn at the tensor
+// 16,384 rows: 138 us, 4.5 TB/s and 1,100 TFLOP/s. 4,096 rows in order over 28,672, 40 heads on
+// 8: 2.03 ms in long runs, at the power limit (1,270 TFLOP/s, 0.68 of the measured burst rate and
+// 0.75 of the sustained), 1.84 ms from rest. 64 channels: 22 us, 105 us and 1.55 ms; the bytes
+// and products are half, the exponentials (32 a clock and SM: 0.54 ms of the last) the same.
+// A stream's turn at the tensor
 // cores, for 16 products that take 1,030 cycles back to back, lasts about 1,400: the wait between
 // the two parts of the weights, the issue beside eight busy warps, and the hand-over to the other
 // stream. A shorter softmax does not change that (weights formed against the last maximum while

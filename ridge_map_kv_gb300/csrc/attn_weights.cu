@@ -9,7 +9,7 @@
 //
 // Bound: the keys' bytes up to a few hundred queries (2 hd bytes a key against 2 R hd
 // flops and R exponentials); beyond, the exponentials and the product. Measured (128 channels):
-// 16 paths of up to 7 nodes, 32 heads on 8, over 913 to 16,384 rows: 62 us, 5.0 TB/s; the last 64
+// 16 paths of up to 7 nodes, 32 heads on 8, over 913 to 16,384 rows: 62 us, 4.9 TB/s; the last 64
 // of 32,768 rows, 20 heads on 2: 24 us, of which 8 are launch and queries (27.5 us with the
 // queries gathered row by row); the exponentials of 672 columns a key fill most of the rest.
 //
@@ -626,8 +626,10 @@ extern "C" rf_status rf_attn_weights(const rf_attn_desc* d, const rf_bf16* q, co
   const int rows = a.j_max * a.group;
   const int steps = std::max(1, (rows + kWtStep - 1) / kWtStep);
   a.rows_cap = std::max(16, (((rows + steps - 1) / steps + 15) & ~15)) * steps;
-  // A second query buffer lets the next item's queries come in early; the ring keeps at
-  // least five slabs (80 KB: more than the bytes in flight that hide memory's latency).
+  // A second query buffer lets the next item's queries come in early, where the ring keeps at
+  // least five slabs beside it (80 KB: more than the bytes in flight that hide memory's latency).
+  // With one buffer the ring gets what is left: three slabs beside 640 query rows of 128 channels,
+  // two with a thousand sequences as well.
   auto fixed = [&](int bufs) {
     return 1024 + static_cast<size_t>(bufs) * a.rows_cap * (hd * 2 + 8) + ((sizeof(WeightShared) + 15) & ~size_t(15)) +
            static_cast<size_t>(B) * 8;

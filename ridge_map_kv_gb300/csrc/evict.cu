@@ -24,7 +24,7 @@
 // Bound: reading scores and positions and writing the kept ones (16 bytes a row) and the
 // moved rows' bytes twice; at a few rows a step, the latency of the selection. Measured (heads of
 // 128 channels): half of 320 units at 4,103 rows with 4,096 to stay 9.8 us, of which the counting
-// steps are most; 160 units of 16,384 rows with 4,096 to stay 121 us, of which the moves take 81
+// steps are most; 160 units of 16,384 rows with 4,096 to stay 122 us, of which the moves take 81
 // (at the memory's rate) and the selection 42 (instructions, and a second wave of 8 CTAs).
 #include <algorithm>
 
@@ -548,7 +548,11 @@ extern "C" rf_status rf_evict(const rf_cache_desc* d, int64_t keep, int64_t n_si
     ProfScope prof(s, RF_STAGE_EVICT_SELECT);
     // By the cache's capacity: every warp pays for a step's sums and barrier, so few warps with
     // many keys each, in registers while they fit (16,384 rows in 160 units: 47 us on 1,024
-    // threads; with keys in shared memory 54 us on 512 threads and 59 us on 1,024).
+    // threads; with keys in shared memory 54 us on 512 threads and 59 us on 1,024). 17 keys a
+    // thread, not 16, so that a cache of a power of two of rows fits with a sixteenth more for
+    // the rows drafted since. Whole calls, 160 units down to 4,096 rows: 17,408 rows 124 us in
+    // registers, 17,409 rows 173 us and 32,768 rows 197 us in shared memory, 49,152 rows 243 us
+    // there, 49,153 rows 578 us with keys formed anew.
     cudaError_t e = cudaSuccess;
     const size_t key_bytes = (static_cast<size_t>(d->capacity) + 31) / 32 * 128;
     if (d->capacity <= 128 * 17) {
