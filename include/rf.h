@@ -108,7 +108,8 @@ enum rf_stage {
   RF_STAGE_COMMIT = 27,        /* rf_commit_draft                                  */
   RF_STAGE_ATTN_WEIGHTS = 28,  /* rf_attn_weights                                  */
   RF_STAGE_EVICT_SELECT = 29,  /* rf_evict: which rows stay                        */
-  RF_STAGE_EVICT_MOVE = 30     /* rf_evict: rows into the holes                    */
+  RF_STAGE_EVICT_MOVE = 30,    /* rf_evict: rows into the holes                    */
+  RF_STAGE_NORM_ROPE = 31      /* rf_norm_rope, rf_norm_rope_backward              */
 };
 rf_status rf_profile_start(int max_records);
 /* Diagnostic: runs the tensor-core GEMM kernel on a problem whose operand copies
@@ -584,6 +585,36 @@ typedef struct rf_rope_desc {
  * multiples of 8 elements; out may be in (with ld_out = ld_in). No workspace. */
 rf_status rf_rope(const rf_rope_desc* desc, const void* in, void* out, const int32_t* positions,
                   rf_stream_t stream);
+
+/* Rotation of normalised queries and keys ("Qwen models normalize keys": a cache filled with
+ * rf_fill_desc.k_norm_gain is decoded from with these). A row holds n_q_heads query heads, then
+ * key heads, rope.n_heads in all. */
+typedef struct rf_norm_rope_desc {
+  rf_rope_desc rope;    /* rows, heads, strides, types and rotation as for rf_rope; transpose 0 */
+  int64_t n_q_heads;    /* 0 .. rope.n_heads: these take q_gain, the others k_gain             */
+  double eps;           /* > 0 (a normal number in fp32)                                        */
+} rf_norm_rope_desc;
+
+/* out[t][h] = amplitude * R(p_t) (g * x / sqrt(mean(x^2) + eps)) for every head x = in[t][h], with
+ * the means over the head's channels, the rotation R and the positions of rf_rope, and g = q_gain
+ * or k_gain, [head_dim] values of the rows' type (16-byte aligned; NULL: ones). Squares, means and
+ * products are fp32 (a head's squares must add up to less than 2^128); there is one rounding, at
+ * the end. out may be in (with ld_out = ld_in). No workspace. */
+rf_status rf_norm_rope(const rf_norm_rope_desc* desc, const void* in, const void* q_gain, const void* k_gain,
+                       void* out, const int32_t* positions, rf_stream_t stream);
+
+/* The gradient of rf_norm_rope, from d_out (laid out as out):
+ *   d_in     (laid out as in; only the heads are written) the rows' gradient. It may be in, or
+ *            d_out (with ld_out = ld_in).
+ *   d_q_gain, d_k_gain  [head_dim] fp32 (either may be NULL), written, not added to: the sums over all
+ *            rows and query heads, or key heads, of the gains' gradients; zero where there are none
+ * in, gains, positions and desc as for the call whose gradient it is. Sums are fp32, in an order that
+ * depends on the sizes and the GPU alone. The workspace is needed for the gains' gradients only. */
+size_t rf_norm_rope_backward_workspace_bytes(const rf_norm_rope_desc* desc);
+rf_status rf_norm_rope_backward(const rf_norm_rope_desc* desc, const void* in, const void* q_gain,
+                                const void* k_gain, const void* d_out, const int32_t* positions, void* d_in,
+                                float* d_q_gain, float* d_k_gain, void* workspace, size_t workspace_bytes,
+                                rf_stream_t stream);
 
 /* Words of a node's mask: bit j % 64 of word j / 64 says whether it sees node j. */
 #define RF_TREE_WORDS(n_nodes) (((n_nodes) + 63) / 64)

@@ -94,6 +94,10 @@ class rf_rope_desc(ctypes.Structure):
                 ("transpose", c_int32), ("scaling", c_int32)]
 
 
+class rf_norm_rope_desc(ctypes.Structure):
+    _fields_ = [("rope", rf_rope_desc), ("n_q_heads", c_int64), ("eps", c_double)]
+
+
 class rf_attn_desc(ctypes.Structure):
     _fields_ = [("n_seqs", c_int64), ("n_q_heads", c_int64), ("n_kv_heads", c_int64), ("head_dim", c_int64),
                 ("n_nodes", c_int64), ("capacity", c_int64), ("q_row_stride", c_int64), ("q_seq_stride", c_int64),
@@ -156,6 +160,9 @@ _SIGS = {
     "rf_select_sources": (c_int, [POINTER(rf_select_desc), POINTER(rf_calib_stats), c_double, c_int, c_void_p,
                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "rf_rope": (c_int, [POINTER(rf_rope_desc), c_void_p, c_void_p, c_void_p, c_void_p]),
+    "rf_norm_rope": (c_int, [POINTER(rf_norm_rope_desc)] + [c_void_p] * 6),
+    "rf_norm_rope_backward_workspace_bytes": (c_size_t, [POINTER(rf_norm_rope_desc)]),
+    "rf_norm_rope_backward": (c_int, [POINTER(rf_norm_rope_desc)] + [c_void_p] * 9 + [c_size_t, c_void_p]),
     "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
     "rf_attn_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
     "rf_tree_attention": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
@@ -408,6 +415,24 @@ def rf_select_sources(desc, stats, lam, alpha_mode, src_layers, r2=None, dev_sta
 def rf_rope(desc, inp, out, positions=None, stream=None):
     """Rotary positions of rows of heads: both pairings, part of a head, stretched frequencies (see include/rf.h)."""
     _check(lib().rf_rope(ctypes.byref(desc), _p(inp), _p(out), _p(positions), _s(stream)), "rf_rope")
+
+
+def rf_norm_rope(desc, inp, q_gain, k_gain, out, positions=None, stream=None):
+    """Query and key heads divided by their root mean squares, times their gains, and rotated (see include/rf.h)."""
+    _check(lib().rf_norm_rope(ctypes.byref(desc), _p(inp), _p(q_gain), _p(k_gain), _p(out), _p(positions), _s(stream)),
+           "rf_norm_rope")
+
+
+def rf_norm_rope_backward_workspace_bytes(desc: rf_norm_rope_desc) -> int:
+    return int(lib().rf_norm_rope_backward_workspace_bytes(ctypes.byref(desc)))
+
+
+def rf_norm_rope_backward(desc, inp, q_gain, k_gain, d_out, positions, d_in, d_q_gain=None, d_k_gain=None,
+                          workspace=None, workspace_bytes=0, stream=None):
+    """The gradient of rf_norm_rope: of its rows and, as sums over all of them, of its gains."""
+    _check(lib().rf_norm_rope_backward(ctypes.byref(desc), _p(inp), _p(q_gain), _p(k_gain), _p(d_out), _p(positions),
+                                       _p(d_in), _p(d_q_gain), _p(d_k_gain), _p(workspace), int(workspace_bytes),
+                                       _s(stream)), "rf_norm_rope_backward")
 
 
 def rf_tree_build(n_seqs, n_nodes, parents, next_pos=None, mask=None, positions=None, dev_status=None, stream=None):

@@ -274,6 +274,7 @@ const char* rf_stage_name(int s) {
     case RF_STAGE_ATTN_WEIGHTS: return "attention_weights";
     case RF_STAGE_EVICT_SELECT: return "evict_select";
     case RF_STAGE_EVICT_MOVE: return "evict_move";
+    case RF_STAGE_NORM_ROPE: return "norm_rope";
     default: return "unknown";
   }
 }

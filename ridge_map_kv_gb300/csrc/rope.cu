@@ -19,15 +19,9 @@
 
 #include "rf_device.cuh"
 #include "rf_host.h"
+#include "rope.cuh"
 
 namespace rf {
-
-constexpr int kRopeMaxPairs = 128;
-
-// Fixed-point turns per position, as in RopeFreqs: g[i] = 2^64 f_i / 2 pi.
-struct RopeTable {
-  unsigned long long g[kRopeMaxPairs];
-};
 
 struct RopeArgs {
   const void* in;
@@ -37,40 +31,6 @@ struct RopeArgs {
   int n_rows, n_heads, head_dim, rot, hpt, items;  // items: chunks of a head
   float amp, sign;
 };
-
-// cos and sin of the angle q g. bf16 rows: the SFU on the reduced angle (absolute error
-// about 2^-21, a thirtieth of a bf16 rounding); fp32 rows: to the last bits of fp32,
-// from the fraction of a turn itself, so that no rounding of pi enters.
-template <class T>
-__device__ __forceinline__ void turn_cs(unsigned long long q, unsigned long long g, float& c, float& s) {
-  const int turns = static_cast<int>(static_cast<unsigned>((q * g) >> 32));
-  if constexpr (sizeof(T) == 2) __sincosf(static_cast<float>(turns) * 1.4629180792671596e-9f, &s, &c);  // 2 pi / 2^32
-  else sincospif(static_cast<float>(turns) * 4.6566128730773926e-10f, &s, &c);                         // 2 / 2^32
-}
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float& d, float x) { d = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
-
-template <class T, int N>
-__device__ __forceinline__ void load_vec(const T* p, T (&v)[N]) {
-  if constexpr (N * sizeof(T) == 16) {
-    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = p[i];
-  }
-}
-template <class T, int N>
-__device__ __forceinline__ void store_vec(T* p, const T (&v)[N]) {
-  if constexpr (N * sizeof(T) == 16) {
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = v[i];
-  }
-}
 
 // kWide: 16-byte pieces; else one pair (or two channels that do not turn) a thread.
 template <class T, bool kWide, bool kHalf>
@@ -147,7 +107,7 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
 
 // The frequency table. theta^(-2i/r) is the product of two powers, one of i mod 8 and one
 // of i - i mod 8: 8 + r/16 calls of pow instead of r/2, each factor within an ulp.
-static RopeTable rope_table(const rf_rope_desc* d) {
+RopeTable rope_table(const rf_rope_desc* d) {
   RopeTable t{};
   const int r = static_cast<int>(d->rot_dim), n = r / 2;
   const double pi = 3.14159265358979323846;
@@ -187,7 +147,7 @@ static RopeTable rope_table(const rf_rope_desc* d) {
   return t;
 }
 
-static rf_status check_rope(const rf_rope_desc* d) {
+rf_status check_rope(const rf_rope_desc* d) {
   if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_rows < 0 || d->n_heads <= 0 || d->head_dim <= 0 || d->rot_dim <= 0)
     return fail(RF_ERR_INVALID_ARG, "need n_rows >= 0, n_heads, head_dim, rot_dim > 0");

@@ -1,0 +1,74 @@
+"""Refusals of the operators of a batched decoding step: all on the host, before any launch, so no
+GPU is touched. Pointers are aligned numbers that nothing dereferences."""
+import os
+
+import pytest
+
+import ridge_map_kv_gb300 as rf
+
+P = 256       # an aligned address
+INV, SHAPE, ALIGN, WS = rf.RF_ERR_INVALID_ARG, rf.RF_ERR_SHAPE, rf.RF_ERR_ALIGN, rf.RF_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built_library():
+    if not os.path.exists(rf.LIB_PATH):
+        from ridge_map_kv_gb300 import build
+        build.build()
+    rf.lib()
+
+
+def _refused(status, call, *a, **kw):
+    with pytest.raises(rf.RFError) as ei:
+        call(*a, **kw, stream=0)
+    assert ei.value.status == status, str(ei.value)
+    assert rf.rf_last_error()
+
+
+# ------------------------------------------------------------------ norm and rotation
+def _norm(n_q_heads=1, eps=1e-5, **kw):
+    d = dict(n_rows=4, n_heads=2, head_dim=64, rot_dim=64, ld_in=128, ld_out=128, pos_offset=0, theta=1e4, factor=2.0,
+             original_rows=4096.0, low_turns=1.0, high_turns=4.0, amplitude=1.0, layout=0, dtype=0, transpose=0, scaling=0)
+    d.update(kw)
+    return rf.rf_norm_rope_desc(rope=rf.rf_rope_desc(**d), n_q_heads=n_q_heads, eps=eps)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_rows=-1), INV), (dict(n_heads=0), INV), (dict(theta=0.0), INV), (dict(layout=2), INV), (dict(dtype=2), INV),
+    (dict(transpose=1), INV), (dict(n_q_heads=-1), INV), (dict(n_q_heads=3), INV), (dict(eps=0.0), INV),
+    (dict(eps=-1e-5), INV), (dict(eps=1e-40), INV), (dict(eps=float("inf")), INV), (dict(eps=float("nan")), INV),
+    (dict(head_dim=60, rot_dim=60), SHAPE), (dict(head_dim=264, rot_dim=64, ld_in=528, ld_out=528), SHAPE),
+    (dict(rot_dim=63), SHAPE), (dict(n_rows=(1 << 24) + 1), SHAPE), (dict(ld_in=120), ALIGN), (dict(ld_out=132), ALIGN)])
+def test_norm_rope_refuses_bad_descriptors(bad, status):
+    d = _norm(**bad)
+    assert rf.rf_norm_rope_backward_workspace_bytes(d) == 0
+    _refused(status, rf.rf_norm_rope, d, P, P, P, 2 * P)
+    _refused(status, rf.rf_norm_rope_backward, d, P, P, P, P, P, P, P, 2 * P, P, 1 << 40)
+
+
+def test_norm_rope_refuses_pointers():
+    _refused(INV, rf.rf_norm_rope, _norm(), None, P, P, P)
+    _refused(INV, rf.rf_norm_rope, _norm(), P, P, P, None)
+    for i in range(4):
+        a = [P, P, P, 2 * P]
+        a[i] += 8
+        _refused(ALIGN, rf.rf_norm_rope, _norm(), *a)
+    _refused(ALIGN, rf.rf_norm_rope, _norm(), P, P, P, P, P + 2)
+    _refused(INV, rf.rf_norm_rope, _norm(ld_out=136), P, P, P, P)       # in place with another stride
+    rf.rf_norm_rope(_norm(n_rows=0), None, None, None, None, stream=0)
+
+
+def test_norm_rope_backward_refuses_pointers():
+    d, far = _norm(), 1 << 20
+    need = rf.rf_norm_rope_backward_workspace_bytes(d)
+    good = [P, P, P, 2 * P, P, 3 * P, P, far, P, need]                    # in, gains, d_out, positions, d_in, sums, workspace
+    for i in (0, 3, 5):
+        _refused(INV, rf.rf_norm_rope_backward, d, *good[:i], None, *good[i + 1:])
+    for i, off in ((0, 8), (1, 8), (2, 8), (3, 8), (5, 8), (4, 2), (6, 2), (7, 2)):
+        _refused(ALIGN, rf.rf_norm_rope_backward, d, *good[:i], good[i] + off, *good[i + 1:])
+    _refused(WS, rf.rf_norm_rope_backward, d, *good[:8], None, need)
+    _refused(WS, rf.rf_norm_rope_backward, d, *good[:8], P, need - 1)
+    _refused(WS, rf.rf_norm_rope_backward, d, *good[:8], P + 128, need)
+    _refused(INV, rf.rf_norm_rope_backward, d, *good[:7], P + 4, P, need)  # the gains' gradients overlap
+    _refused(INV, rf.rf_norm_rope_backward, _norm(ld_out=136), *good[:5], good[3], *good[6:])
+    rf.rf_norm_rope_backward(_norm(n_rows=0), None, None, None, None, None, None, stream=0)
