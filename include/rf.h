@@ -109,7 +109,8 @@ enum rf_stage {
   RF_STAGE_ATTN_WEIGHTS = 28,  /* rf_attn_weights                                  */
   RF_STAGE_EVICT_SELECT = 29,  /* rf_evict: which rows stay                        */
   RF_STAGE_EVICT_MOVE = 30,    /* rf_evict: rows into the holes                    */
-  RF_STAGE_NORM_ROPE = 31      /* rf_norm_rope, rf_norm_rope_backward              */
+  RF_STAGE_NORM_ROPE = 31,     /* rf_norm_rope, rf_norm_rope_backward              */
+  RF_STAGE_SAMPLE = 32         /* rf_sample                                        */
 };
 rf_status rf_profile_start(int max_records);
 /* Diagnostic: runs the tensor-core GEMM kernel on a problem whose operand copies
@@ -705,6 +706,45 @@ rf_status rf_verify_draft(const rf_verify_desc* desc, const float* target, const
                           const int32_t* tokens, const int32_t* parents, const float* u, const float* noise,
                           int32_t* path, int32_t* n_path, int32_t* next_token, int32_t* dev_status,
                           rf_stream_t stream);
+
+typedef struct rf_sample_desc {
+  int64_t n_rows;     /* at most 2^24                                                  */
+  int64_t vocab;      /* 1 .. 2^20                                                     */
+  int64_t ld_logits;  /* row strides, >= vocab (any value up to 2^36)                   */
+  int64_t ld_noise;
+  int64_t ld_probs;
+  int32_t dtype;      /* RF_BF16 or RF_F32, of the logits                               */
+  int32_t reserved;   /* 0                                                             */
+} rf_sample_desc;
+
+/* Draws a token from each row of logits, or gives the probabilities to draw it from (for example
+ * rf_verify_draft's target and draft, for logits after each node).
+ * With w_i = exp((x_i - max x) / temperature) and the tokens by falling logit, the lowest token first
+ * among equals, those that stay are, one filter after another,
+ *   top_k   the first k (0: all);
+ *   top_p   of those the fewest first ones whose weights add up to p times the sum of theirs or more
+ *           (1 or more: all; 0: the first);
+ *   min_p   of those the ones with w_i >= min_p (0: all).
+ *   probs[i] = w_i / (sum of the weights that stay), 0 for the others;
+ *   token    = the lowest argmax of w_i / noise[i] of those that stay; logprob = ln probs[token]
+ * temperature 0 is greedy: the lowest argmax of x, with probability 1. Logits of -inf or NaN never
+ * stay; where some are +inf, they alone do, with equal weights.
+ *   logits       [n_rows][ld_logits] bf16 or fp32
+ *   temperature  [n_rows] fp32, 0 or 2^-100 .. 2^100 (NULL: 1);  top_k [n_rows] int32 >= 0 (NULL: 0);
+ *                top_p [n_rows] fp32 >= 0 (NULL: 1);  min_p [n_rows] fp32 in [0, 1] (NULL: 0)
+ *   noise        [n_rows][ld_noise] fp32, exponentially distributed, > 0; read where tokens stay. Needed
+ *                with token, NULL without
+ *   probs        [n_rows][ld_probs] fp32, NULL: not wanted. May be the logits (fp32, the same stride)
+ *   token, logprob, n_kept  [n_rows] int32, fp32, int32; each may be NULL, but not token and probs both.
+ *                n_kept is how many tokens stay
+ * A row with nothing to choose from gives token -1, logprob -inf, n_kept 0 and probabilities 0, and so
+ * does a row with a setting out of range, which also records RF_ERR_INVALID_ARG in *dev_status.
+ * What stays is decided as with sums in 64 bits (masses are summed as integers, each within about
+ * 2^-39 of the greatest weight); weights, probabilities and scores are fp32, and weights below 2^-126 are
+ * 0. Equal inputs give equal results. No workspace. */
+rf_status rf_sample(const rf_sample_desc* desc, const void* logits, const float* temperature, const int32_t* top_k,
+                    const float* top_p, const float* min_p, const float* noise, float* probs, int32_t* token,
+                    float* logprob, int32_t* n_kept, int32_t* dev_status, rf_stream_t stream);
 
 /* A cache of all layers: element l*layer_stride + b*seq_stride + t*row_stride + h*head_dim + c.
  * Layers, sequences and rows may be nested in any order; no two rows may overlap. */

@@ -111,6 +111,11 @@ class rf_verify_desc(ctypes.Structure):
                 ("ld_draft", c_int64), ("ld_noise", c_int64)]
 
 
+class rf_sample_desc(ctypes.Structure):
+    _fields_ = [("n_rows", c_int64), ("vocab", c_int64), ("ld_logits", c_int64), ("ld_noise", c_int64),
+                ("ld_probs", c_int64), ("dtype", c_int32), ("reserved", c_int32)]
+
+
 class rf_cache_desc(ctypes.Structure):
     _fields_ = [("n_layers", c_int64), ("n_seqs", c_int64), ("n_kv_heads", c_int64), ("head_dim", c_int64),
                 ("capacity", c_int64), ("row_stride", c_int64), ("seq_stride", c_int64), ("layer_stride", c_int64)]
@@ -167,6 +172,7 @@ _SIGS = {
     "rf_attn_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
     "rf_tree_attention": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
     "rf_verify_draft": (c_int, [POINTER(rf_verify_desc)] + [c_void_p] * 11),
+    "rf_sample": (c_int, [POINTER(rf_sample_desc)] + [c_void_p] * 12),
     "rf_commit_draft": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 4 + [c_void_p] * 14),
     "rf_attn_weights_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
     "rf_attn_weights": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 6 + [c_double] + [c_void_p] * 4 +
@@ -459,6 +465,13 @@ def rf_verify_draft(desc, target, draft, tokens, parents, u, noise, path, n_path
     _check(lib().rf_verify_draft(ctypes.byref(desc), _p(target), _p(draft), _p(tokens), _p(parents), _p(u), _p(noise),
                                  _p(path), _p(n_path), _p(next_token), _p(dev_status), _s(stream)),
            "rf_verify_draft")
+
+
+def rf_sample(desc, logits, temperature=None, top_k=None, top_p=None, min_p=None, noise=None, probs=None, token=None,
+              logprob=None, n_kept=None, dev_status=None, stream=None):
+    """A token of each row of logits by temperature, top-k, top-p and min-p, or the probabilities to draw it from."""
+    _check(lib().rf_sample(ctypes.byref(desc), _p(logits), _p(temperature), _p(top_k), _p(top_p), _p(min_p), _p(noise),
+                           _p(probs), _p(token), _p(logprob), _p(n_kept), _p(dev_status), _s(stream)), "rf_sample")
 
 
 def rf_commit_draft(desc, n_nodes, draft_row_stride, draft_seq_stride, draft_layer_stride, path, n_path, lens, next_pos,

@@ -275,6 +275,7 @@ const char* rf_stage_name(int s) {
     case RF_STAGE_EVICT_SELECT: return "evict_select";
     case RF_STAGE_EVICT_MOVE: return "evict_move";
     case RF_STAGE_NORM_ROPE: return "norm_rope";
+    case RF_STAGE_SAMPLE: return "sample";
     default: return "unknown";
   }
 }

@@ -72,3 +72,40 @@ def test_norm_rope_backward_refuses_pointers():
     _refused(INV, rf.rf_norm_rope_backward, d, *good[:7], P + 4, P, need)  # the gains' gradients overlap
     _refused(INV, rf.rf_norm_rope_backward, _norm(ld_out=136), *good[:5], good[3], *good[6:])
     rf.rf_norm_rope_backward(_norm(n_rows=0), None, None, None, None, None, None, stream=0)
+
+
+# ------------------------------------------------------------------------ sampling
+def _sample(**kw):
+    d = dict(n_rows=2, vocab=100, ld_logits=100, ld_noise=100, ld_probs=100, dtype=rf.RF_F32, reserved=0)
+    d.update(kw)
+    return rf.rf_sample_desc(**d)
+
+
+FAR = 1 << 20
+GOOD = [P, P, P, P, P, P, FAR, P, P, P]     # logits, temperature, top_k, top_p, min_p, noise, probs, token, logprob, n_kept
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_rows=-1), INV), (dict(vocab=0), INV), (dict(dtype=2), INV), (dict(reserved=1), INV),
+    (dict(vocab=(1 << 20) + 1, ld_logits=1 << 21, ld_noise=1 << 21, ld_probs=1 << 21), SHAPE),
+    (dict(n_rows=(1 << 24) + 1), SHAPE), (dict(ld_logits=1 << 37), SHAPE), (dict(ld_probs=1 << 62), SHAPE),
+    (dict(ld_logits=99), ALIGN), (dict(ld_noise=99), ALIGN), (dict(ld_probs=99), ALIGN)])
+def test_sample_refuses_bad_descriptors(bad, status):
+    _refused(status, rf.rf_sample, _sample(**bad), *GOOD)
+
+
+def test_sample_refuses_pointers():
+    d = _sample()
+    _refused(INV, rf.rf_sample, d, None, *GOOD[1:])
+    _refused(INV, rf.rf_sample, d, P)                                        # neither token nor probabilities
+    _refused(INV, rf.rf_sample, d, *GOOD[:5], None, *GOOD[6:])                # a token without noise
+    _refused(INV, rf.rf_sample, d, *GOOD[:7], None, None, P)                  # noise without a token
+    _refused(INV, rf.rf_sample, d, *GOOD[:5], None, FAR, None, P, P)          # a log-probability without a token
+    for i in range(10):
+        _refused(ALIGN, rf.rf_sample, d, *GOOD[:i], GOOD[i] + 2, *GOOD[i + 1:])
+    _refused(ALIGN, rf.rf_sample, _sample(dtype=rf.RF_BF16), P + 1, *GOOD[1:])
+    for shift in (4, 4 * 199, -4 * 199):                                      # probabilities over the logits in part
+        _refused(INV, rf.rf_sample, d, FAR, *GOOD[1:6], FAR + shift, *GOOD[7:])
+    _refused(INV, rf.rf_sample, _sample(ld_probs=104), FAR, *GOOD[1:6], FAR, *GOOD[7:])
+    _refused(INV, rf.rf_sample, _sample(dtype=rf.RF_BF16), FAR, *GOOD[1:6], FAR, *GOOD[7:])
+    rf.rf_sample(_sample(n_rows=0), None, stream=0)
