@@ -102,8 +102,8 @@ enum rf_stage {
   RF_STAGE_SELECT_SPLIT = 21,  /* source selection: fp32 -> three bf16 planes      */
   RF_STAGE_ROPE = 22,          /* rf_rope                                          */
   RF_STAGE_TREE_BUILD = 23,    /* rf_tree_build                                    */
-  RF_STAGE_ATTENTION = 24,     /* rf_tree_attention: the attention kernel          */
-  RF_STAGE_ATTN_COMBINE = 25,  /* rf_tree_attention: joining of split sequences     */
+  RF_STAGE_ATTENTION = 24,     /* rf_tree_attention, rf_prefix_attention: the attention kernel */
+  RF_STAGE_ATTN_COMBINE = 25,  /* the same: joining of split sequences, or of a prefix's and others' parts */
   RF_STAGE_VERIFY = 26,        /* rf_verify_draft                                  */
   RF_STAGE_COMMIT = 27,        /* rf_commit_draft                                  */
   RF_STAGE_ATTN_WEIGHTS = 28,  /* rf_attn_weights                                  */
@@ -673,6 +673,32 @@ rf_status rf_tree_attention(const rf_attn_desc* desc, const rf_bf16* q,
                             const rf_bf16* k_draft, const rf_bf16* v_draft, const uint64_t* tree_mask,
                             rf_bf16* out, float* lse, int32_t* dev_status,
                             void* workspace, size_t workspace_bytes, rf_stream_t stream);
+
+/* A batch whose sequences all continue one prompt, for example one that rf_fill_kv has filled. */
+typedef struct rf_prefix_attn_desc {
+  rf_attn_desc attn;          /* queries, the sequences' own caches, drafted rows and output, as for */
+                              /* rf_tree_attention; n_seqs * n_nodes * n_q_heads <= 2^28             */
+  int64_t prefix_capacity;    /* rows of k_prefix and v_prefix, 1 .. 2^30                            */
+  int64_t prefix_row_stride;  /* element t*prefix_row_stride + h*head_dim + c                        */
+} rf_prefix_attn_desc;
+
+/* rf_tree_attention over a prefix that all sequences share, each one's own cache rows and the drafted
+ * rows:
+ *   S = {prefix rows t < *prefix_len} + {cache rows t < lens[b]} + {drafted rows j that node i sees}.
+ * The prefix is held once and read once for all sequences, whose rows make up its matrix products, so a
+ * batch costs about what one sequence does up to 256 query rows per KV head. Own caches may be empty
+ * (lens[b] = 0), and so may the prefix.
+ *   prefix_len  device int32; outside [0, prefix_capacity] it records RF_ERR_INVALID_ARG and nothing is
+ *               written
+ * All other arguments, masks, what is not seen, refusals and the status of lengths as for
+ * rf_tree_attention. Scores, statistics and sums are fp32, joined in a fixed order. */
+size_t rf_prefix_attn_workspace_bytes(const rf_prefix_attn_desc* desc);
+rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const rf_bf16* q,
+                              const rf_bf16* k_prefix, const rf_bf16* v_prefix, const int32_t* prefix_len,
+                              const rf_bf16* k_cache, const rf_bf16* v_cache, const int32_t* lens,
+                              const rf_bf16* k_draft, const rf_bf16* v_draft, const uint64_t* tree_mask,
+                              rf_bf16* out, float* lse, int32_t* dev_status,
+                              void* workspace, size_t workspace_bytes, rf_stream_t stream);
 
 typedef struct rf_verify_desc {
   int64_t n_seqs;     /* at most 2^24                                                  */

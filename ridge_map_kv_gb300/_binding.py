@@ -106,6 +106,10 @@ class rf_attn_desc(ctypes.Structure):
                 ("scale", c_double), ("flags", ctypes.c_uint64)]
 
 
+class rf_prefix_attn_desc(ctypes.Structure):
+    _fields_ = [("attn", rf_attn_desc), ("prefix_capacity", c_int64), ("prefix_row_stride", c_int64)]
+
+
 class rf_verify_desc(ctypes.Structure):
     _fields_ = [("n_seqs", c_int64), ("n_nodes", c_int64), ("vocab", c_int64), ("ld_target", c_int64),
                 ("ld_draft", c_int64), ("ld_noise", c_int64)]
@@ -171,6 +175,8 @@ _SIGS = {
     "rf_tree_build": (c_int, [c_int64, c_int64] + [c_void_p] * 6),
     "rf_attn_workspace_bytes": (c_size_t, [POINTER(rf_attn_desc)]),
     "rf_tree_attention": (c_int, [POINTER(rf_attn_desc)] + [c_void_p] * 11 + [c_size_t, c_void_p]),
+    "rf_prefix_attn_workspace_bytes": (c_size_t, [POINTER(rf_prefix_attn_desc)]),
+    "rf_prefix_attention": (c_int, [POINTER(rf_prefix_attn_desc)] + [c_void_p] * 14 + [c_size_t, c_void_p]),
     "rf_verify_draft": (c_int, [POINTER(rf_verify_desc)] + [c_void_p] * 11),
     "rf_sample": (c_int, [POINTER(rf_sample_desc)] + [c_void_p] * 12),
     "rf_commit_draft": (c_int, [POINTER(rf_cache_desc)] + [c_int64] * 4 + [c_void_p] * 14),
@@ -457,6 +463,18 @@ def rf_tree_attention(desc, q, k_cache, v_cache, lens, k_draft, v_draft, tree_ma
     _check(lib().rf_tree_attention(ctypes.byref(desc), _p(q), _p(k_cache), _p(v_cache), _p(lens), _p(k_draft),
                                    _p(v_draft), _p(tree_mask), _p(out), _p(lse), _p(dev_status), _p(workspace),
                                    int(workspace_bytes), _s(stream)), "rf_tree_attention")
+
+
+def rf_prefix_attn_workspace_bytes(desc: rf_prefix_attn_desc) -> int:
+    return int(lib().rf_prefix_attn_workspace_bytes(ctypes.byref(desc)))
+
+
+def rf_prefix_attention(desc, q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, lens, k_draft, v_draft, tree_mask, out,
+                        lse=None, dev_status=None, workspace=None, workspace_bytes=0, stream=None):
+    """Attention of drafted rows over a prefix that all sequences share, their own caches and each other."""
+    _check(lib().rf_prefix_attention(ctypes.byref(desc), _p(q), _p(k_prefix), _p(v_prefix), _p(prefix_len), _p(k_cache),
+                                     _p(v_cache), _p(lens), _p(k_draft), _p(v_draft), _p(tree_mask), _p(out), _p(lse),
+                                     _p(dev_status), _p(workspace), int(workspace_bytes), _s(stream)), "rf_prefix_attention")
 
 
 def rf_verify_draft(desc, target, draft, tokens, parents, u, noise, path, n_path, next_token, dev_status=None,

@@ -86,6 +86,7 @@ struct AttnShare {
 };
 
 struct AttnArgs {
+  static constexpr bool kPrefix = false;
   CUtensorMap tm_q, tm_k, tm_v, tm_kd, tm_vd;
   const int32_t* lens;
   const unsigned long long* mask;
@@ -103,6 +104,26 @@ struct AttnArgs {
   int m_items;    // items (groups of row tiles) of a sequence and head
   int draft_sum;  // draft tiles summed over those items
   float scale;
+};
+
+// With a prefix that all sequences share (rf_prefix_attention), it is one more sequence, b = -1, before
+// the others: its rows are those of all sequences, so its keys are read once for all. Every row then has
+// parts in two items, its own sequence's and the prefix's, which k_prefix_join adds up. Items that were
+// not cut leave their parts in places of their own.
+struct PrefixArgs : AttnArgs {
+  static constexpr bool kPrefix = true;
+  CUtensorMap tm_qp, tm_kp, tm_vp;
+  const int32_t* prefix_len;
+  int prefix_capacity;
+  // A row tile of the prefix: p_nodes nodes of each of p_seqs sequences. Few nodes: whole sequences, as many
+  // as fit; else p_split tiles a sequence, which is the last of them not full.
+  int p_nodes, p_seqs, p_split;
+  int p_items;       // items of a head
+  int narrow;        // a sequence's rows fit into one row tile
+  int rows, p_rows;  // rows of an item, of a sequence and of the prefix, where they are stored whole
+  float4* whole_o;   // [items][head_dim / 4][rows of the item], the prefix's items first
+  float2* whole_ml;
+  int2* item_ctas;   // [items] the CTAs of an item's first and last tile
 };
 
 struct AttnShared {
@@ -140,9 +161,25 @@ __device__ __forceinline__ int length_of(const AttnArgs& a, int b) {  // -1: out
   const int len = a.lens[b];
   return len < 0 || len > a.capacity ? -1 : len;
 }
-template <bool kDual>
-__device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt) {
+__device__ __forceinline__ int prefix_of(const PrefixArgs& a) {
+  const int len = *a.prefix_len;
+  return len < 0 || len > a.prefix_capacity ? -1 : len;
+}
+template <class Args>
+__device__ __forceinline__ int items_of(const Args& a, int b) {  // of a head
+  if constexpr (Args::kPrefix) return b < 0 ? a.p_items : a.m_items;
+  else return a.m_items;
+}
+template <bool kDual, class Args>
+__device__ __forceinline__ ItemShape item_shape(const Args& a, int b, int mt) {
   ItemShape s;
+  if constexpr (Args::kPrefix) {
+    if (b < 0) {
+      s.len = prefix_of(a);
+      s.cached = s.tiles = (max(s.len, 0) + kAtTile - 1) / kAtTile;
+      return s;
+    }
+  }
   s.len = length_of(a, b);
   s.cached = (max(s.len, 0) + kAtTile - 1) / kAtTile;
   s.tiles = s.len < 0 ? 0 : s.cached + draft_tiles<kDual>(a, mt);
@@ -150,13 +187,13 @@ __device__ __forceinline__ ItemShape item_shape(const AttnArgs& a, int b, int mt
 }
 
 // A CTA's share, segment by segment; every role walks it alike, a converged warp at a time.
-template <bool kDual>
+template <bool kDual, class Args>
 struct Walk {
   int b, h, mt, t0, t1;  // an item and the tiles of it that are the share's
   int at;                // where the share stands in the item's weight
   long long left;        // weight
   ItemShape shape;
-  __device__ __forceinline__ Walk(const AttnArgs& a, const AttnShared* sh) {
+  __device__ __forceinline__ Walk(const Args& a, const AttnShared* sh) {
     b = uniform(sh->share.b);
     h = uniform(sh->share.h);
     mt = uniform(sh->share.mt);
@@ -173,7 +210,7 @@ struct Walk {
     return static_cast<int>(min(static_cast<long long>(shape.tiles + kAtItemCost), at + left));
   }
   // The first tiles from here on (a share may end within an item's extra weight).
-  __device__ __forceinline__ void settle(const AttnArgs& a) {
+  __device__ __forceinline__ void settle(const Args& a) {
     while (true) {
       t0 = max(at - kAtItemCost, 0);
       t1 = max(end() - kAtItemCost, 0);
@@ -182,16 +219,16 @@ struct Walk {
       if (left <= 0) return;
     }
   }
-  __device__ __forceinline__ void next(const AttnArgs& a) {
+  __device__ __forceinline__ void next(const Args& a) {
     next_item(a);
     if (left > 0) settle(a);
   }
-  __device__ __forceinline__ void next_item(const AttnArgs& a) {
+  __device__ __forceinline__ void next_item(const Args& a) {
     left -= end() - at;
     if (left <= 0) return;
     at = 0;
     do {
-      if (++mt == a.m_items) {
+      if (++mt == items_of(a, b)) {
         mt = 0;
         if (++h == a.heads) {
           h = 0;
@@ -212,9 +249,17 @@ struct Walk {
 // The start of share `cta` of `ctas`: one warp sums the sequences' weights, then finds the
 // sequence, head, item and place of its first one. Writes the share to shared memory, and
 // to `plan` what k_attn_combine needs.
-template <bool kDual>
-__device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas) {
+template <bool kDual, class Args>
+__device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
+  int prefix = 0, prefix_tiles = 0;
+  long long prefix_weight = 0;
+  if constexpr (Args::kPrefix) {
+    prefix = prefix_of(a);
+    if (prefix < 0) record_status(a.dev_status, RF_ERR_INVALID_ARG);
+    prefix_tiles = (max(prefix, 0) + kAtTile - 1) / kAtTile;
+    if (prefix_tiles > 0) prefix_weight = static_cast<long long>(a.heads) * a.p_items * (prefix_tiles + kAtItemCost);
+  }
   auto weight_of = [&](int len) -> long long {
     return len < 0 ? 0ll
                    : static_cast<long long>(a.heads) *
@@ -229,13 +274,26 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total = prefix < 0 ? 0 : total + prefix_weight;  // (a prefix that is out of range: no sequence can be answered)
   const long long shares = min(static_cast<long long>(ctas), total);
   AttnShare p{};
   if (cta < shares) {
     const long long first = share_start(total, cta, static_cast<int>(shares));
     p.weight = share_start(total, cta + 1, static_cast<int>(shares)) - first;
-    long long base = 0;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+    long long base = prefix_weight;
+    if constexpr (Args::kPrefix) {
+      if (first < prefix_weight) {
+        p.b = -1;
+        p.len = prefix;
+        p.n_tiles = prefix_tiles;
+        const long long per_head = static_cast<long long>(a.p_items) * (prefix_tiles + kAtItemCost);
+        p.h = static_cast<int>(quick_div(first, per_head));
+        const long long at = first - p.h * per_head;
+        p.mt = static_cast<int>(quick_div(at, prefix_tiles + kAtItemCost));
+        p.at = static_cast<int>(at - static_cast<long long>(p.mt) * (prefix_tiles + kAtItemCost));
+      }
+    }
+    for (int b0 = 0; b0 < a.n_seqs && first >= prefix_weight; b0 += 32) {
       if (a.n_seqs > 32) len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
       const long long own = weight_of(len);
       long long x = own;
@@ -273,7 +331,8 @@ __device__ void find_share(const AttnArgs& a, AttnShared* sh, int cta, int ctas)
   }
   if (lane == 0) sh->share = p;
   __syncwarp();
-  const Walk<kDual> w(a, sh);
+  if constexpr (Args::kPrefix) return;
+  const Walk<kDual, Args> w(a, sh);
   if (lane == 0)
     a.plan[cta] = AttnPlan{w.more() ? (static_cast<long long>(w.b) * a.heads + w.h) * a.m_items + w.mt : -1ll, w.b, w.h, w.mt, w.t0};
 }
@@ -356,8 +415,8 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const ItemShape& s, i
   }
 }
 
-template <int kHD, bool kDual>
-__global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ AttnArgs a) {
+template <int kHD, bool kDual, class Args>
+__global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ Args a) {
   using Cfg = AttnCfg<kHD, kDual>;
   constexpr int kChunks = kHD / 64;                 // 64-channel slabs of a tile, 16 KB each
   constexpr int kSlab = kAtTile * 128;
@@ -365,7 +424,15 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   AttnShared* sh = reinterpret_cast<AttnShared*>(smem + Cfg::kQBytes + Cfg::kStages * Cfg::kTileBytes);
-  AttnExchange& ml = *reinterpret_cast<AttnExchange*>(sh + 1);  // (one row tile)
+  // Items of one row tile exchange maxima and totals: behind the rest, or, where items of two tiles came
+  // before them (a prefix's), in the second query tile, which they do not have.
+  AttnExchange& ml = *reinterpret_cast<AttnExchange*>(kDual ? smem + Cfg::kTileBytes : reinterpret_cast<uint8_t*>(sh + 1));
+  // With two row tiles and a prefix: an item of one tile. Its streams take alternate key tiles as they do where
+  // all items are of one tile, but each stream's products stay with the warp that issues them.
+  const auto narrow = [&](int b) {
+    if constexpr (kDual && Args::kPrefix) return b >= 0 && a.narrow != 0;
+    else return false;
+  };
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + Cfg::kQBytes;
   const int warp = uniform(static_cast<int>(threadIdx.x >> 5)), lane = threadIdx.x & 31;
   volatile int* abort_flag = &sh->abort;
@@ -400,6 +467,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     tma_prefetch_desc(&a.tm_v);
     tma_prefetch_desc(&a.tm_kd);
     tma_prefetch_desc(&a.tm_vd);
+    if constexpr (Args::kPrefix) {
+      tma_prefetch_desc(&a.tm_qp);
+      tma_prefetch_desc(&a.tm_kp);
+      tma_prefetch_desc(&a.tm_vp);
+    }
   }
   if (warp == 9) {
     tmem_alloc(&sh->tmem, 512);
@@ -421,16 +493,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       uint32_t phase = 0, q_phase = 0;
       long long issued = 0;
       bool ok = true, q_inflight = false;
-      auto load = [&](const Walk<kDual>& w, int t, bool v) {
+      auto load = [&](const Walk<kDual, Args>& w, int t, bool v) {
         if (!wait(&sh->empty[stage], phase ^ 1u)) return false;
         const bool draft = t >= w.shape.cached;
         const CUtensorMap* tm = draft ? (v ? &a.tm_vd : &a.tm_kd) : (v ? &a.tm_v : &a.tm_k);
+        if constexpr (Args::kPrefix) {
+          if (w.b < 0) tm = v ? &a.tm_vp : &a.tm_kp;
+        }
         const int row = (draft ? t - w.shape.cached : t) * kAtTile;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, w.b);
+            tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, max(w.b, 0));
         }
         __syncwarp();
         ++issued;
@@ -440,21 +515,38 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         return true;
       };
-      for (Walk<kDual> w(a, sh); w.more() && ok; w.next(a)) {
+      for (Walk<kDual, Args> w(a, sh); w.more() && ok; w.next(a)) {
         if (!wait(&sh->q_empty, q_phase ^ 1u)) break;
         q_inflight = true;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&sh->q_full, (kDual ? 2 : 1) * kChunks * 64 * 2 * a.group * a.npt);
-          for (int s = 0; s < (kDual ? 2 : 1); ++s)
+          const CUtensorMap* tm = &a.tm_q;
+          const int tiles = kDual && !narrow(w.b) ? 2 : 1;
+          int rows = a.group * a.npt;
+          if constexpr (Args::kPrefix) {
+            if (w.b < 0) {
+              tm = &a.tm_qp;
+              rows = a.group * a.p_nodes * a.p_seqs;
+            }
+          }
+          mbar_arrive_expect_tx(&sh->q_full, tiles * kChunks * 64 * 2 * rows);
+          for (int s = 0; s < tiles; ++s) {
+            const int tile = w.mt * (kDual ? 2 : 1) + s;
+            int node = tile * a.npt, seq = w.b;
+            if constexpr (Args::kPrefix) {
+              if (w.b < 0) {
+                seq = a.p_split > 1 ? tile / a.p_split : tile * a.p_seqs;
+                node = a.p_split > 1 ? (tile - seq * a.p_split) * a.p_nodes : 0;
+              }
+            }
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, &a.tm_q, smem_u32(&sh->q_full), c * 64, w.h * a.group,
-                          (w.mt * (kDual ? 2 : 1) + s) * a.npt, w.b);
+              tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->q_full), c * 64, w.h * a.group, node, seq);
+          }
         }
         __syncwarp();
         q_phase ^= 1u;
         // the order in which warp 9 takes them
-        if (kDual) {
+        if (kDual && !narrow(w.b)) {
           for (int t = w.t0; t < w.t1 && ok; ++t) ok = load(w, t, false) && load(w, t, true);
         } else {
           ok = load(w, w.t0, false);
@@ -529,9 +621,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       advance();
       return st;
     };
-    auto to_clean = [&](const Walk<kDual>& w, int t) { return t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len; };
+    auto to_clean = [&](const Walk<kDual, Args>& w, int t) { return t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len; };
     // Clears V elements of stage `st` that no product may see (whole warp).
-    auto clean = [&](const Walk<kDual>& w, int t, int st) {
+    auto clean = [&](const Walk<kDual, Args>& w, int t, int st) {
       const uint32_t v0 = s_ring + st * Cfg::kTileBytes;
       if (t < w.shape.cached) {
         const int rows = w.shape.len - t * kAtTile;
@@ -572,13 +664,61 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       fence_proxy_async_shared();
       __syncwarp();
     };
-    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
       if (warp == 9 && lane == 0) sh->bad[seg & 1] = 0;
       __syncwarp();
       if (!wait(&sh->q_full, q_phase)) goto mma_done;
       q_phase ^= 1u;
-      if (kDual) {
+      if (narrow(w.b)) {
+        // Warp 9 + s issues stream s's products. Both warps walk the whole ring, and give back at once what is
+        // the other's; warp 9 cleans. At most two tiles of such an item are cleaned (the cache's last and
+        // the one of drafted rows), and none of the next item before this one's end: two barriers are enough.
+        const int s = warp - 9;
+        auto give = [&](int st, bool own) {
+          if (own) tc_commit_warp(&sh->empty[st], issue);
+          else if (lane == 0) mbar_arrive(&sh->empty[st]);
+        };
+        for (int i = 0; i < 2 && i < n_tiles; ++i) {
+          const int k = take();
+          if (k < 0) goto mma_done;
+          if (i == s) {
+            qk(s, 0, k);
+            tc_commit_warp(&sh->s_full[s], issue);
+          }
+          give(k, i == s);
+          if (i + 1 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
+        }
+        if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
+        for (int i = 0; i < n_tiles; ++i) {
+          const bool own = (i & 1) == s, more = i + 2 < n_tiles;
+          const int v = take();
+          if (v < 0) goto mma_done;
+          if (to_clean(w, w.t0 + i)) {
+            if (s == 0) {
+              clean(w, w.t0 + i, v);
+              if (lane == 0) mbar_arrive(&sh->v_clean[cleaned & 1u]);
+            } else {
+              if (!wait(&sh->v_clean[cleaned & 1u], (cleaned >> 1) & 1u)) goto mma_done;
+            }
+            ++cleaned;
+          }
+          const int k = more ? take() : 0;
+          if (k < 0) goto mma_done;
+          if (own) {
+            if (!wait(&sh->p_full[s][0], p_phase[s]) || !pv(s, v, i < 2)) goto mma_done;
+          }
+          give(v, own);
+          if (more) {
+            if (own) {
+              qk(s, 0, k);
+              tc_commit_warp(&sh->s_full[s], issue);
+            }
+            give(k, own);
+          }
+          if (i + 3 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
+        }
+      } else if (kDual) {
         // Warp 9 issues stream 0's products, warp 10 stream 1's, a tile's second product and the
         // next tile's first in one go, in turn: so one stream's products run while the other's
         // weights are formed, and a warp's own waits and commits fall into the other's turn.
@@ -669,17 +809,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + s * kAtTile;
     const float sc = a.scale * kAtLog2e;
-    uint32_t s_phase = 0, f_phase = 0;
+    uint32_t s_phase = 0, f_phase = 0, ml_phase = 0;
     int seg = 0;
-    for (Walk<kDual> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
-      const int node0 = (w.mt * (kDual ? 2 : 1) + (kDual ? s : 0)) * a.npt;
-      const int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile
+      const bool joint = !kDual || narrow(w.b);  // the streams share one row tile
+      const int tile = w.mt * (kDual ? 2 : 1) + (joint ? 0 : s);
+      const int node0 = tile * a.npt;
+      int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile
+      if constexpr (Args::kPrefix) {
+        if (w.b < 0) {
+          const int seq = a.p_split > 1 ? tile / a.p_split : tile * a.p_seqs;
+          const int nodes = a.p_split > 1 ? min(a.p_nodes, a.n - (tile - seq * a.p_split) * a.p_nodes)
+                                          : min(a.p_seqs, a.n_seqs - seq) * a.n;
+          rows = seq < a.n_seqs ? nodes * a.group : 0;
+        }
+      }
       const bool idle = (warp & 3) * 32 >= rows;                   // a warp without rows
       const int node = min(node0 + row / a.group, a.n - 1);
       float m = -INFINITY, l = 0.0f;
       bool first = true;
-      for (int i = kDual ? 0 : s; i < n_tiles; i += kDual ? 1 : 2) {
+      for (int i = joint ? s : 0; i < n_tiles; i += joint ? 2 : 1) {
         bool ok = mbar_wait(&sh->s_full[s], s_phase, abort_flag, timeout);
         if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
         s_phase ^= 1u;
@@ -732,11 +882,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         first = false;
       }
       // Epilogue.
-      if (!kDual) {
+      if (joint) {
         ml[seg & 1][s][row] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->ml_full);
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->ml_full, f_phase, abort_flag, timeout))) goto softmax_done;
+        if (!__all_sync(0xffffffffu, mbar_wait(&sh->ml_full, ml_phase, abort_flag, timeout))) goto softmax_done;
+        ml_phase ^= 1u;
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&sh->o_final, f_phase, abort_flag, timeout))) goto softmax_done;
       f_phase ^= 1u;
@@ -744,7 +895,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       {
         // stream sums to join (one row tile): this warp takes half of the channels of both
         float f0 = 1.0f, f1 = 0.0f;
-        if (!kDual) {
+        if (joint) {
           const float2 u = ml[seg & 1][0][row], v = ml[seg & 1][1][row];
           m = fmaxf(u.x, v.x);
           f0 = u.x == -INFINITY ? 0.0f : exp2f_ftz((u.x - m) * sc);
@@ -757,19 +908,40 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         const bool write = row < rows;
         const int head = w.h * a.group + row % a.group;
         const long long slot = 2LL * blockIdx.x + (w.t0 > 0 ? 0 : 1);
-        const int prow = (kDual ? s * kAtTile : 0) + row;
+        const int prow = (joint ? 0 : s * kAtTile) + row;
+        // where the rows' parts go, one after another
+        float4* part_o = a.part_o + slot * (kHD / 4) * Cfg::kRows + prow;
+        float2* part_ml = a.part_ml + slot * Cfg::kRows + prow;
+        int part_rows = Cfg::kRows;
+        if constexpr (Args::kPrefix) {
+          const long long prefix_items = static_cast<long long>(a.heads) * a.p_items;
+          const long long item = w.b < 0 ? static_cast<long long>(w.h) * a.p_items + w.mt
+                                         : (static_cast<long long>(w.b) * a.heads + w.h) * a.m_items + w.mt;
+          if (whole) {
+            part_rows = w.b < 0 ? a.p_rows : a.rows;
+            const int tile_rows = joint ? 0 : part_rows / 2;
+            const long long before = w.b < 0 ? item * a.p_rows : prefix_items * a.p_rows + item * a.rows;
+            part_o = a.whole_o + before * (kHD / 4) + s * tile_rows + row;
+            part_ml = a.whole_ml + before + s * tile_rows + row;
+          }
+          if (threadIdx.x == 0) {
+            int2* at = a.item_ctas + (w.b < 0 ? 0 : prefix_items) + item;
+            if (w.t0 == 0) at->x = static_cast<int>(blockIdx.x);
+            if (w.t1 == w.shape.tiles) at->y = static_cast<int>(blockIdx.x);
+          }
+        }
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         if (!idle) {
-          constexpr int kCols = kDual ? kHD : kHD / 2;
-          const int col0 = kDual ? 0 : s * kCols;
-          const uint32_t to = tmem + lanes + 256 + (kDual ? s * 128 : 0) + col0;
+          const int cols = joint ? kHD / 2 : kHD;
+          const int col0 = joint ? s * cols : 0;
+          const uint32_t to = tmem + lanes + 256 + (joint ? 0 : s * 128) + col0;
 #pragma unroll 1
-          for (int c = 0; c < kCols; c += 16) {
+          for (int c = 0; c < cols; c += 16) {
             uint32_t o[16];
             tmem_ld16(to + c, o);
             tmem_wait_ld16(o);
             float x[16];
-            if (!kDual) {
+            if (joint) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) x[e] = f0 != 0.0f ? u2f(o[e]) * f0 : 0.0f;
               if (n_tiles > 1) {
@@ -789,7 +961,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
                                       ? (a.mask[(static_cast<long long>(w.b) * a.n + node) * a.words + (j >> 6)] >> (j & 63)) & 1u
                                       : j <= node;
                 if (!sees) continue;
-                const __nv_bfloat16* v = a.v_draft + w.b * a.draft_seq + j * a.draft_row + w.h * kHD + col0 + c;
+                const __nv_bfloat16* v = a.v_draft + static_cast<long long>(w.b) * a.draft_seq + j * a.draft_row + w.h * kHD + col0 + c;
                 for (int e = 0; e < 16; ++e) {
                   const float y = __bfloat162float(v[e]);
                   if (!isfinite(y)) x[e] += y;
@@ -797,7 +969,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
               }
             }
             if (write) {
-              if (whole) {
+              if (!Args::kPrefix && whole) {
                 uint32_t pk[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(x[2 * e] * inv, x[2 * e + 1] * inv);
@@ -805,14 +977,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
                 st_global_v4(dst, pk[0], pk[1], pk[2], pk[3]);
                 st_global_v4(dst + 8, pk[4], pk[5], pk[6], pk[7]);
               } else {  // rows side by side: a warp's store is 512 bytes in a row
-                float4* dst = a.part_o + (slot * (kHD / 4) + (col0 + c) / 4) * Cfg::kRows + prow;
+                float4* dst = part_o + static_cast<long long>((col0 + c) / 4) * part_rows;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e * Cfg::kRows] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+                for (int e = 0; e < 4; ++e) dst[e * part_rows] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
               }
             }
           }
-          if (write && (kDual || s == 0)) {
-            if (!whole) a.part_ml[slot * Cfg::kRows + prow] = make_float2(m, l);
+          if (write && (!joint || s == 0)) {
+            if (Args::kPrefix || !whole) *part_ml = make_float2(m, l);
             else if (a.lse != nullptr)
               a.lse[(static_cast<long long>(w.b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
                   l == 0.0f ? -INFINITY : m * a.scale + logf(l);
@@ -953,6 +1125,148 @@ __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant_
         l == 0.0f ? -INFINITY : m * a.scale + logf(l);
 }
 
+// Adds up each row's parts of a call with a prefix: those of the prefix's item, then those of its own
+// sequence's. Block (x, y): rows 32 x .. 32 x + 31 (or 8, see below) of KV head y, counted over the
+// sequences' nodes and the head's queries; a warp takes 16 channels.
+struct JoinArgs {
+  const float4* part_o;
+  const float2* part_ml;
+  const float4* whole_o;
+  const float2* whole_ml;
+  const int2* item_ctas;
+  const int32_t* lens;
+  const int32_t* prefix_len;
+  __nv_bfloat16* out;
+  float* lse;
+  long long out_row, out_seq;
+  int n_seqs, n, heads, group, npt, tiles, m_items, p_nodes, p_seqs, p_split, p_items, rows, p_rows, ctas;
+  int capacity, prefix_capacity;
+  float scale;
+};
+
+// kBatch, kSplit as for k_attn_combine: lanes share a row where there are fewer blocks than SMs otherwise.
+template <int kHD, int kBatch, int kSplit>
+__global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__ JoinArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kLanes = 32 / kSplit;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+  const int r = blockIdx.x * kLanes + lane % kLanes;
+  const int per_seq = a.n * a.group;
+  const int b = r / per_seq, in_seq = r - b * per_seq, node = in_seq / a.group, g = in_seq - node * a.group;
+  const int prefix = *a.prefix_len, len = b < a.n_seqs ? a.lens[b] : -1;
+  const bool live = len >= 0 && len <= a.capacity && prefix >= 0 && prefix <= a.prefix_capacity;
+  // The row's place in the prefix's items and in its own sequence's.
+  struct Place {
+    const float4* whole_o;
+    const float2* whole_ml;
+    int whole_rows, at;  // at: within the rows of a part that was cut
+    int first, parts;
+  } at[2] = {};
+  if (live) {
+    const int tile_rows = a.tiles == 2 ? kAtTile : 0;
+    const long long prefix_items = static_cast<long long>(a.heads) * a.p_items;
+    auto place = [&](int i, int tile, int row, long long before, long long item, int rows) {
+      const int s = tile % a.tiles;
+      at[i].whole_rows = rows;
+      at[i].whole_o = a.whole_o + before * (kHD / 4) + s * (rows / 2) + row;
+      at[i].whole_ml = a.whole_ml + before + s * (rows / 2) + row;
+      at[i].at = s * tile_rows + row;
+      const int2 c = a.item_ctas[item];
+      at[i].first = min(max(c.x, 0), a.ctas - 1);
+      at[i].parts = min(max(c.y, at[i].first), a.ctas - 1) - at[i].first + 1;
+    };
+    if (prefix > 0) {
+      const int tile = a.p_split > 1 ? b * a.p_split + node / a.p_nodes : b / a.p_seqs;
+      const int row = a.p_split > 1 ? (node % a.p_nodes) * a.group + g : (b % a.p_seqs) * per_seq + in_seq;
+      const long long item = static_cast<long long>(h) * a.p_items + tile / a.tiles;
+      place(0, tile, row, item * a.p_rows, item, a.p_rows);
+    }
+    const int tile = node / a.npt;
+    const long long item = (static_cast<long long>(b) * a.heads + h) * a.m_items + tile / a.tiles;
+    place(1, tile, (node - tile * a.npt) * a.group + g, prefix_items * a.p_rows + item * a.rows, prefix_items + item, a.rows);
+  }
+  if (kSplit == 1 && !live) return;
+  const int item_rows = a.tiles * kAtTile, parts = at[0].parts + at[1].parts;
+  const float sc = a.scale * kAtLog2e;
+  float m = -INFINITY, l = 0.0f;
+  float4 x[4] = {};
+  for (int i0 = live ? lane / kLanes : parts; i0 < parts; i0 += kBatch * kSplit) {
+    float2 ml[kBatch];
+    float4 v[kBatch][4];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      int i = i0 + j * kSplit;
+      if (i >= parts) break;
+      const bool own = i >= at[0].parts;
+      if (own) i -= at[0].parts;
+      const Place& p = own ? at[1] : at[0];
+      const float4* o = p.whole_o;
+      const float2* w = p.whole_ml;
+      int stride = p.whole_rows;
+      if (p.parts > 1) {  // the last part of its first CTA, the first part of the others
+        const long long slot = i == 0 ? 2LL * p.first + 1 : 2LL * (p.first + i);
+        o = a.part_o + slot * (kHD / 4) * item_rows + p.at;
+        w = a.part_ml + slot * item_rows + p.at;
+        stride = item_rows;
+      }
+      ml[j] = *w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[j][e] = o[static_cast<long long>(warp * 4 + e) * stride];
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (i0 + j * kSplit >= parts) break;
+      const float mx = fmaxf(m, ml[j].x);
+      const float f = m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc);
+      const float k = ml[j].x == -INFINITY ? 0.0f : exp2f_ftz((ml[j].x - mx) * sc);
+      m = mx;
+      l = l * f + ml[j].y * k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e].x = x[e].x * f + v[j][e].x * k;
+        x[e].y = x[e].y * f + v[j][e].y * k;
+        x[e].z = x[e].z * f + v[j][e].z * k;
+        x[e].w = x[e].w * f + v[j][e].w * k;
+      }
+    }
+  }
+  if constexpr (kSplit > 1) {
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1) {
+      const float m1 = __shfl_xor_sync(0xffffffffu, m, o), l1 = __shfl_xor_sync(0xffffffffu, l, o);
+      const float mx = fmaxf(m, m1);
+      const float f = m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc);
+      const float k = m1 == -INFINITY ? 0.0f : exp2f_ftz((m1 - mx) * sc);
+      m = mx;
+      l = l * f + l1 * k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e].x = x[e].x * f + __shfl_xor_sync(0xffffffffu, x[e].x, o) * k;
+        x[e].y = x[e].y * f + __shfl_xor_sync(0xffffffffu, x[e].y, o) * k;
+        x[e].z = x[e].z * f + __shfl_xor_sync(0xffffffffu, x[e].z, o) * k;
+        x[e].w = x[e].w * f + __shfl_xor_sync(0xffffffffu, x[e].w, o) * k;
+      }
+    }
+    if (!live || lane >= kLanes) return;
+  }
+  if (m == INFINITY) l = NAN;  // inf - inf
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint32_t pk[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    pk[2 * e] = pack_bf16x2(x[e].x * inv, x[e].y * inv);
+    pk[2 * e + 1] = pack_bf16x2(x[e].z * inv, x[e].w * inv);
+  }
+  const int head = h * a.group + g;
+  __nv_bfloat16* dst = a.out + b * a.out_seq + node * a.out_row + static_cast<long long>(head) * kHD + warp * 16;
+  st_global_v4(dst, pk[0], pk[1], pk[2], pk[3]);
+  st_global_v4(dst + 8, pk[4], pk[5], pk[6], pk[7]);
+  if (warp == 0 && a.lse != nullptr)
+    a.lse[(static_cast<long long>(b) * a.n + node) * (static_cast<long long>(a.heads) * a.group) + head] =
+        l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+}
+
 rf_status check_attn_desc(const rf_attn_desc* d) {
   if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
   if (d->n_seqs < 0 || d->n_q_heads <= 0 || d->n_kv_heads <= 0 || d->n_nodes <= 0 || d->capacity <= 0)
@@ -1000,15 +1314,16 @@ static AttnLayout attn_layout(const rf_attn_desc* d, void* ws) {
   return l;
 }
 
-template <int kHD, bool kDual>
-static rf_status launch_attn(const AttnArgs& a, int ctas, cudaStream_t s) {
+template <int kHD, bool kDual, class Args>
+static rf_status launch_attn(const Args& a, int ctas, cudaStream_t s) {
   static uint64_t done = 0;
   using Cfg = AttnCfg<kHD, kDual>;
   static_assert(Cfg::kSmem <= 227 * 1024, "shared memory beyond the 227 KB a CTA may hold");
-  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual>), Cfg::kSmem, &done);
+  static_assert(sizeof(AttnExchange) <= Cfg::kTileBytes, "the exchange does not fit into a query tile");
+  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual, Args>), Cfg::kSmem, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTENTION);
-  return cuda_check(launch_dependent(k_attn<kHD, kDual>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, 1, a),
+  return cuda_check(launch_dependent(k_attn<kHD, kDual, Args>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, 1, a),
                     "k_attn launch");
 }
 
@@ -1019,6 +1334,72 @@ using namespace rf;
 extern "C" size_t rf_attn_workspace_bytes(const rf_attn_desc* desc) {
   if (check_attn_desc(desc) != RF_OK) return 0;
   return attn_layout(desc, nullptr).bytes;
+}
+
+// Checks of the tensors, and the kernel's arguments from them (all but its workspace); `tiles`: row tiles
+// of an item.
+static rf_status attn_args(const rf_attn_desc* d, const rf_bf16* q, const rf_bf16* k_cache, const rf_bf16* v_cache,
+                           const int32_t* lens, const rf_bf16* k_draft, const rf_bf16* v_draft, const uint64_t* tree_mask,
+                           rf_bf16* out, float* lse, int32_t* dev_status, int tiles, AttnArgs* args) {
+  if (!q || !k_cache || !v_cache || !lens || !k_draft || !v_draft || !out)
+    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_draft) || !aligned16(v_draft) ||
+      !aligned16(out))
+    return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return fail(RF_ERR_ALIGN, "arrays must be aligned to their elements");
+  AttnArgs& a = *args;
+  const uint64_t H = d->n_kv_heads, n = d->n_nodes, B = d->n_seqs;
+  a.lens = lens;
+  a.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
+  a.v_draft = reinterpret_cast<const __nv_bfloat16*>(v_draft);
+  a.out = reinterpret_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.dev_status = dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  a.out_row = d->out_row_stride;
+  a.out_seq = d->out_seq_stride;
+  a.draft_row = d->draft_row_stride;
+  a.draft_seq = d->draft_seq_stride;
+  a.n_seqs = static_cast<int>(B);
+  a.heads = static_cast<int>(H);
+  a.group = static_cast<int>(d->n_q_heads / d->n_kv_heads);
+  a.npt = kAtTile / a.group;
+  a.n = static_cast<int>(n);
+  a.capacity = static_cast<int>(d->capacity);
+  a.words = static_cast<int>(RF_TREE_WORDS(n));
+  a.scale = static_cast<float>(d->scale);
+  const int64_t per = static_cast<int64_t>(a.npt) * tiles;  // nodes of an item
+  a.m_items = static_cast<int>((n + per - 1) / per);
+  int64_t draft_sum = 0;
+  for (int64_t mt = 0; mt < a.m_items; ++mt) {
+    const int64_t seen = tree_mask != nullptr ? static_cast<int64_t>(n) : std::min<int64_t>(n, (mt + 1) * per);
+    draft_sum += (seen + kAtTile - 1) / kAtTile;
+  }
+  if (draft_sum >= (int64_t(1) << 31)) return fail(RF_ERR_SHAPE, "n_nodes is too large");
+  a.draft_sum = static_cast<int>(draft_sum);
+  return RF_OK;
+}
+
+// The tensor maps.
+static rf_status attn_maps(const rf_attn_desc* d, const rf_bf16* q, const rf_bf16* k_cache, const rf_bf16* v_cache,
+                           const rf_bf16* k_draft, const rf_bf16* v_draft, AttnArgs* args) {
+  AttnArgs& a = *args;
+  const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs, cap = d->capacity;
+  rf_status st;
+  // a box of a row tile: every head of the group, npt nodes
+  if ((st = make_tmap_bf16_4d(&a.tm_q, q, {hd, Hq, n, B}, {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
+                              {64, (uint32_t)a.group, (uint32_t)a.npt, 1})) != RF_OK)
+    return st;
+  const uint64_t cs[3] = {hd, (uint64_t)d->cache_row_stride, (uint64_t)d->cache_seq_stride};
+  const uint64_t ds[3] = {hd, (uint64_t)d->draft_row_stride, (uint64_t)d->draft_seq_stride};
+  const uint64_t cd[4] = {hd, H, cap, B}, dd[4] = {hd, H, n, B};
+  const uint32_t box[4] = {64, 1, kAtTile, 1};
+  if ((st = make_tmap_bf16_4d(&a.tm_k, k_cache, cd, cs, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_v, v_cache, cd, cs, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_kd, k_draft, dd, ds, box)) != RF_OK) return st;
+  return make_tmap_bf16_4d(&a.tm_vd, v_draft, dd, ds, box);
 }
 
 extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, const rf_bf16* k_cache,
@@ -1032,69 +1413,22 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   if (tree_mask != nullptr && d->n_nodes > RF_TREE_MAX_NODES)
     return fail(RF_ERR_SHAPE, "n_nodes must be <= %d with a mask", RF_TREE_MAX_NODES);
   if (d->n_seqs == 0) return RF_OK;
-  if (!q || !k_cache || !v_cache || !lens || !k_draft || !v_draft || !out)
-    return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
-  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_draft) || !aligned16(v_draft) ||
-      !aligned16(out))
-    return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
-  if ((reinterpret_cast<uintptr_t>(lens) & 3u) || (reinterpret_cast<uintptr_t>(tree_mask) & 7u) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return fail(RF_ERR_ALIGN, "arrays must be aligned to their elements");
   const AttnLayout lay = attn_layout(d, workspace);
+  AttnArgs a{};
+  if ((st = attn_args(d, q, k_cache, v_cache, lens, k_draft, v_draft, tree_mask, out, lse, dev_status, lay.tiles, &a)) != RF_OK)
+    return st;
   if (workspace == nullptr || workspace_bytes < lay.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
   int sms = 0;
   if ((st = current_device(&sms)) != RF_OK) return st;
+  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, &a)) != RF_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs;
-  const int group = static_cast<int>(Hq / H);
-  AttnArgs a{};
-  a.npt = kAtTile / group;
-  const uint64_t cap = d->capacity;
-  // a box of a row tile: every head of the group, npt nodes
-  if ((st = make_tmap_bf16_4d(&a.tm_q, q, {hd, Hq, n, B}, {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
-                              {64, (uint32_t)group, (uint32_t)a.npt, 1})) != RF_OK)
-    return st;
-  const uint64_t cs[3] = {hd, (uint64_t)d->cache_row_stride, (uint64_t)d->cache_seq_stride};
-  const uint64_t ds[3] = {hd, (uint64_t)d->draft_row_stride, (uint64_t)d->draft_seq_stride};
-  const uint64_t cd[4] = {hd, H, cap, B}, dd[4] = {hd, H, n, B};
-  const uint32_t box[4] = {64, 1, kAtTile, 1};
-  if ((st = make_tmap_bf16_4d(&a.tm_k, k_cache, cd, cs, box)) != RF_OK) return st;
-  if ((st = make_tmap_bf16_4d(&a.tm_v, v_cache, cd, cs, box)) != RF_OK) return st;
-  if ((st = make_tmap_bf16_4d(&a.tm_kd, k_draft, dd, ds, box)) != RF_OK) return st;
-  if ((st = make_tmap_bf16_4d(&a.tm_vd, v_draft, dd, ds, box)) != RF_OK) return st;
-  a.lens = lens;
-  a.mask = reinterpret_cast<const unsigned long long*>(tree_mask);
-  a.v_draft = reinterpret_cast<const __nv_bfloat16*>(v_draft);
-  a.out = reinterpret_cast<__nv_bfloat16*>(out);
-  a.lse = lse;
   a.part_o = lay.part_o;
   a.part_ml = lay.part_ml;
   a.plan = lay.plan;
-  a.dev_status = dev_status;
-  a.timeout_ns = wait_timeout_ns();
-  a.out_row = d->out_row_stride;
-  a.out_seq = d->out_seq_stride;
-  a.draft_row = d->draft_row_stride;
-  a.draft_seq = d->draft_seq_stride;
-  a.n_seqs = static_cast<int>(B);
-  a.heads = static_cast<int>(H);
-  a.group = group;
-  a.n = static_cast<int>(n);
-  a.capacity = static_cast<int>(cap);
-  a.words = static_cast<int>(RF_TREE_WORDS(n));
-  a.scale = static_cast<float>(d->scale);
-  const int64_t per = static_cast<int64_t>(a.npt) * lay.tiles;  // nodes of an item
-  a.m_items = static_cast<int>((n + per - 1) / per);
-  int64_t draft_sum = 0;
-  for (int64_t mt = 0; mt < a.m_items; ++mt) {
-    const int64_t seen = tree_mask != nullptr ? static_cast<int64_t>(n) : std::min<int64_t>(n, (mt + 1) * per);
-    draft_sum += (seen + kAtTile - 1) / kAtTile;
-  }
-  if (draft_sum >= (int64_t(1) << 31)) return fail(RF_ERR_SHAPE, "n_nodes is too large");
-  a.draft_sum = static_cast<int>(draft_sum);
+  const uint64_t hd = d->head_dim, H = d->n_kv_heads, n = d->n_nodes, B = d->n_seqs, cap = d->capacity;
   // no more CTAs than weight, which is at least the tiles
-  const int64_t most = static_cast<int64_t>(B * H) * (a.m_items * static_cast<int64_t>((cap + kAtTile - 1) / kAtTile + kAtItemCost) + draft_sum);
+  const int64_t most = static_cast<int64_t>(B * H) * (a.m_items * static_cast<int64_t>((cap + kAtTile - 1) / kAtTile + kAtItemCost) + a.draft_sum);
   const int ctas = static_cast<int>(std::min<int64_t>(most, std::min(sms, kAtMaxCtas)));
   if (hd == 128) st = lay.tiles == 2 ? launch_attn<128, true>(a, ctas, s) : launch_attn<128, false>(a, ctas, s);
   else st = lay.tiles == 2 ? launch_attn<64, true>(a, ctas, s) : launch_attn<64, false>(a, ctas, s);
@@ -1109,13 +1443,13 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
   c.out_seq = a.out_seq;
   c.n = a.n;
   c.heads = a.heads;
-  c.group = group;
+  c.group = a.group;
   c.npt = a.npt;
   c.tiles = lay.tiles;
   c.ctas = ctas;
   c.scale = a.scale;
   // rows of an item that exist, in a tile's numbering (the first tile's are followed by a gap)
-  const int tile_rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * group, a.npt * group));
+  const int tile_rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(n) * a.group, a.npt * a.group));
   const int rows = lay.tiles == 2 ? 2 * kAtTile : tile_rows;
   const bool few = rows <= 32 && B * H * a.m_items * 8 <= ctas;
   const dim3 grid(static_cast<unsigned>(ctas - 1), static_cast<unsigned>((rows + (few ? 7 : 31)) / (few ? 8 : 32)));
@@ -1124,4 +1458,148 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
                                            : (few ? k_attn_combine<64, 8, 4> : k_attn_combine<64, 4, 1>);
   return cuda_check(launch_dependent(combine, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, 1, c),
                     "k_attn_combine launch");
+}
+
+// ------------------------------------------------------------------- with a prefix
+static rf_status check_prefix_desc(const rf_prefix_attn_desc* d) {
+  if (d == nullptr) return fail(RF_ERR_INVALID_ARG, "desc is NULL");
+  const rf_status st = check_attn_desc(&d->attn);
+  if (st != RF_OK) return st;
+  if (d->prefix_capacity <= 0) return fail(RF_ERR_INVALID_ARG, "need prefix_capacity > 0");
+  if (d->prefix_capacity > (int64_t(1) << 30)) return fail(RF_ERR_SHAPE, "need prefix_capacity <= 2^30");
+  if (d->attn.n_seqs * d->attn.n_nodes > (int64_t(1) << 28) / d->attn.n_q_heads)
+    return fail(RF_ERR_SHAPE, "need n_seqs * n_nodes * n_q_heads <= 2^28");
+  if (d->prefix_row_stride < d->attn.n_kv_heads * d->attn.head_dim || d->prefix_row_stride % 8)
+    return fail(RF_ERR_ALIGN, "prefix_row_stride must be a multiple of 8, >= n_kv_heads*head_dim");
+  if (d->prefix_row_stride >= (int64_t(1) << 39)) return fail(RF_ERR_SHAPE, "strides must be < 2^39");
+  return RF_OK;
+}
+
+struct PrefixLayout {
+  float4 *part_o, *whole_o;
+  float2 *part_ml, *whole_ml;
+  int2* item_ctas;
+  int tiles, p_nodes, p_seqs, p_split, p_items, m_items, rows, p_rows;
+  size_t bytes;
+};
+
+static PrefixLayout prefix_layout(const rf_attn_desc* d, void* ws) {
+  PrefixLayout l;
+  const int64_t group = d->n_q_heads / d->n_kv_heads, npt = kAtTile / group, n = d->n_nodes, B = d->n_seqs, H = d->n_kv_heads;
+  l.tiles = B * n * group > kAtTile ? 2 : 1;
+  l.p_nodes = static_cast<int>(std::min(n, npt));
+  l.p_seqs = static_cast<int>(n <= npt ? std::min(npt / n, std::max<int64_t>(B, 1)) : 1);
+  l.p_split = static_cast<int>(n <= npt ? 1 : (n + npt - 1) / npt);
+  const int64_t p_tiles = n <= npt ? (B + l.p_seqs - 1) / l.p_seqs : B * l.p_split;
+  l.p_items = static_cast<int>((p_tiles + l.tiles - 1) / l.tiles);
+  l.m_items = static_cast<int>((n + npt * l.tiles - 1) / (npt * l.tiles));
+  l.p_rows = static_cast<int>(l.tiles * group * l.p_nodes * l.p_seqs);
+  l.rows = static_cast<int>(n <= npt ? n * group : l.tiles * npt * group);
+  const size_t cut = static_cast<size_t>(2 * kAtMaxCtas) * l.tiles * kAtTile;
+  const size_t whole = static_cast<size_t>(H) * l.p_items * l.p_rows + static_cast<size_t>(B * H) * l.m_items * l.rows;
+  Carve c(ws);
+  l.part_o = c.take<float4>(cut * d->head_dim / 4);
+  l.part_ml = c.take<float2>(cut);
+  l.whole_o = c.take<float4>(whole * d->head_dim / 4);
+  l.whole_ml = c.take<float2>(whole);
+  l.item_ctas = c.take<int2>(static_cast<size_t>(H) * l.p_items + static_cast<size_t>(B * H) * l.m_items);
+  l.bytes = c.bytes();
+  return l;
+}
+
+extern "C" size_t rf_prefix_attn_workspace_bytes(const rf_prefix_attn_desc* desc) {
+  if (check_prefix_desc(desc) != RF_OK) return 0;
+  return prefix_layout(&desc->attn, nullptr).bytes;
+}
+
+extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const rf_bf16* q, const rf_bf16* k_prefix,
+                                         const rf_bf16* v_prefix, const int32_t* prefix_len, const rf_bf16* k_cache,
+                                         const rf_bf16* v_cache, const int32_t* lens, const rf_bf16* k_draft,
+                                         const rf_bf16* v_draft, const uint64_t* tree_mask, rf_bf16* out, float* lse,
+                                         int32_t* dev_status, void* workspace, size_t workspace_bytes, rf_stream_t stream) {
+  clear_error();
+  rf_status st = check_prefix_desc(desc);
+  if (st != RF_OK) return st;
+  const rf_attn_desc* d = &desc->attn;
+  if (tree_mask != nullptr && d->n_nodes > RF_TREE_MAX_NODES)
+    return fail(RF_ERR_SHAPE, "n_nodes must be <= %d with a mask", RF_TREE_MAX_NODES);
+  if (d->n_seqs == 0) return RF_OK;
+  const PrefixLayout lay = prefix_layout(d, workspace);
+  PrefixArgs a{};
+  if ((st = attn_args(d, q, k_cache, v_cache, lens, k_draft, v_draft, tree_mask, out, lse, dev_status, lay.tiles, &a)) != RF_OK)
+    return st;
+  if (!k_prefix || !v_prefix || !prefix_len) return fail(RF_ERR_INVALID_ARG, "tensor pointers must be non-NULL");
+  if (!aligned16(k_prefix) || !aligned16(v_prefix)) return fail(RF_ERR_ALIGN, "row buffers must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(prefix_len) & 3u) return fail(RF_ERR_ALIGN, "arrays must be aligned to their elements");
+  if (workspace == nullptr || workspace_bytes < lay.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
+  int sms = 0;
+  if ((st = current_device(&sms)) != RF_OK) return st;
+  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, &a)) != RF_OK) return st;
+  const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs;
+  const uint64_t ps[3] = {hd, (uint64_t)desc->prefix_row_stride, (uint64_t)desc->prefix_row_stride};
+  const uint64_t pd[4] = {hd, H, (uint64_t)desc->prefix_capacity, 1};
+  const uint32_t box[4] = {64, 1, kAtTile, 1};
+  if ((st = make_tmap_bf16_4d(&a.tm_qp, q, {hd, Hq, n, B}, {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
+                              {64, (uint32_t)a.group, (uint32_t)lay.p_nodes, (uint32_t)lay.p_seqs})) != RF_OK)
+    return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_kp, k_prefix, pd, ps, box)) != RF_OK) return st;
+  if ((st = make_tmap_bf16_4d(&a.tm_vp, v_prefix, pd, ps, box)) != RF_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  a.part_o = lay.part_o;
+  a.part_ml = lay.part_ml;
+  a.whole_o = lay.whole_o;
+  a.whole_ml = lay.whole_ml;
+  a.item_ctas = lay.item_ctas;
+  a.prefix_len = prefix_len;
+  a.prefix_capacity = static_cast<int>(desc->prefix_capacity);
+  a.p_nodes = lay.p_nodes;
+  a.p_seqs = lay.p_seqs;
+  a.p_split = lay.p_split;
+  a.p_items = lay.p_items;
+  a.narrow = a.n <= a.npt;
+  a.rows = lay.rows;
+  a.p_rows = lay.p_rows;
+  const int ctas = std::min(sms, kAtMaxCtas);
+  if (hd == 128) st = lay.tiles == 2 ? launch_attn<128, true>(a, ctas, s) : launch_attn<128, false>(a, ctas, s);
+  else st = lay.tiles == 2 ? launch_attn<64, true>(a, ctas, s) : launch_attn<64, false>(a, ctas, s);
+  if (st != RF_OK) return st;
+  JoinArgs j{};
+  j.part_o = lay.part_o;
+  j.part_ml = lay.part_ml;
+  j.whole_o = lay.whole_o;
+  j.whole_ml = lay.whole_ml;
+  j.item_ctas = lay.item_ctas;
+  j.lens = lens;
+  j.prefix_len = prefix_len;
+  j.out = a.out;
+  j.lse = lse;
+  j.out_row = a.out_row;
+  j.out_seq = a.out_seq;
+  j.n_seqs = a.n_seqs;
+  j.n = a.n;
+  j.heads = a.heads;
+  j.group = a.group;
+  j.npt = a.npt;
+  j.tiles = lay.tiles;
+  j.m_items = a.m_items;
+  j.p_nodes = lay.p_nodes;
+  j.p_seqs = lay.p_seqs;
+  j.p_split = lay.p_split;
+  j.p_items = lay.p_items;
+  j.rows = lay.rows;
+  j.p_rows = lay.p_rows;
+  j.ctas = ctas;
+  j.capacity = a.capacity;
+  j.prefix_capacity = a.prefix_capacity;
+  j.scale = a.scale;
+  const int64_t rows = static_cast<int64_t>(B * n) * a.group;  // of a KV head
+  const bool few = (rows + 31) / 32 * static_cast<int64_t>(H) < sms;
+  const int64_t blocks = (rows + (few ? 7 : 31)) / (few ? 8 : 32);
+  ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
+  void (*join)(JoinArgs) = hd == 128 ? (few ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 1>)
+                                     : (few ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 1>);
+  return cuda_check(launch_dependent(join, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H)), dim3(static_cast<unsigned>(2 * hd)),
+                                     0, s, 1, j),
+                    "k_prefix_join launch");
 }

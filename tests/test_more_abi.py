@@ -109,3 +109,45 @@ def test_sample_refuses_pointers():
     _refused(INV, rf.rf_sample, _sample(ld_probs=104), FAR, *GOOD[1:6], FAR, *GOOD[7:])
     _refused(INV, rf.rf_sample, _sample(dtype=rf.RF_BF16), FAR, *GOOD[1:6], FAR, *GOOD[7:])
     rf.rf_sample(_sample(n_rows=0), None, stream=0)
+
+
+# ------------------------------------------------------------ attention over a shared prefix
+def _prefix(prefix_capacity=50, prefix_row_stride=256, **kw):
+    d = dict(n_seqs=2, n_q_heads=8, n_kv_heads=2, head_dim=128, n_nodes=4, capacity=100, q_row_stride=1024,
+             q_seq_stride=4096, draft_row_stride=256, draft_seq_stride=1024, cache_row_stride=256, cache_seq_stride=25600,
+             out_row_stride=1024, out_seq_stride=4096, scale=0.1)
+    d.update(kw)
+    return rf.rf_prefix_attn_desc(attn=rf.rf_attn_desc(**d), prefix_capacity=prefix_capacity,
+                                  prefix_row_stride=prefix_row_stride)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(n_seqs=-1), INV), (dict(n_nodes=0), INV), (dict(capacity=0), INV), (dict(scale=0.0), INV), (dict(flags=1), INV),
+    (dict(head_dim=96), SHAPE), (dict(n_q_heads=7), SHAPE), (dict(q_row_stride=1016), ALIGN),
+    (dict(cache_row_stride=260), ALIGN), (dict(prefix_capacity=0), INV), (dict(prefix_capacity=(1 << 30) + 1), SHAPE),
+    (dict(prefix_row_stride=248), ALIGN), (dict(prefix_row_stride=260), ALIGN), (dict(prefix_row_stride=1 << 39), SHAPE),
+    (dict(n_seqs=1 << 20, n_nodes=64), SHAPE)])
+def test_prefix_attention_refuses_bad_descriptors(bad, status):
+    d = _prefix(**bad)
+    assert rf.rf_prefix_attn_workspace_bytes(d) == 0
+    _refused(status, rf.rf_prefix_attention, d, *[P] * 12, None, P, 1 << 50)
+
+
+def test_prefix_attention_refuses_pointers():
+    d = _prefix()
+    need = rf.rf_prefix_attn_workspace_bytes(d)
+    # q, k_prefix, v_prefix, prefix_len, k_cache, v_cache, lens, k_draft, v_draft, tree_mask, out, lse
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 10):
+        a = [P] * 12
+        a[i] = None
+        _refused(INV, rf.rf_prefix_attention, d, *a, None, P, need)
+    for i in range(12):
+        a = [P] * 12
+        a[i] += 2
+        _refused(ALIGN, rf.rf_prefix_attention, d, *a, None, P, need)
+    _refused(WS, rf.rf_prefix_attention, d, *[P] * 12, None, None, need)
+    _refused(WS, rf.rf_prefix_attention, d, *[P] * 12, None, P, need - 1)
+    _refused(WS, rf.rf_prefix_attention, d, *[P] * 12, None, P + 128, need)
+    wide = _prefix(n_nodes=1025, q_seq_stride=1 << 21, draft_seq_stride=1 << 19, out_seq_stride=1 << 21)
+    _refused(SHAPE, rf.rf_prefix_attention, wide, *[P] * 12, None, P, 1 << 50)            # with a mask
+    rf.rf_prefix_attention(_prefix(n_seqs=0), *[None] * 12, stream=0)
