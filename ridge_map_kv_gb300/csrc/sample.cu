@@ -6,9 +6,10 @@
 // last token. Weights are w = 2^-t, t = (max - logit) log2(e) / T.
 //
 // Where the runs end is decided as in 64 bits. Logits are compared as they are. Masses are integers,
-// so that sums do not depend on their order: t is a sum of two fp32 numbers, and 2^-t comes from a table
-// of 64 powers and a polynomial, within about 2^-39 of the greatest weight (token_mass). In fp32 sums a
-// flat row's nucleus would end a token early or late every few dozen rows.
+// so that sums do not depend on their order: t is a sum of two fp32 numbers, and falls into one of 2,048
+// bins of 1/64 each; within a bin the weights differ by a factor 1 - q that a polynomial gives to 2^-30,
+// so a bin needs the count of its tokens and the sum of their q, which one 64-bit addition to shared
+// memory updates. In fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
 //
 // One cluster of up to eight CTAs a row, each with a share of the vocabulary, which it reads once for the
 // maximum and then again, from L2:
@@ -16,17 +17,18 @@
 //             of the groups' maxima is a logit that at least so many tokens reach: what lies below it
 //             cannot stay. The others, a few hundred, are listed and sorted; all filters and the draw then
 //             take the list alone.
-//   any other  A table of counts and masses by octaves of weight (each thread adds to 24 entries of its own
-//             in shared memory: no atomics). A run's end lies in one octave; finer tables, of 2048 bins
-//             over the octave's (logit, token) pairs, narrow it down to a few tokens, which are sorted. A
-//             pass over all then adds up the weights and draws, another writes probabilities.
+//   any other  The bins' table is built and summed over the cluster. A run's end lies in one bin, whose tokens
+//             are listed and sorted (where they are too many, finer tables over the bin's (logit, token)
+//             pairs narrow them down). A pass over all then adds up the weights that stay and draws, another
+//             writes probabilities.
 //
-// Bound: the logits' bytes (and the probabilities'), beside some 40 operations a token where masses
+// Bound: the logits' bytes (and the probabilities'), beside some 30 operations a token where masses
 // are formed.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <cfloat>
+#include <cstddef>
 #include <cmath>
 
 #include "rf_device.cuh"
@@ -39,18 +41,19 @@ constexpr int kSampleThreads = 512;
 constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleCtas = 8;        // CTAs of a cluster (the portable limit)
 constexpr int kSampleShare = 2048;    // least tokens of a CTA
-constexpr int kOctaves = 24;          // the last one holds every smaller weight as well
-constexpr int kBins = 2048;
+constexpr int kSampleLong = 32768;    // tokens from which on a row has two CTAs at least
+constexpr int kBins = 2048;           // of the table of masses: 64 an octave; the last one holds all smaller weights
 constexpr int kListed = 1024;         // tokens that are sorted at most
 constexpr int kFewTokens = 128;       // top-k up to which tokens are listed at once: G groups leave about
                                       // G (ln G + 0.6) tokens, some 700 of 128
 constexpr int kSampleMaxVocab = 1 << 20;
-constexpr int kMassBits = 40;         // a weight of 1, within its octave
-constexpr int kCommonBits = 43;       // a weight of 1, over all octaves: 2^20 of them are 2^63
-static_assert(kSampleMaxVocab / kSampleThreads < (1 << (64 - kMassBits - 12)), "a thread's counts and masses share 64 bits");
+constexpr int kMassBits = 29;         // a weight of 1, within its bin
+constexpr int kCommonBits = 42;       // a weight of 1, over all bins
+constexpr int kCountShift = 44;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
+static_assert(kSampleMaxVocab <= 1 << (64 - kCountShift) && 23 + 20 < kCountShift, "counts and masses share 64 bits");
 
 struct PowerTable {
-  unsigned long long t[65];  // 2^(40 - i/64)
+  unsigned long long t[64];  // 2^(63 - i/64)
 };
 
 struct SampleArgs {
@@ -69,130 +72,150 @@ struct SampleArgs {
   int vocab;
 };
 
-// A token's place in the order: falling logit, then rising token. -0 and 0 are equal.
+// A token's place in the order: falling logit, then rising token. -0 and 0 are equal. A bf16 logit takes 16
+// bits, so that tables over places tell its many equals apart by their tokens the sooner.
 __device__ __forceinline__ unsigned rising_key(float x) {
   const unsigned b = __float_as_uint(x + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float key_value(unsigned k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); }
+template <bool kShort>
 __device__ __forceinline__ unsigned long long place_of(float x, int i) {
-  return (static_cast<unsigned long long>(~rising_key(x)) << 20) | static_cast<unsigned>(i);
+  return (static_cast<unsigned long long>(~rising_key(x) >> (kShort ? 16 : 0)) << 20) | static_cast<unsigned>(i);
 }
-__device__ __forceinline__ float place_value(unsigned long long p) { return key_value(~static_cast<unsigned>(p >> 20)); }
+template <bool kShort>
+__device__ __forceinline__ float place_value(unsigned long long p) {
+  const unsigned k = static_cast<unsigned>(p >> 20);
+  if (!kShort) return key_value(~k);
+  return __uint_as_float((k & 0x8000u ? k : 0x7fffu ^ k) << 16);
+}
 __device__ __forceinline__ int place_token(unsigned long long p) { return static_cast<int>(p & 0xfffffu); }
 
 struct Scale {
   float m, c, c_lo;  // the row's maximum; log2(e) / T = c + c_lo
 };
 
-// t = (m - x) c as hi + lo, to about 2^-46 of itself.
+// t = (m - x) c as hi + lo, to about 2^-46 of itself. (A difference of bf16 numbers is exact but for those
+// that are 2^16 times smaller than the other one.)
+template <bool kExact>
 __device__ __forceinline__ void distance(const Scale& s, float x, float& hi, float& lo) {
-  const float d = s.m - x, b = d - s.m;
-  const float e = (s.m - (d - b)) - (x + b);  // m - x = d + e
+  const float d = s.m - x;
   hi = d * s.c;
   lo = fmaf(d, s.c, -hi);
   lo = fmaf(d, s.c_lo, lo);
-  lo = fmaf(e, s.c, lo);
+  if (!kExact) {
+    const float b = d - s.m;
+    lo = fmaf((s.m - (d - b)) - (x + b), s.c, lo);
+  }
 }
 // 2^-t in fp32 (0 below 2^-126).
+template <bool kExact>
 __device__ __forceinline__ float weight_of(const Scale& s, float x) {
   float hi, lo;
-  distance(s, x, hi, lo);
+  distance<kExact>(s, x, hi, lo);
   return hi < 150.0f ? exp2f_ftz(-hi) * fmaf(lo, -0.693147181f, 1.0f) : 0.0f;
 }
 
-// A token's octave and its mass there, 2^(40 + octave - t). With r = t - its whole part = k/64 + r',
-// 2^-r = 2^(-k/64) (1 - q), q = z - z^2/2 + z^3/6 - z^4/24, z = r' ln 2 < 0.0055: the next term is
-// 2^-44. z is kept as a sum of two numbers; the other terms are below 2^-16, their rounding below 2^-39.
-__device__ __forceinline__ int token_mass(const Scale& s, float x, const unsigned long long* power, unsigned long long& mass) {
-  float hi, lo;
-  distance(s, x, hi, lo);
-  if (!(hi < static_cast<float>(kOctaves + kMassBits))) {
-    mass = 0;
-    return kOctaves - 1;
-  }
-  const int n = static_cast<int>(hi);
-  const float r = hi - static_cast<float>(n);
-  constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it rounds to whole numbers
-  const float y = fmaf(r, 64.0f, kRound);
-  const int k = __float_as_int(y) - 0x4b400000;
-  const float rest = fmaf(y - kRound, -0.015625f, r);
-  const float a = rest + lo, b = lo - (a - rest);
-  constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;
-  const float z = a * kLn2;
-  float tail = fmaf(a, kLn2, -z);
-  tail = fmaf(a, kLn2Lo, tail);
-  tail = fmaf(b, kLn2, tail);
-  tail = fmaf(-z * z, fmaf(-z, fmaf(-z, 0.0416666667f, 0.166666667f), 0.5f), tail);
-  // q in units of 2^-38
-  const float u = fmaf(z, 16777216.0f, kRound);
-  const float left = fmaf(u - kRound, -5.9604644775390625e-8f, z) + tail;
-  const int q = (__float_as_int(u) - 0x4b400000) * 16384 + (__float_as_int(fmaf(left, 274877906944.0f, kRound)) - 0x4b400000);
-  const unsigned long long p = power[k];
-  const long long cut = (static_cast<long long>(static_cast<int>((p + 512) >> 10)) * q) >> 28;
-  const int octave = min(n, kOctaves - 1);
-  mass = (p - static_cast<unsigned long long>(cut)) >> (n - octave);
-  return octave;
+constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it rounds to whole numbers
+constexpr float kTail = (kBins - 2) / 64.0f;
+// The bin of t = hi + lo: the whole number nearest to 64 hi, or the last.
+__device__ __forceinline__ int near_bin(float hi) { return __float_as_int(fmaf(hi, 64.0f, kRound)) - 0x4b400000; }
+__device__ __forceinline__ int bin_of(float hi) { return hi < kTail ? near_bin(hi) : kBins - 1; }
+// A bin's entry is its count above a sum (kCountShift). What a token adds to the sum: in the bins,
+// 2^-t = 2^(-bin/64) (1 - q) with q = z - z^2/2 + z^3/6, z = (t - bin/64) ln 2 within 0.0055 (the next term is
+// 2^-34); in the last one, 2^22 times the weight as a part of 2^(-2047/64).
+__device__ __forceinline__ unsigned bin_part(float hi, float lo) {
+  const float y = fmaf(hi, 64.0f, kRound);
+  const float z = (fmaf(y - kRound, -0.015625f, hi) + lo) * 0.693147181f;
+  const float q = fmaf(-z * z, fmaf(-z, 0.166666667f, 0.5f), z);
+  return __float_as_uint(fmaf(q, 536870912.0f, kRound)) - 0x4b000000u;
 }
-// An octave's mass over all octaves, rounded down.
-__device__ __forceinline__ unsigned long long common_mass(unsigned long long mass, int octave) {
-  return (mass << (kCommonBits - kMassBits)) >> octave;
+__device__ __forceinline__ unsigned tail_part(float hi) {
+  return __float2uint_rn(exp2f_ftz(fminf((kBins - 1) / 64.0f - hi, 0.0f)) * 4194304.0f);
+}
+__device__ __forceinline__ unsigned part_of(float hi, float lo) { return hi < kTail ? bin_part(hi, lo) : tail_part(hi); }
+__device__ __forceinline__ unsigned long long entry_of(float hi, float lo) { return (1ull << kCountShift) + part_of(hi, lo); }
+__device__ __forceinline__ unsigned entry_count(unsigned long long e) { return static_cast<unsigned>(e >> kCountShift); }
+// An entry's mass, in units of 2^-29 of its bin's weight.
+__device__ __forceinline__ unsigned long long entry_mass(unsigned long long e, int bin) {
+  const unsigned long long sum = e & ((1ull << kCountShift) - 1);
+  return bin < kBins - 1 ? (e >> kCountShift) * ((1ull << kMassBits) + (1ull << 22)) - sum : sum << (kMassBits - 22);
+}
+// That mass in units of 2^-42, rounded down: mass 2^13 2^(-bin/64). (mass < 2^50)
+__device__ __forceinline__ unsigned long long common_mass(const unsigned long long* power, unsigned long long mass, int bin) {
+  return __umul64hi(mass << (kCommonBits - kMassBits + 1), power[bin & 63]) >> (bin >> 6);
 }
 
-// f(first token, values) for the tokens v0 <= i < v1 of a row: 16 bytes at a time between the row's
-// first and last 16-byte boundaries, one token at a time outside them. A thread's tokens rise.
-template <class T, class F>
-__device__ __forceinline__ void for_tokens(const T* row, int v0, int v1, F f) {
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kBatch = 2;
+// f(first token, values, others) for the tokens v0 <= i < v1 of a row: 16 bytes at a time between the row's
+// first and last 16-byte boundaries, one token at a time outside them. A thread's tokens rise. `other`: a
+// second row that is read along with the first (kOther).
+template <bool kOther, class T, class F>
+__device__ __forceinline__ void for_both(const T* row, const float* other, int v0, int v1, F f) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kBatch = kOther ? 8 / kVec : 4;
   const int tid = threadIdx.x;
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row + v0) & 15u) / sizeof(T));
   const int head = min(v1 - v0, (kVec - off) % kVec);
   auto one = [&](int i) {
-    float x[1];
+    float x[1], e[1] = {};
     if constexpr (sizeof(T) == 2) x[0] = __bfloat162float(row[i]);
     else x[0] = row[i];
-    f(i, x);
+    if constexpr (kOther) e[0] = other[i];
+    f(i, x, e);
   };
   if (tid < head) one(v0 + tid);
   const int first = v0 + head, pieces = (v1 - first) / kVec;
+  const bool even = (reinterpret_cast<uintptr_t>(other + first) & 15u) == 0;
   for (int p0 = tid; p0 < pieces; p0 += kBatch * kSampleThreads) {
     uint4 raw[kBatch];
+    alignas(16) float e[kBatch][kOther ? kVec : 1];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if (p0 + j * kSampleThreads < pieces) raw[j] = reinterpret_cast<const uint4*>(row + first)[p0 + j * kSampleThreads];
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = p0 + j * kSampleThreads;
+      if (p >= pieces) break;
+      raw[j] = reinterpret_cast<const uint4*>(row + first)[p];
+      if constexpr (kOther) {
+        const float* o = other + first + p * kVec;
+        if (even) {
+#pragma unroll
+          for (int k = 0; k < kVec; k += 4) *reinterpret_cast<float4*>(e[j] + k) = *reinterpret_cast<const float4*>(o + k);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kVec; ++k) e[j][k] = o[k];
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (p0 + j * kSampleThreads >= pieces) break;
       const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
       float x[kVec];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        if constexpr (sizeof(T) == 2) x[e] = u2f(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-        else x[e] = u2f(w[e]);
+      for (int k = 0; k < kVec; ++k) {
+        if constexpr (sizeof(T) == 2) x[k] = u2f(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+        else x[k] = u2f(w[k]);
       }
-      f(first + (p0 + j * kSampleThreads) * kVec, x);
+      f(first + (p0 + j * kSampleThreads) * kVec, x, e[j]);
     }
   }
   const int last = first + pieces * kVec + tid;
   if (last < v1) one(last);
 }
+template <class T, class F>
+__device__ __forceinline__ void for_tokens(const T* row, int v0, int v1, F f) {
+  for_both<false>(row, nullptr, v0, v1, [&](int i, const auto& x, const auto&) { f(i, x); });
+}
 
 struct SampleShared {
-  unsigned long long power[65];
+  unsigned long long power[64];
   unsigned long long warp_sum[kSampleWarps];
   unsigned warp_count[kSampleWarps];
-  float warp_key[kSampleWarps];
+  float warp_total[kSampleWarps];
   // from every CTA of the cluster, by the parity of the turn
   unsigned long long best[2][kSampleCtas];
   unsigned least[2][kSampleCtas];
   float sum[2][kSampleCtas];
   unsigned kept[2][kSampleCtas];
   unsigned listed[2][kSampleCtas];
-  // counts and masses by octaves: every CTA's, then the row's
-  unsigned octave_count[kSampleCtas][kOctaves];
-  unsigned long long octave_mass[kSampleCtas][kOctaves];
-  unsigned count[kOctaves];
-  unsigned long long mass[kOctaves];
   // where a run ends
   unsigned long long found_place, found_mass;
   unsigned found_bin, found_count, found_in;
@@ -200,16 +223,12 @@ struct SampleShared {
   double min_away;  // T ln(min_p)
   float lowest;     // the least logit that min_p lets pass
 };
-// One area for what is not needed at the same time: the threads' octaves, or tables and lists.
 struct SampleTables {
-  unsigned long long mass[kBins];      // of this CTA
-  unsigned count[kBins];
-  unsigned long long all_mass[kBins];  // of the cluster
-  unsigned all_count[kBins];
-  unsigned long long own_place[kListed], own_mass[kListed];
-  unsigned long long place[kListed], list_mass[kListed];
+  unsigned count[kBins], low[kBins], high[kBins];  // this CTA's counts and sums, by additions of 32 bits
+  unsigned long long all[kBins];    // the cluster's, of the weights' bins
+  unsigned long long finer[kBins];  // the cluster's, of finer tables
+  unsigned long long own_place[kListed], place[kListed];
 };
-constexpr size_t kSampleArea = std::max(sizeof(SampleTables), sizeof(unsigned long long) * kOctaves * kSampleThreads);
 
 // What all threads of a row's cluster know.
 struct Row {
@@ -261,31 +280,48 @@ __device__ __forceinline__ void before_sums(SampleShared& sh, unsigned& count, u
   mass = m0 + m - mass;
 }
 
-// Sorts the list by place (whole CTA), padded to a power of two with places beyond all.
+// Sorts the list by place (whole CTA), padded to a power of two with places beyond all: a bitonic network with
+// an element a thread (two for the longest lists), which exchanges within warps by shuffles and between them
+// through the two lists in turns, one barrier an exchange. (With all exchanges in shared memory 300 tokens took 6 us.)
 __device__ __forceinline__ void sort_list(SampleTables& t, int n) {
-  int size = 2;
+  static_assert(kListed == 2 * kSampleThreads, "two elements a thread");
+  const int tid = threadIdx.x;
+  int size = 32;
   while (size < n) size *= 2;
-  for (int i = n + static_cast<int>(threadIdx.x); i < size; i += kSampleThreads) {
-    t.place[i] = ~0ull;
-    t.list_mass[i] = 0;
-  }
+  unsigned long long v[2] = {tid < n ? t.place[tid] : ~0ull, tid + kSampleThreads < n ? t.place[tid + kSampleThreads] : ~0ull};
+  const bool two = size > kSampleThreads;
+  unsigned long long* from = t.own_place;
+  unsigned long long* other = t.place;
+  auto keep = [](unsigned long long a, unsigned long long b, bool least) { return (a < b) == least ? a : b; };
   __syncthreads();
   for (int k = 2; k <= size; k *= 2) {
     for (int j = k / 2; j > 0; j /= 2) {
-      for (int p = threadIdx.x; p < size / 2; p += kSampleThreads) {
-        const int i = 2 * p - (p & (j - 1)), o = i + j;
-        const unsigned long long a = t.place[i], b = t.place[o];
-        if ((a > b) == ((i & k) == 0)) {
-          t.place[i] = b;
-          t.place[o] = a;
-          const unsigned long long m = t.list_mass[i];
-          t.list_mass[i] = t.list_mass[o];
-          t.list_mass[o] = m;
+      const bool least = ((tid & j) == 0) == ((tid & k) == 0);
+      if (j >= 32) {
+        if (j == kSampleThreads) {
+          const unsigned long long a = v[0], b = v[1];
+          v[0] = min(a, b);
+          v[1] = max(a, b);
+          continue;
         }
+        if (tid < size) from[tid] = v[0];
+        if (two) from[tid + kSampleThreads] = v[1];
+        __syncthreads();
+        if (tid < size) v[0] = keep(v[0], from[tid ^ j], least);
+        if (two) v[1] = keep(v[1], from[(tid ^ j) + kSampleThreads], ((tid & j) == 0) == (((tid + kSampleThreads) & k) == 0));
+        unsigned long long* x = from;
+        from = other;
+        other = x;
+      } else {
+        v[0] = keep(v[0], __shfl_xor_sync(0xffffffffu, v[0], j), least);
+        if (two) v[1] = keep(v[1], __shfl_xor_sync(0xffffffffu, v[1], j), ((tid & j) == 0) == (((tid + kSampleThreads) & k) == 0));
       }
-      __syncthreads();
     }
   }
+  __syncthreads();
+  if (tid < size) t.place[tid] = v[0];
+  if (two) t.place[tid + kSampleThreads] = v[1];
+  __syncthreads();
 }
 
 // Every CTA's listed tokens into the lists of all; false (for all of the cluster) where they are more
@@ -307,10 +343,45 @@ __device__ __forceinline__ bool join_lists(cg::cluster_group& cl, SampleShared& 
   for (int x = threadIdx.x; x < own * r.ctas; x += kSampleThreads) {
     const int c = x / own, i = x - c * own;
     *cl.map_shared_rank(&t.place[before + i], c) = t.own_place[i];
-    *cl.map_shared_rank(&t.list_mass[before + i], c) = t.own_mass[i];
   }
   cl.sync();
   return true;
+}
+
+// Adds a token's part to a bin of this CTA's. (An addition of 64 bits to shared memory is a loop that tries until no
+// other lane is in its way; a carry out of the sum's low word comes once in some 500 additions.)
+__device__ __forceinline__ void add_to(SampleTables& t, int bin, unsigned count, unsigned part) {
+  atomicAdd(&t.count[bin], count);
+  if (atomicAdd(&t.low[bin], part) > ~part) atomicAdd(&t.high[bin], 1u);
+}
+
+// The CTAs' tables, summed over the cluster (a power of two of CTAs): each CTA sends the others their parts of its
+// bins, sums the part that it gets and sends that to all. Stores to other CTAs' shared memory do not wait, as loads
+// do. The parts arrive where the lists are otherwise: `again` if another CTA may still be reading one.
+__device__ __forceinline__ void join_tables(cg::cluster_group& cl, SampleTables& t, unsigned long long* all, const Row& r, bool again) {
+  static_assert(2 * kListed == kBins && offsetof(SampleTables, place) == offsetof(SampleTables, own_place) + kListed * 8, "the lists hold a table");
+  __syncthreads();
+  if (again) cl.sync();
+  const int per = kBins / r.ctas;
+#pragma unroll
+  for (int i = 0; i < kBins / kSampleThreads; ++i) {
+    const int bin = static_cast<int>(threadIdx.x) + i * kSampleThreads, to = bin / per;
+    const unsigned long long e = (static_cast<unsigned long long>(t.count[bin]) << kCountShift) +
+                                 (static_cast<unsigned long long>(t.high[bin]) << 32) + t.low[bin];
+    cl.map_shared_rank(t.own_place, to)[r.rank * per + bin - to * per] = e;
+  }
+  cl.sync();
+  for (int i = threadIdx.x; i < per; i += kSampleThreads) {
+    unsigned long long e = 0;
+    for (int k = 0; k < r.ctas; ++k) e += t.own_place[k * per + i];
+    for (int k = 0; k < r.ctas; ++k) cl.map_shared_rank(all, k)[r.rank * per + i] = e;
+  }
+  cl.sync();
+}
+__device__ __forceinline__ void clear_table(SampleTables& t) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kSampleThreads) t.count[i] = t.low[i] = t.high[i] = 0;
+  __syncthreads();
 }
 
 // Where a run ends: its last token's place, and the mass up to there, the token's own included.
@@ -319,79 +390,22 @@ struct End {
 };
 
 // The end of the run of `target` tokens (kByMass false), or of the shortest run of mass `target`, from the
-// octaves' table. Every CTA of the cluster comes to the same result.
+// bins' table. Every CTA of the cluster comes to the same result.
 template <bool kByMass, class T>
 __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t, Row& r, const T* row, float temperature,
                         unsigned long long target) {
-  int octave = 0;
-  unsigned long long base = 0;  // mass before the octave
-  for (; octave < kOctaves - 1; ++octave) {
-    const unsigned long long step = kByMass ? common_mass(sh.mass[octave], octave) : sh.count[octave];
-    if (target <= step) break;
-    target -= step;
-    base += common_mass(sh.mass[octave], octave);
-  }
-  unsigned in = sh.count[octave];
-  if (kByMass) target = ((target << octave) + ((1ull << (kCommonBits - kMassBits)) - 1)) >> (kCommonBits - kMassBits);
-  unsigned long long inside = 0;  // mass of the octave before the range below
-  // The octave's places, a little wider than it is: what is not of the octave is left out by its octave.
-  const float step = temperature * 0.693147181f;
-  float high = r.scale.m - step * static_cast<float>(octave), low = r.scale.m - step * static_cast<float>(octave + 1);
-  const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(octave + 1));
-  high = octave == 0 ? r.scale.m : fminf(high + slack, r.scale.m);
-  low = octave == kOctaves - 1 ? -FLT_MAX : fmaxf(low - slack, -FLT_MAX);
-  unsigned long long lo = place_of(high, 0), hi = place_of(low, kSampleMaxVocab - 1);
-  auto place_in = [&](float x, int i, unsigned long long& p, unsigned long long& m) {
-    if (!(x > -INFINITY)) return false;
-    p = place_of(x, i);
-    if (p < lo || p > hi) return false;
-    return token_mass(r.scale, x, sh.power, m) == octave;
-  };
-  while (in > kListed) {
-    const int width = 64 - __clzll(static_cast<long long>(hi - lo));
-    const int shift = max(0, width - 11);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += kSampleThreads) {
-      t.mass[i] = 0;
-      t.count[i] = 0;
-    }
-    __syncthreads();
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
-#pragma unroll
-      for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-        unsigned long long p, m;
-        if (place_in(seen(r, x[e]), i + e, p, m)) {
-          const int bin = static_cast<int>((p - lo) >> shift);
-          atomicAdd(&t.count[bin], 1u);
-          atomicAdd(&t.mass[bin], m);
-        }
-      }
-    });
-    __syncthreads();
-    cl.sync();
-    // the CTA's share of the bins, summed over the cluster and given to all
-    const int per = kBins / r.ctas;
-    for (int i = threadIdx.x; i < per; i += kSampleThreads) {
-      const int bin = r.rank * per + i;
-      unsigned c = 0;
-      unsigned long long m = 0;
-      for (int k = 0; k < r.ctas; ++k) {
-        c += *cl.map_shared_rank(&t.count[bin], k);
-        m += *cl.map_shared_rank(&t.mass[bin], k);
-      }
-      for (int k = 0; k < r.ctas; ++k) {
-        *cl.map_shared_rank(&t.all_count[bin], k) = c;
-        *cl.map_shared_rank(&t.all_mass[bin], k) = m;
-      }
-    }
-    cl.sync();
-    const int b0 = threadIdx.x * (kBins / kSampleThreads);
+  constexpr bool kExact = sizeof(T) == 2;
+  constexpr int kEach = kBins / kSampleThreads;  // bins of a thread
+  // The bin of the run's end, in a table whose bins hold tokens of `weights_bin` (-1: each its own).
+  auto find_bin = [&](const unsigned long long* table, int weights_bin, unsigned long long mass_before) {
+    const int b0 = threadIdx.x * kEach;
     unsigned c = 0;
     unsigned long long m = 0;
 #pragma unroll
-    for (int i = 0; i < kBins / kSampleThreads; ++i) {
-      c += t.all_count[b0 + i];
-      m += t.all_mass[b0 + i];
+    for (int i = 0; i < kEach; ++i) {
+      const unsigned long long e = table[b0 + i];
+      c += entry_count(e);
+      m += weights_bin < 0 ? common_mass(sh.power, entry_mass(e, b0 + i), b0 + i) : entry_mass(e, weights_bin);
     }
     if (threadIdx.x == 0) {  // (logits that change under the kernel: all CTAs still agree)
       sh.found_bin = 0;
@@ -399,11 +413,14 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
       sh.found_mass = 0;
     }
     before_sums(sh, c, m);
+    // the mass before, as the target counts it
+    auto common = [&](unsigned long long x) { return weights_bin < 0 ? x : common_mass(sh.power, mass_before + x, weights_bin); };
 #pragma unroll
-    for (int i = 0; i < kBins / kSampleThreads; ++i) {
-      const unsigned c1 = c + t.all_count[b0 + i];
-      const unsigned long long m1 = m + t.all_mass[b0 + i];
-      if (kByMass ? (m < target && target <= m1) : (c < target && target <= c1)) {
+    for (int i = 0; i < kEach; ++i) {
+      const unsigned long long e = table[b0 + i];
+      const unsigned c1 = c + entry_count(e);
+      const unsigned long long m1 = m + (weights_bin < 0 ? common_mass(sh.power, entry_mass(e, b0 + i), b0 + i) : entry_mass(e, weights_bin));
+      if (kByMass ? (common(m) < target && target <= common(m1)) : (c < target && target <= c1)) {
         sh.found_bin = b0 + i;
         sh.found_count = c;
         sh.found_mass = m;
@@ -413,11 +430,48 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
       m = m1;
     }
     __syncthreads();
+  };
+  __syncthreads();
+  find_bin(t.all, -1, 0);
+  const int bin = static_cast<int>(sh.found_bin);
+  unsigned in = sh.found_in;
+  const unsigned long long base = sh.found_mass;  // of the bins before, in common units
+  target -= kByMass ? base : sh.found_count;      // from here on within the bin
+  unsigned long long inside = 0;                  // mass of the bin before the range below
+  unsigned long long lo = 0, hi = ~0ull;
+  auto place_in = [&](float x, int i, unsigned long long& p, float& away, float& away_lo) {
+    distance<kExact>(r.scale, x, away, away_lo);
+    if (bin_of(away) != bin || !(x > -INFINITY)) return false;
+    p = place_of<kExact>(x, i);
+    return p >= lo && p <= hi;
+  };
+  if (in > kListed) {
+    // The bin's places, a little wider than it is.
+    const float step = temperature * (0.693147181f / 64.0f);
+    const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(bin + 1));
+    const float high = r.scale.m - step * (static_cast<float>(bin) - 0.5f) + slack, low = r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack;
+    lo = place_of<kExact>(fminf(high, r.scale.m), 0);
+    hi = place_of<kExact>(bin == kBins - 1 ? -FLT_MAX : fmaxf(low, -FLT_MAX), kSampleMaxVocab - 1);
+  }
+  while (in > kListed) {
+    const int width = 64 - __clzll(static_cast<long long>(hi - lo));
+    const int shift = max(0, width - 11);
+    clear_table(t);
+    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+#pragma unroll
+      for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
+        unsigned long long p;
+        float away, away_lo;
+        if (place_in(seen(r, x[e]), i + e, p, away, away_lo)) add_to(t, static_cast<int>((p - lo) >> shift), 1, part_of(away, away_lo));
+      }
+    });
+    join_tables(cl, t, t.finer, r, true);
+    find_bin(t.finer, bin, inside);
     lo += static_cast<unsigned long long>(sh.found_bin) << shift;
     hi = min(hi, lo + ((1ull << shift) - 1));
     in = sh.found_in;
     inside += sh.found_mass;
-    target -= kByMass ? sh.found_mass : sh.found_count;
+    if (!kByMass) target -= sh.found_count;
   }
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
@@ -425,13 +479,11 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
   for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
     for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-      unsigned long long p, m;
-      if (place_in(seen(r, x[e]), i + e, p, m)) {
+      unsigned long long p;
+      float away, away_lo;
+      if (place_in(seen(r, x[e]), i + e, p, away, away_lo)) {
         const int at = atomicAdd(&sh.n_list, 1);
-        if (at < kListed) {
-          t.own_place[at] = p;
-          t.own_mass[at] = m;
-        }
+        if (at < kListed) t.own_place[at] = p;
       }
     }
   });
@@ -443,21 +495,31 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     sh.found_mass = 0;
   }
   sort_list(t, n);
+  // the tokens' masses in the bin's units
   const int i0 = threadIdx.x * 2;
+  unsigned long long each[2] = {};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (i0 + j < n) {
+      float away, away_lo;
+      distance<kExact>(r.scale, place_value<kExact>(t.place[i0 + j]), away, away_lo);
+      each[j] = entry_mass(entry_of(away, away_lo), bin);
+    }
   unsigned c = 0;
-  unsigned long long m = 0;
-  for (int i = i0; i < min(i0 + 2, n); ++i) m += t.list_mass[i];
+  unsigned long long m = each[0] + each[1];
   before_sums(sh, c, m);
-  for (int i = i0; i < min(i0 + 2, n); ++i) {
-    const unsigned long long m1 = m + t.list_mass[i];
-    if (kByMass ? (m < target && target <= m1) : static_cast<unsigned long long>(i + 1) == target) {
-      sh.found_place = t.place[i];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const unsigned long long m1 = m + each[j];
+    if (i0 + j < n && (kByMass ? (common_mass(sh.power, inside + m, bin) < target && target <= common_mass(sh.power, inside + m1, bin))
+                               : static_cast<unsigned long long>(i0 + j + 1) == target)) {
+      sh.found_place = t.place[i0 + j];
       sh.found_mass = m1;
     }
     m = m1;
   }
   __syncthreads();
-  const End end{sh.found_place, base + common_mass(inside + sh.found_mass, octave)};
+  const End end{sh.found_place, base + common_mass(sh.power, inside + sh.found_mass, bin)};
   __syncthreads();
   return end;
 }
@@ -479,12 +541,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   r.rank = static_cast<int>(cl.block_rank());
   r.ctas = static_cast<int>(cl.num_blocks());
   const long long row_of = blockIdx.x / static_cast<unsigned>(r.ctas);
+  constexpr bool kExact = sizeof(T) == 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = ((a.vocab + r.ctas - 1) / r.ctas + 7) & ~7;
   r.v0 = min(r.rank * share, a.vocab);
   r.v1 = min(r.v0 + share, a.vocab);
   pdl_launch_dependents();
-  for (int i = tid; i < 65; i += kSampleThreads) sh.power[i] = powers.t[i];
+  if (tid < 64) sh.power[tid] = powers.t[tid];
   if (tid == 0) sh.n_list = 0;
   cl.barrier_arrive();  // (waited for below: every CTA of the cluster runs before another writes to it)
   pdl_wait();
@@ -550,8 +613,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 
   auto token_of = [](unsigned long long pair) { return static_cast<int>(0xffffffffu - static_cast<unsigned>(pair & 0xffffffffu)); };
   auto zero_probs = [&] {
-    if (probs != nullptr)
-      for (int i = r.v0 + tid; i < r.v1; i += kSampleThreads) probs[i] = 0.0f;
+    if (probs == nullptr) return;
+    const int head = min(r.v1 - r.v0, static_cast<int>(4 - ((reinterpret_cast<uintptr_t>(probs + r.v0) >> 2) & 3)) & 3);
+    const int v = r.v0 + head, pieces = (r.v1 - v) / 4;
+    if (tid < head) probs[r.v0 + tid] = 0.0f;
+    for (int i = tid; i < pieces; i += kSampleThreads) reinterpret_cast<float4*>(probs + v)[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (v + pieces * 4 + tid < r.v1) probs[v + pieces * 4 + tid] = 0.0f;
   };
   auto answer = [&](int token, float logprob, int kept) {
     if (a.token != nullptr) a.token[row_of] = token;
@@ -597,10 +664,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   auto pair_of = [](float score, int i) {
     return (static_cast<unsigned long long>(__float_as_uint(score)) << 32) | (0xffffffffu - static_cast<unsigned>(i));
   };
-  auto score_of = [&](float w, int i) { return w > 0.0f ? __fdiv_rn(w, noise[i]) : 0.0f; };
+  auto score_of = [](float w, float e) { return w > 0.0f ? __fdividef(w, e) : 0.0f; };
   auto logprob_of = [&](float x, float total) {
     float hi, lo;
-    distance(r.scale, x, hi, lo);
+    distance<kExact>(r.scale, x, hi, lo);
     return -(hi + lo) * 0.693147181f - logf(total);
   };
 
@@ -613,12 +680,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         const float y = seen(r, x[e]);
         if (rising_key(y) >= least) {
           const int at = atomicAdd(&sh.n_list, 1);
-          if (at < kListed) {
-            unsigned long long m;
-            const int octave = token_mass(r.scale, y, sh.power, m);
-            t.own_place[at] = place_of(y, i + e);
-            t.own_mass[at] = common_mass(m, octave);
-          }
+          if (at < kListed) t.own_place[at] = place_of<kExact>(y, i + e);
         }
       }
     });
@@ -626,41 +688,37 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       sort_list(t, n);
       int kept = min(top_k, n);
       if (top_p < 1.0f) {
-        const int i0 = tid * 2;
+        // (of the first top_k, a quarter of the threads)
         unsigned c = 0;
-        unsigned long long m = 0;
-        for (int i = i0; i < min(i0 + 2, n); ++i) m += t.list_mass[i];
-        before_sums(sh, c, m);
-        unsigned long long x = m;
-        for (int i = i0; i < min(i0 + 2, n); ++i) {
-          x += t.list_mass[i];
-          if (i == kept - 1) sh.found_mass = x;
+        unsigned long long each = 0;
+        if (tid < kept) {
+          float hi, lo;
+          distance<kExact>(r.scale, place_value<kExact>(t.place[tid]), hi, lo);
+          each = common_mass(sh.power, entry_mass(entry_of(hi, lo), bin_of(hi)), bin_of(hi));
         }
+        unsigned long long m = each;
+        before_sums(sh, c, m);
+        if (tid == kept - 1) sh.found_mass = m + each;
         __syncthreads();
         const unsigned long long target = mass_target(top_p, sh.found_mass);
-        for (int i = i0; i < min(i0 + 2, n); ++i) {
-          const unsigned long long m1 = m + t.list_mass[i];
-          if (m < target && target <= m1) sh.found_count = i + 1;
-          m = m1;
-        }
+        if (tid < kept && m < target && target <= m + each) sh.found_count = tid + 1;
         __syncthreads();
         kept = min(kept, static_cast<int>(sh.found_count));
       }
-      // (at most top_k tokens, a quarter of the threads)
-      kept = __syncthreads_count(tid < kept && place_value(t.place[tid]) >= lowest);
+      kept = __syncthreads_count(tid < kept && place_value<kExact>(t.place[tid]) >= lowest);
       float w = 0.0f, score = 0.0f;
       int i = 0;
       if (tid < kept) {
         i = place_token(t.place[tid]);
-        w = weight_of(r.scale, place_value(t.place[tid]));
-        if (a.token != nullptr && r.rank == 0) score = score_of(w, i);
+        w = weight_of<kExact>(r.scale, place_value<kExact>(t.place[tid]));
+        if (a.token != nullptr && r.rank == 0) score = score_of(w, noise[i]);
       }
       float total = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
       const unsigned long long pick = warp_max(tid < kept ? pair_of(score, i) : 0ull);
       if (lane == 0) {
-        sh.warp_key[warp] = total;
+        sh.warp_total[warp] = total;
         sh.warp_sum[warp] = pick;
       }
       zero_probs();
@@ -668,13 +726,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       total = 0.0f;
       best = 0;
       for (int x = 0; x < kFewTokens / 32; ++x) {
-        total += sh.warp_key[x];
+        total += sh.warp_total[x];
         best = max(best, sh.warp_sum[x]);
       }
       if (probs != nullptr && tid < kept && i >= r.v0 && i < r.v1) probs[i] = w / total;
       // the token's own thread, or the first one's where none is drawn
       if (r.rank == 0 && tid < kept && i == (a.token != nullptr ? token_of(best) : place_token(t.place[0])))
-        answer(i, logprob_of(place_value(t.place[tid]), total), kept);
+        answer(i, logprob_of(place_value<kExact>(t.place[tid]), total), kept);
       return;
     }
   }
@@ -683,58 +741,46 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   float last = -INFINITY;
   int last_i = -1;
   if ((top_k > 0 && top_k < a.vocab) || top_p < 1.0f) {
-    unsigned long long* column = reinterpret_cast<unsigned long long*>(area) + tid;
-    __syncthreads();
-#pragma unroll
-    for (int o = 0; o < kOctaves; ++o) column[o * kSampleThreads] = 0;
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+    clear_table(t);
+    unsigned long long tail = 0;
+    for_tokens(row, r.v0, r.v1, [&](int, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
         const float y = seen(r, x[e]);
-        if (y > -INFINITY) {
-          unsigned long long m;
-          const int o = token_mass(r.scale, y, sh.power, m);
-          column[o * kSampleThreads] += m + (1ull << 52);
-        }
+        float hi, lo;
+        distance<kExact>(r.scale, y, hi, lo);
+        if (hi < kTail) add_to(t, near_bin(hi), 1, bin_part(hi, lo));
+        else if (y > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi);  // (many share the last bin)
       }
     });
-    __syncthreads();
-    for (int o = warp; o < kOctaves; o += kSampleWarps) {
-      const unsigned long long* of = reinterpret_cast<const unsigned long long*>(area) + o * kSampleThreads + lane;
-      unsigned c = 0;
-      unsigned long long m = 0;
 #pragma unroll
-      for (int i = 0; i < kSampleThreads; i += 32) {
-        c += static_cast<unsigned>(of[i] >> 52);
-        m += of[i] & ((1ull << 52) - 1);
-      }
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) {
-        c += __shfl_xor_sync(0xffffffffu, c, s);
-        m += __shfl_xor_sync(0xffffffffu, m, s);
-      }
-      if (lane < r.ctas) {
-        *cl.map_shared_rank(&sh.octave_count[r.rank][o], lane) = c;
-        *cl.map_shared_rank(&sh.octave_mass[r.rank][o], lane) = m;
-      }
+    for (int o = 16; o > 0; o >>= 1) tail += __shfl_xor_sync(0xffffffffu, tail, o);
+    if (lane == 0 && tail != 0) {
+      add_to(t, kBins - 1, entry_count(tail), static_cast<unsigned>(tail));
+      atomicAdd(&t.high[kBins - 1], static_cast<unsigned>(tail >> 32) & ((1u << (kCountShift - 32)) - 1u));
     }
-    cl.sync();
-    if (tid < kOctaves) {
-      unsigned c = 0;
-      unsigned long long m = 0;
-      for (int k = 0; k < r.ctas; ++k) {
-        c += sh.octave_count[k][tid];
-        m += sh.octave_mass[k][tid];
-      }
-      sh.count[tid] = c;
-      sh.mass[tid] = m;
-    }
-    __syncthreads();
-    unsigned long long all = 0;
+    join_tables(cl, t, t.all, r, false);
     unsigned valid = 0;
-    for (int o = 0; o < kOctaves; ++o) {
-      all += common_mass(sh.mass[o], o);
-      valid += sh.count[o];
+    unsigned long long all = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / kSampleThreads; ++i) {
+      const int bin = tid * (kBins / kSampleThreads) + i;
+      valid += entry_count(t.all[bin]);
+      all += common_mass(sh.power, entry_mass(t.all[bin], bin), bin);
+    }
+    valid = __reduce_add_sync(0xffffffffu, valid);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) {
+      sh.warp_count[warp] = valid;
+      sh.warp_sum[warp] = all;
+    }
+    __syncthreads();
+    valid = 0;
+    all = 0;
+    for (int w = 0; w < kSampleWarps; ++w) {
+      valid += sh.warp_count[w];
+      all += sh.warp_sum[w];
     }
     End end{~0ull, all};
     if (top_k > 0 && static_cast<unsigned>(top_k) < valid) end = find_end<false>(cl, sh, t, r, row, temperature, top_k);
@@ -743,7 +789,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       end.place = min(end.place, by_mass.place);
     }
     if (end.place != ~0ull) {
-      last = place_value(end.place);
+      last = place_value<kExact>(end.place);
       last_i = place_token(end.place);
     }
   }
@@ -752,34 +798,60 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     last_i = kSampleMaxVocab;
   }
   auto stays = [&](float x, int i) { return x > last || (x == last && i <= last_i); };
-  float total = 0.0f;
+  float total = 0.0f, leader = -1.0f;  // the greatest score and its token: the lowest, as a thread's tokens rise
   unsigned kept = 0;
-  best = 0;
-  for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+  int lead_i = 0;
+  auto count_in = [&](int i, const auto& y, const auto& e) {
 #pragma unroll
-    for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-      const float y = seen(r, x[e]);
-      if (stays(y, i + e)) {
-        const float w = weight_of(r.scale, y);
+    for (int j = 0; j < static_cast<int>(sizeof(y) / sizeof(float)); ++j)
+      if (stays(y[j], i + j)) {
+        const float w = weight_of<kExact>(r.scale, y[j]);
         total += w;
         ++kept;
-        if (a.token != nullptr) best = max(best, pair_of(score_of(w, i + e), i + e));
+        const float score = score_of(w, e[j]);
+        if (score > leader) {
+          leader = score;
+          lead_i = i + j;
+        }
       }
-    }
-  });
+  };
+  if (noise != nullptr && last == -INFINITY) {  // nothing is filtered out: the noise comes along with the logits
+    for_both<true>(row, noise, r.v0, r.v1, [&](int i, const auto& x, const auto& e) {
+      constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
+      float y[kN];
+#pragma unroll
+      for (int j = 0; j < kN; ++j) y[j] = seen(r, x[j]);
+      count_in(i, y, e);
+    });
+  } else {
+    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+      constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
+      float y[kN], e[kN];
+      bool any = false;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) {
+        y[j] = seen(r, x[j]);
+        any |= stays(y[j], i + j);
+      }
+      if (!any) return;
+#pragma unroll
+      for (int j = 0; j < kN; ++j) e[j] = noise != nullptr && stays(y[j], i + j) ? noise[i + j] : 1.0f;
+      count_in(i, y, e);
+    });
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   kept = __reduce_add_sync(0xffffffffu, kept);
-  best = warp_max(best);
+  best = warp_max(leader >= 0.0f ? pair_of(leader, lead_i) : 0ull);
   __syncthreads();
   if (lane == 0) {
-    sh.warp_key[warp] = total;
+    sh.warp_total[warp] = total;
     sh.warp_count[warp] = kept;
     sh.warp_sum[warp] = best;
   }
   __syncthreads();
   if (warp == 0) {
-    total = lane < kSampleWarps ? sh.warp_key[lane] : 0.0f;
+    total = lane < kSampleWarps ? sh.warp_total[lane] : 0.0f;
     kept = lane < kSampleWarps ? sh.warp_count[lane] : 0u;
     best = warp_max(lane < kSampleWarps ? sh.warp_sum[lane] : 0ull);
 #pragma unroll
@@ -804,7 +876,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   const int token = a.token != nullptr ? token_of(best) : first;
   if (tid == 0 && token >= r.v0 && token < r.v1) {
     float x;
-    if constexpr (sizeof(T) == 2) x = __bfloat162float(row[token]);
+    if constexpr (kExact) x = __bfloat162float(row[token]);
     else x = row[token];
     answer(token, logprob_of(seen(r, x), total), static_cast<int>(kept));
   }
@@ -817,7 +889,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
       const float y = seen(r, x[e]);
-      p[e] = stays(y, i + e) ? weight_of(r.scale, y) * inverse : 0.0f;
+      p[e] = stays(y, i + e) ? weight_of<kExact>(r.scale, y) * inverse : 0.0f;
     }
     if (kN % 4 == 0 && (reinterpret_cast<uintptr_t>(probs + i) & 15u) == 0) {
 #pragma unroll
@@ -832,15 +904,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
 template <class T>
 static rf_status launch_sample(const SampleArgs& a, int64_t rows, int sms, cudaStream_t s) {
   static uint64_t done = 0;
-  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_sample<T>), kSampleArea, &done);
+  rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_sample<T>), sizeof(SampleTables), &done);
   if (st != RF_OK) return st;
   PowerTable p;
-  for (int i = 0; i <= 64; ++i) p.t[i] = static_cast<unsigned long long>(std::llrint(std::ldexp(std::exp2(-i / 64.0), kMassBits)));
-  // a power of two of CTAs a row: as many as run at once, each with enough tokens for its threads
-  unsigned ctas = 1;
+  for (int i = 0; i < 64; ++i) p.t[i] = static_cast<unsigned long long>(std::ldexp(std::exp2(-i / 64.0), 63));
+  // CTAs a row: a power of two, as many as run at once, each with enough tokens for its threads; long rows at least
+  // two, so that rows that take longer than others are shared out and fewer are in L2 at a time (256 rows of
+  // 131,072, half of them without a small top-k: 283 us with one, 173 with two, 175 with four, 221 with eight).
+  unsigned ctas = a.vocab >= kSampleLong ? 2 : 1;
   while (ctas < kSampleCtas && static_cast<int64_t>(ctas) * kSampleShare < a.vocab && rows * ctas * 2 <= 2 * sms) ctas *= 2;
   ProfScope prof(s, RF_STAGE_SAMPLE);
-  return cuda_check(launch_dependent(k_sample<T>, dim3(static_cast<unsigned>(rows) * ctas), dim3(kSampleThreads), kSampleArea, s,
+  return cuda_check(launch_dependent(k_sample<T>, dim3(static_cast<unsigned>(rows) * ctas), dim3(kSampleThreads), sizeof(SampleTables), s,
                                      ctas, a, p),
                     "k_sample launch");
 }
