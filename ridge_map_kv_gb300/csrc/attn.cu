@@ -67,6 +67,7 @@ constexpr int kAtRegsSoftmax = 208, kAtRegsOther = 88;
 static_assert(256 * kAtRegsSoftmax + 128 * kAtRegsOther <= kAtThreads * 168, "more registers than the launch has");
 constexpr int kAtFirst = 96;      // keys of the first part in which a tile's weights are handed over
 constexpr int kAtItemCost = 4;    // tiles that an item weighs beyond its own
+constexpr int kPfRows = 256;      // rows that a part may have
 constexpr int kAtMaxCtas = 160;   // bounds the workspace
 constexpr int kAtMaxStages = 8;
 constexpr float kAtLog2e = 1.4426950408889634f;
@@ -119,8 +120,14 @@ struct PrefixArgs : AttnArgs {
   // as fit; else p_split tiles a sequence, which is the last of them not full.
   int p_nodes, p_seqs, p_split;
   int p_items;       // items of a head
-  int narrow;        // a sequence's rows fit into one row tile
-  int rows, p_rows;  // rows of an item, of a sequence and of the prefix, where they are stored whole
+  // Where the prefix takes two row tiles and a sequence's rows of a head fit into one, a sequence's items are pairs of
+  // heads, one to a stream; rows that are at most 32 are there four times (see k_attn).
+  int pairs;         // 1 or 0
+  int own_heads;     // items of a sequence (heads, or pairs of them) at a time of its rows
+  int copies;        // 4 or 1
+  // What an item, a tile of the prefix and a tile of a sequence's own weigh in the shares.
+  int w_item, w_prefix, w_own;
+  int rows, p_rows;      // rows of an item's stored part, of a sequence and of the prefix
   float4* whole_o;   // [items][head_dim / 4][rows of the item], the prefix's items first
   float2* whole_ml;
   int2* item_ctas;   // [items] the CTAs of an item's first and last tile
@@ -130,7 +137,7 @@ struct AttnShared {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean[2], mma_done[2];
   AttnShare share;
-  int bad[2];                // a drafted V row of the segment is not finite
+  int bad[2][2];             // [segment parity][stream]: a drafted V row of the segment is not finite
   uint32_t tmem;
   int abort;
 };
@@ -166,9 +173,32 @@ __device__ __forceinline__ int prefix_of(const PrefixArgs& a) {
   return len < 0 || len > a.prefix_capacity ? -1 : len;
 }
 template <class Args>
+__device__ __forceinline__ int heads_of(const Args& a, int b) {  // or pairs of heads
+  if constexpr (Args::kPrefix) return b < 0 ? a.heads : a.own_heads;
+  else return a.heads;
+}
+template <class Args>
 __device__ __forceinline__ int items_of(const Args& a, int b) {  // of a head
   if constexpr (Args::kPrefix) return b < 0 ? a.p_items : a.m_items;
   else return a.m_items;
+}
+// An item weighs item_weight and tile_weight for each of its tiles.
+template <class Args>
+__device__ __forceinline__ int item_weight(const Args& a) {
+  if constexpr (Args::kPrefix) return a.w_item;
+  else return kAtItemCost;
+}
+template <class Args>
+__device__ __forceinline__ int tile_weight(const Args& a, int b) {
+  if constexpr (Args::kPrefix) return b < 0 ? a.w_prefix : a.w_own;
+  else return 1;
+}
+// The first tile that lies behind `at` in the weight of an item of sequence b.
+template <class Args>
+__device__ __forceinline__ int tile_behind(const Args& a, int at, int b) {
+  const int x = max(at - item_weight(a), 0);
+  if constexpr (Args::kPrefix) return x / tile_weight(a, b);
+  else return x;
 }
 template <bool kDual, class Args>
 __device__ __forceinline__ ItemShape item_shape(const Args& a, int b, int mt) {
@@ -206,14 +236,20 @@ struct Walk {
     if (left > 0) settle(a);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ int end() const {
-    return static_cast<int>(min(static_cast<long long>(shape.tiles + kAtItemCost), at + left));
+  __device__ __forceinline__ int end(const Args& a) const {
+    return static_cast<int>(min(static_cast<long long>(shape.tiles) * tile_weight(a, b) + item_weight(a), at + left));
   }
   // The first tiles from here on (a share may end within an item's extra weight).
   __device__ __forceinline__ void settle(const Args& a) {
     while (true) {
-      t0 = max(at - kAtItemCost, 0);
-      t1 = max(end() - kAtItemCost, 0);
+      if constexpr (Args::kPrefix) {  // (most items are whole ones)
+        const int whole = shape.tiles * tile_weight(a, b) + item_weight(a);
+        t0 = at == 0 ? 0 : tile_behind(a, at, b);
+        t1 = at + left >= whole ? shape.tiles : tile_behind(a, end(a), b);
+      } else {
+        t0 = tile_behind(a, at, b);
+        t1 = tile_behind(a, end(a), b);
+      }
       if (t1 > t0) return;
       next_item(a);
       if (left <= 0) return;
@@ -224,18 +260,20 @@ struct Walk {
     if (left > 0) settle(a);
   }
   __device__ __forceinline__ void next_item(const Args& a) {
-    left -= end() - at;
+    left -= end(a) - at;
     if (left <= 0) return;
     at = 0;
     do {
       if (++mt == items_of(a, b)) {
         mt = 0;
-        if (++h == a.heads) {
+        if (++h == heads_of(a, b)) {
           h = 0;
           if (++b >= a.n_seqs) {  // lengths that changed under the kernel: no sequence is left
             left = 0;
             return;
           }
+        } else if (Args::kPrefix && items_of(a, b) == 1) {
+          continue;  // another head of the same sequence: the same shape
         }
       }
       shape = item_shape<kDual>(a, b, mt);
@@ -254,28 +292,35 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
   const int lane = threadIdx.x & 31;
   int prefix = 0, prefix_tiles = 0;
   long long prefix_weight = 0;
+  const int len_0 = lane < a.n_seqs ? length_of(a, lane) : -1;
   if constexpr (Args::kPrefix) {
     prefix = prefix_of(a);
     if (prefix < 0) record_status(a.dev_status, RF_ERR_INVALID_ARG);
     prefix_tiles = (max(prefix, 0) + kAtTile - 1) / kAtTile;
-    if (prefix_tiles > 0) prefix_weight = static_cast<long long>(a.heads) * a.p_items * (prefix_tiles + kAtItemCost);
+    if (prefix_tiles > 0)
+      prefix_weight = static_cast<long long>(a.heads) * a.p_items * (static_cast<long long>(prefix_tiles) * a.w_prefix + a.w_item);
   }
   auto weight_of = [&](int len) -> long long {
     return len < 0 ? 0ll
-                   : static_cast<long long>(a.heads) *
-                         (static_cast<long long>(a.m_items) * ((len + kAtTile - 1) / kAtTile + kAtItemCost) + a.draft_sum);
+                   : static_cast<long long>(heads_of(a, 0)) *
+                         (static_cast<long long>(a.m_items) *
+                              (static_cast<long long>((len + kAtTile - 1) / kAtTile) * tile_weight(a, 0) + item_weight(a)) +
+                          static_cast<long long>(a.draft_sum) * tile_weight(a, 0));
   };
   long long total = 0;
   int len = -1;  // of sequence `lane`, then of later ones
   for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-    len = b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
+    len = b0 == 0 ? len_0 : b0 + lane < a.n_seqs ? length_of(a, b0 + lane) : -1;
     if (len < 0 && b0 + lane < a.n_seqs) record_status(a.dev_status, RF_ERR_INVALID_ARG);
     total += weight_of(len);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total = prefix < 0 ? 0 : total + prefix_weight;  // (a prefix that is out of range: no sequence can be answered)
-  const long long shares = min(static_cast<long long>(ctas), total);
+  // (no share is less than a tile: every CTA between an item's first and last one has a part of it)
+  long long most = total;
+  if constexpr (Args::kPrefix) most = total / max(a.w_prefix, a.w_own);
+  const long long shares = min(static_cast<long long>(ctas), most);
   AttnShare p{};
   if (cta < shares) {
     const long long first = share_start(total, cta, static_cast<int>(shares));
@@ -286,11 +331,11 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
         p.b = -1;
         p.len = prefix;
         p.n_tiles = prefix_tiles;
-        const long long per_head = static_cast<long long>(a.p_items) * (prefix_tiles + kAtItemCost);
+        const long long per_item = static_cast<long long>(prefix_tiles) * a.w_prefix + a.w_item, per_head = a.p_items * per_item;
         p.h = static_cast<int>(quick_div(first, per_head));
         const long long at = first - p.h * per_head;
-        p.mt = static_cast<int>(quick_div(at, prefix_tiles + kAtItemCost));
-        p.at = static_cast<int>(at - static_cast<long long>(p.mt) * (prefix_tiles + kAtItemCost));
+        p.mt = static_cast<int>(quick_div(at, per_item));
+        p.at = static_cast<int>(at - p.mt * per_item);
       }
     }
     for (int b0 = 0; b0 < a.n_seqs && first >= prefix_weight; b0 += 32) {
@@ -309,17 +354,18 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
         p.len = __shfl_sync(0xffffffffu, len, at);
         const int cached = (p.len + kAtTile - 1) / kAtTile;
         long long r = first - base - __shfl_sync(0xffffffffu, x - own, at);
-        const long long per_head = quick_div(__shfl_sync(0xffffffffu, own, at), a.heads);
+        const long long per_head = quick_div(__shfl_sync(0xffffffffu, own, at), heads_of(a, 0));
         p.h = static_cast<int>(quick_div(r, per_head));
         r -= p.h * per_head;
         p.mt = 0;
         p.n_tiles = cached + draft_tiles<kDual>(a, 0);
+        const auto weight = [&] { return static_cast<long long>(p.n_tiles) * tile_weight(a, 0) + item_weight(a); };
         if (a.mask != nullptr) {
-          p.mt = static_cast<int>(quick_div(r, p.n_tiles + kAtItemCost));
-          r -= static_cast<long long>(p.mt) * (p.n_tiles + kAtItemCost);
+          p.mt = static_cast<int>(quick_div(r, weight()));
+          r -= p.mt * weight();
         } else {
-          while (r >= p.n_tiles + kAtItemCost) {
-            r -= p.n_tiles + kAtItemCost;
+          while (r >= weight()) {
+            r -= weight();
             p.n_tiles = cached + draft_tiles<kDual>(a, ++p.mt);
           }
         }
@@ -389,6 +435,39 @@ __device__ __forceinline__ void row_weights(uint32_t ts, uint32_t (&r)[4][32], i
   tmem_wait_st();
 }
 
+// Multiplies a row of the accumulator.
+template <int kHD>
+__device__ __forceinline__ void rescale_row(uint32_t to, float f) {
+#pragma unroll 1
+  for (int c = 0; c < kHD; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(to + c, o);
+    tmem_wait_ld16(o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(u2f(o[e]) * f);
+    tmem_st16(to + c, o);
+  }
+}
+
+// The same as row_weights for 32 keys.
+__device__ __forceinline__ void quarter_weights(uint32_t to, uint32_t (&r)[32], float sc, float off, float2& t0, float2& t1) {
+  const float2 sc2 = make_float2(sc, sc), off2 = make_float2(off, off);
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    float2 x = fma_x2(make_float2(u2f(r[i]), u2f(r[i + 1])), sc2, off2);
+    float2 y = fma_x2(make_float2(u2f(r[i + 2]), u2f(r[i + 3])), sc2, off2);
+    x = make_float2(exp2f_ftz(x.x), exp2f_ftz(x.y));
+    y = make_float2(exp2f_ftz(y.x), exp2f_ftz(y.y));
+    t0 = add_x2(t0, x);
+    t1 = add_x2(t1, y);
+    w[i / 2] = pack_bf16x2(x.x, x.y);
+    w[i / 2 + 1] = pack_bf16x2(y.x, y.y);
+  }
+  tmem_st16(to, w);
+  tmem_wait_st();
+}
+
 // Bits of the keys of tile `t` that query node `node` sees.
 __device__ __forceinline__ void visible(const AttnArgs& a, const ItemShape& s, int b, int node, int t, uint32_t (&keep)[4]) {
   int limit;  // keys of the tile that exist for this row
@@ -415,6 +494,20 @@ __device__ __forceinline__ void visible(const AttnArgs& a, const ItemShape& s, i
   }
 }
 
+// Those of its keys 32 c .. 32 c + 31.
+__device__ __forceinline__ uint32_t visible_quarter(const AttnArgs& a, const ItemShape& s, int b, int node, int t, int c) {
+  const bool draft = t >= s.cached;
+  const int j0 = (t - s.cached) * kAtTile;
+  const int k = (!draft ? s.len - t * kAtTile : (a.mask != nullptr ? a.n : min(a.n, node + 1)) - j0) - c * 32;
+  uint32_t keep = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+  if (draft && a.mask != nullptr) {
+    const int w = (t - s.cached) * 2 + (c >> 1);
+    const unsigned long long m = w < a.words ? a.mask[(static_cast<long long>(b) * a.n + node) * a.words + w] : 0ull;
+    keep &= static_cast<uint32_t>(m >> ((c & 1) * 32));
+  }
+  return keep;
+}
+
 template <int kHD, bool kDual, class Args>
 __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ Args a) {
   using Cfg = AttnCfg<kHD, kDual>;
@@ -424,13 +517,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   AttnShared* sh = reinterpret_cast<AttnShared*>(smem + Cfg::kQBytes + Cfg::kStages * Cfg::kTileBytes);
-  // Items of one row tile exchange maxima and totals: behind the rest, or, where items of two tiles came
-  // before them (a prefix's), in the second query tile, which they do not have.
-  AttnExchange& ml = *reinterpret_cast<AttnExchange*>(kDual ? smem + Cfg::kTileBytes : reinterpret_cast<uint8_t*>(sh + 1));
-  // With two row tiles and a prefix: an item of one tile. Its streams take alternate key tiles as they do where
-  // all items are of one tile, but each stream's products stay with the warp that issues them.
-  const auto narrow = [&](int b) {
-    if constexpr (kDual && Args::kPrefix) return b >= 0 && a.narrow != 0;
+  // Items of one row tile, whose streams take alternate key tiles, exchange maxima and totals.
+  AttnExchange& ml = *reinterpret_cast<AttnExchange*>(sh + 1);
+  // With a prefix: two heads of a sequence, each of whose rows fit into one row tile, are an item, a head to a
+  // stream with key tiles of its own. (One head at a time, its key tiles in turns on both streams, an item of
+  // one to five tiles took 5 us beside them for its first and last steps; two go side by side.)
+  const auto paired = [&](int b) {
+    if constexpr (kDual && Args::kPrefix) return b >= 0 && a.pairs != 0;
+    else return false;
+  };
+  const auto heads_in = [&](int h) { return min(2, a.heads - 2 * h); };  // of a pair
+  // Of those, heads of at most 32 rows: a row tile's four warps read 32 TMEM lanes each, so one of them would take
+  // all exponentials. Instead the rows are there four times, 32 rows apart, and each copy's warp sees a quarter of
+  // every tile's keys: four parts with their own maxima and totals, which the join adds up. (64 sequences of one token,
+  // 4 query heads on one, over 484 rows: a tile's weights took 1.0 us of one warp.)
+  const auto copied = [&](int b) {
+    if constexpr (kDual && Args::kPrefix) return b >= 0 && a.copies > 1;
     else return false;
   };
   const uint32_t s_q = smem_u32(smem), s_ring = s_q + Cfg::kQBytes;
@@ -450,7 +552,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       mbar_init(&sh->s_full[s], 1);
       for (int i = 0; i < 2; ++i) mbar_init(&sh->p_full[s][i], 4);
     }
-    mbar_init(&sh->o_final, kMmaWarps + 1);
+    mbar_init(&sh->o_final, 2 * kMmaWarps);
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->ml_full, 8);
     for (int i = 0; i < 2; ++i) {
@@ -493,7 +595,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       uint32_t phase = 0, q_phase = 0;
       long long issued = 0;
       bool ok = true, q_inflight = false;
-      auto load = [&](const Walk<kDual, Args>& w, int t, bool v) {
+      auto load = [&](const Walk<kDual, Args>& w, int t, bool v, int h) {
         if (!wait(&sh->empty[stage], phase ^ 1u)) return false;
         const bool draft = t >= w.shape.cached;
         const CUtensorMap* tm = draft ? (v ? &a.tm_vd : &a.tm_kd) : (v ? &a.tm_v : &a.tm_k);
@@ -505,7 +607,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           mbar_arrive_expect_tx(&sh->full[stage], Cfg::kTileBytes);
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
-            tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, w.h, row, max(w.b, 0));
+            tma_load_4d(s_ring + stage * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->full[stage]), c * 64, h, row, max(w.b, 0));
         }
         __syncwarp();
         ++issued;
@@ -516,21 +618,31 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         return true;
       };
       for (Walk<kDual, Args> w(a, sh); w.more() && ok; w.next(a)) {
+        const bool pair = paired(w.b);
+        const int heads = pair ? heads_in(w.h) : 1, h0 = pair ? 2 * w.h : w.h;
+        // With a prefix there are many short items, so the first K tiles are loaded before the queries, which wait
+        // until the last item's are done with.
+        int ahead = 0;
+        if constexpr (Args::kPrefix) {
+          ok = load(w, w.t0, false, h0);
+          if (ok && heads > 1) ok = load(w, w.t0, false, h0 + 1);
+          ahead = 1;
+          if (!ok) break;
+        }
         if (!wait(&sh->q_empty, q_phase ^ 1u)) break;
         q_inflight = true;
         if (lane == 0) {
           const CUtensorMap* tm = &a.tm_q;
-          const int tiles = kDual && !narrow(w.b) ? 2 : 1;
-          int rows = a.group * a.npt;
+          const int tiles = pair ? heads : kDual ? 2 : 1;
+          int rows = a.group * a.npt, copies = 1;
           if constexpr (Args::kPrefix) {
-            if (w.b < 0) {
-              tm = &a.tm_qp;
-              rows = a.group * a.p_nodes * a.p_seqs;
-            }
+            if (w.b < 0) tm = &a.tm_qp;
+            rows = a.group * a.p_nodes * (w.b < 0 ? a.p_seqs : 1);
+            if (pair) copies = a.copies;
           }
-          mbar_arrive_expect_tx(&sh->q_full, tiles * kChunks * 64 * 2 * rows);
+          mbar_arrive_expect_tx(&sh->q_full, tiles * copies * kChunks * 64 * 2 * rows);
           for (int s = 0; s < tiles; ++s) {
-            const int tile = w.mt * (kDual ? 2 : 1) + s;
+            const int tile = pair ? 0 : w.mt * (kDual ? 2 : 1) + s;
             int node = tile * a.npt, seq = w.b;
             if constexpr (Args::kPrefix) {
               if (w.b < 0) {
@@ -538,20 +650,25 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
                 node = a.p_split > 1 ? (tile - seq * a.p_split) * a.p_nodes : 0;
               }
             }
+            for (int copy = 0; copy < copies; ++copy)
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab, tm, smem_u32(&sh->q_full), c * 64, w.h * a.group, node, seq);
+              for (int c = 0; c < kChunks; ++c)
+                tma_load_4d(s_q + s * Cfg::kTileBytes + c * kSlab + copy * 32 * 128, tm, smem_u32(&sh->q_full), c * 64,
+                            (pair ? h0 + s : h0) * a.group, node, seq);
           }
         }
         __syncwarp();
         q_phase ^= 1u;
         // the order in which warp 9 takes them
-        if (kDual && !narrow(w.b)) {
-          for (int t = w.t0; t < w.t1 && ok; ++t) ok = load(w, t, false) && load(w, t, true);
+        if (pair) {
+          for (int t = w.t0; t < w.t1 && ok; ++t)
+            for (int x = t == w.t0 ? heads : 0; x < 2 * heads && ok; ++x) ok = load(w, t, x >= heads, h0 + x % heads);
+        } else if (kDual) {
+          for (int t = w.t0; t < w.t1 && ok; ++t) ok = (t - w.t0 < ahead || load(w, t, false, h0)) && load(w, t, true, h0);
         } else {
-          ok = load(w, w.t0, false);
-          for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load(w, t, false) && load(w, t - 1, true);
-          ok = ok && load(w, w.t1 - 1, true);
+          ok = ahead > 0 || load(w, w.t0, false, h0);
+          for (int t = w.t0 + 1; t < w.t1 && ok; ++t) ok = load(w, t, false, h0) && load(w, t - 1, true, h0);
+          ok = ok && load(w, w.t1 - 1, true, h0);
         }
       }
       // Drain: every issued copy lands before the CTA may exit.
@@ -658,7 +775,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
             }
             st_shared_v4(at, x[0], x[1], x[2], x[3]);
           }
-          sh->bad[seg & 1] = 1;
+          sh->bad[seg & 1][warp - 9] = 1;
         }
       }
       fence_proxy_async_shared();
@@ -666,57 +783,38 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     };
     for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
-      if (warp == 9 && lane == 0) sh->bad[seg & 1] = 0;
+      if (lane == 0) sh->bad[seg & 1][warp - 9] = 0;
       __syncwarp();
       if (!wait(&sh->q_full, q_phase)) goto mma_done;
       q_phase ^= 1u;
-      if (narrow(w.b)) {
-        // Warp 9 + s issues stream s's products. Both warps walk the whole ring, and give back at once what is
-        // the other's; warp 9 cleans. At most two tiles of such an item are cleaned (the cache's last and
-        // the one of drafted rows), and none of the next item before this one's end: two barriers are enough.
-        const int s = warp - 9;
-        auto give = [&](int st, bool own) {
-          if (own) tc_commit_warp(&sh->empty[st], issue);
-          else if (lane == 0) mbar_arrive(&sh->empty[st]);
+      if (paired(w.b)) {
+        // Warp 9 + s issues the products of the pair's head s. Both warps walk the whole ring, and give back at once what
+        // is the other's.
+        const int s = warp - 9, heads = heads_in(w.h);
+        auto next = [&](bool own) {  // the next tile: its stage where it is this warp's, else given back
+          const int st = take();
+          if (st >= 0 && !own && lane == 0) mbar_arrive(&sh->empty[st]);
+          return st;
         };
-        for (int i = 0; i < 2 && i < n_tiles; ++i) {
-          const int k = take();
-          if (k < 0) goto mma_done;
-          if (i == s) {
-            qk(s, 0, k);
-            tc_commit_warp(&sh->s_full[s], issue);
-          }
-          give(k, i == s);
-          if (i + 1 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
-        }
-        if (!wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
         for (int i = 0; i < n_tiles; ++i) {
-          const bool own = (i & 1) == s, more = i + 2 < n_tiles;
-          const int v = take();
-          if (v < 0) goto mma_done;
-          if (to_clean(w, w.t0 + i)) {
-            if (s == 0) {
-              clean(w, w.t0 + i, v);
-              if (lane == 0) mbar_arrive(&sh->v_clean[cleaned & 1u]);
-            } else {
-              if (!wait(&sh->v_clean[cleaned & 1u], (cleaned >> 1) & 1u)) goto mma_done;
-            }
-            ++cleaned;
+          for (int x = 0; x < heads; ++x) {
+            const int k = next(x == s);
+            if (k < 0) goto mma_done;
+            if (x != s) continue;
+            qk(s, s, k);
+            tc_commit_warp(&sh->s_full[s], issue);
+            tc_commit_warp(&sh->empty[k], issue);
           }
-          const int k = more ? take() : 0;
-          if (k < 0) goto mma_done;
-          if (own) {
-            if (!wait(&sh->p_full[s][0], p_phase[s]) || !pv(s, v, i < 2)) goto mma_done;
+          if (i + 1 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
+          if (i == 0 && !wait(&sh->o_empty, o_phase ^ 1u)) goto mma_done;
+          for (int x = 0; x < heads; ++x) {
+            const int v = next(x == s);
+            if (v < 0) goto mma_done;
+            if (x != s) continue;
+            if (to_clean(w, w.t0 + i)) clean(w, w.t0 + i, v);
+            if (!wait(&sh->p_full[s][0], p_phase[s]) || !pv(s, v, i == 0)) goto mma_done;
+            tc_commit_warp(&sh->empty[v], issue);
           }
-          give(v, own);
-          if (more) {
-            if (own) {
-              qk(s, 0, k);
-              tc_commit_warp(&sh->s_full[s], issue);
-            }
-            give(k, own);
-          }
-          if (i + 3 == n_tiles) tc_commit_warp(&sh->q_empty, issue);
         }
       } else if (kDual) {
         // Warp 9 issues stream 0's products, warp 10 stream 1's, a tile's second product and the
@@ -789,7 +887,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
       }
       tc_commit_warp(&sh->o_final, issue);
-      if (warp == 9 && lane == 0) mbar_arrive(&sh->o_final);  // and what it found in V
+      if (lane == 0) mbar_arrive(&sh->o_final);  // and what it found in V
       o_phase ^= 1u;
       ++seg;
     }
@@ -813,8 +911,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     int seg = 0;
     for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
       const int n_tiles = w.t1 - w.t0;
-      const bool joint = !kDual || narrow(w.b);  // the streams share one row tile
-      const int tile = w.mt * (kDual ? 2 : 1) + (joint ? 0 : s);
+      const bool quarter = copied(w.b);                       // the warp sees a quarter of a tile's keys
+      const bool pair = paired(w.b);                           // each stream has a head of its own
+      constexpr bool joint = !kDual;                          // the streams share one row tile and join their sums
+      const int tile = pair ? 0 : w.mt * (kDual ? 2 : 1) + (joint ? 0 : s);
+      const bool none = pair && s >= heads_in(w.h);           // no head for this stream
       const int node0 = tile * a.npt;
       int rows = max(0, min(a.npt, a.n - node0)) * a.group;  // of this tile
       if constexpr (Args::kPrefix) {
@@ -825,11 +926,56 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           rows = seq < a.n_seqs ? nodes * a.group : 0;
         }
       }
-      const bool idle = (warp & 3) * 32 >= rows;                   // a warp without rows
-      const int node = min(node0 + row / a.group, a.n - 1);
+      const bool idle = !quarter && (warp & 3) * 32 >= rows;       // a warp without rows
+      const int in_item = quarter ? lane : row;
+      const int node = min(node0 + in_item / a.group, a.n - 1);
       float m = -INFINITY, l = 0.0f;
       bool first = true;
-      for (int i = joint ? s : 0; i < n_tiles; i += joint ? 2 : 1) {
+      if constexpr (Args::kPrefix) {
+        for (int i = 0; quarter && !none && i < n_tiles; ++i) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sh->s_full[s], s_phase, abort_flag, timeout))) goto softmax_done;
+          s_phase ^= 1u;
+          tc_fence_after();
+          const int t = w.t0 + i;
+          uint32_t r[32];
+          tmem_ld32(ts + (warp & 3) * 32, r);
+          uint32_t keep = 0xffffffffu;
+          if (t >= w.shape.cached || (t + 1) * kAtTile > w.shape.len) keep = visible_quarter(a, w.shape, w.b, node, t, warp & 3);
+          tmem_wait_ld32(r);
+          if (keep != 0xffffffffu) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = (keep >> e) & 1u ? r[e] : 0xff800000u;
+          }
+          float mx = fmaxf(u2f(r[0]), u2f(r[1]));
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) mx = fmaxf(fmaxf(mx, u2f(r[e])), u2f(r[e + 1]));
+          mx = fmaxf(mx, m);
+          const bool grown = m == -INFINITY ? mx > -INFINITY : (mx - m) * sc > kAtRescale;
+          if (__any_sync(0xffffffffu, grown)) {
+            const float f = grown ? (m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc)) : 1.0f;
+            if (!first) rescale_row<kHD>(tmem + lanes + 256 + s * 128, f);
+            l *= f;
+            if (grown) m = mx;
+          }
+          const float off = m == -INFINITY ? 0.0f : -m * sc;
+          // the other copies' keys have no weight in this one
+          const uint32_t none[16] = {};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c != (warp & 3)) tmem_st16(ts + c * 16, none);
+          float2 l0 = make_float2(l, 0.0f), l1 = make_float2(0.0f, 0.0f);
+          quarter_weights(ts + (warp & 3) * 16, r, sc, off, l0, l1);
+          l = (l0.x + l0.y) + (l1.x + l1.y);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sh->p_full[s][0]);
+            mbar_arrive(&sh->p_full[s][1]);
+          }
+          first = false;
+        }
+      }
+      for (int i = joint ? s : 0; !quarter && !none && i < n_tiles; i += joint ? 2 : 1) {
         bool ok = mbar_wait(&sh->s_full[s], s_phase, abort_flag, timeout);
         if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
         s_phase ^= 1u;
@@ -850,17 +996,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           if (__any_sync(0xffffffffu, grown)) {
             // With nothing seen so far l and the accumulator's row are 0 (or not written yet).
             const float f = grown ? (m == -INFINITY ? 0.0f : exp2f_ftz((m - mx) * sc)) : 1.0f;
-            if (!first) {  // the previous product is done: this tile's scores were issued behind it
-#pragma unroll 1
-              for (int c = 0; c < kHD; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(tmem + lanes + 256 + s * 128 + c, o);
-                tmem_wait_ld16(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(u2f(o[e]) * f);
-                tmem_st16(tmem + lanes + 256 + s * 128 + c, o);
-              }
-            }
+            if (!first) rescale_row<kHD>(tmem + lanes + 256 + s * 128, f);  // (the previous product is done:
+                                                                          // this tile's scores were issued behind it)
             l *= f;
             if (grown) m = mx;
           }
@@ -904,25 +1041,30 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
           if (m == INFINITY) l = NAN;  // inf - inf above
         }
         const bool whole = w.t0 == 0 && w.t1 == w.shape.tiles;
-        const bool bad = *reinterpret_cast<volatile int*>(&sh->bad[seg & 1]) != 0;
-        const bool write = row < rows;
-        const int head = w.h * a.group + row % a.group;
+        const bool bad = *reinterpret_cast<volatile int*>(&sh->bad[seg & 1][pair ? s : 0]) != 0;
+        const bool write = in_item < rows && !none;
+        const int kv = pair ? 2 * w.h + s : w.h;
+        const int head = kv * a.group + in_item % a.group;
         const long long slot = 2LL * blockIdx.x + (w.t0 > 0 ? 0 : 1);
-        const int prow = (joint ? 0 : s * kAtTile) + row;
+        int prow = (joint ? 0 : s * kAtTile) + row;
+        if constexpr (Args::kPrefix) {
+          if (pair) prow = (s * a.copies + (quarter ? warp & 3 : 0)) * rows + in_item;
+        }
         // where the rows' parts go, one after another
-        float4* part_o = a.part_o + slot * (kHD / 4) * Cfg::kRows + prow;
-        float2* part_ml = a.part_ml + slot * Cfg::kRows + prow;
-        int part_rows = Cfg::kRows;
+        constexpr int kRows = Args::kPrefix ? kPfRows : Cfg::kRows;
+        float4* part_o = a.part_o + slot * (kHD / 4) * kRows + prow;
+        float2* part_ml = a.part_ml + slot * kRows + prow;
+        int part_rows = kRows;
         if constexpr (Args::kPrefix) {
           const long long prefix_items = static_cast<long long>(a.heads) * a.p_items;
           const long long item = w.b < 0 ? static_cast<long long>(w.h) * a.p_items + w.mt
-                                         : (static_cast<long long>(w.b) * a.heads + w.h) * a.m_items + w.mt;
+                                         : (static_cast<long long>(w.b) * a.own_heads + w.h) * a.m_items + w.mt;
           if (whole) {
             part_rows = w.b < 0 ? a.p_rows : a.rows;
-            const int tile_rows = joint ? 0 : part_rows / 2;
+            const int at = pair ? prow : (joint ? 0 : s * (part_rows / 2)) + row;
             const long long before = w.b < 0 ? item * a.p_rows : prefix_items * a.p_rows + item * a.rows;
-            part_o = a.whole_o + before * (kHD / 4) + s * tile_rows + row;
-            part_ml = a.whole_ml + before + s * tile_rows + row;
+            part_o = a.whole_o + before * (kHD / 4) + at;
+            part_ml = a.whole_ml + before + at;
           }
           if (threadIdx.x == 0) {
             int2* at = a.item_ctas + (w.b < 0 ? 0 : prefix_items) + item;
@@ -932,8 +1074,28 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         if (!idle) {
-          const int cols = joint ? kHD / 2 : kHD;
-          const int col0 = joint ? s * cols : 0;
+          if constexpr (Args::kPrefix) {
+            if (quarter && !bad) {
+              const uint32_t from = tmem + lanes + 256 + s * 128;
+#pragma unroll 1
+              for (int c = 0; c < kHD; c += 64) {
+                uint32_t o[2][32];
+                tmem_ld32(from + c, o[0]);
+                tmem_ld32(from + c + 32, o[1]);
+                tmem_wait_ld32(o[0]);
+                tmem_wait_ld32(o[1]);
+                if (write) {
+                  float4* dst = part_o + static_cast<long long>(c / 4) * part_rows;
+#pragma unroll
+                  for (int e = 0; e < 64; e += 4)
+                    dst[e / 4 * part_rows] = make_float4(u2f(o[e / 32][e % 32]), u2f(o[e / 32][e % 32 + 1]), u2f(o[e / 32][e % 32 + 2]),
+                                                         u2f(o[e / 32][e % 32 + 3]));
+                }
+              }
+            }
+          }
+          const int cols = quarter && !bad ? 0 : joint ? kHD / 2 : kHD;
+          const int col0 = joint ? s * (kHD / 2) : 0;
           const uint32_t to = tmem + lanes + 256 + (joint ? 0 : s * 128) + col0;
 #pragma unroll 1
           for (int c = 0; c < cols; c += 16) {
@@ -961,7 +1123,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
                                       ? (a.mask[(static_cast<long long>(w.b) * a.n + node) * a.words + (j >> 6)] >> (j & 63)) & 1u
                                       : j <= node;
                 if (!sees) continue;
-                const __nv_bfloat16* v = a.v_draft + static_cast<long long>(w.b) * a.draft_seq + j * a.draft_row + w.h * kHD + col0 + c;
+                if (quarter && ((j >> 5) & 3) != (warp & 3)) continue;  // (of four parts, the one that has the key)
+                const __nv_bfloat16* v = a.v_draft + static_cast<long long>(w.b) * a.draft_seq + j * a.draft_row + kv * kHD + col0 + c;
                 for (int e = 0; e < 16; ++e) {
                   const float y = __bfloat162float(v[e]);
                   if (!isfinite(y)) x[e] += y;
@@ -1140,11 +1303,13 @@ struct JoinArgs {
   float* lse;
   long long out_row, out_seq;
   int n_seqs, n, heads, group, npt, tiles, m_items, p_nodes, p_seqs, p_split, p_items, rows, p_rows, ctas;
+  int pairs, own_heads, copies;
   int capacity, prefix_capacity;
   float scale;
 };
 
-// kBatch, kSplit as for k_attn_combine: lanes share a row where there are fewer blocks than SMs otherwise.
+// kBatch, kSplit as for k_attn_combine: lanes share a row where there are fewer blocks than SMs otherwise, and more parts
+// are in flight where an item has many (one row tile).
 template <int kHD, int kBatch, int kSplit>
 __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__ JoinArgs a) {
   pdl_launch_dependents();
@@ -1154,40 +1319,49 @@ __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__
   const int r = blockIdx.x * kLanes + lane % kLanes;
   const int per_seq = a.n * a.group;
   const int b = r / per_seq, in_seq = r - b * per_seq, node = in_seq / a.group, g = in_seq - node * a.group;
-  const int prefix = *a.prefix_len, len = b < a.n_seqs ? a.lens[b] : -1;
-  const bool live = len >= 0 && len <= a.capacity && prefix >= 0 && prefix <= a.prefix_capacity;
+  const bool there = b < a.n_seqs;
   // The row's place in the prefix's items and in its own sequence's.
   struct Place {
     const float4* whole_o;
     const float2* whole_ml;
     int whole_rows, at;  // at: within the rows of a part that was cut
-    int first, parts;
+    int first, parts;    // CTAs
+    int of, apart;       // parts of a CTA's (4 of copied rows) and the rows between them
   } at[2] = {};
-  if (live) {
+  bool live = false;
+  if (there) {
     const int tile_rows = a.tiles == 2 ? kAtTile : 0;
     const long long prefix_items = static_cast<long long>(a.heads) * a.p_items;
-    auto place = [&](int i, int tile, int row, long long before, long long item, int rows) {
-      const int s = tile % a.tiles;
+    // `in`: the row's place among those of its item's stored part
+    auto place = [&](int i, int in, int in_cut, long long before, int rows, int copies, int apart) {
       at[i].whole_rows = rows;
-      at[i].whole_o = a.whole_o + before * (kHD / 4) + s * (rows / 2) + row;
-      at[i].whole_ml = a.whole_ml + before + s * (rows / 2) + row;
-      at[i].at = s * tile_rows + row;
-      const int2 c = a.item_ctas[item];
-      at[i].first = min(max(c.x, 0), a.ctas - 1);
-      at[i].parts = min(max(c.y, at[i].first), a.ctas - 1) - at[i].first + 1;
+      at[i].whole_o = a.whole_o + before * (kHD / 4) + in;
+      at[i].whole_ml = a.whole_ml + before + in;
+      at[i].at = in_cut;
+      at[i].of = copies;
+      at[i].apart = apart;
     };
-    if (prefix > 0) {
-      const int tile = a.p_split > 1 ? b * a.p_split + node / a.p_nodes : b / a.p_seqs;
-      const int row = a.p_split > 1 ? (node % a.p_nodes) * a.group + g : (b % a.p_seqs) * per_seq + in_seq;
-      const long long item = static_cast<long long>(h) * a.p_items + tile / a.tiles;
-      place(0, tile, row, item * a.p_rows, item, a.p_rows);
+    const int p_tile = a.p_split > 1 ? b * a.p_split + node / a.p_nodes : b / a.p_seqs;
+    const int p_row = a.p_split > 1 ? (node % a.p_nodes) * a.group + g : (b % a.p_seqs) * per_seq + in_seq;
+    const long long p_item = static_cast<long long>(h) * a.p_items + p_tile / a.tiles;
+    const int tile = node / a.npt, own_row = (node - tile * a.npt) * a.group + g;
+    const long long item = (static_cast<long long>(b) * a.own_heads + (a.pairs ? h >> 1 : h)) * a.m_items + tile / a.tiles;
+    // (loads that do not wait for one another; without prefix rows what lies there is not used)
+    const int prefix = *a.prefix_len, len = a.lens[b];
+    const int2 c[2] = {a.item_ctas[p_item], a.item_ctas[prefix_items + item]};
+    const int p_s = p_tile % a.tiles, s = tile % a.tiles, in_pair = (h & 1) * a.copies * per_seq + in_seq;
+    place(0, p_s * (a.p_rows / 2) + p_row, p_s * tile_rows + p_row, p_item * a.p_rows, a.p_rows, 1, 0);
+    place(1, a.pairs ? in_pair : s * (a.rows / 2) + own_row, a.pairs ? in_pair : s * tile_rows + own_row,
+          prefix_items * a.p_rows + item * a.rows, a.rows, a.copies, per_seq);
+    live = len >= 0 && len <= a.capacity && prefix >= 0 && prefix <= a.prefix_capacity;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      at[i].first = min(max(c[i].x, 0), a.ctas - 1);
+      at[i].parts = i == 0 && prefix <= 0 ? 0 : min(max(c[i].y, at[i].first), a.ctas - 1) - at[i].first + 1;
     }
-    const int tile = node / a.npt;
-    const long long item = (static_cast<long long>(b) * a.heads + h) * a.m_items + tile / a.tiles;
-    place(1, tile, (node - tile * a.npt) * a.group + g, prefix_items * a.p_rows + item * a.rows, prefix_items + item, a.rows);
   }
   if (kSplit == 1 && !live) return;
-  const int item_rows = a.tiles * kAtTile, parts = at[0].parts + at[1].parts;
+  const int parts_0 = at[0].parts * at[0].of, parts = parts_0 + at[1].parts * at[1].of;
   const float sc = a.scale * kAtLog2e;
   float m = -INFINITY, l = 0.0f;
   float4 x[4] = {};
@@ -1198,18 +1372,22 @@ __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__
     for (int j = 0; j < kBatch; ++j) {
       int i = i0 + j * kSplit;
       if (i >= parts) break;
-      const bool own = i >= at[0].parts;
-      if (own) i -= at[0].parts;
+      const bool own = i >= parts_0;
+      if (own) i -= parts_0;
       const Place& p = own ? at[1] : at[0];
+      const int in_cta = p.of > 1 ? i & 3 : 0;
+      if (p.of > 1) i >>= 2;
       const float4* o = p.whole_o;
       const float2* w = p.whole_ml;
       int stride = p.whole_rows;
       if (p.parts > 1) {  // the last part of its first CTA, the first part of the others
         const long long slot = i == 0 ? 2LL * p.first + 1 : 2LL * (p.first + i);
-        o = a.part_o + slot * (kHD / 4) * item_rows + p.at;
-        w = a.part_ml + slot * item_rows + p.at;
-        stride = item_rows;
+        o = a.part_o + slot * (kHD / 4) * kPfRows + p.at;
+        w = a.part_ml + slot * kPfRows + p.at;
+        stride = kPfRows;
       }
+      o += in_cta * p.apart;
+      w += in_cta * p.apart;
       ml[j] = *w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[j][e] = o[static_cast<long long>(warp * 4 + e) * stride];
@@ -1323,6 +1501,13 @@ static rf_status launch_attn(const Args& a, int ctas, cudaStream_t s) {
   rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_attn<kHD, kDual, Args>), Cfg::kSmem, &done);
   if (st != RF_OK) return st;
   ProfScope prof(s, RF_STAGE_ATTENTION);
+  // CTAs of unlike work are launched when the kernel before is done: those that come up as its CTAs leave take their
+  // places in the order in which these finish, and the ones with the prefix's products then end up side by side (64
+  // sequences over 16,384 shared rows: 72 us as dependents, 63 so).
+  if (Args::kPrefix && kDual) {
+    k_attn<kHD, kDual, Args><<<dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s>>>(a);
+    return cuda_check(cudaGetLastError(), "k_attn launch");
+  }
   return cuda_check(launch_dependent(k_attn<kHD, kDual, Args>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, 1, a),
                     "k_attn launch");
 }
@@ -1384,13 +1569,13 @@ static rf_status attn_args(const rf_attn_desc* d, const rf_bf16* q, const rf_bf1
 
 // The tensor maps.
 static rf_status attn_maps(const rf_attn_desc* d, const rf_bf16* q, const rf_bf16* k_cache, const rf_bf16* v_cache,
-                           const rf_bf16* k_draft, const rf_bf16* v_draft, AttnArgs* args) {
+                           const rf_bf16* k_draft, const rf_bf16* v_draft, int nodes, AttnArgs* args) {
   AttnArgs& a = *args;
   const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs, cap = d->capacity;
   rf_status st;
-  // a box of a row tile: every head of the group, npt nodes
+  // a box of a row tile: every head of the group, `nodes` nodes
   if ((st = make_tmap_bf16_4d(&a.tm_q, q, {hd, Hq, n, B}, {hd, (uint64_t)d->q_row_stride, (uint64_t)d->q_seq_stride},
-                              {64, (uint32_t)a.group, (uint32_t)a.npt, 1})) != RF_OK)
+                              {64, (uint32_t)a.group, (uint32_t)nodes, 1})) != RF_OK)
     return st;
   const uint64_t cs[3] = {hd, (uint64_t)d->cache_row_stride, (uint64_t)d->cache_seq_stride};
   const uint64_t ds[3] = {hd, (uint64_t)d->draft_row_stride, (uint64_t)d->draft_seq_stride};
@@ -1421,7 +1606,7 @@ extern "C" rf_status rf_tree_attention(const rf_attn_desc* d, const rf_bf16* q, 
     return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
   int sms = 0;
   if ((st = current_device(&sms)) != RF_OK) return st;
-  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, &a)) != RF_OK) return st;
+  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, a.npt, &a)) != RF_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.part_o = lay.part_o;
   a.part_ml = lay.part_ml;
@@ -1479,7 +1664,7 @@ struct PrefixLayout {
   float4 *part_o, *whole_o;
   float2 *part_ml, *whole_ml;
   int2* item_ctas;
-  int tiles, p_nodes, p_seqs, p_split, p_items, m_items, rows, p_rows;
+  int tiles, p_nodes, p_seqs, p_split, p_items, m_items, rows, p_rows, pairs, own_heads, copies;
   size_t bytes;
 };
 
@@ -1494,15 +1679,18 @@ static PrefixLayout prefix_layout(const rf_attn_desc* d, void* ws) {
   l.p_items = static_cast<int>((p_tiles + l.tiles - 1) / l.tiles);
   l.m_items = static_cast<int>((n + npt * l.tiles - 1) / (npt * l.tiles));
   l.p_rows = static_cast<int>(l.tiles * group * l.p_nodes * l.p_seqs);
-  l.rows = static_cast<int>(n <= npt ? n * group : l.tiles * npt * group);
-  const size_t cut = static_cast<size_t>(2 * kAtMaxCtas) * l.tiles * kAtTile;
-  const size_t whole = static_cast<size_t>(H) * l.p_items * l.p_rows + static_cast<size_t>(B * H) * l.m_items * l.rows;
+  l.pairs = l.tiles == 2 && n <= npt;
+  l.own_heads = static_cast<int>(l.pairs ? (H + 1) / 2 : H);
+  l.copies = l.pairs && n * group <= 32 ? 4 : 1;
+  l.rows = static_cast<int>(l.pairs ? 2 * l.copies * n * group : n <= npt ? n * group : l.tiles * npt * group);
+  const size_t cut = static_cast<size_t>(2 * kAtMaxCtas) * kPfRows;
+  const size_t whole = static_cast<size_t>(H) * l.p_items * l.p_rows + static_cast<size_t>(B) * l.own_heads * l.m_items * l.rows;
   Carve c(ws);
   l.part_o = c.take<float4>(cut * d->head_dim / 4);
   l.part_ml = c.take<float2>(cut);
   l.whole_o = c.take<float4>(whole * d->head_dim / 4);
   l.whole_ml = c.take<float2>(whole);
-  l.item_ctas = c.take<int2>(static_cast<size_t>(H) * l.p_items + static_cast<size_t>(B * H) * l.m_items);
+  l.item_ctas = c.take<int2>(static_cast<size_t>(H) * l.p_items + static_cast<size_t>(B) * l.own_heads * l.m_items);
   l.bytes = c.bytes();
   return l;
 }
@@ -1535,7 +1723,7 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
     return fail(RF_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned (got %zu)", lay.bytes, workspace_bytes);
   int sms = 0;
   if ((st = current_device(&sms)) != RF_OK) return st;
-  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, &a)) != RF_OK) return st;
+  if ((st = attn_maps(d, q, k_cache, v_cache, k_draft, v_draft, lay.p_nodes, &a)) != RF_OK) return st;
   const uint64_t hd = d->head_dim, H = d->n_kv_heads, Hq = d->n_q_heads, n = d->n_nodes, B = d->n_seqs;
   const uint64_t ps[3] = {hd, (uint64_t)desc->prefix_row_stride, (uint64_t)desc->prefix_row_stride};
   const uint64_t pd[4] = {hd, H, (uint64_t)desc->prefix_capacity, 1};
@@ -1557,7 +1745,15 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   a.p_seqs = lay.p_seqs;
   a.p_split = lay.p_split;
   a.p_items = lay.p_items;
-  a.narrow = a.n <= a.npt;
+  // In tenths of a microsecond: a prefix tile with two row tiles takes 1.7 (products) to 2.0 (beside CTAs that stream
+  // caches), a tile of a pair, two of each head's, 1.8, an item's first and last steps some 6. Up to 128 rows a tile is
+  // its bytes, whoever's it is, and an item weighs four of them, as in rf_tree_attention.
+  a.w_item = lay.pairs ? 60 : 68;
+  a.w_prefix = lay.pairs ? 20 : 17;
+  a.w_own = lay.pairs ? 18 : 17;
+  a.pairs = lay.pairs;
+  a.own_heads = lay.own_heads;
+  a.copies = lay.copies;
   a.rows = lay.rows;
   a.p_rows = lay.p_rows;
   const int ctas = std::min(sms, kAtMaxCtas);
@@ -1587,6 +1783,9 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   j.p_seqs = lay.p_seqs;
   j.p_split = lay.p_split;
   j.p_items = lay.p_items;
+  j.copies = lay.copies;
+  j.pairs = lay.pairs;
+  j.own_heads = lay.own_heads;
   j.rows = lay.rows;
   j.p_rows = lay.p_rows;
   j.ctas = ctas;
@@ -1594,11 +1793,12 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   j.prefix_capacity = a.prefix_capacity;
   j.scale = a.scale;
   const int64_t rows = static_cast<int64_t>(B * n) * a.group;  // of a KV head
-  const bool few = (rows + 31) / 32 * static_cast<int64_t>(H) < sms;
+  const bool few = (rows + 31) / 32 * static_cast<int64_t>(H) < sms, fewest = rows <= 32;
   const int64_t blocks = (rows + (few ? 7 : 31)) / (few ? 8 : 32);
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
-  void (*join)(JoinArgs) = hd == 128 ? (few ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 1>)
-                                     : (few ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 1>);
+  void (*join)(JoinArgs) =
+      hd == 128 ? (!few ? k_prefix_join<128, 4, 1> : fewest ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 4>)
+                : (!few ? k_prefix_join<64, 4, 1> : fewest ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 4>);
   return cuda_check(launch_dependent(join, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H)), dim3(static_cast<unsigned>(2 * hd)),
                                      0, s, 1, j),
                     "k_prefix_join launch");
