@@ -8,7 +8,9 @@
 // Every row is read and written once, so memory is the bound. The lanes that share a head
 // (a power of two up to 32, in one warp) hold two 16-byte pieces of it each: its sums are
 // exchanged by shuffles and nothing is read twice. Channels' angles and gains are formed once
-// for the heads of a row. Three forms say which pieces those are:
+// for the heads of a row. A thread's pieces of its next heads are on their way to shared memory
+// while it works on those that are there (asynchronous copies; each thread reads what it copied
+// itself, so there is no barrier). Three forms say which pieces those are:
 //   kPieces   halves turn against each other and divide into pieces: a piece of the first half
 //             and its partner of the second, as in rf_rope
 //   kPairs    neighbouring channels turn against each other: any two pieces
@@ -55,12 +57,18 @@ struct NormLane {
   static constexpr int kVec = 16 / static_cast<int>(sizeof(T));
   static constexpr int kChannels = 2 * kVec;
   static constexpr int kAngles = kForm == kShared ? kChannels : kVec;
+  using Raw = T[2][kVec];
   int start[2];  // first channels of its pieces
   bool ok[2];    // whether they exist
   bool turns;    // kPieces: its channels turn
   float c[kAngles], s[kAngles], g[kChannels];
 
   __device__ __forceinline__ void place(const NormArgs& a, int lane) {
+#pragma unroll
+    for (int i = 0; i < kAngles; ++i) {  // (a group without a row turns zeros)
+      c[i] = 1.0f;
+      s[i] = 0.0f;
+    }
     if (kForm == kPieces) {
       turns = 2 * lane * kVec < a.rot;
       start[0] = turns ? lane * kVec : lane * kChannels;
@@ -108,10 +116,15 @@ struct NormLane {
       for (int i = 0; i < kVec; ++i) g[p * kVec + i] = there ? to_f(v[i]) : 1.0f;
     }
   }
-  __device__ __forceinline__ void load(const T* head, T (&v)[2][kVec]) const {
+  // Copies a head's pieces to `slot` (of this thread, its second piece kNormThreads places on), and reads them there.
+  __device__ __forceinline__ void copy(uint32_t slot, const T* head) const {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      if (ok[p]) load_vec(head + start[p], v[p]);
+      if (ok[p]) copy_async16(slot + p * kNormThreads * 16, head + start[p]);
+  }
+  __device__ __forceinline__ void take(uint32_t slot, Raw& v) const {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<uint4*>(v[p]) = ld_shared_v4(slot + p * kNormThreads * 16);
   }
   __device__ __forceinline__ void widen(const T (&v)[2][kVec], float (&x)[kChannels]) const {
 #pragma unroll
@@ -158,6 +171,17 @@ struct NormLane {
   }
 };
 
+// A thread's places for pieces in flight: `kHeads` heads (of one array) in each of kNormStages.
+constexpr int kNormStages = 2;
+template <int kHeads>
+constexpr size_t norm_ring_bytes() {
+  return static_cast<size_t>(kNormStages) * kHeads * 2 * kNormThreads * 16;
+}
+template <int kHeads>
+__device__ __forceinline__ uint32_t norm_slot(uint32_t ring, int stage, int j) {
+  return ring + static_cast<uint32_t>(((stage * kHeads + j) * 2 * kNormThreads + static_cast<int>(threadIdx.x)) * 16);
+}
+
 // Sum over the lanes of a head.
 __device__ __forceinline__ float head_sum(float x, int lanes) {
   for (int o = 1; o < lanes; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -170,10 +194,10 @@ __device__ __forceinline__ float inverse_root(float v) {
   else return __frcp_rn(__fsqrt_rn(v));
 }
 
-constexpr int kNormHeads = 4;  // heads whose loads are in flight together
+constexpr int kNormHeads = 4;  // heads of a batch
 
 template <class T, int kForm>
-__global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constant__ NormArgs a,
+__global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_constant__ NormArgs a,
                                                             const __grid_constant__ RopeTable tab) {
   using Lane = NormLane<T, kForm>;
   __shared__ __align__(16) float staged[kForm == kShared ? kNormThreads * Lane::kChannels : 4];
@@ -187,22 +211,41 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
   float* sh = staged + (kForm == kShared ? (threadIdx.x - at) * Lane::kChannels : 0);
   Lane l;
   l.place(a, at);
-  l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset, 1.0f);
   const T* in = static_cast<const T*>(a.in) + row * a.ld_in;
   T* out = static_cast<T*>(a.out) + row * a.ld_out;
   const int h0 = static_cast<int>(blockIdx.y) * a.hpt, h1 = min(h0 + a.hpt, a.n_heads);
   const float part = 1.0f / static_cast<float>(a.head_dim);
-  for (int h = h0; h < h1;) {
-    const int end = min(h + kNormHeads, h < a.n_q ? min(h1, a.n_q) : h1);
-    alignas(16) T v[kNormHeads][2][Lane::kVec];
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const uint32_t ring = smem_u32(norm_smem);
+  // Batches of up to kNormHeads heads that are all queries or all keys.
+  auto batch_end = [&](int h) { return min(h + kNormHeads, h < a.n_q ? min(h1, a.n_q) : h1); };
+  int ahead = h0, filled = 0;  // the next batch to be copied, and its stage
+  auto copy_next = [&] {
+    if (ahead < h1) {
+      const int end = batch_end(ahead);
 #pragma unroll
-    for (int j = 0; j < kNormHeads; ++j)
-      if (h + j < end) l.load(in + (h + j) * a.head_dim, v[j]);
+      for (int j = 0; j < kNormHeads; ++j)
+        if (ahead + j < end) l.copy(norm_slot<kNormHeads>(ring, filled, j), in + (ahead + j) * a.head_dim);
+      ahead = end;
+    }
+    copy_async_commit();
+    filled = filled + 1 == kNormStages ? 0 : filled + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < kNormStages - 1; ++i) copy_next();
+  l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset, 1.0f);
+  int stage = 0;
+  for (int h = h0; h < h1;) {
+    const int end = batch_end(h);
+    copy_next();
     if (h == h0 || h == a.n_q) l.gains(h < a.n_q ? a.q_gain : a.k_gain);
+    copy_async_wait<kNormStages - 1>();
+    alignas(16) typename Lane::Raw v[kNormHeads];
     float x[Lane::kChannels], r[kNormHeads];
 #pragma unroll
     for (int j = 0; j < kNormHeads; ++j) {
       if (h + j >= end) break;
+      l.take(norm_slot<kNormHeads>(ring, stage, j), v[j]);
       l.widen(v[j], x);
       float ss = 0.0f;
 #pragma unroll
@@ -222,6 +265,7 @@ __global__ void __launch_bounds__(kNormThreads) k_norm_rope(const __grid_constan
       if (live) l.store(out + (h + j) * a.head_dim, x);
     }
     h = end;
+    stage = stage + 1 == kNormStages ? 0 : stage + 1;
   }
 }
 
@@ -245,64 +289,88 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
   Lane l;
   l.place(a, at);
   l.gains(keys ? a.k_gain : a.q_gain);
-  const int chunks = (heads + a.hpt - 1) / a.hpt;
-  const long long units = static_cast<long long>(a.n_rows) * chunks;
+  // The kind's heads, kNormBackHeads of a row together, in the order of the rows: each group takes an equal run of
+  // them, so that it forms a row's angles once, and as many copies are in flight at the end of a run as before.
+  const int batches = (heads + kNormBackHeads - 1) / kNormBackHeads;  // of a row
+  const long long total = static_cast<long long>(a.n_rows) * batches, all_groups = static_cast<long long>(ctas) * groups;
+  const long long me = static_cast<long long>(cta) * groups + group;
+  const long long t0 = total * me / all_groups, t1 = total * (me + 1) / all_groups;
+  const int turns = static_cast<int>((total + all_groups - 1) / all_groups);  // (every group of a warp makes as many)
   const float part = 1.0f / static_cast<float>(a.head_dim);
   float dg[kC] = {};
-  // The CTA's groups take units side by side; a round's last ones may be none of this call's.
-  for (long long u0 = static_cast<long long>(cta) * groups; u0 < units; u0 += static_cast<long long>(ctas) * groups) {
-    const bool live = u0 + group < units;
-    const long long u = live ? u0 + group : units - 1;
-    const int row = static_cast<int>(quick_div(u, chunks));
-    const int c0 = static_cast<int>(u - static_cast<long long>(row) * chunks) * a.hpt;
-    // (every group of the warp runs the same number of turns, whatever its chunk's heads are)
-    l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset, -1.0f);
-    const T* in = static_cast<const T*>(a.in) + row * a.ld_in + static_cast<long long>(first) * a.head_dim;
-    const T* dy = static_cast<const T*>(a.dy) + row * a.ld_dy + static_cast<long long>(first) * a.head_dim;
-    T* dx = static_cast<T*>(a.out) + row * a.ld_out + static_cast<long long>(first) * a.head_dim;
-    for (int k = 0; k < a.hpt; k += kNormBackHeads) {
-      alignas(16) T xv[kNormBackHeads][2][Lane::kVec], yv[kNormBackHeads][2][Lane::kVec];
-      bool there[kNormBackHeads];
-#pragma unroll
-      for (int j = 0; j < kNormBackHeads; ++j) {
-        const int h = c0 + k + j;
-        there[j] = live && k + j < a.hpt && h < heads;
-        if (there[j]) {
-          l.load(in + h * a.head_dim, xv[j]);
-          l.load(dy + h * a.head_dim, yv[j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kC; ++i) {
-            from_f(xv[j][i / Lane::kVec][i % Lane::kVec], 0.0f);
-            from_f(yv[j][i / Lane::kVec][i % Lane::kVec], 0.0f);
-          }
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < kNormBackHeads; ++j) {
-        if (k + j >= a.hpt) break;
-        float x[kC], w[kC];
-        l.widen(xv[j], x);
-        l.widen(yv[j], w);
-        l.turn(a, sh, w);
-        float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
-          ss += x[i] * x[i];
-          dot += w[i] * l.g[i] * x[i];
-        }
-        ss = head_sum(ss, a.lanes);
-        dot = head_sum(dot, a.lanes);
-        const float r = inverse_root<T>(ss * part + a.eps);
-        const float b = dot * part * (r * r);
-#pragma unroll
-        for (int i = 0; i < kC; ++i) {
-          if (there[j]) dg[i] += w[i] * (x[i] * r);
-          x[i] = r * (w[i] * l.g[i] - x[i] * b);
-        }
-        if (there[j]) l.store(dx + (c0 + k + j) * a.head_dim, x);
-      }
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  const uint32_t ring = smem_u32(norm_smem);
+  struct Spot {  // a batch: its place in the run, its row and place in the row
+    long long t;
+    int row, batch;
+  };
+  auto advance = [&](Spot& p) {
+    ++p.t;
+    if (++p.batch == batches) {
+      p.batch = 0;
+      ++p.row;
     }
+  };
+  auto has = [&](const Spot& p, int j) { return p.t < t1 && p.batch * kNormBackHeads + j < heads; };
+  Spot now{t0, static_cast<int>(t0 / batches), 0};
+  now.batch = static_cast<int>(t0 - static_cast<long long>(now.row) * batches);
+  Spot next = now;
+  int filled = 0, stage = 0;
+  auto copy_next = [&] {
+#pragma unroll
+    for (int j = 0; j < kNormBackHeads; ++j)
+      if (has(next, j)) {
+        const long long h = first + next.batch * kNormBackHeads + j;
+        l.copy(norm_slot<2 * kNormBackHeads>(ring, filled, 2 * j), static_cast<const T*>(a.in) + next.row * a.ld_in + h * a.head_dim);
+        l.copy(norm_slot<2 * kNormBackHeads>(ring, filled, 2 * j + 1), static_cast<const T*>(a.dy) + next.row * a.ld_dy + h * a.head_dim);
+      }
+    advance(next);
+    copy_async_commit();
+    filled = filled + 1 == kNormStages ? 0 : filled + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < kNormStages - 1; ++i) copy_next();
+  for (int i = 0; i < turns; ++i) {
+    copy_next();
+    if (now.t < t1 && (i == 0 || now.batch == 0))
+      l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[now.row]) : now.row + a.pos_offset, -1.0f);
+    __syncwarp();
+    copy_async_wait<kNormStages - 1>();
+#pragma unroll
+    for (int j = 0; j < kNormBackHeads; ++j) {
+      const bool there = has(now, j);
+      alignas(16) typename Lane::Raw raw;
+      float x[kC], w[kC];
+      l.take(norm_slot<2 * kNormBackHeads>(ring, stage, 2 * j), raw);
+      l.widen(raw, x);
+      l.take(norm_slot<2 * kNormBackHeads>(ring, stage, 2 * j + 1), raw);
+      l.widen(raw, w);
+      if (!there) {  // (what lies there is of an earlier batch, or nothing)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) x[i] = w[i] = 0.0f;
+      }
+      l.turn(a, sh, w);
+      float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        ss += x[i] * x[i];
+        dot += w[i] * l.g[i] * x[i];
+      }
+      ss = head_sum(ss, a.lanes);
+      dot = head_sum(dot, a.lanes);
+      const float r = inverse_root<T>(ss * part + a.eps);
+      const float b = dot * part * (r * r);
+#pragma unroll
+      for (int i = 0; i < kC; ++i) {
+        dg[i] += w[i] * (x[i] * r);
+        x[i] = r * (w[i] * l.g[i] - x[i] * b);
+      }
+      if (there)
+        l.store(static_cast<T*>(a.out) + now.row * a.ld_out +
+                    static_cast<long long>(first + now.batch * kNormBackHeads + j) * a.head_dim, x);
+    }
+    advance(now);
+    stage = stage + 1 == kNormStages ? 0 : stage + 1;
   }
   if (a.part == nullptr) return;
   // The CTA's sums: its groups' lanes by shuffles, then its warps through shared memory.
@@ -383,7 +451,7 @@ static NormArgs norm_args(const rf_norm_rope_desc* d, NormForm* form) {
 }
 
 template <class T, int kForm>
-static cudaError_t launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
+static rf_status launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
   // Heads per thread: as many as still leave two waves of threads, so that a small call spreads
   // over the GPU and a large one forms its angles once for many heads.
   const long long threads1 = static_cast<long long>(a.n_rows) * a.lanes;
@@ -391,36 +459,47 @@ static cudaError_t launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStr
   while (a.hpt < 16 && threads1 * a.n_heads / (2 * a.hpt) >= 4096LL * sms) a.hpt *= 2;
   const dim3 grid(static_cast<unsigned>((threads1 + kNormThreads - 1) / kNormThreads),
                   static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
-  return launch_dependent(k_norm_rope<T, kForm>, grid, dim3(kNormThreads), 0, s, 1, a, t);
+  static uint64_t done = 0;
+  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope<T, kForm>), norm_ring_bytes<kNormHeads>(), &done);
+  if (st != RF_OK) return st;
+  return cuda_check(launch_dependent(k_norm_rope<T, kForm>, grid, dim3(kNormThreads), norm_ring_bytes<kNormHeads>(), s, 1, a, t),
+                    "k_norm_rope launch");
 }
 template <class T>
-static cudaError_t launch_norm(NormArgs& a, const RopeTable& t, NormForm form, int sms, cudaStream_t s) {
+static rf_status launch_norm(NormArgs& a, const RopeTable& t, NormForm form, int sms, cudaStream_t s) {
   return form == kPieces ? launch_norm<T, kPieces>(a, t, sms, s)
          : form == kPairs ? launch_norm<T, kPairs>(a, t, sms, s)
                           : launch_norm<T, kShared>(a, t, sms, s);
 }
 
-// CTAs of the backward pass: two an SM, no more than there are heads to share out among their groups,
-// the query heads' and the key heads' in proportion. `hpt`: heads of a row that go together.
-static int norm_ctas(const NormArgs& a, int sms, int* hpt, int* q_ctas) {
+// CTAs of the backward pass: two an SM, no more than there are batches to share out among their groups, the query
+// heads' and the key heads' in proportion.
+static int norm_ctas(const NormArgs& a, int sms, int* q_ctas) {
   const int groups = kNormThreads / a.lanes;
   const long long most = std::min(2 * sms, kNormMaxCtas - 1);
-  const long long heads = static_cast<long long>(a.n_rows) * a.n_heads;
-  *hpt = heads >= 4 * most * groups ? 4 : 1;
-  auto needed = [&](long long h) { return (a.n_rows * ((h + *hpt - 1) / *hpt) + groups - 1) / groups; };
+  auto needed = [&](long long h) { return (a.n_rows * ((h + kNormBackHeads - 1) / kNormBackHeads) + groups - 1) / groups; };
   const int n_k = a.n_heads - a.n_q;
-  long long q = std::min<long long>(needed(a.n_q), std::max<long long>(a.n_q > 0, most * a.n_q / a.n_heads));
-  long long k = std::min<long long>(needed(n_k), std::max<long long>(n_k > 0, most - most * a.n_q / a.n_heads));
+  const long long q = std::min<long long>(needed(a.n_q), std::max<long long>(a.n_q > 0, most * a.n_q / a.n_heads));
+  const long long k = std::min<long long>(needed(n_k), std::max<long long>(n_k > 0, most - most * a.n_q / a.n_heads));
   *q_ctas = static_cast<int>(q);
   return static_cast<int>(q + k);
 }
 
+template <class T, int kForm>
+static rf_status launch_norm_backward(const NormArgs& a, const RopeTable& t, int ctas, cudaStream_t s) {
+  static uint64_t done = 0;
+  constexpr size_t bytes = norm_ring_bytes<2 * kNormBackHeads>();
+  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope_backward<T, kForm>), bytes, &done);
+  if (st != RF_OK) return st;
+  return cuda_check(launch_dependent(k_norm_rope_backward<T, kForm>, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), bytes, s,
+                                     1, a, t),
+                    "k_norm_rope_backward launch");
+}
 template <class T>
-static cudaError_t launch_norm_backward(const NormArgs& a, const RopeTable& t, NormForm form, int ctas, cudaStream_t s) {
-  void (*kernel)(NormArgs, RopeTable) = form == kPieces ? k_norm_rope_backward<T, kPieces>
-                                        : form == kPairs ? k_norm_rope_backward<T, kPairs>
-                                                         : k_norm_rope_backward<T, kShared>;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), 0, s, 1, a, t);
+static rf_status launch_norm_backward(const NormArgs& a, const RopeTable& t, NormForm form, int ctas, cudaStream_t s) {
+  return form == kPieces ? launch_norm_backward<T, kPieces>(a, t, ctas, s)
+         : form == kPairs ? launch_norm_backward<T, kPairs>(a, t, ctas, s)
+                          : launch_norm_backward<T, kShared>(a, t, ctas, s);
 }
 
 }  // namespace rf
@@ -452,9 +531,7 @@ extern "C" rf_status rf_norm_rope(const rf_norm_rope_desc* d, const void* in, co
   a.ld_in = d->rope.ld_in;
   a.ld_out = d->rope.ld_out;
   ProfScope prof(s, RF_STAGE_NORM_ROPE);
-  return cuda_check(d->rope.dtype == RF_BF16 ? launch_norm<__nv_bfloat16>(a, tab, form, sms, s)
-                                             : launch_norm<float>(a, tab, form, sms, s),
-                    "k_norm_rope launch");
+  return d->rope.dtype == RF_BF16 ? launch_norm<__nv_bfloat16>(a, tab, form, sms, s) : launch_norm<float>(a, tab, form, sms, s);
 }
 
 extern "C" size_t rf_norm_rope_backward_workspace_bytes(const rf_norm_rope_desc* d) {
@@ -501,12 +578,11 @@ extern "C" rf_status rf_norm_rope_backward(const rf_norm_rope_desc* d, const voi
   a.ld_in = d->rope.ld_in;
   a.ld_dy = d->rope.ld_out;
   a.ld_out = d->rope.ld_in;
-  const int ctas = norm_ctas(a, sms, &a.hpt, &a.q_ctas);
+  const int ctas = norm_ctas(a, sms, &a.q_ctas);
   if (ctas > 0) {
     ProfScope prof(s, RF_STAGE_NORM_ROPE);
-    st = cuda_check(d->rope.dtype == RF_BF16 ? launch_norm_backward<__nv_bfloat16>(a, tab, form, ctas, s)
-                                             : launch_norm_backward<float>(a, tab, form, ctas, s),
-                    "k_norm_rope_backward launch");
+    st = d->rope.dtype == RF_BF16 ? launch_norm_backward<__nv_bfloat16>(a, tab, form, ctas, s)
+                                  : launch_norm_backward<float>(a, tab, form, ctas, s);
     if (st != RF_OK) return st;
   }
   if (!sums) return RF_OK;

@@ -156,6 +156,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void* tmap,
       "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+// 16 bytes from global to shared memory, asynchronously; groups of such copies, in the order of their commits.
+__device__ __forceinline__ void copy_async16(uint32_t smem_dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most kLeft of this thread's groups are in flight.
+template <int kLeft>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 // Orders this thread's generic shared-memory writes before later async-proxy reads.
 __device__ __forceinline__ void fence_proxy_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
