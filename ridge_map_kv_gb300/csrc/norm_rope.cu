@@ -10,15 +10,20 @@
 // exchanged by shuffles and nothing is read twice. Channels' angles and gains are formed once
 // for the heads of a row. A thread's pieces of its next heads are on their way to shared memory
 // while it works on those that are there (asynchronous copies; each thread reads what it copied
-// itself, so there is no barrier). Three forms say which pieces those are:
+// itself, so there is no barrier); with the pieces loaded to registers instead the forward pass
+// took 151 us for 126 and the backward pass 69 for 60, as fewer bytes were in flight. Measured,
+// of bf16 heads of 128: 32,768 rows of 48 in 124 us (6.5 TB/s), 0.96 of a plain copy's rate; the
+// gradient of 8,191 rows of 40 in 54 us (4.6 TB/s), where issue slots share the bound (0.6 of
+// them used before its products were packed in pairs, 60 us); a step of 8 rows of 48 in 5 us,
+// which is a launch. Three forms say which pieces those are:
 //   kPieces   halves turn against each other and divide into pieces: a piece of the first half
 //             and its partner of the second, as in rf_rope
 //   kPairs    neighbouring channels turn against each other: any two pieces
 //   kShared   halves that do not divide into pieces: any two pieces, partners read from shared
 //             memory (16-byte accesses of global memory even so)
 //
-// The gains' gradients are sums over all rows: a thread keeps its channels' sums over its share
-// of rows, a CTA joins its threads' and leaves a row of partial sums in the workspace, and
+// The gains' gradients are sums over all rows: a thread keeps its channels' sums over its run of
+// heads, a CTA joins its threads' and leaves a row of partial sums in the workspace, and
 // k_gain_sum adds those in order. No atomics, so that the order, and the result, depends on the
 // sizes alone.
 #include <algorithm>
@@ -126,16 +131,29 @@ struct NormLane {
 #pragma unroll
     for (int p = 0; p < 2; ++p) *reinterpret_cast<uint4*>(v[p]) = ld_shared_v4(slot + p * kNormThreads * 16);
   }
+  // Zeros in the places of pieces that do not exist: nothing is copied there.
+  __device__ __forceinline__ void clear(uint32_t slot) const {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+      if (!ok[p]) st_shared_v4(slot + p * kNormThreads * 16, 0, 0, 0, 0);
+  }
   __device__ __forceinline__ void widen(const T (&v)[2][kVec], float (&x)[kChannels]) const {
 #pragma unroll
-    for (int i = 0; i < kChannels; ++i) x[i] = ok[i / kVec] ? to_f(v[i / kVec][i % kVec]) : 0.0f;
+    for (int i = 0; i < kChannels; ++i) x[i] = to_f(v[i / kVec][i % kVec]);
   }
   __device__ __forceinline__ void store(T* head, const float (&x)[kChannels]) const {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
       alignas(16) T v[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) from_f(v[i], x[p * kVec + i]);
+      for (int i = 0; i < kVec; i += 2) {
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<__nv_bfloat162*>(v + i) = __floats2bfloat162_rn(x[p * kVec + i], x[p * kVec + i + 1]);
+        } else {
+          v[i] = x[p * kVec + i];
+          v[i + 1] = x[p * kVec + i + 1];
+        }
+      }
       if (ok[p]) store_vec(head + start[p], v);
     }
   }
@@ -171,18 +189,55 @@ struct NormLane {
   }
 };
 
-// A thread's places for pieces in flight: `kHeads` heads (of one array) in each of kNormStages.
+// The same for a head in packed pairs of channels.
+template <class T, int kForm>
+__device__ __forceinline__ void turn_x2(const NormArgs& a, const NormLane<T, kForm>& l, float* sh, float2 (&x)[NormLane<T, kForm>::kChannels / 2]) {
+  constexpr int kHalf = NormLane<T, kForm>::kVec / 2;
+  if constexpr (kForm == kPieces) {
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) {
+      const float2 c = make_float2(l.c[2 * i], l.c[2 * i + 1]), s = make_float2(l.s[2 * i], l.s[2 * i + 1]);
+      const float2 x1 = x[i], x2 = x[kHalf + i];
+      x[i] = fma_x2(x1, c, mul_x2(x2, make_float2(-s.x, -s.y)));
+      x[kHalf + i] = fma_x2(x2, c, mul_x2(x1, s));
+    }
+  } else {
+    float y[4 * kHalf];
+#pragma unroll
+    for (int i = 0; i < 2 * kHalf; ++i) {
+      y[2 * i] = x[i].x;
+      y[2 * i + 1] = x[i].y;
+    }
+    l.turn(a, sh, y);
+#pragma unroll
+    for (int i = 0; i < 2 * kHalf; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+  }
+}
+
+// A thread's places for pieces in flight: `kHeads` heads (of one array) in each of kNormStages. Two stages carry both
+// passes: three or four change their times by less than 3%, or cost a small call its ramp (22 and 25 us for 20).
 constexpr int kNormStages = 2;
-template <int kHeads>
-constexpr size_t norm_ring_bytes() {
-  return static_cast<size_t>(kNormStages) * kHeads * 2 * kNormThreads * 16;
+constexpr size_t norm_ring_bytes(int heads) {
+  return static_cast<size_t>(kNormStages) * heads * 2 * kNormThreads * 16;
 }
 template <int kHeads>
 __device__ __forceinline__ uint32_t norm_slot(uint32_t ring, int stage, int j) {
   return ring + static_cast<uint32_t>(((stage * kHeads + j) * 2 * kNormThreads + static_cast<int>(threadIdx.x)) * 16);
 }
 
-// Sum over the lanes of a head.
+// Two neighbouring channels in fp32.
+__device__ __forceinline__ float2 pair_of(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* v) {
+  return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(v));
+}
+// Sums over the lanes of a head.
+__device__ __forceinline__ void head_sums(float& x, float& y, int lanes) {
+  for (int o = 1; o < lanes; o <<= 1) {
+    const float dx = __shfl_xor_sync(0xffffffffu, x, o), dy = __shfl_xor_sync(0xffffffffu, y, o);
+    x += dx;
+    y += dy;
+  }
+}
 __device__ __forceinline__ float head_sum(float x, int lanes) {
   for (int o = 1; o < lanes; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -194,7 +249,7 @@ __device__ __forceinline__ float inverse_root(float v) {
   else return __frcp_rn(__fsqrt_rn(v));
 }
 
-constexpr int kNormHeads = 4;  // heads of a batch
+constexpr int kNormHeads = 4;  // heads that a thread takes together
 
 template <class T, int kForm>
 __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_constant__ NormArgs a,
@@ -217,7 +272,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_cons
   const float part = 1.0f / static_cast<float>(a.head_dim);
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const uint32_t ring = smem_u32(norm_smem);
-  // Batches of up to kNormHeads heads that are all queries or all keys.
+  // Up to kNormHeads heads that are all queries or all keys.
   auto batch_end = [&](int h) { return min(h + kNormHeads, h < a.n_q ? min(h1, a.n_q) : h1); };
   int ahead = h0, filled = 0;  // the next batch to be copied, and its stage
   auto copy_next = [&] {
@@ -231,6 +286,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_cons
     copy_async_commit();
     filled = filled + 1 == kNormStages ? 0 : filled + 1;
   };
+#pragma unroll
+  for (int j = 0; j < kNormStages * kNormHeads; ++j) l.clear(norm_slot<kNormHeads>(ring, 0, j));
 #pragma unroll
   for (int i = 0; i < kNormStages - 1; ++i) copy_next();
   l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset, 1.0f);
@@ -297,7 +354,12 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
   const long long t0 = total * me / all_groups, t1 = total * (me + 1) / all_groups;
   const int turns = static_cast<int>((total + all_groups - 1) / all_groups);  // (every group of a warp makes as many)
   const float part = 1.0f / static_cast<float>(a.head_dim);
-  float dg[kC] = {};
+  float2 g[kC / 2], dg[kC / 2];
+#pragma unroll
+  for (int i = 0; i < kC / 2; ++i) {
+    g[i] = make_float2(l.g[2 * i], l.g[2 * i + 1]);
+    dg[i] = make_float2(0.0f, 0.0f);
+  }
   extern __shared__ __align__(16) uint8_t norm_smem[];
   const uint32_t ring = smem_u32(norm_smem);
   struct Spot {  // a batch: its place in the run, its row and place in the row
@@ -329,6 +391,8 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
     filled = filled + 1 == kNormStages ? 0 : filled + 1;
   };
 #pragma unroll
+  for (int j = 0; j < kNormStages * 2 * kNormBackHeads; ++j) l.clear(norm_slot<2 * kNormBackHeads>(ring, 0, j));
+#pragma unroll
   for (int i = 0; i < kNormStages - 1; ++i) copy_next();
   for (int i = 0; i < turns; ++i) {
     copy_next();
@@ -340,34 +404,41 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
     for (int j = 0; j < kNormBackHeads; ++j) {
       const bool there = has(now, j);
       alignas(16) typename Lane::Raw raw;
-      float x[kC], w[kC];
+      float2 x[kC / 2], w[kC / 2];
       l.take(norm_slot<2 * kNormBackHeads>(ring, stage, 2 * j), raw);
-      l.widen(raw, x);
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) x[i] = pair_of(&raw[0][0] + 2 * i);
       l.take(norm_slot<2 * kNormBackHeads>(ring, stage, 2 * j + 1), raw);
-      l.widen(raw, w);
+#pragma unroll
+      for (int i = 0; i < kC / 2; ++i) w[i] = pair_of(&raw[0][0] + 2 * i);
       if (!there) {  // (what lies there is of an earlier batch, or nothing)
 #pragma unroll
-        for (int i = 0; i < kC; ++i) x[i] = w[i] = 0.0f;
+        for (int i = 0; i < kC / 2; ++i) x[i] = w[i] = make_float2(0.0f, 0.0f);
       }
-      l.turn(a, sh, w);
-      float ss = 0.0f, dot = 0.0f;
+      turn_x2(a, l, sh, w);
+      float2 ss2 = make_float2(0.0f, 0.0f), dot2 = ss2;
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        ss += x[i] * x[i];
-        dot += w[i] * l.g[i] * x[i];
+      for (int i = 0; i < kC / 2; ++i) {
+        ss2 = fma_x2(x[i], x[i], ss2);
+        dot2 = fma_x2(mul_x2(w[i], g[i]), x[i], dot2);
       }
-      ss = head_sum(ss, a.lanes);
-      dot = head_sum(dot, a.lanes);
+      float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
+      head_sums(ss, dot, a.lanes);
       const float r = inverse_root<T>(ss * part + a.eps);
-      const float b = dot * part * (r * r);
+      const float b = dot * part * (r * r) * r;
+      const float2 rr = make_float2(r, r), bb = make_float2(-b, -b);
+      float y[kC];
 #pragma unroll
-      for (int i = 0; i < kC; ++i) {
-        dg[i] += w[i] * (x[i] * r);
-        x[i] = r * (w[i] * l.g[i] - x[i] * b);
+      for (int i = 0; i < kC / 2; ++i) {
+        const float2 u = mul_x2(w[i], rr);
+        dg[i] = fma_x2(u, x[i], dg[i]);
+        const float2 v = fma_x2(u, g[i], mul_x2(x[i], bb));
+        y[2 * i] = v.x;
+        y[2 * i + 1] = v.y;
       }
       if (there)
         l.store(static_cast<T*>(a.out) + now.row * a.ld_out +
-                    static_cast<long long>(first + now.batch * kNormBackHeads + j) * a.head_dim, x);
+                    static_cast<long long>(first + now.batch * kNormBackHeads + j) * a.head_dim, y);
     }
     advance(now);
     stage = stage + 1 == kNormStages ? 0 : stage + 1;
@@ -376,13 +447,16 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
   // The CTA's sums: its groups' lanes by shuffles, then its warps through shared memory.
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < kC; ++i)
-    for (int o = a.lanes; o < 32; o <<= 1) dg[i] += __shfl_xor_sync(0xffffffffu, dg[i], o);
+  for (int i = 0; i < kC / 2; ++i)
+    for (int o = a.lanes; o < 32; o <<= 1) {
+      dg[i].x += __shfl_xor_sync(0xffffffffu, dg[i].x, o);
+      dg[i].y += __shfl_xor_sync(0xffffffffu, dg[i].y, o);
+    }
   __syncthreads();
   if (lane < a.lanes) {
 #pragma unroll
     for (int i = 0; i < kC; ++i)
-      if (l.ok[i / Lane::kVec]) staged[warp * 256 + l.start[i / Lane::kVec] + i % Lane::kVec] = dg[i];
+      if (l.ok[i / Lane::kVec]) staged[warp * 256 + l.start[i / Lane::kVec] + i % Lane::kVec] = i & 1 ? dg[i / 2].y : dg[i / 2].x;
   }
   __syncthreads();
   for (int ch = threadIdx.x; ch < a.head_dim; ch += kNormThreads) {
@@ -460,9 +534,9 @@ static rf_status launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStrea
   const dim3 grid(static_cast<unsigned>((threads1 + kNormThreads - 1) / kNormThreads),
                   static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
   static uint64_t done = 0;
-  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope<T, kForm>), norm_ring_bytes<kNormHeads>(), &done);
+  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope<T, kForm>), norm_ring_bytes(kNormHeads), &done);
   if (st != RF_OK) return st;
-  return cuda_check(launch_dependent(k_norm_rope<T, kForm>, grid, dim3(kNormThreads), norm_ring_bytes<kNormHeads>(), s, 1, a, t),
+  return cuda_check(launch_dependent(k_norm_rope<T, kForm>, grid, dim3(kNormThreads), norm_ring_bytes(kNormHeads), s, 1, a, t),
                     "k_norm_rope launch");
 }
 template <class T>
@@ -488,7 +562,7 @@ static int norm_ctas(const NormArgs& a, int sms, int* q_ctas) {
 template <class T, int kForm>
 static rf_status launch_norm_backward(const NormArgs& a, const RopeTable& t, int ctas, cudaStream_t s) {
   static uint64_t done = 0;
-  constexpr size_t bytes = norm_ring_bytes<2 * kNormBackHeads>();
+  constexpr size_t bytes = norm_ring_bytes(2 * kNormBackHeads);
   const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope_backward<T, kForm>), bytes, &done);
   if (st != RF_OK) return st;
   return cuda_check(launch_dependent(k_norm_rope_backward<T, kForm>, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), bytes, s,
