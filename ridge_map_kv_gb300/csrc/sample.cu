@@ -446,10 +446,10 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     return p >= lo && p <= hi;
   };
   if (in > kListed) {
-    // The bin's places, a little wider than it is.
-    const float step = temperature * (0.693147181f / 64.0f);
+    // The bin's places, a little wider than it is. (The last bin begins at kTail, half a bin early.)
+    const float step = temperature * (0.693147181f / 64.0f), begin = static_cast<float>(bin) - (bin == kBins - 1 ? 1.0f : 0.5f);
     const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(bin + 1));
-    const float high = r.scale.m - step * (static_cast<float>(bin) - 0.5f) + slack, low = r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack;
+    const float high = r.scale.m - step * begin + slack, low = r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack;
     lo = place_of<kExact>(fminf(high, r.scale.m), 0);
     hi = place_of<kExact>(bin == kBins - 1 ? -FLT_MAX : fmaxf(low, -FLT_MAX), kSampleMaxVocab - 1);
   }

@@ -140,6 +140,20 @@ def test_sample_matches_its_definition(kind, V, dtype):
         _check_row(V, x[r], T[r], k[r], p[r], mp[r], P[r], tok[r], lp[r], cnt[r], noise[r], True)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sample_borders_among_many_equal_tokens_where_the_last_bin_begins(dtype):
+    """2,000 tokens 31.9725 octaves below the first, 3,000 twice as far: runs that end among them."""
+    V = 8192
+    x = torch.full((3, V), -math.inf, device="cuda", dtype=dtype)
+    x[:, 17] = 0.0
+    x[:, 100:2100] = -16.0
+    x[:, 3000:6000] = -32.0
+    T, k, p, mp = [16.0 * math.log2(math.e) / 31.9725] * 3, [1500, 2001, 4500], [1.0] * 3, [0.0] * 3
+    P, tok, lp, cnt, st, noise = _run(x, T, k, p, mp)
+    for r in range(3):
+        _check_row(V, x[r], T[r], k[r], p[r], mp[r], P[r], tok[r], lp[r], cnt[r], noise[r], True)
+
+
 @pytest.mark.parametrize("R,V,pad,ldp", [(1, 1 << 20, 0, 0), (3, 100003, 5, 100010), (40, 5001, 1, 5001), (170, 3001, 0, 3004),
                                          (700, 257, 3, 257), (1, 2049, 7, 2050)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
