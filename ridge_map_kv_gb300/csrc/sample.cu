@@ -22,8 +22,11 @@
 //             pairs narrow them down). A pass over all then adds up the weights that stay and draws, another
 //             writes probabilities.
 //
-// Bound: the logits' bytes (and the probabilities'), beside some 30 operations a token where masses
-// are formed.
+// Bound: the logits' bytes (and the probabilities') from memory are the floor, but instructions bound what is
+// here: some 30 a token where masses are formed, and as many where weights and scores are, 90 of a row with a
+// nucleus. Measured: one row of 32,000 in 12 to 17 us by its filters, of which some ten barriers of a cluster
+// are most; 64 bf16 rows of 131,072 with nuclei in 50 us; 256 fp32 rows of 131,072 with every filter and their
+// probabilities in 154 us (1.7 TB/s); 48 unfiltered rows of 100,003 with theirs in 32 us (1.8 TB/s).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -47,6 +50,9 @@ constexpr int kListed = 1024;         // tokens that are sorted at most
 constexpr int kFewTokens = 128;       // top-k up to which tokens are listed at once: G groups leave about
                                       // G (ln G + 0.6) tokens, some 700 of 128
 constexpr int kSampleMaxVocab = 1 << 20;
+constexpr unsigned kSparse = 32;      // where more than one token in so many stays, the noise is read along with the
+                                      // logits; below that only at the tokens that stay, each a wait of its own (64
+                                      // bf16 rows of 131,072 with nuclei: 56 us that way for all, 50 with this rule)
 constexpr int kMassBits = 29;         // a weight of 1, within its bin
 constexpr int kCommonBits = 42;       // a weight of 1, over all bins
 constexpr int kCountShift = 44;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
@@ -146,12 +152,18 @@ __device__ __forceinline__ unsigned long long common_mass(const unsigned long lo
   return __umul64hi(mass << (kCommonBits - kMassBits + 1), power[bin & 63]) >> (bin >> 6);
 }
 
+// A logit of a row whose maximum is +inf, as the filters see it.
+__device__ __forceinline__ float infinite(float x) { return x == INFINITY ? 0.0f : -INFINITY; }
+
 // f(first token, values, others) for the tokens v0 <= i < v1 of a row: 16 bytes at a time between the row's
-// first and last 16-byte boundaries, one token at a time outside them. A thread's tokens rise. `other`: a
-// second row that is read along with the first (kOther).
+// first and last 16-byte boundaries, one token at a time outside them; the next pieces are on their way while f
+// works on the last ones, so that its code stands here twice and not once for each piece in flight (four pieces
+// loaded at a time, and f unrolled for them, took 5% longer). A thread's tokens rise. `other`: a
+// second row that is read along with the first (kOther). `top_inf` as in Row. NaN comes as it is: it fails every
+// comparison.
 template <bool kOther, class T, class F>
-__device__ __forceinline__ void for_both(const T* row, const float* other, int v0, int v1, F f) {
-  constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kBatch = kOther ? 8 / kVec : 4;
+__device__ __forceinline__ void for_both(const T* row, const float* other, bool top_inf, int v0, int v1, F f) {
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T)), kBatch = kOther ? 1 : 2;
   const int tid = threadIdx.x;
   const int off = static_cast<int>((reinterpret_cast<uintptr_t>(row + v0) & 15u) / sizeof(T));
   const int head = min(v1 - v0, (kVec - off) % kVec);
@@ -160,30 +172,42 @@ __device__ __forceinline__ void for_both(const T* row, const float* other, int v
     if constexpr (sizeof(T) == 2) x[0] = __bfloat162float(row[i]);
     else x[0] = row[i];
     if constexpr (kOther) e[0] = other[i];
+    if (top_inf) x[0] = infinite(x[0]);
     f(i, x, e);
   };
   if (tid < head) one(v0 + tid);
   const int first = v0 + head, pieces = (v1 - first) / kVec;
   const bool even = (reinterpret_cast<uintptr_t>(other + first) & 15u) == 0;
-  for (int p0 = tid; p0 < pieces; p0 += kBatch * kSampleThreads) {
-    uint4 raw[kBatch];
-    alignas(16) float e[kBatch][kOther ? kVec : 1];
+  uint4 raw[kBatch] = {}, next[kBatch] = {};
+  alignas(16) float e[kBatch][kOther ? kVec : 1], after[kBatch][kOther ? kVec : 1];
+  auto load = [&](int p0) {
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int p = p0 + j * kSampleThreads;
       if (p >= pieces) break;
-      raw[j] = reinterpret_cast<const uint4*>(row + first)[p];
+      next[j] = reinterpret_cast<const uint4*>(row + first)[p];
       if constexpr (kOther) {
         const float* o = other + first + p * kVec;
         if (even) {
 #pragma unroll
-          for (int k = 0; k < kVec; k += 4) *reinterpret_cast<float4*>(e[j] + k) = *reinterpret_cast<const float4*>(o + k);
+          for (int k = 0; k < kVec; k += 4) *reinterpret_cast<float4*>(after[j] + k) = *reinterpret_cast<const float4*>(o + k);
         } else {
 #pragma unroll
-          for (int k = 0; k < kVec; ++k) e[j][k] = o[k];
+          for (int k = 0; k < kVec; ++k) after[j][k] = o[k];
         }
       }
     }
+  };
+  load(tid);
+#pragma unroll 1
+  for (int p0 = tid; p0 < pieces; p0 += kBatch * kSampleThreads) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      raw[j] = next[j];
+#pragma unroll
+      for (int k = 0; k < (kOther ? kVec : 1); ++k) e[j][k] = after[j][k];
+    }
+    load(p0 + kBatch * kSampleThreads);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (p0 + j * kSampleThreads >= pieces) break;
@@ -194,6 +218,10 @@ __device__ __forceinline__ void for_both(const T* row, const float* other, int v
         if constexpr (sizeof(T) == 2) x[k] = u2f(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
         else x[k] = u2f(w[k]);
       }
+      if (top_inf) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) x[k] = infinite(x[k]);
+      }
       f(first + (p0 + j * kSampleThreads) * kVec, x, e[j]);
     }
   }
@@ -201,8 +229,8 @@ __device__ __forceinline__ void for_both(const T* row, const float* other, int v
   if (last < v1) one(last);
 }
 template <class T, class F>
-__device__ __forceinline__ void for_tokens(const T* row, int v0, int v1, F f) {
-  for_both<false>(row, nullptr, v0, v1, [&](int i, const auto& x, const auto&) { f(i, x); });
+__device__ __forceinline__ void for_tokens(const T* row, bool top_inf, int v0, int v1, F f) {
+  for_both<false>(row, nullptr, top_inf, v0, v1, [&](int i, const auto& x, const auto&) { f(i, x); });
 }
 
 struct SampleShared {
@@ -237,12 +265,6 @@ struct Row {
   bool top_inf;  // the maximum is +inf: those tokens share all weight, as if theirs were 0 and all others' -inf
   int turn;
 };
-
-// A logit as the filters see it: NaN as -inf.
-__device__ __forceinline__ float seen(const Row& r, float x) {
-  x = fmaxf(x, -INFINITY);
-  return r.top_inf ? (x == INFINITY ? 0.0f : -INFINITY) : x;
-}
 
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
 #pragma unroll
@@ -384,9 +406,11 @@ __device__ __forceinline__ void clear_table(SampleTables& t) {
   __syncthreads();
 }
 
-// Where a run ends: its last token's place, and the mass up to there, the token's own included.
+// Where a run ends: its last token's place, the mass up to there, the token's own included, and the count of tokens
+// up to the end of that token's bin.
 struct End {
   unsigned long long place, mass;
+  unsigned about;
 };
 
 // The end of the run of `target` tokens (kByMass false), or of the shortest run of mass `target`, from the
@@ -435,34 +459,33 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
   find_bin(t.all, -1, 0);
   const int bin = static_cast<int>(sh.found_bin);
   unsigned in = sh.found_in;
+  const unsigned about = sh.found_count + in;
   const unsigned long long base = sh.found_mass;  // of the bins before, in common units
   target -= kByMass ? base : sh.found_count;      // from here on within the bin
   unsigned long long inside = 0;                  // mass of the bin before the range below
-  unsigned long long lo = 0, hi = ~0ull;
+  // The bin's logits, a little wider than it is, so that most others fall out by a comparison. (The last bin begins at
+  // kTail, half a bin early.)
+  const float step = temperature * (0.693147181f / 64.0f), begin = static_cast<float>(bin) - (bin == kBins - 1 ? 1.0f : 0.5f);
+  const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(bin + 1));
+  const float high = fminf(r.scale.m - step * begin + slack, r.scale.m);
+  const float low = bin == kBins - 1 ? -FLT_MAX : fmaxf(r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack, -FLT_MAX);
+  unsigned long long lo = place_of<kExact>(high, 0), hi = place_of<kExact>(low, kSampleMaxVocab - 1);
   auto place_in = [&](float x, int i, unsigned long long& p, float& away, float& away_lo) {
+    if (!(x >= low && x <= high)) return false;
     distance<kExact>(r.scale, x, away, away_lo);
-    if (bin_of(away) != bin || !(x > -INFINITY)) return false;
     p = place_of<kExact>(x, i);
-    return p >= lo && p <= hi;
+    return bin_of(away) == bin && p >= lo && p <= hi;
   };
-  if (in > kListed) {
-    // The bin's places, a little wider than it is. (The last bin begins at kTail, half a bin early.)
-    const float step = temperature * (0.693147181f / 64.0f), begin = static_cast<float>(bin) - (bin == kBins - 1 ? 1.0f : 0.5f);
-    const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(bin + 1));
-    const float high = r.scale.m - step * begin + slack, low = r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack;
-    lo = place_of<kExact>(fminf(high, r.scale.m), 0);
-    hi = place_of<kExact>(bin == kBins - 1 ? -FLT_MAX : fmaxf(low, -FLT_MAX), kSampleMaxVocab - 1);
-  }
   while (in > kListed) {
     const int width = 64 - __clzll(static_cast<long long>(hi - lo));
     const int shift = max(0, width - 11);
     clear_table(t);
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+    for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
         unsigned long long p;
         float away, away_lo;
-        if (place_in(seen(r, x[e]), i + e, p, away, away_lo)) add_to(t, static_cast<int>((p - lo) >> shift), 1, part_of(away, away_lo));
+        if (place_in(x[e], i + e, p, away, away_lo)) add_to(t, static_cast<int>((p - lo) >> shift), 1, part_of(away, away_lo));
       }
     });
     join_tables(cl, t, t.finer, r, true);
@@ -476,12 +499,12 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
   __syncthreads();
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
-  for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+  for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
     for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
       unsigned long long p;
       float away, away_lo;
-      if (place_in(seen(r, x[e]), i + e, p, away, away_lo)) {
+      if (place_in(x[e], i + e, p, away, away_lo)) {
         const int at = atomicAdd(&sh.n_list, 1);
         if (at < kListed) t.own_place[at] = p;
       }
@@ -519,7 +542,7 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     m = m1;
   }
   __syncthreads();
-  const End end{sh.found_place, base + common_mass(sh.power, inside + sh.found_mass, bin)};
+  const End end{sh.found_place, base + common_mass(sh.power, inside + sh.found_mass, bin), about};
   __syncthreads();
   return end;
 }
@@ -560,17 +583,22 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   const bool good = (temperature == 0.0f || (temperature >= 0x1p-100f && temperature <= 0x1p100f)) && top_k >= 0 &&
                     top_p >= 0.0f && min_p >= 0.0f && min_p <= 1.0f;
 
-  // The maximum and its lowest token; the threads' maxima.
+  // The threads' maxima; at temperature 0, where nothing else is done, with their lowest tokens.
   float top = -INFINITY;
   int top_i = 0;
-  if (good)
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+  if (temperature == 0.0f && good)
+    for_tokens(row, false, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e)
         if (x[e] > top) {
           top = x[e];
           top_i = i + e;
         }
+    });
+  else if (good)
+    for_tokens(row, false, r.v0, r.v1, [&](int, const auto& x) {
+#pragma unroll
+      for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) top = fmaxf(top, x[e]);
     });
   if (min_p > 0.0f && tid == kSampleThreads - 1) sh.min_away = static_cast<double>(temperature) * log(static_cast<double>(min_p));
   const unsigned long long mine =
@@ -633,9 +661,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     }
     return;
   }
-  const int first = token_of(best);
   r.scale.m = key_value(static_cast<unsigned>(best >> 32));
   if (temperature == 0.0f) {
+    const int first = token_of(best);
     zero_probs();
     __syncthreads();
     if (probs != nullptr && tid == 0 && first >= r.v0 && first < r.v1) probs[first] = 1.0f;
@@ -674,15 +702,14 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   // Few tokens: list what reaches the least group's maximum.
   int n = 0;
   if (groups > 0 && least > rising_key(-INFINITY)) {
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+    const float from = key_value(least);
+    for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
-      for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-        const float y = seen(r, x[e]);
-        if (rising_key(y) >= least) {
+      for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e)
+        if (x[e] >= from) {
           const int at = atomicAdd(&sh.n_list, 1);
-          if (at < kListed) t.own_place[at] = place_of<kExact>(y, i + e);
+          if (at < kListed) t.own_place[at] = place_of<kExact>(x[e], i + e);
         }
-      }
     });
     if (join_lists(cl, sh, t, r, &n)) {
       sort_list(t, n);
@@ -740,17 +767,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   // Any number of tokens. The last one that stays, by logit and token:
   float last = -INFINITY;
   int last_i = -1;
+  unsigned about = static_cast<unsigned>(a.vocab);  // of them
   if ((top_k > 0 && top_k < a.vocab) || top_p < 1.0f) {
     clear_table(t);
     unsigned long long tail = 0;
-    for_tokens(row, r.v0, r.v1, [&](int, const auto& x) {
+    for_tokens(row, r.top_inf, r.v0, r.v1, [&](int, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-        const float y = seen(r, x[e]);
         float hi, lo;
-        distance<kExact>(r.scale, y, hi, lo);
+        distance<kExact>(r.scale, x[e], hi, lo);
         if (hi < kTail) add_to(t, near_bin(hi), 1, bin_part(hi, lo));
-        else if (y > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi);  // (many share the last bin)
+        else if (x[e] > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi);  // (many share the last bin)
       }
     });
 #pragma unroll
@@ -782,30 +809,33 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       valid += sh.warp_count[w];
       all += sh.warp_sum[w];
     }
-    End end{~0ull, all};
+    End end{~0ull, all, valid};
     if (top_k > 0 && static_cast<unsigned>(top_k) < valid) end = find_end<false>(cl, sh, t, r, row, temperature, top_k);
     if (top_p < 1.0f) {
       const End by_mass = find_end<true>(cl, sh, t, r, row, temperature, mass_target(top_p, end.mass));
       end.place = min(end.place, by_mass.place);
+      end.about = min(end.about, by_mass.about);
     }
     if (end.place != ~0ull) {
       last = place_value<kExact>(end.place);
       last_i = place_token(end.place);
+      about = end.about;
     }
   }
   if (lowest > last) {
     last = lowest;
     last_i = kSampleMaxVocab;
+    about = 0;  // (unknown)
   }
   auto stays = [&](float x, int i) { return x > last || (x == last && i <= last_i); };
   float total = 0.0f, leader = -1.0f;  // the greatest score and its token: the lowest, as a thread's tokens rise
   unsigned kept = 0;
   int lead_i = 0;
-  auto count_in = [&](int i, const auto& y, const auto& e) {
+  auto count_in = [&](int i, const auto& x, const auto& e) {
 #pragma unroll
-    for (int j = 0; j < static_cast<int>(sizeof(y) / sizeof(float)); ++j)
-      if (stays(y[j], i + j)) {
-        const float w = weight_of<kExact>(r.scale, y[j]);
+    for (int j = 0; j < static_cast<int>(sizeof(x) / sizeof(float)); ++j)
+      if (stays(x[j], i + j)) {
+        const float w = weight_of<kExact>(r.scale, x[j]);
         total += w;
         ++kept;
         const float score = score_of(w, e[j]);
@@ -815,28 +845,18 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         }
       }
   };
-  if (noise != nullptr && last == -INFINITY) {  // nothing is filtered out: the noise comes along with the logits
-    for_both<true>(row, noise, r.v0, r.v1, [&](int i, const auto& x, const auto& e) {
-      constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
-      float y[kN];
-#pragma unroll
-      for (int j = 0; j < kN; ++j) y[j] = seen(r, x[j]);
-      count_in(i, y, e);
-    });
+  if (noise != nullptr && about > static_cast<unsigned>(a.vocab) / kSparse) {  // the noise comes along with the logits
+    for_both<true>(row, noise, r.top_inf, r.v0, r.v1, count_in);
   } else {
-    for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+    for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
       constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
-      float y[kN], e[kN];
-      bool any = false;
+      float e[kN], top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) {
-        y[j] = seen(r, x[j]);
-        any |= stays(y[j], i + j);
-      }
-      if (!any) return;
+      for (int j = 0; j < kN; ++j) top = fmaxf(top, x[j]);
+      if (!(top >= last)) return;
 #pragma unroll
-      for (int j = 0; j < kN; ++j) e[j] = noise != nullptr && stays(y[j], i + j) ? noise[i + j] : 1.0f;
-      count_in(i, y, e);
+      for (int j = 0; j < kN; ++j) e[j] = noise != nullptr && stays(x[j], i + j) ? noise[i + j] : 1.0f;
+      count_in(i, x, e);
     });
   }
 #pragma unroll
@@ -873,23 +893,24 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     best = max(best, sh.best[r.turn & 1][c]);
   }
   // The CTA that holds the token answers: its logit is read before probabilities are written over it.
-  const int token = a.token != nullptr ? token_of(best) : first;
-  if (tid == 0 && token >= r.v0 && token < r.v1) {
-    float x;
-    if constexpr (kExact) x = __bfloat162float(row[token]);
-    else x = row[token];
-    answer(token, logprob_of(seen(r, x), total), static_cast<int>(kept));
+  const int token = token_of(best);
+  if (tid == 0 && (a.token != nullptr ? token >= r.v0 && token < r.v1 : r.rank == 0)) {
+    float x = r.scale.m;
+    if (a.token != nullptr && !r.top_inf) {
+      if constexpr (kExact) x = __bfloat162float(row[token]);
+      else x = row[token];
+    }
+    answer(token, logprob_of(x, total), static_cast<int>(kept));
   }
   if (probs == nullptr) return;
   __syncthreads();
   const float inverse = 1.0f / total;
-  for_tokens(row, r.v0, r.v1, [&](int i, const auto& x) {
+  for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
     constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
     float p[kN];
 #pragma unroll
     for (int e = 0; e < kN; ++e) {
-      const float y = seen(r, x[e]);
-      p[e] = stays(y, i + e) ? weight_of<kExact>(r.scale, y) * inverse : 0.0f;
+      p[e] = stays(x[e], i + e) ? weight_of<kExact>(r.scale, x[e]) * inverse : 0.0f;
     }
     if (kN % 4 == 0 && (reinterpret_cast<uintptr_t>(probs + i) & 15u) == 0) {
 #pragma unroll
