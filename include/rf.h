@@ -1,8 +1,9 @@
 /*
  * rf.h — C ABI of librf.so: the RidgeFill upper-layer KV fill, its calibration
  * statistics and closed-form ridge solve, the cross-model per-head ridge
- * mapper, and the operators that decode from a filled cache (rotation, attention
- * of drafted trees, verification, eviction), for one NVIDIA GB300 (sm_103a).
+ * mapper, and the operators that decode from a filled cache (norms and rotation of
+ * queries and keys, attention of drafted trees over one sequence's cache or a shared
+ * prefix, sampling, verification, eviction), for one NVIDIA GB300 (sm_103a).
  *
  * Sources cited below:
  *   [RF] RidgeFill review (jaehun.me, English edition of the review of arXiv
@@ -686,12 +687,13 @@ typedef struct rf_prefix_attn_desc {
  * rows:
  *   S = {prefix rows t < *prefix_len} + {cache rows t < lens[b]} + {drafted rows j that node i sees}.
  * The prefix is held once and read once for all sequences, whose rows make up its matrix products, so a
- * batch costs about what one sequence does up to 256 query rows per KV head. Own caches may be empty
- * (lens[b] = 0), and so may the prefix.
+ * prefix costs a batch about what it costs one sequence, up to 256 query rows per KV head. Own caches may
+ * be empty (lens[b] = 0), and so may the prefix.
  *   prefix_len  device int32; outside [0, prefix_capacity] it records RF_ERR_INVALID_ARG and nothing is
  *               written
  * All other arguments, masks, what is not seen, refusals and the status of lengths as for
- * rf_tree_attention. Scores, statistics and sums are fp32, joined in a fixed order. */
+ * rf_tree_attention; an infinity in a V row that is seen may come out as NaN. Scores, statistics and sums are
+ * fp32, joined in a fixed order. */
 size_t rf_prefix_attn_workspace_bytes(const rf_prefix_attn_desc* desc);
 rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const rf_bf16* q,
                               const rf_bf16* k_prefix, const rf_bf16* v_prefix, const int32_t* prefix_len,

@@ -1,4 +1,5 @@
-// Attention of drafted rows over a cache and over each other (rf_tree_attention).
+// Attention of drafted rows over a cache and over each other (rf_tree_attention), and over a prefix that
+// all sequences share besides (rf_prefix_attention).
 //
 // out = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q.k_j - m): one pass over the keys with
 // a running maximum m and sum per query row. The G query heads of a KV head share its
@@ -51,6 +52,17 @@
 // stream. A shorter softmax does not change that (weights formed against the last maximum while
 // the tile's own is taken: 1.87 ms), nor do sums behind the hand-over (1.89 ms) or streams
 // without turns (2.33 ms).
+//
+// With a shared prefix, softmax sums are joined over two sets of keys: the prefix, as one more sequence whose
+// rows are those of all sequences, so that its keys are read once and serve one matrix product; and each
+// sequence's own. Bound: the bytes of the prefix and of all own rows up to some 275 query rows per KV head (all
+// sequences together), the products over the prefix beyond. See PrefixArgs, and k_attn where it forms pairs of heads
+// and copies of few rows. Measured (128 channels, 8 KV heads): 4 sequences of one token, 5 query heads on one, over
+// 32,767 shared rows and up to 200 of their own: 37 us (3.7 TB/s; 20 would be the bytes). 64 of one token, 4 on
+// one, over 16,384 and up to 1,024: 63 us (3.2 TB/s, 30). 16 trees of 64 nodes, 4 on one, over 28,672 and up to
+// 300: 370 us from rest, 406 in long runs (1,190 TFLOP/s, 256 at the burst rate). 100 times three rows, 10 on one of 2
+// heads of 64 channels, over 4,099 and up to 4,000: 56 us (1.9 TB/s, 16). One sequence's cache at a time, the prefix in
+// each, would read the prefix 64 times in the second case.
 #include <algorithm>
 #include <cmath>
 
@@ -1505,8 +1517,12 @@ static rf_status launch_attn(const Args& a, int ctas, cudaStream_t s) {
   // places in the order in which these finish, and the ones with the prefix's products then end up side by side (64
   // sequences over 16,384 shared rows: 72 us as dependents, 63 so).
   if (Args::kPrefix && kDual) {
-    k_attn<kHD, kDual, Args><<<dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s>>>(a);
-    return cuda_check(cudaGetLastError(), "k_attn launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kAtThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
+    cfg.stream = s;
+    return cuda_check(cudaLaunchKernelEx(&cfg, k_attn<kHD, kDual, Args>, a), "k_attn launch");
   }
   return cuda_check(launch_dependent(k_attn<kHD, kDual, Args>, dim3(static_cast<unsigned>(ctas)), dim3(kAtThreads), Cfg::kSmem, s, 1, a),
                     "k_attn launch");
