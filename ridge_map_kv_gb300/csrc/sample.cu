@@ -50,9 +50,10 @@ constexpr int kListed = 1024;         // tokens that are sorted at most
 constexpr int kFewTokens = 128;       // top-k up to which tokens are listed at once: G groups leave about
                                       // G (ln G + 0.6) tokens, some 700 of 128
 constexpr int kSampleMaxVocab = 1 << 20;
-constexpr unsigned kSparse = 32;      // where more than one token in so many stays, the noise is read along with the
+constexpr unsigned kSparse = 64;      // where more than one token in so many stays, the noise is read along with the
                                       // logits; below that only at the tokens that stay, each a wait of its own (64
-                                      // bf16 rows of 131,072 with nuclei: 56 us that way for all, 50 with this rule)
+                                      // bf16 rows of 131,072 with nuclei: 51 us that way for all, 44.5 with this
+                                      // rule, 46 with 32 for 64 and 52 with 4)
 constexpr int kMassBits = 29;         // a weight of 1, within its bin
 constexpr int kCommonBits = 42;       // a weight of 1, over all bins
 constexpr int kCountShift = 44;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
@@ -294,10 +295,12 @@ __device__ __forceinline__ void before_sums(SampleShared& sh, unsigned& count, u
   __syncthreads();
   unsigned c0 = 0;
   unsigned long long m0 = 0;
-  for (int w = 0; w < warp; ++w) {
-    c0 += sh.warp_count[w];
-    m0 += sh.warp_sum[w];
-  }
+#pragma unroll
+  for (int w = 0; w < kSampleWarps - 1; ++w)
+    if (w < warp) {
+      c0 += sh.warp_count[w];
+      m0 += sh.warp_sum[w];
+    }
   count = c0 + c - count;
   mass = m0 + m - mass;
 }
@@ -377,6 +380,10 @@ __device__ __forceinline__ void add_to(SampleTables& t, int bin, unsigned count,
   if (atomicAdd(&t.low[bin], part) > ~part) atomicAdd(&t.high[bin], 1u);
 }
 
+__device__ __forceinline__ unsigned long long own_entry(const SampleTables& t, int bin) {
+  return (static_cast<unsigned long long>(t.count[bin]) << kCountShift) + (static_cast<unsigned long long>(t.high[bin]) << 32) + t.low[bin];
+}
+
 // The CTAs' tables, summed over the cluster (a power of two of CTAs): each CTA sends the others their parts of its
 // bins, sums the part that it gets and sends that to all. Stores to other CTAs' shared memory do not wait, as loads
 // do. The parts arrive where the lists are otherwise: `again` if another CTA may still be reading one.
@@ -388,9 +395,7 @@ __device__ __forceinline__ void join_tables(cg::cluster_group& cl, SampleTables&
 #pragma unroll
   for (int i = 0; i < kBins / kSampleThreads; ++i) {
     const int bin = static_cast<int>(threadIdx.x) + i * kSampleThreads, to = bin / per;
-    const unsigned long long e = (static_cast<unsigned long long>(t.count[bin]) << kCountShift) +
-                                 (static_cast<unsigned long long>(t.high[bin]) << 32) + t.low[bin];
-    cl.map_shared_rank(t.own_place, to)[r.rank * per + bin - to * per] = e;
+    cl.map_shared_rank(t.own_place, to)[r.rank * per + bin - to * per] = own_entry(t, bin);
   }
   cl.sync();
   for (int i = threadIdx.x; i < per; i += kSampleThreads) {
@@ -413,39 +418,50 @@ struct End {
   unsigned about;
 };
 
+constexpr int kEach = kBins / kSampleThreads;  // bins of a thread
+// The mass of a table's bin: a bin of weights (weights_bin < 0) in common units, or one of a finer table over those of
+// one bin in that bin's units.
+__device__ __forceinline__ unsigned long long mass_in(const SampleShared& sh, unsigned long long e, int bin, int weights_bin) {
+  return weights_bin < 0 ? common_mass(sh.power, entry_mass(e, bin), bin) : entry_mass(e, weights_bin);
+}
+// Counts and masses of the bins before this thread's (whole CTA).
+__device__ __forceinline__ void before_bins(SampleShared& sh, const unsigned long long* table, int weights_bin, unsigned& count,
+                                            unsigned long long& mass) {
+  count = 0;
+  mass = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int bin = threadIdx.x * kEach + i;
+    count += entry_count(table[bin]);
+    mass += mass_in(sh, table[bin], bin, weights_bin);
+  }
+  before_sums(sh, count, mass);
+}
+
 // The end of the run of `target` tokens (kByMass false), or of the shortest run of mass `target`, from the
-// bins' table. Every CTA of the cluster comes to the same result.
+// bins' table and what lies before each thread's part of it. Every CTA of the cluster comes to the same result.
 template <bool kByMass, class T>
 __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t, Row& r, const T* row, float temperature,
-                        unsigned long long target) {
+                        unsigned long long target, unsigned count, unsigned long long mass) {
   constexpr bool kExact = sizeof(T) == 2;
-  constexpr int kEach = kBins / kSampleThreads;  // bins of a thread
-  // The bin of the run's end, in a table whose bins hold tokens of `weights_bin` (-1: each its own).
-  auto find_bin = [&](const unsigned long long* table, int weights_bin, unsigned long long mass_before) {
-    const int b0 = threadIdx.x * kEach;
-    unsigned c = 0;
-    unsigned long long m = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const unsigned long long e = table[b0 + i];
-      c += entry_count(e);
-      m += weights_bin < 0 ? common_mass(sh.power, entry_mass(e, b0 + i), b0 + i) : entry_mass(e, weights_bin);
-    }
+  // The bin of the run's end, from the counts and masses before each thread's bins.
+  auto find_bin = [&](const unsigned long long* table, int weights_bin, unsigned long long mass_before, unsigned c, unsigned long long m) {
+    __syncthreads();
     if (threadIdx.x == 0) {  // (logits that change under the kernel: all CTAs still agree)
       sh.found_bin = 0;
       sh.found_count = sh.found_in = 0;
       sh.found_mass = 0;
     }
-    before_sums(sh, c, m);
+    __syncthreads();
     // the mass before, as the target counts it
     auto common = [&](unsigned long long x) { return weights_bin < 0 ? x : common_mass(sh.power, mass_before + x, weights_bin); };
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const unsigned long long e = table[b0 + i];
-      const unsigned c1 = c + entry_count(e);
-      const unsigned long long m1 = m + (weights_bin < 0 ? common_mass(sh.power, entry_mass(e, b0 + i), b0 + i) : entry_mass(e, weights_bin));
+      const int at = threadIdx.x * kEach + i;
+      const unsigned c1 = c + entry_count(table[at]);
+      const unsigned long long m1 = m + mass_in(sh, table[at], at, weights_bin);
       if (kByMass ? (common(m) < target && target <= common(m1)) : (c < target && target <= c1)) {
-        sh.found_bin = b0 + i;
+        sh.found_bin = at;
         sh.found_count = c;
         sh.found_mass = m;
         sh.found_in = c1 - c;
@@ -455,8 +471,7 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     }
     __syncthreads();
   };
-  __syncthreads();
-  find_bin(t.all, -1, 0);
+  find_bin(t.all, -1, 0, count, mass);
   const int bin = static_cast<int>(sh.found_bin);
   unsigned in = sh.found_in;
   const unsigned about = sh.found_count + in;
@@ -489,7 +504,8 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
       }
     });
     join_tables(cl, t, t.finer, r, true);
-    find_bin(t.finer, bin, inside);
+    before_bins(sh, t.finer, bin, count, mass);
+    find_bin(t.finer, bin, inside, count, mass);
     lo += static_cast<unsigned long long>(sh.found_bin) << shift;
     hi = min(hi, lo + ((1ull << shift) - 1));
     in = sh.found_in;
@@ -513,33 +529,62 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
   int n = 0;
   join_lists(cl, sh, t, r, &n);
   n = min(n, kListed);
-  if (threadIdx.x == 0) {  // (as above)
-    sh.found_place = hi;
-    sh.found_mass = 0;
-  }
-  sort_list(t, n);
-  // the tokens' masses in the bin's units
-  const int i0 = threadIdx.x * 2;
-  unsigned long long each[2] = {};
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (i0 + j < n) {
+  // Tables over the list's places narrow it down to a warp's tokens. (Sorting it took 8 us of 1,000 tokens, a table takes
+  // 1.5. Places differ, so that the loop ends.)
+  unsigned long long *list = t.place, *rest = t.own_place;
+  while (n > 32 && lo < hi) {
+    const int shift = max(0, 64 - __clzll(static_cast<long long>(hi - lo)) - 11);
+    clear_table(t);
+    for (int i = threadIdx.x; i < n; i += kSampleThreads) {
+      if (list[i] < lo || list[i] > hi) continue;  // (logits that change under the kernel)
       float away, away_lo;
-      distance<kExact>(r.scale, place_value<kExact>(t.place[i0 + j]), away, away_lo);
-      each[j] = entry_mass(entry_of(away, away_lo), bin);
+      distance<kExact>(r.scale, place_value<kExact>(list[i]), away, away_lo);
+      add_to(t, static_cast<int>((list[i] - lo) >> shift), 1, part_of(away, away_lo));
     }
-  unsigned c = 0;
-  unsigned long long m = each[0] + each[1];
-  before_sums(sh, c, m);
+    __syncthreads();
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const unsigned long long m1 = m + each[j];
-    if (i0 + j < n && (kByMass ? (common_mass(sh.power, inside + m, bin) < target && target <= common_mass(sh.power, inside + m1, bin))
-                               : static_cast<unsigned long long>(i0 + j + 1) == target)) {
-      sh.found_place = t.place[i0 + j];
-      sh.found_mass = m1;
+    for (int i = 0; i < kEach; ++i) t.finer[threadIdx.x + i * kSampleThreads] = own_entry(t, threadIdx.x + i * kSampleThreads);
+    if (threadIdx.x == 0) sh.n_list = 0;
+    __syncthreads();
+    before_bins(sh, t.finer, bin, count, mass);
+    find_bin(t.finer, bin, inside, count, mass);
+    lo += static_cast<unsigned long long>(sh.found_bin) << shift;
+    hi = min(hi, lo + ((1ull << shift) - 1));
+    inside += sh.found_mass;
+    if (!kByMass) target -= sh.found_count;
+    for (int i = threadIdx.x; i < n; i += kSampleThreads)
+      if (list[i] >= lo && list[i] <= hi) rest[atomicAdd(&sh.n_list, 1)] = list[i];
+    __syncthreads();
+    n = sh.n_list;
+    unsigned long long* x = list;
+    list = rest;
+    rest = x;
+  }
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    n = min(n, 32);
+    if (lane == 0) {  // (as above)
+      sh.found_place = hi;
+      sh.found_mass = 0;
     }
-    m = m1;
+    __syncwarp();
+    const unsigned long long place = lane < n ? list[lane] : ~0ull;
+    float away, away_lo;
+    distance<kExact>(r.scale, place_value<kExact>(place), away, away_lo);
+    const unsigned long long own = lane < n ? entry_mass(entry_of(away, away_lo), bin) : 0ull;
+    unsigned long long m = 0, rank = 0;
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long other = __shfl_sync(0xffffffffu, place, i), its = __shfl_sync(0xffffffffu, own, i);
+      if (other < place) {
+        m += its;
+        ++rank;
+      }
+    }
+    if (lane < n && (kByMass ? (common_mass(sh.power, inside + m, bin) < target && target <= common_mass(sh.power, inside + m + own, bin))
+                             : rank + 1 == target)) {
+      sh.found_place = place;
+      sh.found_mass = m + own;
+    }
   }
   __syncthreads();
   const End end{sh.found_place, base + common_mass(sh.power, inside + sh.found_mass, bin), about};
@@ -787,32 +832,20 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       atomicAdd(&t.high[kBins - 1], static_cast<unsigned>(tail >> 32) & ((1u << (kCountShift - 32)) - 1u));
     }
     join_tables(cl, t, t.all, r, false);
+    unsigned before;
+    unsigned long long mass_before;
+    before_bins(sh, t.all, -1, before, mass_before);
     unsigned valid = 0;
     unsigned long long all = 0;
 #pragma unroll
-    for (int i = 0; i < kBins / kSampleThreads; ++i) {
-      const int bin = tid * (kBins / kSampleThreads) + i;
-      valid += entry_count(t.all[bin]);
-      all += common_mass(sh.power, entry_mass(t.all[bin], bin), bin);
-    }
-    valid = __reduce_add_sync(0xffffffffu, valid);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    if (lane == 0) {
-      sh.warp_count[warp] = valid;
-      sh.warp_sum[warp] = all;
-    }
-    __syncthreads();
-    valid = 0;
-    all = 0;
     for (int w = 0; w < kSampleWarps; ++w) {
       valid += sh.warp_count[w];
       all += sh.warp_sum[w];
     }
     End end{~0ull, all, valid};
-    if (top_k > 0 && static_cast<unsigned>(top_k) < valid) end = find_end<false>(cl, sh, t, r, row, temperature, top_k);
+    if (top_k > 0 && static_cast<unsigned>(top_k) < valid) end = find_end<false>(cl, sh, t, r, row, temperature, top_k, before, mass_before);
     if (top_p < 1.0f) {
-      const End by_mass = find_end<true>(cl, sh, t, r, row, temperature, mass_target(top_p, end.mass));
+      const End by_mass = find_end<true>(cl, sh, t, r, row, temperature, mass_target(top_p, end.mass), before, mass_before);
       end.place = min(end.place, by_mass.place);
       end.about = min(end.about, by_mass.about);
     }
