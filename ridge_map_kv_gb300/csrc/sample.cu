@@ -8,15 +8,14 @@
 // Where the runs end is decided as in 64 bits. Logits are compared as they are. Masses are integers,
 // so that sums do not depend on their order: t is a sum of two fp32 numbers, and falls into one of 2,048
 // bins of 1/64 each; within a bin the weights differ by a factor 1 - q that a polynomial gives to 2^-30,
-// so a bin needs the count of its tokens and the sum of their q, which one 64-bit addition to shared
-// memory updates. In fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
+// so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. In fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
 //
 // One cluster of up to eight CTAs a row, each with a share of the vocabulary, which it reads once for the
 // maximum and then again, from L2:
-//   few tokens (top-k of at most 128)   The threads of the cluster form 128 (or 64, ...) groups. The least
-//             of the groups' maxima is a logit that at least so many tokens reach: what lies below it
-//             cannot stay. The others, a few hundred, are listed and sorted; all filters and the draw then
-//             take the list alone.
+//   few tokens (top-k of at most 256)   The threads of the cluster form 2 k groups or more. What lies below the
+//             k-th greatest of the groups' maxima, which k tokens reach, cannot stay. The others, some 1.4 k, are
+//             listed and sorted; all filters and the draw then take the list alone. (The least maximum of k groups
+//             leaves k (ln k + 0.6) tokens, and of 128 in one row of 20 more than a list holds.)
 //   any other  The bins' table is built and summed over the cluster. A run's end lies in one bin, whose tokens
 //             are listed and sorted (where they are too many, finer tables over the bin's (logit, token)
 //             pairs narrow them down). A pass over all then adds up the weights that stay and draws, another
@@ -24,9 +23,10 @@
 //
 // Bound: the logits' bytes (and the probabilities') from memory are the floor, but instructions bound what is
 // here: some 30 a token where masses are formed, and as many where weights and scores are, 90 of a row with a
-// nucleus. Measured: one row of 32,000 in 12 to 17 us by its filters, of which some ten barriers of a cluster
-// are most; 64 bf16 rows of 131,072 with nuclei in 50 us; 256 fp32 rows of 131,072 with every filter and their
-// probabilities in 154 us (1.7 TB/s); 48 unfiltered rows of 100,003 with theirs in 32 us (1.8 TB/s).
+// nucleus. Measured: one row of 32,000 in 8 to 11 us with a top-k of 1 to 256, 12 to 17 without, of which some ten
+// barriers of a cluster are most; 64 fp32 rows of 131,072 in 14 to 18 us with such a top-k, 64 bf16 rows with nuclei
+// in 44.5 us; 256 fp32 rows of 131,072 with every filter and their probabilities in 147 us
+// (1.8 TB/s); 48 unfiltered rows of 100,003 with theirs in 32 us (1.8 TB/s).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -47,8 +47,8 @@ constexpr int kSampleShare = 2048;    // least tokens of a CTA
 constexpr int kSampleLong = 32768;    // tokens from which on a row has two CTAs at least
 constexpr int kBins = 2048;           // of the table of masses: 64 an octave; the last one holds all smaller weights
 constexpr int kListed = 1024;         // tokens that are sorted at most
-constexpr int kFewTokens = 128;       // top-k up to which tokens are listed at once: G groups leave about
-                                      // G (ln G + 0.6) tokens, some 700 of 128
+constexpr int kFewTokens = 256;       // top-k up to which tokens are listed at once
+static_assert(2 * kFewTokens <= kSampleThreads && kSampleWarps * kSampleCtas <= 2 * kFewTokens, "groups of a cluster");
 constexpr int kSampleMaxVocab = 1 << 20;
 constexpr unsigned kSparse = 64;      // where more than one token in so many stays, the noise is read along with the
                                       // logits; below that only at the tokens that stay, each a wait of its own (64
@@ -241,13 +241,14 @@ struct SampleShared {
   float warp_total[kSampleWarps];
   // from every CTA of the cluster, by the parity of the turn
   unsigned long long best[2][kSampleCtas];
-  unsigned least[2][kSampleCtas];
+  unsigned group[2 * kFewTokens];  // (or one a warp of the cluster, which are fewer)
   float sum[2][kSampleCtas];
   unsigned kept[2][kSampleCtas];
   unsigned listed[2][kSampleCtas];
   // where a run ends
   unsigned long long found_place, found_mass;
   unsigned found_bin, found_count, found_in;
+  unsigned least;
   int n_list;
   double min_away;  // T ln(min_p)
   float lowest;     // the least logit that min_p lets pass
@@ -271,6 +272,35 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
+}
+
+// A key that at least k of the groups' maxima reach, about the greatest such (one warp): halving the range between the
+// least and the greatest one until just k do, or 20 times.
+__device__ __forceinline__ void least_of_groups(SampleShared& sh, int groups, int k) {
+  constexpr int kEach = 2 * kFewTokens / 32;
+  const int lane = threadIdx.x & 31;
+  unsigned key[kEach], lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    key[i] = i * 32 + lane < groups ? sh.group[i * 32 + lane] : 0u;
+    if (i * 32 + lane < groups) {
+      lo = min(lo, key[i]);
+      hi = max(hi, key[i]);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi) + 1;
+  for (int turn = 0; turn < 20 && hi - lo > 1; ++turn) {
+    const unsigned mid = lo + (hi - lo) / 2;
+    int reach = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) reach += key[i] >= mid;
+    reach = __reduce_add_sync(0xffffffffu, reach);
+    if (reach >= k) lo = mid;
+    else hi = mid;
+    if (reach == k) break;
+  }
+  if (lane == 0) sh.least = lo;
 }
 
 // The sums of the pairs of the CTA's threads before this one (whole CTA).
@@ -649,38 +679,29 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   const unsigned long long mine =
       top > -INFINITY ? (static_cast<unsigned long long>(rising_key(top)) << 32) | (0xffffffffu - static_cast<unsigned>(top_i)) : 0ull;
   unsigned long long best = warp_max(mine);
-  // few tokens: groups of threads of this CTA, at least top_k of them in the cluster
+  // few tokens: groups of up to 32 threads of this CTA, at least twice top_k of them in the cluster
   int groups = 0;
-  unsigned least = 0xffffffffu;
+  unsigned group_max = rising_key(top);
   if (top_k > 0 && top_k <= kFewTokens) {
-    groups = 1;
-    while (groups * r.ctas < top_k) groups *= 2;
-    const int size = kSampleThreads / groups;  // threads of a group, a power of two
-    unsigned k = rising_key(top);
-    for (int o = 1; o < min(size, 32); o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-    if (size < 32) k = __reduce_min_sync(0xffffffffu, k);
-    if (lane == 0) sh.warp_count[warp] = k;
+    groups = kSampleWarps;
+    while (groups * r.ctas < 2 * top_k) groups *= 2;
+    for (int o = 1; o < kSampleThreads / groups; o <<= 1) group_max = max(group_max, __shfl_xor_sync(0xffffffffu, group_max, o));
   }
   if (lane == 0) sh.warp_sum[warp] = best;
   __syncthreads();
+  cl.barrier_wait();
+  if (groups > 0 && tid % (kSampleThreads / groups) == 0)
+    for (int c = 0; c < r.ctas; ++c) cl.map_shared_rank(sh.group, c)[r.rank * groups + tid / (kSampleThreads / groups)] = group_max;
   if (warp == 0) {
     best = warp_max(lane < kSampleWarps ? sh.warp_sum[lane] : 0ull);
-    if (groups > 0) {
-      unsigned k = lane < kSampleWarps ? sh.warp_count[lane] : 0u;
-      for (int o = 1; o < kSampleThreads / groups / 32; o <<= 1) k = max(k, __shfl_xor_sync(0xffffffffu, k, o));
-      least = __reduce_min_sync(0xffffffffu, lane < kSampleWarps ? k : 0xffffffffu);
-    }
-  }
-  cl.barrier_wait();
-  if (warp == 0 && lane < r.ctas) {
-    *cl.map_shared_rank(&sh.best[0][r.rank], lane) = best;
-    *cl.map_shared_rank(&sh.least[0][r.rank], lane) = least;
+    if (lane < r.ctas) *cl.map_shared_rank(&sh.best[0][r.rank], lane) = best;
   }
   cl.sync();
   best = 0;
-  for (int c = 0; c < r.ctas; ++c) {
-    best = max(best, sh.best[0][c]);
-    least = c == 0 ? sh.least[0][c] : min(least, sh.least[0][c]);
+  for (int c = 0; c < r.ctas; ++c) best = max(best, sh.best[0][c]);
+  if (groups > 0) {  // (whole cluster, each CTA the same)
+    if (warp == 0) least_of_groups(sh, groups * r.ctas, top_k);
+    __syncthreads();
   }
   r.turn = 1;
 
@@ -718,7 +739,6 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   r.top_inf = r.scale.m == INFINITY;
   if (r.top_inf) {
     r.scale.m = 0.0f;
-    least = least == rising_key(INFINITY) ? rising_key(0.0f) : 0u;
   }
   {
     constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-8f;
@@ -744,10 +764,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     return -(hi + lo) * 0.693147181f - logf(total);
   };
 
-  // Few tokens: list what reaches the least group's maximum.
+  // Few tokens: list what reaches the least of the top_k greatest group maxima.
   int n = 0;
-  if (groups > 0 && least > rising_key(-INFINITY)) {
-    const float from = key_value(least);
+  if (groups > 0 && !r.top_inf && sh.least > rising_key(-INFINITY)) {
+    const float from = key_value(sh.least);
     for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e)
@@ -760,7 +780,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       sort_list(t, n);
       int kept = min(top_k, n);
       if (top_p < 1.0f) {
-        // (of the first top_k, a quarter of the threads)
+        // (of the first top_k, up to half of the threads)
         unsigned c = 0;
         unsigned long long each = 0;
         if (tid < kept) {

@@ -141,6 +141,24 @@ def test_sample_matches_its_definition(kind, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [257, 1030, 5001, 131072])
+@pytest.mark.parametrize("kind", ["normal", "steps", "masked", "ranked"])
+def test_sample_top_k_from_one_to_more_than_are_listed_at_once(kind, V, dtype):
+    k = [1, 2, 16, 17, 64, 65, 127, 200, 255, 256, 257, 300]
+    R = len(k)
+    x = _logits(kind, R, V, 7 * V + len(kind), dtype)
+    if kind == "masked":
+        x[4:6, 5:] = -math.inf                          # fewer tokens than top_k
+    T, p, mp = [0.9] * R, [1.0, 0.97] * (R // 2), [0.0, 0.0, 1e-3] * (R // 3)
+    if kind == "steps":                                 # (as above)
+        p = [min(1.0, q * 1.0000172) for q in p]
+    P, tok, lp, cnt, st, noise = _run(x, T, k, p, mp)
+    assert st == 0
+    for r in range(R):
+        _check_row(V, x[r], T[r], k[r], p[r], mp[r], P[r], tok[r], lp[r], cnt[r], noise[r], True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_sample_borders_among_many_equal_tokens_where_the_last_bin_begins(dtype):
     """2,000 tokens 31.9725 octaves below the first, 3,000 twice as far: runs that end among them."""
     V = 8192
