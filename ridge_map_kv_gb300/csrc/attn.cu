@@ -60,7 +60,7 @@
 // and copies of few rows. Measured (128 channels, 8 KV heads): 4 sequences of one token, 5 query heads on one, over
 // 32,767 shared rows and up to 200 of their own: 37 us (3.7 TB/s; 20 would be the bytes). 64 of one token, 4 on
 // one, over 16,384 and up to 1,024: 63 us (3.2 TB/s, 30). 16 trees of 64 nodes, 4 on one, over 28,672 and up to
-// 300: 370 us from rest, 406 in long runs (1,190 TFLOP/s, 256 at the burst rate). 100 times three rows, 10 on one of 2
+// 300: 365 us (1,330 TFLOP/s, 256 at the burst rate). 100 times three rows, 10 on one of 2
 // heads of 64 channels, over 4,099 and up to 4,000: 56 us (1.9 TB/s, 16). One sequence's cache at a time, the prefix in
 // each, would read the prefix 64 times in the second case.
 #include <algorithm>
@@ -137,6 +137,7 @@ struct PrefixArgs : AttnArgs {
   int pairs;         // 1 or 0
   int own_heads;     // items of a sequence (heads, or pairs of them) at a time of its rows
   int copies;        // 4 or 1
+  int in_step;           // tiles of a prefix beyond which its items go in step (see Walk)
   // What an item, a tile of the prefix and a tile of a sequence's own weigh in the shares.
   int w_item, w_prefix, w_own;
   int rows, p_rows;      // rows of an item's stored part, of a sequence and of the prefix
@@ -148,7 +149,7 @@ struct PrefixArgs : AttnArgs {
 struct AttnShared {
   uint64_t full[kAtMaxStages], empty[kAtMaxStages];
   uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_final, o_empty, ml_full, turn[2], v_clean[2], mma_done[2];
-  AttnShare share;
+  AttnShare share, beginning;  // beginning: what of the share comes last (see Walk), of weight 0 where nothing does
   int bad[2][2];             // [segment parity][stream]: a drafted V row of the segment is not finite
   uint32_t tmem;
   int abort;
@@ -235,15 +236,27 @@ struct Walk {
   int at;                // where the share stands in the item's weight
   long long left;        // weight
   ItemShape shape;
+  // Where the prefix has several items a head, its keys are read from memory about once if their CTAs go through them in
+  // step. So a share that begins within one of them and goes on into the next does that beginning last: every CTA is
+  // then near the tile whose number is the time. (16 trees of 64 nodes over 28,672 rows: 395 us in the order of the
+  // shares, 1.4 GB read for 0.12, and 366 so. It takes a prefix that L2 does not hold beside the rest: 133 us either way
+  // over 8,192 rows, 33 MB; 91 and 96 over 4,096.)
+  static constexpr bool kInStep = kDual && Args::kPrefix;
   __device__ __forceinline__ Walk(const Args& a, const AttnShared* sh) {
-    b = uniform(sh->share.b);
-    h = uniform(sh->share.h);
-    mt = uniform(sh->share.mt);
-    at = uniform(sh->share.at);
-    left = uniform(sh->share.weight);
-    shape.len = uniform(sh->share.len);
+    begin(a, sh->share);
+    if constexpr (kInStep) {
+      if (left <= 0) begin(a, sh->beginning);
+    }
+  }
+  __device__ __forceinline__ void begin(const Args& a, const AttnShare& share) {
+    b = uniform(share.b);
+    h = uniform(share.h);
+    mt = uniform(share.mt);
+    at = uniform(share.at);
+    left = uniform(share.weight);
+    shape.len = uniform(share.len);
     shape.cached = (shape.len + kAtTile - 1) / kAtTile;
-    shape.tiles = uniform(sh->share.n_tiles);
+    shape.tiles = uniform(share.n_tiles);
     t0 = t1 = 0;
     if (left > 0) settle(a);
   }
@@ -267,9 +280,13 @@ struct Walk {
       if (left <= 0) return;
     }
   }
-  __device__ __forceinline__ void next(const Args& a) {
+  __device__ __forceinline__ void next(const Args& a, const AttnShared* sh) {
+    const bool ahead = t0 == 0;  // (not the beginning: what comes before that begins at its item's first tile)
     next_item(a);
     if (left > 0) settle(a);
+    if constexpr (kInStep) {
+      if (left <= 0 && ahead) begin(a, sh->beginning);
+    }
   }
   __device__ __forceinline__ void next_item(const Args& a) {
     left -= end(a) - at;
@@ -386,6 +403,21 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
       }
       base += __shfl_sync(0xffffffffu, x, 31);
     }
+  }
+  if constexpr (Walk<kDual, Args>::kInStep) {
+    AttnShare first{};
+    const int whole = prefix_tiles * a.w_prefix + a.w_item;
+    if (p.weight > whole - p.at && p.b < 0 && prefix_tiles > a.in_step && a.p_items > 1 && tile_behind(a, p.at, -1) > 0 && (p.h + 1 < a.heads || p.mt + 1 < a.p_items)) {
+      first = p;
+      first.weight = whole - p.at;
+      p.weight -= first.weight;
+      p.at = 0;
+      if (++p.mt == a.p_items) {
+        p.mt = 0;
+        ++p.h;
+      }
+    }
+    if (lane == 0) sh->beginning = first;
   }
   if (lane == 0) sh->share = p;
   __syncwarp();
@@ -629,7 +661,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
         }
         return true;
       };
-      for (Walk<kDual, Args> w(a, sh); w.more() && ok; w.next(a)) {
+      for (Walk<kDual, Args> w(a, sh); w.more() && ok; w.next(a, sh)) {
         const bool pair = paired(w.b);
         const int heads = pair ? heads_in(w.h) : 1, h0 = pair ? 2 * w.h : w.h;
         // With a prefix there are many short items, so the first K tiles are loaded before the queries, which wait
@@ -793,7 +825,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
       fence_proxy_async_shared();
       __syncwarp();
     };
-    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a, sh)) {
       const int n_tiles = w.t1 - w.t0;
       if (lane == 0) sh->bad[seg & 1][warp - 9] = 0;
       __syncwarp();
@@ -921,7 +953,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn(const __grid_constant__ 
     const float sc = a.scale * kAtLog2e;
     uint32_t s_phase = 0, f_phase = 0, ml_phase = 0;
     int seg = 0;
-    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a)) {
+    for (Walk<kDual, Args> w(a, sh); w.more(); w.next(a, sh)) {
       const int n_tiles = w.t1 - w.t0;
       const bool quarter = copied(w.b);                       // the warp sees a quarter of a tile's keys
       const bool pair = paired(w.b);                           // each stream has a head of its own
@@ -1767,6 +1799,7 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   a.w_item = lay.pairs ? 60 : 68;
   a.w_prefix = lay.pairs ? 20 : 17;
   a.w_own = lay.pairs ? 18 : 17;
+  a.in_step = static_cast<int>((32 << 20) / (static_cast<int64_t>(kAtTile) * 4 * hd * H));  // 32 MB of keys and values
   a.pairs = lay.pairs;
   a.own_heads = lay.own_heads;
   a.copies = lay.copies;

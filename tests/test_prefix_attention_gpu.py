@@ -102,6 +102,8 @@ CASES = [
     (3, 2, 1, 128, 128, 900, [9, 0, 130], "order"),            # every row of a tile is one node
     (300, 1, 1, 1, 64, 20000, [b % 3 for b in range(300)], "order"),   # three row tiles, many short items
     (5, 1, 3, 1, 128, 20000, [0] * 5, "order"),
+    (20, 13, 8, 4, 128, 8500, [(29 * b) % 90 for b in range(20)], "tree"),      # five items a head over more than 32 MB: in step
+    (33, 7, 7, 3, 128, 9500, [(29 * b) % 300 for b in range(33)], "random"),
 ]
 
 
