@@ -760,7 +760,7 @@ typedef struct rf_sample_desc {
  *   logits       [n_rows][ld_logits] bf16 or fp32
  *   temperature  [n_rows] fp32, 0 or 2^-100 .. 2^100 (NULL: 1);  top_k [n_rows] int32 >= 0 (NULL: 0);
  *                top_p [n_rows] fp32 >= 0 (NULL: 1);  min_p [n_rows] fp32 in [0, 1] (NULL: 0)
- *   noise        [n_rows][ld_noise] fp32, exponentially distributed, > 0; read where tokens stay. Needed
+ *   noise        [n_rows][ld_noise] fp32, exponentially distributed, > 0; used where tokens stay. Needed
  *                with token, NULL without
  *   probs        [n_rows][ld_probs] fp32, NULL: not wanted. May be the logits (fp32, the same stride)
  *   token, logprob, n_kept  [n_rows] int32, fp32, int32; each may be NULL, but not token and probs both.
