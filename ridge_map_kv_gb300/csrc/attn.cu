@@ -61,7 +61,7 @@
 // 32,767 shared rows and up to 200 of their own: 37 us (3.7 TB/s; 20 would be the bytes). 64 of one token, 4 on
 // one, over 16,384 and up to 1,024: 63 us (3.2 TB/s, 30). 16 trees of 64 nodes, 4 on one, over 28,672 and up to
 // 300: 365 us (1,330 TFLOP/s, 256 at the burst rate). 100 times three rows, 10 on one of 2
-// heads of 64 channels, over 4,099 and up to 4,000: 56 us (1.9 TB/s, 16). One sequence's cache at a time, the prefix in
+// heads of 64 channels, over 4,099 and up to 4,000: 57 us (1.9 TB/s, 16). One sequence's cache at a time, the prefix in
 // each, would read the prefix 64 times in the second case.
 #include <algorithm>
 #include <cmath>
@@ -407,7 +407,8 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
   if constexpr (Walk<kDual, Args>::kInStep) {
     AttnShare first{};
     const int whole = prefix_tiles * a.w_prefix + a.w_item;
-    if (p.weight > whole - p.at && p.b < 0 && prefix_tiles > a.in_step && a.p_items > 1 && tile_behind(a, p.at, -1) > 0 && (p.h + 1 < a.heads || p.mt + 1 < a.p_items)) {
+    if (p.weight > whole - p.at && p.b < 0 && prefix_tiles > a.in_step && a.p_items > 1 && tile_behind(a, p.at, -1) > 0 &&
+        (p.h + 1 < a.heads || p.mt + 1 < a.p_items)) {
       first = p;
       first.weight = whole - p.at;
       p.weight -= first.weight;

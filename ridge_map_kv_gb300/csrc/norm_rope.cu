@@ -191,7 +191,8 @@ struct NormLane {
 
 // The same for a head in packed pairs of channels.
 template <class T, int kForm>
-__device__ __forceinline__ void turn_x2(const NormArgs& a, const NormLane<T, kForm>& l, float* sh, float2 (&x)[NormLane<T, kForm>::kChannels / 2]) {
+__device__ __forceinline__ void turn_x2(const NormArgs& a, const NormLane<T, kForm>& l, float* sh,
+                                        float2 (&x)[NormLane<T, kForm>::kChannels / 2]) {
   constexpr int kHalf = NormLane<T, kForm>::kVec / 2;
   if constexpr (kForm == kPieces) {
 #pragma unroll

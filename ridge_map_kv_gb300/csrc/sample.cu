@@ -8,7 +8,8 @@
 // Where the runs end is decided as in 64 bits. Logits are compared as they are. Masses are integers,
 // so that sums do not depend on their order: t is a sum of two fp32 numbers, and falls into one of 2,048
 // bins of 1/64 each; within a bin the weights differ by a factor 1 - q that a polynomial gives to 2^-30,
-// so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. In fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
+// so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. In
+// fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
 //
 // One cluster of up to eight CTAs a row, each with a share of the vocabulary, which it reads once for the
 // maximum and then again, from L2:
@@ -418,7 +419,8 @@ __device__ __forceinline__ unsigned long long own_entry(const SampleTables& t, i
 // bins, sums the part that it gets and sends that to all. Stores to other CTAs' shared memory do not wait, as loads
 // do. The parts arrive where the lists are otherwise: `again` if another CTA may still be reading one.
 __device__ __forceinline__ void join_tables(cg::cluster_group& cl, SampleTables& t, unsigned long long* all, const Row& r, bool again) {
-  static_assert(2 * kListed == kBins && offsetof(SampleTables, place) == offsetof(SampleTables, own_place) + kListed * 8, "the lists hold a table");
+  static_assert(2 * kListed == kBins && offsetof(SampleTables, place) == offsetof(SampleTables, own_place) + kListed * 8,
+                "the lists hold a table");
   __syncthreads();
   if (again) cl.sync();
   const int per = kBins / r.ctas;
@@ -863,7 +865,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       all += sh.warp_sum[w];
     }
     End end{~0ull, all, valid};
-    if (top_k > 0 && static_cast<unsigned>(top_k) < valid) end = find_end<false>(cl, sh, t, r, row, temperature, top_k, before, mass_before);
+    if (top_k > 0 && static_cast<unsigned>(top_k) < valid)
+      end = find_end<false>(cl, sh, t, r, row, temperature, top_k, before, mass_before);
     if (top_p < 1.0f) {
       const End by_mass = find_end<true>(cl, sh, t, r, row, temperature, mass_target(top_p, end.mass), before, mass_before);
       end.place = min(end.place, by_mass.place);
