@@ -57,8 +57,9 @@ constexpr unsigned kSparse = 64;      // where more than one token in so many st
                                       // rule, 46 with 32 for 64 and 52 with 4)
 constexpr int kMassBits = 29;         // a weight of 1, within its bin
 constexpr int kCommonBits = 42;       // a weight of 1, over all bins
-constexpr int kCountShift = 44;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
-static_assert(kSampleMaxVocab <= 1 << (64 - kCountShift) && 23 + 20 < kCountShift, "counts and masses share 64 bits");
+constexpr int kCountShift = 43;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
+static_assert(kSampleMaxVocab < 1 << (64 - kCountShift) && (static_cast<long long>(kSampleMaxVocab) << 23) <= 1ll << kCountShift,
+              "all tokens may share a bin, whose count and sum share 64 bits");
 
 struct PowerTable {
   unsigned long long t[64];  // 2^(63 - i/64)
