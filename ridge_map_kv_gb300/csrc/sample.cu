@@ -132,17 +132,17 @@ __device__ __forceinline__ int near_bin(float hi) { return __float_as_int(fmaf(h
 __device__ __forceinline__ int bin_of(float hi) { return hi < kTail ? near_bin(hi) : kBins - 1; }
 // A bin's entry is its count above a sum (kCountShift). What a token adds to the sum: in the bins,
 // 2^-t = 2^(-bin/64) (1 - q) with q = z - z^2/2 + z^3/6, z = (t - bin/64) ln 2 within 0.0055 (the next term is
-// 2^-34); in the last one, 2^22 times the weight as a part of 2^(-2047/64).
+// 2^-34); in the last one, which begins at kTail, 2^22 times the weight as a part of 2^(-2047/64): at most 1.011 2^22.
 __device__ __forceinline__ unsigned bin_part(float hi, float lo) {
   const float y = fmaf(hi, 64.0f, kRound);
   const float z = (fmaf(y - kRound, -0.015625f, hi) + lo) * 0.693147181f;
   const float q = fmaf(-z * z, fmaf(-z, 0.166666667f, 0.5f), z);
   return __float_as_uint(fmaf(q, 536870912.0f, kRound)) - 0x4b000000u;
 }
-__device__ __forceinline__ unsigned tail_part(float hi) {
-  return __float2uint_rn(exp2f_ftz(fminf((kBins - 1) / 64.0f - hi, 0.0f)) * 4194304.0f);
+__device__ __forceinline__ unsigned tail_part(float hi, float lo) {
+  return hi < 150.0f ? __float2uint_rn(exp2f_ftz(((kBins - 1) / 64.0f - hi) - lo) * 4194304.0f) : 0u;
 }
-__device__ __forceinline__ unsigned part_of(float hi, float lo) { return hi < kTail ? bin_part(hi, lo) : tail_part(hi); }
+__device__ __forceinline__ unsigned part_of(float hi, float lo) { return hi < kTail ? bin_part(hi, lo) : tail_part(hi, lo); }
 __device__ __forceinline__ unsigned long long entry_of(float hi, float lo) { return (1ull << kCountShift) + part_of(hi, lo); }
 __device__ __forceinline__ unsigned entry_count(unsigned long long e) { return static_cast<unsigned>(e >> kCountShift); }
 // An entry's mass, in units of 2^-29 of its bin's weight.
@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         float hi, lo;
         distance<kExact>(r.scale, x[e], hi, lo);
         if (hi < kTail) add_to(t, near_bin(hi), 1, bin_part(hi, lo));
-        else if (x[e] > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi);  // (many share the last bin)
+        else if (x[e] > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi, lo);  // (many share the last bin)
       }
     });
 #pragma unroll
