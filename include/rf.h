@@ -767,9 +767,9 @@ typedef struct rf_sample_desc {
  *                n_kept is how many tokens stay
  * A row with nothing to choose from gives token -1, logprob -inf, n_kept 0 and probabilities 0, and so
  * does a row with a setting out of range, which also records RF_ERR_INVALID_ARG in *dev_status.
- * What stays is decided as with sums in 64 bits (masses are summed as integers, each within about
- * 2^-39 of the greatest weight); weights, probabilities and scores are fp32, and weights below 2^-126 are
- * 0. Equal inputs give equal results. No workspace. */
+ * What stays is decided by sums of integers, in which a weight counts to 2^-29 of itself (of those below
+ * 2^-32 to 2^-53), and the weights of each 1/64 octave together to 2^-42; weights, probabilities and scores are
+ * fp32, and weights below 2^-126 are 0. Equal inputs give equal results. No workspace. */
 rf_status rf_sample(const rf_sample_desc* desc, const void* logits, const float* temperature, const int32_t* top_k,
                     const float* top_p, const float* min_p, const float* noise, float* probs, int32_t* token,
                     float* logprob, int32_t* n_kept, int32_t* dev_status, rf_stream_t stream);

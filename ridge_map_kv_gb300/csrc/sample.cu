@@ -6,10 +6,11 @@
 // last token. Weights are w = 2^-t, t = (max - logit) log2(e) / T.
 //
 // Where the runs end is decided as in 64 bits. Logits are compared as they are. Masses are integers,
-// so that sums do not depend on their order: t is a sum of two fp32 numbers, and falls into one of 2,048
-// bins of 1/64 each; within a bin the weights differ by a factor 1 - q that a polynomial gives to 2^-30,
-// so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. In
-// fp32 sums a flat row's nucleus would end a token early or late every few dozen rows.
+// so that sums do not depend on their order: t falls into one of 2,048 bins of 1/64 each; within a bin the
+// weights differ by a factor 1 - q that a polynomial of the rest of t gives to 2^-29, with the rounding to whole
+// numbers, so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. The
+// last bin's are off by 2^-53 of the greatest weight, and a bin's sum by 2^-42 of it. In fp32 sums a flat row's
+// nucleus would end a token early or late every few dozen rows.
 //
 // One cluster of up to eight CTAs a row, each with a share of the vocabulary, which it reads once for the
 // maximum and then again, from L2:
@@ -101,49 +102,89 @@ __device__ __forceinline__ float place_value(unsigned long long p) {
 __device__ __forceinline__ int place_token(unsigned long long p) { return static_cast<int>(p & 0xfffffu); }
 
 struct Scale {
-  float m, c, c_lo;  // the row's maximum; log2(e) / T = c + c_lo
+  float m, c, c_lo;  // the row's reference (see reference_of); log2(e) / T = c + c_lo
 };
 
-// t = (m - x) c as hi + lo, to about 2^-46 of itself. (A difference of bf16 numbers is exact but for those
-// that are 2^16 times smaller than the other one.)
-template <bool kExact>
+// What the weights of a bf16 row are relative to: the maximum, or 0 where that is next to it (all weights then change by
+// less than 2^0.005, which cancels out).
+__device__ __forceinline__ float reference_of(float top, float c) { return fabsf(top) * c < 0.005f ? 0.0f : top; }
+// What the rounding of the difference d = m - x leaves of it. fp32: as for any two numbers, five operations. bf16 (kShort),
+// two: d is exact unless one of the two is more than 2^15 times the other. If m is, m - d is exact and the rest is
+// what it differs from x by; if x is, then m is 0 and d exact, or t beyond 160 and the weight 0 all the same.
+template <bool kShort>
+__device__ __forceinline__ float rounded_off(const Scale& s, float x, float d) {
+  if (kShort) return (s.m - d) - x;
+  const float b = d - s.m;
+  return (s.m - (d - b)) - (x + b);
+}
+// t = (m - x) c as hi + lo, to about 2^-46 of itself.
+template <bool kShort>
 __device__ __forceinline__ void distance(const Scale& s, float x, float& hi, float& lo) {
   const float d = s.m - x;
   hi = d * s.c;
   lo = fmaf(d, s.c, -hi);
   lo = fmaf(d, s.c_lo, lo);
-  if (!kExact) {
-    const float b = d - s.m;
-    lo = fmaf((s.m - (d - b)) - (x + b), s.c, lo);
-  }
+  lo = fmaf(rounded_off<kShort>(s, x, d), s.c, lo);
+}
+// The same of two bf16 tokens, in packed operations with the bits of the scalar ones. (256 rows of 131,072, unfiltered, with
+// their probabilities: 96 us, 102 in scalar operations.)
+__device__ __forceinline__ void distance_x2(const Scale& s, float2 x, float2& hi, float2& lo) {
+  const float2 m = make_float2(s.m, s.m), c = make_float2(s.c, s.c), minus = make_float2(-1.0f, -1.0f);
+  const float2 d = fma_x2(x, minus, m);
+  hi = mul_x2(d, c);
+  lo = fma_x2(d, c, make_float2(-hi.x, -hi.y));
+  lo = fma_x2(d, make_float2(s.c_lo, s.c_lo), lo);
+  lo = fma_x2(fma_x2(x, minus, fma_x2(d, minus, m)), c, lo);
 }
 // 2^-t in fp32 (0 below 2^-126).
-template <bool kExact>
+__device__ __forceinline__ float weight_at(float hi, float lo) {
+  return hi < 150.0f ? exp2f_ftz(-hi) * fmaf(lo, -0.693147181f, 1.0f) : 0.0f;
+}
+template <bool kShort>
 __device__ __forceinline__ float weight_of(const Scale& s, float x) {
   float hi, lo;
-  distance<kExact>(s, x, hi, lo);
-  return hi < 150.0f ? exp2f_ftz(-hi) * fmaf(lo, -0.693147181f, 1.0f) : 0.0f;
+  distance<kShort>(s, x, hi, lo);
+  return weight_at(hi, lo);
 }
 
 constexpr float kRound = 12582912.0f;  // 1.5 2^23: adding it rounds to whole numbers
-constexpr float kTail = (kBins - 2) / 64.0f;
-// The bin of t = hi + lo: the whole number nearest to 64 hi, or the last.
-__device__ __forceinline__ int near_bin(float hi) { return __float_as_int(fmaf(hi, 64.0f, kRound)) - 0x4b400000; }
-__device__ __forceinline__ int bin_of(float hi) { return hi < kTail ? near_bin(hi) : kBins - 1; }
-// A bin's entry is its count above a sum (kCountShift). What a token adds to the sum: in the bins,
-// 2^-t = 2^(-bin/64) (1 - q) with q = z - z^2/2 + z^3/6, z = (t - bin/64) ln 2 within 0.0055 (the next term is
-// 2^-34); in the last one, which begins at kTail, 2^22 times the weight as a part of 2^(-2047/64): at most 1.011 2^22.
-__device__ __forceinline__ unsigned bin_part(float hi, float lo) {
-  const float y = fmaf(hi, 64.0f, kRound);
-  const float z = (fmaf(y - kRound, -0.015625f, hi) + lo) * 0.693147181f;
-  const float q = fmaf(-z * z, fmaf(-z, 0.166666667f, 0.5f), z);
-  return __float_as_uint(fmaf(q, 536870912.0f, kRound)) - 0x4b000000u;
+constexpr float kLastNear = kRound + static_cast<float>(kBins - 2);
+// t in 64ths of an octave, as kRound + a whole number and the rest, within 0.54 (anything where t is beyond all bins).
+template <bool kShort>
+__device__ __forceinline__ void parts_of(const Scale& s, float x, float& whole, float& rest) {
+  const float c = 64.0f * s.c, d = s.m - x;
+  whole = fmaf(d, c, kRound);
+  rest = fmaf(d, c, kRound - whole);
+  rest = fmaf(d, 64.0f * s.c_lo, rest);
+  rest = fmaf(rounded_off<kShort>(s, x, d), c, rest);
 }
-__device__ __forceinline__ unsigned tail_part(float hi, float lo) {
+// The bin of t: the whole number nearest to 64 t, or the last.
+__device__ __forceinline__ int near_bin(float whole) { return __float_as_int(whole) - 0x4b400000; }
+// A bin's entry is its count above a sum (kCountShift). What a token adds to the sum: in the bins, 2^22 + 2^29 q with
+// 2^-t = 2^(-bin/64) (1 - q), q = z - z^2/2 + z^3/6, z = ln 2 / 64 of the rest, within 0.0059 (the next term is 2^-34); in
+// the last one 2^22 times the weight as a part of 2^(-2047/64): at most 1.006 2^22.
+__device__ __forceinline__ unsigned bin_part(float rest) {
+  constexpr float k1 = 5814539.98f, k2 = 31486.9687f, k3 = 113.672415f;
+  return __float_as_uint(fmaf(fmaf(fmaf(rest, k3, -k2), rest, k1), rest, kRound)) - 0x4b000000u;
+}
+template <bool kShort>
+__device__ __forceinline__ unsigned tail_part(const Scale& s, float x) {
+  float hi, lo;
+  distance<kShort>(s, x, hi, lo);
   return hi < 150.0f ? __float2uint_rn(exp2f_ftz(((kBins - 1) / 64.0f - hi) - lo) * 4194304.0f) : 0u;
 }
-__device__ __forceinline__ unsigned part_of(float hi, float lo) { return hi < kTail ? bin_part(hi, lo) : tail_part(hi, lo); }
-__device__ __forceinline__ unsigned long long entry_of(float hi, float lo) { return (1ull << kCountShift) + part_of(hi, lo); }
+struct Mass {
+  int bin;
+  unsigned part;
+};
+template <bool kShort>
+__device__ __forceinline__ Mass mass_of(const Scale& s, float x) {
+  float whole, rest;
+  parts_of<kShort>(s, x, whole, rest);
+  if (whole <= kLastNear) return {near_bin(whole), bin_part(rest)};
+  return {kBins - 1, tail_part<kShort>(s, x)};
+}
+__device__ __forceinline__ unsigned long long entry_of(unsigned part) { return (1ull << kCountShift) + part; }
 __device__ __forceinline__ unsigned entry_count(unsigned long long e) { return static_cast<unsigned>(e >> kCountShift); }
 // An entry's mass, in units of 2^-29 of its bin's weight.
 __device__ __forceinline__ unsigned long long entry_mass(unsigned long long e, int bin) {
@@ -266,6 +307,7 @@ struct SampleTables {
 struct Row {
   int rank, ctas, v0, v1;
   Scale scale;
+  float top;     // the maximum
   bool top_inf;  // the maximum is +inf: those tokens share all weight, as if theirs were 0 and all others' -inf
   int turn;
 };
@@ -476,7 +518,7 @@ __device__ __forceinline__ void before_bins(SampleShared& sh, const unsigned lon
 template <bool kByMass, class T>
 __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t, Row& r, const T* row, float temperature,
                         unsigned long long target, unsigned count, unsigned long long mass) {
-  constexpr bool kExact = sizeof(T) == 2;
+  constexpr bool kShort = sizeof(T) == 2;
   // The bin of the run's end, from the counts and masses before each thread's bins.
   auto find_bin = [&](const unsigned long long* table, int weights_bin, unsigned long long mass_before, unsigned c, unsigned long long m) {
     __syncthreads();
@@ -511,18 +553,18 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
   const unsigned long long base = sh.found_mass;  // of the bins before, in common units
   target -= kByMass ? base : sh.found_count;      // from here on within the bin
   unsigned long long inside = 0;                  // mass of the bin before the range below
-  // The bin's logits, a little wider than it is, so that most others fall out by a comparison. (The last bin begins at
-  // kTail, half a bin early.)
-  const float step = temperature * (0.693147181f / 64.0f), begin = static_cast<float>(bin) - (bin == kBins - 1 ? 1.0f : 0.5f);
+  // The bin's logits, a little wider than it is, so that most others fall out by a comparison.
+  const float step = temperature * (0.693147181f / 64.0f), begin = static_cast<float>(bin) - 0.5f;
   const float slack = 4e-6f * (fabsf(r.scale.m) + step * static_cast<float>(bin + 1));
-  const float high = fminf(r.scale.m - step * begin + slack, r.scale.m);
+  const float high = fminf(r.scale.m - step * begin + slack, r.top);
   const float low = bin == kBins - 1 ? -FLT_MAX : fmaxf(r.scale.m - step * (static_cast<float>(bin) + 0.5f) - slack, -FLT_MAX);
-  unsigned long long lo = place_of<kExact>(high, 0), hi = place_of<kExact>(low, kSampleMaxVocab - 1);
-  auto place_in = [&](float x, int i, unsigned long long& p, float& away, float& away_lo) {
+  unsigned long long lo = place_of<kShort>(high, 0), hi = place_of<kShort>(low, kSampleMaxVocab - 1);
+  auto place_in = [&](float x, int i, unsigned long long& p, unsigned& part) {
     if (!(x >= low && x <= high)) return false;
-    distance<kExact>(r.scale, x, away, away_lo);
-    p = place_of<kExact>(x, i);
-    return bin_of(away) == bin && p >= lo && p <= hi;
+    const Mass m = mass_of<kShort>(r.scale, x);
+    part = m.part;
+    p = place_of<kShort>(x, i);
+    return m.bin == bin && p >= lo && p <= hi;
   };
   while (in > kListed) {
     const int width = 64 - __clzll(static_cast<long long>(hi - lo));
@@ -532,8 +574,8 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
         unsigned long long p;
-        float away, away_lo;
-        if (place_in(x[e], i + e, p, away, away_lo)) add_to(t, static_cast<int>((p - lo) >> shift), 1, part_of(away, away_lo));
+        unsigned part;
+        if (place_in(x[e], i + e, p, part)) add_to(t, static_cast<int>((p - lo) >> shift), 1, part);
       }
     });
     join_tables(cl, t, t.finer, r, true);
@@ -552,8 +594,8 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
 #pragma unroll
     for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
       unsigned long long p;
-      float away, away_lo;
-      if (place_in(x[e], i + e, p, away, away_lo)) {
+      unsigned part;
+      if (place_in(x[e], i + e, p, part)) {
         const int at = atomicAdd(&sh.n_list, 1);
         if (at < kListed) t.own_place[at] = p;
       }
@@ -570,9 +612,7 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     clear_table(t);
     for (int i = threadIdx.x; i < n; i += kSampleThreads) {
       if (list[i] < lo || list[i] > hi) continue;  // (logits that change under the kernel)
-      float away, away_lo;
-      distance<kExact>(r.scale, place_value<kExact>(list[i]), away, away_lo);
-      add_to(t, static_cast<int>((list[i] - lo) >> shift), 1, part_of(away, away_lo));
+      add_to(t, static_cast<int>((list[i] - lo) >> shift), 1, mass_of<kShort>(r.scale, place_value<kShort>(list[i])).part);
     }
     __syncthreads();
 #pragma unroll
@@ -602,9 +642,8 @@ __device__ End find_end(cg::cluster_group& cl, SampleShared& sh, SampleTables& t
     }
     __syncwarp();
     const unsigned long long place = lane < n ? list[lane] : ~0ull;
-    float away, away_lo;
-    distance<kExact>(r.scale, place_value<kExact>(place), away, away_lo);
-    const unsigned long long own = lane < n ? entry_mass(entry_of(away, away_lo), bin) : 0ull;
+    const Mass mass_here = mass_of<kShort>(r.scale, place_value<kShort>(place));
+    const unsigned long long own = lane < n ? entry_mass(entry_of(mass_here.part), bin) : 0ull;
     unsigned long long m = 0, rank = 0;
     for (int i = 0; i < n; ++i) {
       const unsigned long long other = __shfl_sync(0xffffffffu, place, i), its = __shfl_sync(0xffffffffu, own, i);
@@ -642,7 +681,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   r.rank = static_cast<int>(cl.block_rank());
   r.ctas = static_cast<int>(cl.num_blocks());
   const long long row_of = blockIdx.x / static_cast<unsigned>(r.ctas);
-  constexpr bool kExact = sizeof(T) == 2;
+  constexpr bool kShort = sizeof(T) == 2;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int share = ((a.vocab + r.ctas - 1) / r.ctas + 7) & ~7;
   r.v0 = min(r.rank * share, a.vocab);
@@ -730,7 +769,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     }
     return;
   }
-  r.scale.m = key_value(static_cast<unsigned>(best >> 32));
+  r.top = key_value(static_cast<unsigned>(best >> 32));
   if (temperature == 0.0f) {
     const int first = token_of(best);
     zero_probs();
@@ -739,18 +778,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     if (r.rank == 0 && tid == 0) answer(first, 0.0f, 1);
     return;
   }
-  r.top_inf = r.scale.m == INFINITY;
-  if (r.top_inf) {
-    r.scale.m = 0.0f;
-  }
+  r.top_inf = r.top == INFINITY;
+  if (r.top_inf) r.top = 0.0f;
   {
     constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596303e-8f;
     r.scale.c = kLog2e / temperature;
     r.scale.c_lo = (fmaf(-r.scale.c, temperature, kLog2e) + kLog2eLo) / temperature;
+    r.scale.m = kShort ? reference_of(r.top, r.scale.c) : r.top;
   }
   if (tid == 0) {
     float f = -INFINITY;
-    if (min_p > 0.0f) f = __double2float_ru(static_cast<double>(r.scale.m) + sh.min_away);
+    if (min_p > 0.0f) f = __double2float_ru(static_cast<double>(r.top) + sh.min_away);
     sh.lowest = f;
   }
   __syncthreads();
@@ -763,7 +801,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   auto score_of = [](float w, float e) { return w > 0.0f ? __fdividef(w, e) : 0.0f; };
   auto logprob_of = [&](float x, float total) {
     float hi, lo;
-    distance<kExact>(r.scale, x, hi, lo);
+    distance<kShort>(r.scale, x, hi, lo);
     return -(hi + lo) * 0.693147181f - logf(total);
   };
 
@@ -776,7 +814,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e)
         if (x[e] >= from) {
           const int at = atomicAdd(&sh.n_list, 1);
-          if (at < kListed) t.own_place[at] = place_of<kExact>(x[e], i + e);
+          if (at < kListed) t.own_place[at] = place_of<kShort>(x[e], i + e);
         }
     });
     if (join_lists(cl, sh, t, r, &n)) {
@@ -787,9 +825,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         unsigned c = 0;
         unsigned long long each = 0;
         if (tid < kept) {
-          float hi, lo;
-          distance<kExact>(r.scale, place_value<kExact>(t.place[tid]), hi, lo);
-          each = common_mass(sh.power, entry_mass(entry_of(hi, lo), bin_of(hi)), bin_of(hi));
+          const Mass m = mass_of<kShort>(r.scale, place_value<kShort>(t.place[tid]));
+          each = common_mass(sh.power, entry_mass(entry_of(m.part), m.bin), m.bin);
         }
         unsigned long long m = each;
         before_sums(sh, c, m);
@@ -800,12 +837,12 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
         __syncthreads();
         kept = min(kept, static_cast<int>(sh.found_count));
       }
-      kept = __syncthreads_count(tid < kept && place_value<kExact>(t.place[tid]) >= lowest);
+      kept = __syncthreads_count(tid < kept && place_value<kShort>(t.place[tid]) >= lowest);
       float w = 0.0f, score = 0.0f;
       int i = 0;
       if (tid < kept) {
         i = place_token(t.place[tid]);
-        w = weight_of<kExact>(r.scale, place_value<kExact>(t.place[tid]));
+        w = weight_of<kShort>(r.scale, place_value<kShort>(t.place[tid]));
         if (a.token != nullptr && r.rank == 0) score = score_of(w, noise[i]);
       }
       float total = w;
@@ -827,7 +864,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       if (probs != nullptr && tid < kept && i >= r.v0 && i < r.v1) probs[i] = w / total;
       // the token's own thread, or the first one's where none is drawn
       if (r.rank == 0 && tid < kept && i == (a.token != nullptr ? token_of(best) : place_token(t.place[0])))
-        answer(i, logprob_of(place_value<kExact>(t.place[tid]), total), kept);
+        answer(i, logprob_of(place_value<kShort>(t.place[tid]), total), kept);
       return;
     }
   }
@@ -842,10 +879,10 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     for_tokens(row, r.top_inf, r.v0, r.v1, [&](int, const auto& x) {
 #pragma unroll
       for (int e = 0; e < static_cast<int>(sizeof(x) / sizeof(float)); ++e) {
-        float hi, lo;
-        distance<kExact>(r.scale, x[e], hi, lo);
-        if (hi < kTail) add_to(t, near_bin(hi), 1, bin_part(hi, lo));
-        else if (x[e] > -INFINITY) tail += (1ull << kCountShift) + tail_part(hi, lo);  // (many share the last bin)
+        float whole, rest;
+        parts_of<kShort>(r.scale, x[e], whole, rest);
+        if (whole <= kLastNear) add_to(t, near_bin(whole), 1, bin_part(rest));
+        else if (x[e] > -INFINITY) tail += (1ull << kCountShift) + tail_part<kShort>(r.scale, x[e]);  // (many share the last bin)
       }
     });
 #pragma unroll
@@ -874,7 +911,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       end.about = min(end.about, by_mass.about);
     }
     if (end.place != ~0ull) {
-      last = place_value<kExact>(end.place);
+      last = place_value<kShort>(end.place);
       last_i = place_token(end.place);
       about = end.about;
     }
@@ -888,22 +925,36 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   float total = 0.0f, leader = -1.0f;  // the greatest score and its token: the lowest, as a thread's tokens rise
   unsigned kept = 0;
   int lead_i = 0;
+  auto count = [&](int i, float w, float e) {
+    total += w;
+    ++kept;
+    const float score = score_of(w, e);
+    if (score > leader) {
+      leader = score;
+      lead_i = i;
+    }
+  };
   auto count_in = [&](int i, const auto& x, const auto& e) {
 #pragma unroll
     for (int j = 0; j < static_cast<int>(sizeof(x) / sizeof(float)); ++j)
-      if (stays(x[j], i + j)) {
-        const float w = weight_of<kExact>(r.scale, x[j]);
-        total += w;
-        ++kept;
-        const float score = score_of(w, e[j]);
-        if (score > leader) {
-          leader = score;
-          lead_i = i + j;
-        }
+      if (stays(x[j], i + j)) count(i + j, weight_of<kShort>(r.scale, x[j]), e[j]);
+  };
+  auto count_dense = [&](int i, const auto& x, const auto& e) {
+    constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
+    if constexpr (kShort && kN > 1) {
+#pragma unroll
+      for (int j = 0; j < kN; j += 2) {
+        float2 hi, lo;
+        distance_x2(r.scale, make_float2(x[j], x[j + 1]), hi, lo);
+        if (stays(x[j], i + j)) count(i + j, weight_at(hi.x, lo.x), e[j]);
+        if (stays(x[j + 1], i + j + 1)) count(i + j + 1, weight_at(hi.y, lo.y), e[j + 1]);
       }
+    } else {
+      count_in(i, x, e);
+    }
   };
   if (noise != nullptr && about > static_cast<unsigned>(a.vocab) / kSparse) {  // the noise comes along with the logits
-    for_both<true>(row, noise, r.top_inf, r.v0, r.v1, count_in);
+    for_both<true>(row, noise, r.top_inf, r.v0, r.v1, count_dense);
   } else {
     for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
       constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
@@ -952,9 +1003,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   // The CTA that holds the token answers: its logit is read before probabilities are written over it.
   const int token = token_of(best);
   if (tid == 0 && (a.token != nullptr ? token >= r.v0 && token < r.v1 : r.rank == 0)) {
-    float x = r.scale.m;
+    float x = r.top;
     if (a.token != nullptr && !r.top_inf) {
-      if constexpr (kExact) x = __bfloat162float(row[token]);
+      if constexpr (kShort) x = __bfloat162float(row[token]);
       else x = row[token];
     }
     answer(token, logprob_of(x, total), static_cast<int>(kept));
@@ -965,9 +1016,17 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   for_tokens(row, r.top_inf, r.v0, r.v1, [&](int i, const auto& x) {
     constexpr int kN = static_cast<int>(sizeof(x) / sizeof(float));
     float p[kN];
+    if constexpr (kShort && kN > 1) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) {
-      p[e] = stays(x[e], i + e) ? weight_of<kExact>(r.scale, x[e]) * inverse : 0.0f;
+      for (int e = 0; e < kN; e += 2) {
+        float2 hi, lo;
+        distance_x2(r.scale, make_float2(x[e], x[e + 1]), hi, lo);
+        p[e] = stays(x[e], i + e) ? weight_at(hi.x, lo.x) * inverse : 0.0f;
+        p[e + 1] = stays(x[e + 1], i + e + 1) ? weight_at(hi.y, lo.y) * inverse : 0.0f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kN; ++e) p[e] = stays(x[e], i + e) ? weight_of<kShort>(r.scale, x[e]) * inverse : 0.0f;
     }
     if (kN % 4 == 0 && (reinterpret_cast<uintptr_t>(probs + i) & 15u) == 0) {
 #pragma unroll
