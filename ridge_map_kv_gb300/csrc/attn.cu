@@ -1335,7 +1335,8 @@ __global__ void __launch_bounds__(kHD * 2) k_attn_combine(const __grid_constant_
 
 // Adds up each row's parts of a call with a prefix: those of the prefix's item, then those of its own
 // sequence's. Block (x, y): rows 32 x .. 32 x + 31 (or 8, see below) of KV head y, counted over the
-// sequences' nodes and the head's queries; a warp takes 16 channels.
+// sequences' nodes and the head's queries; a warp takes 16 channels. (With more heads than a grid has places
+// along y: rows 32 y .., head x.)
 struct JoinArgs {
   const float4* part_o;
   const float2* part_ml;
@@ -1350,6 +1351,7 @@ struct JoinArgs {
   int n_seqs, n, heads, group, npt, tiles, m_items, p_nodes, p_seqs, p_split, p_items, rows, p_rows, ctas;
   int pairs, own_heads, copies;
   int capacity, prefix_capacity;
+  int heads_along_x;  // 1 or 0
   float scale;
 };
 
@@ -1360,8 +1362,9 @@ __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kLanes = 32 / kSplit;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-  const int r = blockIdx.x * kLanes + lane % kLanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = a.heads_along_x ? blockIdx.x : blockIdx.y;
+  const int r = (a.heads_along_x ? blockIdx.y : blockIdx.x) * kLanes + lane % kLanes;
   const int per_seq = a.n * a.group;
   const int b = r / per_seq, in_seq = r - b * per_seq, node = in_seq / a.group, g = in_seq - node * a.group;
   const bool there = b < a.n_seqs;
@@ -1845,11 +1848,13 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   const int64_t rows = static_cast<int64_t>(B * n) * a.group;  // of a KV head
   const bool few = (rows + 31) / 32 * static_cast<int64_t>(H) < sms, fewest = rows <= 32;
   const int64_t blocks = (rows + (few ? 7 : 31)) / (few ? 8 : 32);
+  // (n_seqs * n_nodes * n_q_heads <= 2^28: with more than 65,535 heads the blocks of one are 512 at most)
+  j.heads_along_x = H > 65535;
+  const dim3 grid = j.heads_along_x ? dim3(static_cast<unsigned>(H), static_cast<unsigned>(blocks))
+                                    : dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H));
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
   void (*join)(JoinArgs) =
       hd == 128 ? (!few ? k_prefix_join<128, 4, 1> : fewest ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 4>)
                 : (!few ? k_prefix_join<64, 4, 1> : fewest ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 4>);
-  return cuda_check(launch_dependent(join, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H)), dim3(static_cast<unsigned>(2 * hd)),
-                                     0, s, 1, j),
-                    "k_prefix_join launch");
+  return cuda_check(launch_dependent(join, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, 1, j), "k_prefix_join launch");
 }
