@@ -601,7 +601,8 @@ typedef struct rf_norm_rope_desc {
  * the means over the head's channels, the rotation R and the positions of rf_rope, and g = q_gain
  * or k_gain, [head_dim] values of the rows' type (16-byte aligned; NULL: ones). Squares, means and
  * products are fp32 (a head's squares must add up to less than 2^128); there is one rounding, at
- * the end. out may be in (with ld_out = ld_in). No workspace. */
+ * the end. A gain that is not finite stays within its channel, or, if that turns, its pair of channels.
+ * out may be in (with ld_out = ld_in). No workspace. */
 rf_status rf_norm_rope(const rf_norm_rope_desc* desc, const void* in, const void* q_gain, const void* k_gain,
                        void* out, const int32_t* positions, rf_stream_t stream);
 
@@ -610,7 +611,8 @@ rf_status rf_norm_rope(const rf_norm_rope_desc* desc, const void* in, const void
  *            d_out (with ld_out = ld_in).
  *   d_q_gain, d_k_gain  [head_dim] fp32 (either may be NULL), written, not added to: the sums over all
  *            rows and query heads, or key heads, of the gains' gradients; zero where there are none
- * in, gains, positions and desc as for the call whose gradient it is. Sums are fp32, in an order that
+ * in, gains, positions and desc as for the call whose gradient it is. What is not finite in d_out stays within
+ * its head's gradient, and in the gains' within its channel or pair of channels. Sums are fp32, in an order that
  * depends on the sizes and the GPU alone. The workspace is needed for the gains' gradients only. */
 size_t rf_norm_rope_backward_workspace_bytes(const rf_norm_rope_desc* desc);
 rf_status rf_norm_rope_backward(const rf_norm_rope_desc* desc, const void* in, const void* q_gain,

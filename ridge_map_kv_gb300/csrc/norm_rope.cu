@@ -28,6 +28,7 @@
 // sizes alone.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "rf_device.cuh"
 #include "rf_host.h"
@@ -157,11 +158,22 @@ struct NormLane {
       if (ok[p]) store_vec(head + start[p], v);
     }
   }
-  // Turns a head's channels; `sh`: the head's channels in shared memory (kShared; whole warp).
+  // Whether a gain is an infinity or NaN, or may become an infinity by an inverse root (2^63 at most).
+  __device__ __forceinline__ bool odd_gains() const {
+    float zero = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChannels; ++i) zero = fmaf(g[i] * 0x1p63f, 0.0f, zero);
+    return zero != zero;
+  }
+  // Turns a head's channels; `sh`: the head's channels in shared memory (kShared; whole warp). Channels that do not turn
+  // have an angle of 0; 0 times an infinity or NaN of one would be a NaN of another, so where there may be one they are left
+  // alone (kOdd; done so always, heads of which a part turns took 2 to 6% longer).
+  template <bool kOdd>
   __device__ __forceinline__ void turn(const NormArgs& a, float* sh, float (&x)[kChannels]) const {
     if (kForm == kPieces) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
+        if (kOdd && !turns) break;
         const float x1 = x[i], x2 = x[kVec + i];
         x[i] = x1 * c[i] - x2 * s[i];
         x[kVec + i] = x2 * c[i] + x1 * s[i];
@@ -169,6 +181,7 @@ struct NormLane {
     } else if (kForm == kPairs) {
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
+        if (kOdd && start[2 * i / kVec] + 2 * i % kVec >= a.rot) continue;
         const float x1 = x[2 * i], x2 = x[2 * i + 1];
         x[2 * i] = x1 * c[i] - x2 * s[i];
         x[2 * i + 1] = x2 * c[i] + x1 * s[i];
@@ -190,11 +203,12 @@ struct NormLane {
 };
 
 // The same for a head in packed pairs of channels.
-template <class T, int kForm>
+template <bool kOdd, class T, int kForm>
 __device__ __forceinline__ void turn_x2(const NormArgs& a, const NormLane<T, kForm>& l, float* sh,
                                         float2 (&x)[NormLane<T, kForm>::kChannels / 2]) {
   constexpr int kHalf = NormLane<T, kForm>::kVec / 2;
   if constexpr (kForm == kPieces) {
+    if (kOdd && !l.turns) return;
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) {
       const float2 c = make_float2(l.c[2 * i], l.c[2 * i + 1]), s = make_float2(l.s[2 * i], l.s[2 * i + 1]);
@@ -209,7 +223,7 @@ __device__ __forceinline__ void turn_x2(const NormArgs& a, const NormLane<T, kFo
       y[2 * i] = x[i].x;
       y[2 * i + 1] = x[i].y;
     }
-    l.turn(a, sh, y);
+    l.template turn<kOdd>(a, sh, y);
 #pragma unroll
     for (int i = 0; i < 2 * kHalf; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
   }
@@ -252,7 +266,8 @@ __device__ __forceinline__ float inverse_root(float v) {
 
 constexpr int kNormHeads = 4;  // heads that a thread takes together
 
-template <class T, int kForm>
+// kPart: some channels do not turn (kPieces, kPairs).
+template <class T, int kForm, bool kPart>
 __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_constant__ NormArgs a,
                                                             const __grid_constant__ RopeTable tab) {
   using Lane = NormLane<T, kForm>;
@@ -293,6 +308,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_cons
   for (int i = 0; i < kNormStages - 1; ++i) copy_next();
   l.angles(a, tab, a.positions != nullptr ? static_cast<long long>(a.positions[row]) : row + a.pos_offset, 1.0f);
   int stage = 0;
+  bool odd = false;
   for (int h = h0; h < h1;) {
     const int end = batch_end(h);
     copy_next();
@@ -313,15 +329,20 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_cons
 #pragma unroll
     for (int j = 0; j < kNormHeads; ++j)
       if (h + j < end) r[j] = inverse_root<T>(head_sum(r[j], a.lanes) * part + a.eps);
+    if (kPart && (h == h0 || h == a.n_q)) odd = l.odd_gains();
+    auto finish = [&](auto with_odd) {
 #pragma unroll
-    for (int j = 0; j < kNormHeads; ++j) {
-      if (h + j >= end) break;
-      l.widen(v[j], x);
+      for (int j = 0; j < kNormHeads; ++j) {
+        if (h + j >= end) break;
+        l.widen(v[j], x);
 #pragma unroll
-      for (int i = 0; i < Lane::kChannels; ++i) x[i] *= r[j] * l.g[i];
-      l.turn(a, sh, x);
-      if (live) l.store(out + (h + j) * a.head_dim, x);
-    }
+        for (int i = 0; i < Lane::kChannels; ++i) x[i] *= r[j] * l.g[i];
+        l.template turn<with_odd.value>(a, sh, x);
+        if (live) l.store(out + (h + j) * a.head_dim, x);
+      }
+    };
+    if (kPart && odd) finish(std::true_type());
+    else finish(std::false_type());
     h = end;
     stage = stage + 1 == kNormStages ? 0 : stage + 1;
   }
@@ -329,7 +350,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope(const __grid_cons
 
 constexpr int kNormBackHeads = 2;
 
-template <class T, int kForm>
+template <class T, int kForm, bool kPart>
 __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __grid_constant__ NormArgs a,
                                                                         const __grid_constant__ RopeTable tab) {
   using Lane = NormLane<T, kForm>;
@@ -416,7 +437,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
 #pragma unroll
         for (int i = 0; i < kC / 2; ++i) x[i] = w[i] = make_float2(0.0f, 0.0f);
       }
-      turn_x2(a, l, sh, w);
+      turn_x2<false>(a, l, sh, w);
       float2 ss2 = make_float2(0.0f, 0.0f), dot2 = ss2;
 #pragma unroll
       for (int i = 0; i < kC / 2; ++i) {
@@ -425,6 +446,12 @@ __global__ void __launch_bounds__(kNormThreads, 2) k_norm_rope_backward(const __
       }
       float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
       head_sums(ss, dot, a.lanes);
+      if (kPart && !isfinite(dot)) {  // as with any infinity or NaN of w: the pieces are turned once more, each channel by itself
+        l.take(norm_slot<2 * kNormBackHeads>(ring, stage, 2 * j + 1), raw);
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) w[i] = there ? pair_of(&raw[0][0] + 2 * i) : make_float2(0.0f, 0.0f);
+        turn_x2<true>(a, l, sh, w);
+      }
       const float r = inverse_root<T>(ss * part + a.eps);
       const float b = dot * part * (r * r) * r;
       const float2 rr = make_float2(r, r), bb = make_float2(-b, -b);
@@ -525,7 +552,7 @@ static NormArgs norm_args(const rf_norm_rope_desc* d, NormForm* form) {
   return a;
 }
 
-template <class T, int kForm>
+template <class T, int kForm, bool kPart>
 static rf_status launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStream_t s) {
   // Heads per thread: as many as still leave two waves of threads, so that a small call spreads
   // over the GPU and a large one forms its angles once for many heads.
@@ -535,16 +562,17 @@ static rf_status launch_norm(NormArgs& a, const RopeTable& t, int sms, cudaStrea
   const dim3 grid(static_cast<unsigned>((threads1 + kNormThreads - 1) / kNormThreads),
                   static_cast<unsigned>((a.n_heads + a.hpt - 1) / a.hpt));
   static uint64_t done = 0;
-  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope<T, kForm>), norm_ring_bytes(kNormHeads), &done);
+  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope<T, kForm, kPart>), norm_ring_bytes(kNormHeads), &done);
   if (st != RF_OK) return st;
-  return cuda_check(launch_dependent(k_norm_rope<T, kForm>, grid, dim3(kNormThreads), norm_ring_bytes(kNormHeads), s, 1, a, t),
+  return cuda_check(launch_dependent(k_norm_rope<T, kForm, kPart>, grid, dim3(kNormThreads), norm_ring_bytes(kNormHeads), s, 1, a, t),
                     "k_norm_rope launch");
 }
 template <class T>
 static rf_status launch_norm(NormArgs& a, const RopeTable& t, NormForm form, int sms, cudaStream_t s) {
-  return form == kPieces ? launch_norm<T, kPieces>(a, t, sms, s)
-         : form == kPairs ? launch_norm<T, kPairs>(a, t, sms, s)
-                          : launch_norm<T, kShared>(a, t, sms, s);
+  const bool part = a.rot < a.head_dim;
+  if (form == kPieces) return part ? launch_norm<T, kPieces, true>(a, t, sms, s) : launch_norm<T, kPieces, false>(a, t, sms, s);
+  if (form == kPairs) return part ? launch_norm<T, kPairs, true>(a, t, sms, s) : launch_norm<T, kPairs, false>(a, t, sms, s);
+  return launch_norm<T, kShared, false>(a, t, sms, s);
 }
 
 // CTAs of the backward pass: two an SM, no more than there are batches to share out among their groups, the query
@@ -560,21 +588,24 @@ static int norm_ctas(const NormArgs& a, int sms, int* q_ctas) {
   return static_cast<int>(q + k);
 }
 
-template <class T, int kForm>
+template <class T, int kForm, bool kPart>
 static rf_status launch_norm_backward(const NormArgs& a, const RopeTable& t, int ctas, cudaStream_t s) {
   static uint64_t done = 0;
   constexpr size_t bytes = norm_ring_bytes(2 * kNormBackHeads);
-  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope_backward<T, kForm>), bytes, &done);
+  const rf_status st = set_smem_attr(reinterpret_cast<const void*>(&k_norm_rope_backward<T, kForm, kPart>), bytes, &done);
   if (st != RF_OK) return st;
-  return cuda_check(launch_dependent(k_norm_rope_backward<T, kForm>, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), bytes, s,
+  return cuda_check(launch_dependent(k_norm_rope_backward<T, kForm, kPart>, dim3(static_cast<unsigned>(ctas)), dim3(kNormThreads), bytes, s,
                                      1, a, t),
                     "k_norm_rope_backward launch");
 }
 template <class T>
 static rf_status launch_norm_backward(const NormArgs& a, const RopeTable& t, NormForm form, int ctas, cudaStream_t s) {
-  return form == kPieces ? launch_norm_backward<T, kPieces>(a, t, ctas, s)
-         : form == kPairs ? launch_norm_backward<T, kPairs>(a, t, ctas, s)
-                          : launch_norm_backward<T, kShared>(a, t, ctas, s);
+  const bool part = a.rot < a.head_dim;
+  if (form == kPieces)
+    return part ? launch_norm_backward<T, kPieces, true>(a, t, ctas, s) : launch_norm_backward<T, kPieces, false>(a, t, ctas, s);
+  if (form == kPairs)
+    return part ? launch_norm_backward<T, kPairs, true>(a, t, ctas, s) : launch_norm_backward<T, kPairs, false>(a, t, ctas, s);
+  return launch_norm_backward<T, kShared, false>(a, t, ctas, s);
 }
 
 }  // namespace rf
