@@ -764,7 +764,8 @@ typedef struct rf_sample_desc {
  *                top_p [n_rows] fp32 >= 0 (NULL: 1);  min_p [n_rows] fp32 in [0, 1] (NULL: 0)
  *   noise        [n_rows][ld_noise] fp32, exponentially distributed, > 0; used where tokens stay. Needed
  *                with token, NULL without
- *   probs        [n_rows][ld_probs] fp32, NULL: not wanted. May be the logits (fp32, the same stride)
+ *   probs        [n_rows][ld_probs] fp32, NULL: not wanted. May be the logits (fp32, the same stride), but
+ *                not the noise
  *   token, logprob, n_kept  [n_rows] int32, fp32, int32; each may be NULL, but not token and probs both.
  *                n_kept is how many tokens stay
  * A row with nothing to choose from gives token -1, logprob -inf, n_kept 0 and probabilities 0, and so

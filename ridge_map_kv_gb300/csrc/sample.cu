@@ -1087,9 +1087,17 @@ extern "C" rf_status rf_sample(const rf_sample_desc* d, const void* logits, cons
   if (d->ld_logits > (int64_t(1) << 36) || (noise && d->ld_noise > (int64_t(1) << 36)) || (probs && d->ld_probs > (int64_t(1) << 36)))
     return fail(RF_ERR_SHAPE, "row strides must be <= 2^36");
   const bool in_place = static_cast<const void*>(probs) == logits && d->dtype == RF_F32 && d->ld_probs == d->ld_logits;
-  const int64_t span = (d->n_rows - 1) * d->ld_logits + d->vocab, wide = (d->n_rows - 1) * d->ld_probs + d->vocab;
-  if (probs != nullptr && !in_place && overlap(static_cast<const char*>(logits), span * static_cast<int64_t>(size), probs, wide))
+  const auto span = [&](int64_t ld) { return (d->n_rows - 1) * ld + d->vocab; };
+  if (probs != nullptr && !in_place &&
+      overlap(static_cast<const char*>(logits), span(d->ld_logits) * static_cast<int64_t>(size), probs, span(d->ld_probs)))
     return fail(RF_ERR_INVALID_ARG, "probs must be the logits (fp32, the same stride) or lie apart from them");
+  // A row's CTAs write probabilities while others still read noise. Rows of one stride may lie beside each other.
+  if (probs != nullptr && noise != nullptr && overlap(noise, span(d->ld_noise), probs, span(d->ld_probs))) {
+    const int64_t ld = d->ld_noise;
+    const int64_t from = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(probs) - reinterpret_cast<uintptr_t>(noise)) / 4 % ld + ld) % ld;
+    if (ld != d->ld_probs || from < d->vocab || ld - from < d->vocab)
+      return fail(RF_ERR_INVALID_ARG, "probs must lie apart from the noise");
+  }
   int sms = 0;
   rf_status st = current_device(&sms);
   if (st != RF_OK) return st;
