@@ -769,7 +769,8 @@ typedef struct rf_sample_desc {
  *   token, logprob, n_kept  [n_rows] int32, fp32, int32; each may be NULL, but not token and probs both.
  *                n_kept is how many tokens stay
  * A row with nothing to choose from gives token -1, logprob -inf, n_kept 0 and probabilities 0, and so
- * does a row with a setting out of range, which also records RF_ERR_INVALID_ARG in *dev_status.
+ * does a row with a setting out of range, which also records RF_ERR_INVALID_ARG in *dev_status. So does a row
+ * without noise above 0 at any token that stays, whose token is -1 and logprob -inf.
  * What stays is decided by sums of integers, in which a weight counts to 2^-29 of itself (of those below
  * 2^-32 to 2^-53), and the weights of each 1/64 octave together to 2^-42; weights, probabilities and scores are
  * fp32, and weights below 2^-126 are 0. Equal inputs give equal results. No workspace. */

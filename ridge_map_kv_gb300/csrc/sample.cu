@@ -805,6 +805,13 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
     return -(hi + lo) * 0.693147181f - logf(total);
   };
 
+  // No token that stays has a score: its noise is no number above 0.
+  auto no_score = [&](int kept) {
+    if (r.rank != 0 || tid != 0) return;
+    answer(-1, -INFINITY, kept);
+    record_status(a.dev_status, RF_ERR_INVALID_ARG);
+  };
+
   // Few tokens: list what reaches the least of the top_k greatest group maxima.
   int n = 0;
   if (groups > 0 && !r.top_inf && sh.least > rising_key(-INFINITY)) {
@@ -848,7 +855,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       float total = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-      const unsigned long long pick = warp_max(tid < kept ? pair_of(score, i) : 0ull);
+      const unsigned long long pick = warp_max(tid < kept && score >= 0.0f ? pair_of(score, i) : 0ull);
       if (lane == 0) {
         sh.warp_total[warp] = total;
         sh.warp_sum[warp] = pick;
@@ -863,7 +870,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
       }
       if (probs != nullptr && tid < kept && i >= r.v0 && i < r.v1) probs[i] = w / total;
       // the token's own thread, or the first one's where none is drawn
-      if (r.rank == 0 && tid < kept && i == (a.token != nullptr ? token_of(best) : place_token(t.place[0])))
+      if (a.token != nullptr && best == 0) no_score(kept);
+      else if (r.rank == 0 && tid < kept && i == (a.token != nullptr ? token_of(best) : place_token(t.place[0])))
         answer(i, logprob_of(place_value<kShort>(t.place[tid]), total), kept);
       return;
     }
@@ -1002,7 +1010,9 @@ __global__ void __launch_bounds__(kSampleThreads, 2) k_sample(const __grid_const
   }
   // The CTA that holds the token answers: its logit is read before probabilities are written over it.
   const int token = token_of(best);
-  if (tid == 0 && (a.token != nullptr ? token >= r.v0 && token < r.v1 : r.rank == 0)) {
+  if (a.token != nullptr && best == 0) {
+    no_score(static_cast<int>(kept));
+  } else if (tid == 0 && (a.token != nullptr ? token >= r.v0 && token < r.v1 : r.rank == 0)) {
     float x = r.top;
     if (a.token != nullptr && !r.top_inf) {
       if constexpr (kShort) x = __bfloat162float(row[token]);
