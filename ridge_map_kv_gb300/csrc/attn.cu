@@ -1351,20 +1351,18 @@ struct JoinArgs {
   int n_seqs, n, heads, group, npt, tiles, m_items, p_nodes, p_seqs, p_split, p_items, rows, p_rows, ctas;
   int pairs, own_heads, copies;
   int capacity, prefix_capacity;
-  int heads_along_x;  // 1 or 0
   float scale;
 };
 
 // kBatch, kSplit as for k_attn_combine: lanes share a row where there are fewer blocks than SMs otherwise, and more parts
 // are in flight where an item has many (one row tile).
-template <int kHD, int kBatch, int kSplit>
+template <int kHD, int kBatch, int kSplit, bool kHeadsAlongX = false>
 __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__ JoinArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kLanes = 32 / kSplit;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = a.heads_along_x ? blockIdx.x : blockIdx.y;
-  const int r = (a.heads_along_x ? blockIdx.y : blockIdx.x) * kLanes + lane % kLanes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = kHeadsAlongX ? blockIdx.x : blockIdx.y;
+  const int r = (kHeadsAlongX ? blockIdx.y : blockIdx.x) * kLanes + lane % kLanes;
   const int per_seq = a.n * a.group;
   const int b = r / per_seq, in_seq = r - b * per_seq, node = in_seq / a.group, g = in_seq - node * a.group;
   const bool there = b < a.n_seqs;
@@ -1849,12 +1847,13 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   const bool few = (rows + 31) / 32 * static_cast<int64_t>(H) < sms, fewest = rows <= 32;
   const int64_t blocks = (rows + (few ? 7 : 31)) / (few ? 8 : 32);
   // (n_seqs * n_nodes * n_q_heads <= 2^28: with more than 65,535 heads the blocks of one are 512 at most)
-  j.heads_along_x = H > 65535;
-  const dim3 grid = j.heads_along_x ? dim3(static_cast<unsigned>(H), static_cast<unsigned>(blocks))
-                                    : dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H));
+  const bool along_x = H > 65535;
+  const dim3 grid = along_x ? dim3(static_cast<unsigned>(H), static_cast<unsigned>(blocks))
+                            : dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(H));
   ProfScope prof(s, RF_STAGE_ATTN_COMBINE);
   void (*join)(JoinArgs) =
-      hd == 128 ? (!few ? k_prefix_join<128, 4, 1> : fewest ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 4>)
-                : (!few ? k_prefix_join<64, 4, 1> : fewest ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 4>);
+      along_x     ? (hd == 128 ? k_prefix_join<128, 4, 1, true> : k_prefix_join<64, 4, 1, true>)
+      : hd == 128 ? (!few ? k_prefix_join<128, 4, 1> : fewest ? k_prefix_join<128, 8, 4> : k_prefix_join<128, 4, 4>)
+                  : (!few ? k_prefix_join<64, 4, 1> : fewest ? k_prefix_join<64, 8, 4> : k_prefix_join<64, 4, 4>);
   return cuda_check(launch_dependent(join, grid, dim3(static_cast<unsigned>(2 * hd)), 0, s, 1, j), "k_prefix_join launch");
 }
