@@ -195,22 +195,23 @@ __device__ __forceinline__ int items_of(const Args& a, int b) {  // of a head
   if constexpr (Args::kPrefix) return b < 0 ? a.p_items : a.m_items;
   else return a.m_items;
 }
-// An item weighs item_weight and tile_weight for each of its tiles.
-template <class Args>
+// An item weighs item_weight and tile_weight for each of its tiles. With one row tile all tiles weigh alike, with a prefix
+// or without: a tile is its bytes. (Weights that are known at run time only cost a call of 37 us one.)
+template <bool kDual, class Args>
 __device__ __forceinline__ int item_weight(const Args& a) {
-  if constexpr (Args::kPrefix) return a.w_item;
+  if constexpr (kDual && Args::kPrefix) return a.w_item;
   else return kAtItemCost;
 }
-template <class Args>
+template <bool kDual, class Args>
 __device__ __forceinline__ int tile_weight(const Args& a, int b) {
-  if constexpr (Args::kPrefix) return b < 0 ? a.w_prefix : a.w_own;
+  if constexpr (kDual && Args::kPrefix) return b < 0 ? a.w_prefix : a.w_own;
   else return 1;
 }
 // The first tile that lies behind `at` in the weight of an item of sequence b.
-template <class Args>
+template <bool kDual, class Args>
 __device__ __forceinline__ int tile_behind(const Args& a, int at, int b) {
-  const int x = max(at - item_weight(a), 0);
-  if constexpr (Args::kPrefix) return x / tile_weight(a, b);
+  const int x = max(at - item_weight<kDual>(a), 0);
+  if constexpr (kDual && Args::kPrefix) return x / tile_weight<kDual>(a, b);
   else return x;
 }
 template <bool kDual, class Args>
@@ -262,18 +263,18 @@ struct Walk {
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ int end(const Args& a) const {
-    return static_cast<int>(min(static_cast<long long>(shape.tiles) * tile_weight(a, b) + item_weight(a), at + left));
+    return static_cast<int>(min(static_cast<long long>(shape.tiles) * tile_weight<kDual>(a, b) + item_weight<kDual>(a), at + left));
   }
   // The first tiles from here on (a share may end within an item's extra weight).
   __device__ __forceinline__ void settle(const Args& a) {
     while (true) {
       if constexpr (Args::kPrefix) {  // (most items are whole ones)
-        const int whole = shape.tiles * tile_weight(a, b) + item_weight(a);
-        t0 = at == 0 ? 0 : tile_behind(a, at, b);
-        t1 = at + left >= whole ? shape.tiles : tile_behind(a, end(a), b);
+        const int whole = shape.tiles * tile_weight<kDual>(a, b) + item_weight<kDual>(a);
+        t0 = at == 0 ? 0 : tile_behind<kDual>(a, at, b);
+        t1 = at + left >= whole ? shape.tiles : tile_behind<kDual>(a, end(a), b);
       } else {
-        t0 = tile_behind(a, at, b);
-        t1 = tile_behind(a, end(a), b);
+        t0 = tile_behind<kDual>(a, at, b);
+        t1 = tile_behind<kDual>(a, end(a), b);
       }
       if (t1 > t0) return;
       next_item(a);
@@ -327,14 +328,14 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
     if (prefix < 0) record_status(a.dev_status, RF_ERR_INVALID_ARG);
     prefix_tiles = (max(prefix, 0) + kAtTile - 1) / kAtTile;
     if (prefix_tiles > 0)
-      prefix_weight = static_cast<long long>(a.heads) * a.p_items * (static_cast<long long>(prefix_tiles) * a.w_prefix + a.w_item);
+      prefix_weight = static_cast<long long>(a.heads) * a.p_items * (static_cast<long long>(prefix_tiles) * tile_weight<kDual>(a, -1) + item_weight<kDual>(a));
   }
   auto weight_of = [&](int len) -> long long {
     return len < 0 ? 0ll
                    : static_cast<long long>(heads_of(a, 0)) *
                          (static_cast<long long>(a.m_items) *
-                              (static_cast<long long>((len + kAtTile - 1) / kAtTile) * tile_weight(a, 0) + item_weight(a)) +
-                          static_cast<long long>(a.draft_sum) * tile_weight(a, 0));
+                              (static_cast<long long>((len + kAtTile - 1) / kAtTile) * tile_weight<kDual>(a, 0) + item_weight<kDual>(a)) +
+                          static_cast<long long>(a.draft_sum) * tile_weight<kDual>(a, 0));
   };
   long long total = 0;
   int len = -1;  // of sequence `lane`, then of later ones
@@ -348,7 +349,7 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
   total = prefix < 0 ? 0 : total + prefix_weight;  // (a prefix that is out of range: no sequence can be answered)
   // (no share is less than a tile: every CTA between an item's first and last one has a part of it)
   long long most = total;
-  if constexpr (Args::kPrefix) most = total / max(a.w_prefix, a.w_own);
+  if constexpr (kDual && Args::kPrefix) most = total / max(a.w_prefix, a.w_own);
   const long long shares = min(static_cast<long long>(ctas), most);
   AttnShare p{};
   if (cta < shares) {
@@ -360,7 +361,7 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
         p.b = -1;
         p.len = prefix;
         p.n_tiles = prefix_tiles;
-        const long long per_item = static_cast<long long>(prefix_tiles) * a.w_prefix + a.w_item, per_head = a.p_items * per_item;
+        const long long per_item = static_cast<long long>(prefix_tiles) * tile_weight<kDual>(a, -1) + item_weight<kDual>(a), per_head = a.p_items * per_item;
         p.h = static_cast<int>(quick_div(first, per_head));
         const long long at = first - p.h * per_head;
         p.mt = static_cast<int>(quick_div(at, per_item));
@@ -388,7 +389,7 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
         r -= p.h * per_head;
         p.mt = 0;
         p.n_tiles = cached + draft_tiles<kDual>(a, 0);
-        const auto weight = [&] { return static_cast<long long>(p.n_tiles) * tile_weight(a, 0) + item_weight(a); };
+        const auto weight = [&] { return static_cast<long long>(p.n_tiles) * tile_weight<kDual>(a, 0) + item_weight<kDual>(a); };
         if (a.mask != nullptr) {
           p.mt = static_cast<int>(quick_div(r, weight()));
           r -= p.mt * weight();
@@ -407,7 +408,7 @@ __device__ void find_share(const Args& a, AttnShared* sh, int cta, int ctas) {
   if constexpr (Walk<kDual, Args>::kInStep) {
     AttnShare first{};
     const int whole = prefix_tiles * a.w_prefix + a.w_item;
-    if (p.weight > whole - p.at && p.b < 0 && prefix_tiles > a.in_step && a.p_items > 1 && tile_behind(a, p.at, -1) > 0 &&
+    if (p.weight > whole - p.at && p.b < 0 && prefix_tiles > a.in_step && a.p_items > 1 && tile_behind<kDual>(a, p.at, -1) > 0 &&
         (p.h + 1 < a.heads || p.mt + 1 < a.p_items)) {
       first = p;
       first.weight = whole - p.at;
@@ -1421,8 +1422,9 @@ __global__ void __launch_bounds__(kHD * 2) k_prefix_join(const __grid_constant__
       const bool own = i >= parts_0;
       if (own) i -= parts_0;
       const Place& p = own ? at[1] : at[0];
-      const int in_cta = p.of > 1 ? i & 3 : 0;
-      if (p.of > 1) i >>= 2;
+      const bool copied = kBatch < 8 && p.of > 1;  // (at most 32 rows of all sequences are one row tile, without copies)
+      const int in_cta = copied ? i & 3 : 0;
+      if (copied) i >>= 2;
       const float4* o = p.whole_o;
       const float2* w = p.whole_ml;
       int stride = p.whole_rows;
@@ -1795,9 +1797,9 @@ extern "C" rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const 
   a.p_seqs = lay.p_seqs;
   a.p_split = lay.p_split;
   a.p_items = lay.p_items;
-  // In tenths of a microsecond: a prefix tile with two row tiles takes 1.7 (products) to 2.0 (beside CTAs that stream
-  // caches), a tile of a pair, two of each head's, 1.8, an item's first and last steps some 6. Up to 128 rows a tile is
-  // its bytes, whoever's it is, and an item weighs four of them, as in rf_tree_attention.
+  // With two row tiles, in tenths of a microsecond: a prefix tile takes 1.7 (products) to 2.0 (beside CTAs that stream
+  // caches), a tile of a pair, two of each head's, 1.8, an item's first and last steps some 6. Where there are no pairs a
+  // tile is as long whoever's it is, and an item weighs four of them, as in rf_tree_attention.
   a.w_item = lay.pairs ? 60 : 68;
   a.w_prefix = lay.pairs ? 20 : 17;
   a.w_own = lay.pairs ? 18 : 17;
