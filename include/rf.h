@@ -695,7 +695,7 @@ typedef struct rf_prefix_attn_desc {
  *               written
  * All other arguments, masks, what is not seen, refusals and the status of lengths as for
  * rf_tree_attention; an infinity in a V row that is seen may come out as NaN. Scores, statistics and sums are
- * fp32, joined in a fixed order. */
+ * fp32, joined in a fixed order; a weight is rounded to bf16 for its product with v. */
 size_t rf_prefix_attn_workspace_bytes(const rf_prefix_attn_desc* desc);
 rf_status rf_prefix_attention(const rf_prefix_attn_desc* desc, const rf_bf16* q,
                               const rf_bf16* k_prefix, const rf_bf16* v_prefix, const int32_t* prefix_len,

@@ -58,11 +58,12 @@
 // sequence's own. Bound: the bytes of the prefix and of all own rows up to some 275 query rows per KV head (all
 // sequences together), the products over the prefix beyond. See PrefixArgs, and k_attn where it forms pairs of heads
 // and copies of few rows. Measured (128 channels, 8 KV heads): 4 sequences of one token, 5 query heads on one, over
-// 32,767 shared rows and up to 200 of their own: 37 us (3.7 TB/s; 20 would be the bytes). 64 of one token, 4 on
+// 32,767 shared rows and up to 200 of their own: 35 us (3.9 TB/s; 20 would be the bytes). 64 of one token, 4 on
 // one, over 16,384 and up to 1,024: 63 us (3.2 TB/s, 30). 16 trees of 64 nodes, 4 on one, over 28,672 and up to
-// 300: 365 us (1,330 TFLOP/s, 256 at the burst rate). 100 times three rows, 10 on one of 2
+// 300: 352 us from rest and 368 in long runs (1,370 and 1,310 TFLOP/s, 249 at the burst rate). 100 times three rows, 10 on one of 2
 // heads of 64 channels, over 4,099 and up to 4,000: 57 us (1.9 TB/s, 16). One sequence's cache at a time, the prefix in
-// each, would read the prefix 64 times in the second case.
+// each, would read the prefix 64 times in the second case. With two row tiles and 128 channels the kernel's four kinds of
+// items leave 60 bytes of a thread without a register; those without a prefix, and of 64 channels, have room.
 #include <algorithm>
 #include <cmath>
 

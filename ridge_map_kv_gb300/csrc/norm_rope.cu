@@ -13,14 +13,20 @@
 // itself, so there is no barrier); with the pieces loaded to registers instead the forward pass
 // took 151 us for 126 and the backward pass 69 for 60, as fewer bytes were in flight. Measured,
 // of bf16 heads of 128: 32,768 rows of 48 in 124 us (6.5 TB/s), 0.96 of a plain copy's rate; the
-// gradient of 8,191 rows of 40 in 54 us (4.6 TB/s), where issue slots share the bound (0.6 of
-// them used before its products were packed in pairs, 60 us); a step of 8 rows of 48 in 5 us,
-// which is a launch. Three forms say which pieces those are:
+// gradient of 8,191 rows of 40 in 54.5 us (4.6 TB/s; 60 before its products were packed in
+// pairs), where neither memory (53% of its peak) nor issue slots (46%) are full: 16 warps an SM
+// take one head after another through rotation, exchanges, root and stores; a step of 8 rows of
+// 48 in 5 us, which is a launch. fp32: 8,191 rows of 40 in 57 us (5.9 TB/s), their gradient in 93
+// (5.4 TB/s); rows of few heads are bound by their angles, which serve those only: 32,768 of 3 in 39.5 us
+// (2.5 TB/s). Where half of the channels turn, a lane's pieces lie further apart: 32,768 rows of
+// 48 bf16 heads in 153 us. Three forms say which pieces those are:
 //   kPieces   halves turn against each other and divide into pieces: a piece of the first half
 //             and its partner of the second, as in rf_rope
 //   kPairs    neighbouring channels turn against each other: any two pieces
 //   kShared   halves that do not divide into pieces: any two pieces, partners read from shared
-//             memory (16-byte accesses of global memory even so)
+//             memory (16-byte accesses of global memory even so). Of bf16 rows it holds an angle for
+//             each channel, and 20 bytes of the forward pass and 112 of the backward pass do not find a
+//             register
 //
 // The gains' gradients are sums over all rows: a thread keeps its channels' sums over its run of
 // heads, a CTA joins its threads' and leaves a row of partial sums in the workspace, and

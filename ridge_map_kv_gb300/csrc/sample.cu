@@ -19,16 +19,16 @@
 //             listed and sorted; all filters and the draw then take the list alone. (The least maximum of k groups
 //             leaves k (ln k + 0.6) tokens, and of 128 in one row of 20 more than a list holds.)
 //   any other  The bins' table is built and summed over the cluster. A run's end lies in one bin, whose tokens
-//             are listed and sorted (where they are too many, finer tables over the bin's (logit, token)
-//             pairs narrow them down). A pass over all then adds up the weights that stay and draws, another
-//             writes probabilities.
+//             are listed and narrowed down to 32 by tables over their (logit, token) pairs (as they are before,
+//             where a list does not hold them). A pass over all then adds up the weights that stay and draws,
+//             another writes probabilities.
 //
-// Bound: the logits' bytes (and the probabilities') from memory are the floor, but instructions bound what is
-// here: some 30 a token where masses are formed, and as many where weights and scores are, 90 of a row with a
-// nucleus. Measured: one row of 32,000 in 8 to 11 us with a top-k of 1 to 256, 12 to 17 without, of which some ten
-// barriers of a cluster are most; 64 fp32 rows of 131,072 in 14 to 18 us with such a top-k, 64 bf16 rows with nuclei
-// in 44.5 us; 256 fp32 rows of 131,072 with every filter and their probabilities in 147 us
-// (1.8 TB/s); 48 unfiltered rows of 100,003 with theirs in 32 us (1.8 TB/s).
+// Bound: the logits' bytes (and the probabilities') from memory are the floor. What takes the time of a row with a
+// nucleus is some 80 instructions a token (bf16; a third of the issue slots) and the waits between its passes,
+// each behind barriers of the cluster. Measured: one row of 32,000 in 9 to 11 us with a top-k of 1 to 256, 14 to 18
+// without, of which some ten such barriers are most; 64 fp32 rows of 131,072 in 14 to 18 us with such a top-k, 64 bf16
+// rows with nuclei in 43.8 us; 256 fp32 rows of 131,072 with every filter and their probabilities in 145 us
+// (1.9 TB/s); 48 unfiltered rows of 100,003 with theirs in 32 us (1.8 TB/s).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -48,14 +48,14 @@ constexpr int kSampleCtas = 8;        // CTAs of a cluster (the portable limit)
 constexpr int kSampleShare = 2048;    // least tokens of a CTA
 constexpr int kSampleLong = 32768;    // tokens from which on a row has two CTAs at least
 constexpr int kBins = 2048;           // of the table of masses: 64 an octave; the last one holds all smaller weights
-constexpr int kListed = 1024;         // tokens that are sorted at most
+constexpr int kListed = 1024;         // tokens that are listed at most
 constexpr int kFewTokens = 256;       // top-k up to which tokens are listed at once
 static_assert(2 * kFewTokens <= kSampleThreads && kSampleWarps * kSampleCtas <= 2 * kFewTokens, "groups of a cluster");
 constexpr int kSampleMaxVocab = 1 << 20;
 constexpr unsigned kSparse = 64;      // where more than one token in so many stays, the noise is read along with the
                                       // logits; below that only at the tokens that stay, each a wait of its own (64
-                                      // bf16 rows of 131,072 with nuclei: 51 us that way for all, 44.5 with this
-                                      // rule, 46 with 32 for 64 and 52 with 4)
+                                      // bf16 rows of 131,072 with nuclei: 47.5 us that way for all, 43.8 with this
+                                      // rule, the same with 32 for 64, 45.4 with 4)
 constexpr int kMassBits = 29;         // a weight of 1, within its bin
 constexpr int kCommonBits = 42;       // a weight of 1, over all bins
 constexpr int kCountShift = 43;       // a bin's entry: its count above the sum of 2^22 + q 2^29, each below 2^23
@@ -1057,7 +1057,7 @@ static rf_status launch_sample(const SampleArgs& a, int64_t rows, int sms, cudaS
   for (int i = 0; i < 64; ++i) p.t[i] = static_cast<unsigned long long>(std::ldexp(std::exp2(-i / 64.0), 63));
   // CTAs a row: a power of two, as many as run at once, each with enough tokens for its threads; long rows at least
   // two, so that rows that take longer than others are shared out and fewer are in L2 at a time (256 rows of
-  // 131,072, half of them without a small top-k: 283 us with one, 173 with two, 175 with four, 221 with eight).
+  // 131,072, half of them without a small top-k: 177 us with one, 145 with two, 149 with four, 190 with eight).
   unsigned ctas = a.vocab >= kSampleLong ? 2 : 1;
   while (ctas < kSampleCtas && static_cast<int64_t>(ctas) * kSampleShare < a.vocab && rows * ctas * 2 <= 2 * sms) ctas *= 2;
   ProfScope prof(s, RF_STAGE_SAMPLE);
