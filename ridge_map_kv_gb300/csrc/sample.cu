@@ -5,7 +5,7 @@
 // the ones of at least min_p of the first one's weight. So what stays is a run too, and is given by its
 // last token. Weights are w = 2^-t, t = (max - logit) log2(e) / T.
 //
-// Where the runs end is decided as in 64 bits. Logits are compared as they are. Masses are integers,
+// Where the runs end is decided by integers of 64 bits. Logits are compared as they are. Masses are integers,
 // so that sums do not depend on their order: t falls into one of 2,048 bins of 1/64 each; within a bin the
 // weights differ by a factor 1 - q that a polynomial of the rest of t gives to 2^-29, with the rounding to whole
 // numbers, so a bin needs the count of its tokens and the sum of their q, additions of integers to shared memory. The
